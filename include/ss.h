@@ -249,6 +249,70 @@ int ss_step(const ss_dims* dims,
             const void* Bm, const void* Cm, const float* Dskip, const void* z,
             const float* h_in, float* h_out, float* y, hipStream_t stream);
 
+/* ---- Linear attention with a decay for each head ------------------------------------------
+ *
+ * The recurrence of the scan with a matrix for a state: per batch row b and value head h
+ * (u = h / (heads / kheads) the key head it shares),
+ *   S_t = e^{g_t} S_{t-1} + k_t v_tᵀ        S [dk, dv]
+ *   o_t = scale · S_tᵀ q_t
+ * with S before the first token = s0[b,h] (or 0) and s_final[b,h] = S after the last one.
+ *   q, k : [B, T, Hk, dk]      v, o : [B, T, H, dv]   (in_dtype; o and the gradients of q, k, v
+ *                                                      have it too, each rounded once)
+ *   g    : the natural log of the decay, float32; by dims.decay absent (NULL: no decay), one
+ *          value a head [H], or one a token and head [B, T, H].  Meant for g <= 0; positive
+ *          values follow the formula until float32 overflows; -inf clears the state.
+ *   s0, s_final, ds_final, ds0 : [B, H, dk, dv] float32.
+ *   lengths : NULL, or [B] int32 on the device: row b has lengths[b] tokens (clamped to
+ *          [0, T]).  What the places behind hold is not used; o and the gradients are 0 there.
+ * q, k and v may be strided: dims.*_stride are elements from batch row to batch row, token to
+ * token and head to head (the last axis is contiguous); all three 0 means dense.  They need
+ * only their type's alignment, g and lengths 4 bytes; every other pointer 16 bytes.  Rows that
+ * start on 16 bytes and hold whole 16-byte pieces load fastest.  States, sums and log decays
+ * are kept in float32 or more; bfloat16 products round the scores and the state once where
+ * they feed o, dq, dk, dv (never where they feed s_final, ds0 or dg). */
+typedef enum { SS_LA_DECAY_NONE = 0, SS_LA_DECAY_HEAD = 1, SS_LA_DECAY_TOKEN = 2 } ss_la_decay;
+
+typedef struct ss_la_dims {
+    int64_t batch;        /* B >= 1 */
+    int64_t seqlen;       /* T >= 1 */
+    int64_t heads;        /* H: value heads */
+    int64_t kheads;       /* Hk: query and key heads, H % Hk == 0 */
+    int64_t dk, dv;       /* 1 .. 256 */
+    int64_t q_stride[3];  /* batch row, token, head; all 0: dense */
+    int64_t k_stride[3];
+    int64_t v_stride[3];
+    int32_t in_dtype;     /* ss_dtype of q, k, v, o, dO and the gradients of q, k, v */
+    int32_t decay;        /* ss_la_decay */
+    float scale;          /* finite */
+} ss_la_dims;
+
+/* Workspace bytes ss_la_fwd / ss_la_bwd need (may be 0 for the forward). */
+int ss_la_fwd_workspace_size(const ss_la_dims* dims, size_t* bytes);
+int ss_la_bwd_workspace_size(const ss_la_dims* dims, size_t* bytes);
+
+/* Chunked form over T tokens.  s0, s_final, lengths optional; g as dims.decay says. */
+int ss_la_fwd(const ss_la_dims* dims, const void* q, const void* k, const void* v, const float* g,
+              const float* s0, const int32_t* lengths, void* o, float* s_final,
+              void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Gradients of sum(dO·o) + sum(ds_final·s_final), the states recomputed from the inputs.
+ *   dO [B, T, H, dv] (in_dtype, dense); ds_final NULL = zero.
+ *   dq, dk [B, T, Hk, dk], dv [B, T, H, dv] (in_dtype, dense): required; a shared key head's
+ *   gradients are summed over its value heads in float32, in order.
+ *   dg : required unless there is no decay; shaped like g, float32.
+ *   ds0: required iff s0 is given (else must be NULL). */
+int ss_la_bwd(const ss_la_dims* dims, const void* q, const void* k, const void* v, const float* g,
+              const float* s0, const int32_t* lengths, const void* dO, const float* ds_final,
+              void* dq, void* dk, void* dv, float* dg, float* ds0,
+              void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* One token: q, k [B, Hk, dk], v, o [B, H, dv], g [B, H] or [H]; dims.seqlen must be 1 (token
+ * strides are not used).  s_in [B, H, dk, dv] is the state before the token, s_out the state
+ * after it; s_out may equal s_in (updated in place), otherwise they must not overlap.  Needs
+ * no workspace. */
+int ss_la_step(const ss_la_dims* dims, const void* q, const void* k, const void* v, const float* g,
+               const float* s_in, float* s_out, void* o, hipStream_t stream);
+
 /* Static description of a return code. */
 const char* ss_strerror(int code);
 

@@ -10,12 +10,17 @@ PyTorch fallback: if the compiled library is missing, ``load()`` raises.
     grads = ss_bwd(x, dt_raw, dt_bias, A, Bm, Cm, Dskip, dy, z=None, h0=None, dh_final=None,
                    h_ckpt=None)
     y_t = ss_step(x_t, dt_raw_t, dt_bias, A, B_t, C_t, Dskip, h, z_t=None)   # h updated in place
+    o = ss_la_fwd(q, k, v, g=None, s0=None, scale=1.0)      # linear attention, decay per head
+    grads = ss_la_bwd(q, k, v, do, g=None, s0=None, ds_final=None, scale=1.0)
+    o_t = ss_la_step(q_t, k_t, v_t, s, g_t=None, scale=1.0)                  # s updated in place
 
 Layouts: x, dt_raw, z, y [B, D, L]; Bm, Cm [B, N, L]; A [D, N]; dt_bias, Dskip [D];
 h0, h_final [B, D, N]; h_ckpt [B, D, ceil(L/16), N] (state entering every 16th step).  x, dt_raw, z, Bm, Cm are float32 or bfloat16 (all the same);
 everything else is float32.
 """
+import contextlib
 import ctypes
+import functools
 import os
 
 from ._build import LIB, build, stale, tree_id  # noqa: F401
@@ -26,13 +31,16 @@ SS_LAYOUT_AUTO, SS_LAYOUT_QUAD, SS_LAYOUT_LANE, SS_LAYOUT_OCT = 0, 1, 2, 3
 SS_DISC_EULER, SS_DISC_ZOH = 0, 1
 SS_ORDER_BDL, SS_ORDER_BLD = 0, 1
 SS_DT_FULL, SS_DT_SHARED = 0, 1
+SS_LA_DECAY_NONE, SS_LA_DECAY_HEAD, SS_LA_DECAY_TOKEN = 0, 1, 2
 
 ERRORS = {0: "SS_OK", -1: "SS_ERR_NULL", -2: "SS_ERR_DIMS", -3: "SS_ERR_DTYPE", -4: "SS_ERR_ALIGN",
           -5: "SS_ERR_WORKSPACE", -6: "SS_ERR_HIP", -7: "SS_ERR_UNSUPPORTED", -8: "SS_ERR_SCRATCH"}
 
 EXPORTS = ("ss_fwd", "ss_bwd", "ss_step", "ss_fwd_workspace_size", "ss_bwd_workspace_size",
            "ss_block_fwd", "ss_block_fwd_workspace_size", "ss_in_proj", "ss_strerror",
-           "ss_last_hip_error", "ss_version", "ss_build_id", "ss_fwd_noalloc")
+           "ss_last_hip_error", "ss_version", "ss_build_id", "ss_fwd_noalloc",
+           "ss_la_fwd", "ss_la_bwd", "ss_la_step", "ss_la_fwd_workspace_size",
+           "ss_la_bwd_workspace_size")
 
 
 class ss_dims(ctypes.Structure):
@@ -46,6 +54,14 @@ class ss_block_dims(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("d_in", ctypes.c_int64),
                 ("dim", ctypes.c_int64), ("dstate", ctypes.c_int64), ("plan", ctypes.c_int32),
                 ("layout", ctypes.c_int32)]
+
+
+class ss_la_dims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("heads", ctypes.c_int64),
+                ("kheads", ctypes.c_int64), ("dk", ctypes.c_int64), ("dv", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64 * 3), ("k_stride", ctypes.c_int64 * 3),
+                ("v_stride", ctypes.c_int64 * 3), ("in_dtype", ctypes.c_int32),
+                ("decay", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 class SSError(RuntimeError):
@@ -98,6 +114,16 @@ def load(path: str = LIB, expect: str = None):
     lib.ss_block_fwd_workspace_size.restype = ctypes.c_int
     lib.ss_in_proj.argtypes = [BD] + [P] * 5
     lib.ss_in_proj.restype = ctypes.c_int
+    LD = ctypes.POINTER(ss_la_dims)
+    lib.ss_la_fwd.argtypes = [LD] + [P] * 9 + [ctypes.c_size_t, P]
+    lib.ss_la_fwd.restype = ctypes.c_int
+    lib.ss_la_bwd.argtypes = [LD] + [P] * 14 + [ctypes.c_size_t, P]
+    lib.ss_la_bwd.restype = ctypes.c_int
+    lib.ss_la_step.argtypes = [LD] + [P] * 8
+    lib.ss_la_step.restype = ctypes.c_int
+    for f in ("ss_la_fwd_workspace_size", "ss_la_bwd_workspace_size"):
+        getattr(lib, f).argtypes = [LD, ctypes.POINTER(ctypes.c_size_t)]
+        getattr(lib, f).restype = ctypes.c_int
     lib.ss_strerror.argtypes = [ctypes.c_int]
     lib.ss_strerror.restype = ctypes.c_char_p
     lib.ss_last_hip_error.restype = ctypes.c_int
@@ -445,3 +471,207 @@ def ss_in_proj(u, W_in, *, x=None, z=None, stream=None):
     if rc != 0:
         raise SSError(rc, lib)
     return x, z
+
+
+# ---- linear attention with a decay for each head --------------------------------------------
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(device, stream, used):
+    """Context in which a call allocates and launches: the given stream (else the current one of
+    the tensors' device).  Memory made inside belongs to that stream, and the tensors that come
+    from elsewhere are recorded on it, so neither is handed out again while the call runs."""
+    import torch
+    if stream is None and device.index == torch.cuda.current_device():
+        return _HERE
+    s = torch.cuda.current_stream(device) if stream is None else stream
+    if stream is not None:
+        for t in used:
+            if t is not None and t.is_cuda:
+                t.record_stream(s)
+    return torch.cuda.stream(s)
+
+
+def _bytes(n, device):
+    import torch
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream():
+    import torch
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _in_dtype(x, name):
+    import torch
+    if x.dtype == torch.bfloat16:
+        return SS_BF16
+    if x.dtype == torch.float32:
+        return SS_F32
+    raise ValueError(f"{name} dtype must be float32 or bfloat16, got {x.dtype}")
+
+
+def make_la_dims(batch, seqlen, heads, kheads, dk, dv, in_dtype=SS_BF16,
+                 decay=SS_LA_DECAY_TOKEN, scale=1.0, q_stride=(0, 0, 0), k_stride=(0, 0, 0),
+                 v_stride=(0, 0, 0)):
+    T3 = ctypes.c_int64 * 3
+    return ss_la_dims(batch, seqlen, heads, kheads, dk, dv, T3(*q_stride), T3(*k_stride),
+                      T3(*v_stride), in_dtype, decay, scale)
+
+
+def la_workspace_size(dims, backward=False) -> int:
+    lib = load()
+    n = ctypes.c_size_t(0)
+    fn = lib.ss_la_bwd_workspace_size if backward else lib.ss_la_fwd_workspace_size
+    rc = fn(ctypes.byref(dims), ctypes.byref(n))
+    if rc != 0:
+        raise SSError(rc, lib)
+    return n.value
+
+
+@functools.lru_cache(maxsize=512)
+def _la_plan(key, backward):
+    """The dims structure of a call's shapes and strides, and the workspace they need."""
+    dims = make_la_dims(*key)
+    return dims, la_workspace_size(dims, backward)
+
+
+def _la_rows(t, name, shape, dtype, device):
+    """Checks a [.., head, width] input that may be strided; its element strides."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device or t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}, expected {dtype} "
+                         f"{shape} on {device}")
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous, got strides {st}")
+    if not any(st[:-1]) and t.numel() > shape[-1]:
+        raise ValueError(f"{name}: one row broadcast over every axis is not taken")
+    return st[:-1]
+
+
+def _la_key(q, k, v, g, s0, scale, lengths, step):
+    """Checks the inputs that the three calls share; the key of their dims, and (B, T, H, dk, dv)."""
+    import torch
+    nd = 3 if step else 4
+    if not isinstance(v, torch.Tensor) or not isinstance(q, torch.Tensor):
+        raise TypeError("q, k, v must be torch.Tensors")
+    if v.dim() != nd or q.dim() != nd:
+        raise ValueError(f"q, k, v must be {nd}-D, got shapes {tuple(q.shape)}, {tuple(v.shape)}")
+    dev, dt = v.device, v.dtype
+    lead = tuple(v.shape[:-2])
+    H, dv = v.shape[-2:]
+    Hk, dk = q.shape[-2:]
+    qs = _la_rows(q, "q", lead + (Hk, dk), dt, dev)
+    ks = _la_rows(k, "k", lead + (Hk, dk), dt, dev)
+    vs = _la_rows(v, "v", lead + (H, dv), dt, dev)
+    B, T = (lead[0], 1) if step else lead
+    if step:
+        qs, ks, vs = ((s[0], s[0], s[1]) for s in (qs, ks, vs))
+    f32 = torch.float32
+    decay = SS_LA_DECAY_NONE
+    if g is not None:
+        decay = SS_LA_DECAY_HEAD if g.dim() == 1 else SS_LA_DECAY_TOKEN
+        _check(g, "g", (H,) if g.dim() == 1 else lead + (H,), f32, dev)
+    _check(s0, "s" if step else "s0", (B, H, dk, dv), f32, dev)
+    _check(lengths, "lengths", (B,), torch.int32, dev)
+    key = (B, T, H, Hk, dk, dv, _in_dtype(v, "v"), decay, float(scale), qs, ks, vs)
+    return key, (B, T, H, dk, dv)
+
+
+def ss_la_fwd(q, k, v, g=None, s0=None, *, scale=1.0, lengths=None, return_final=False, o=None,
+              s_final=None, workspace=None, stream=None):
+    """Linear attention over T tokens through the C ABI: S_t = e^{g_t} S_{t-1} + k_t v_tᵀ,
+    o_t = scale · S_tᵀ q_t.  q, k [B, T, Hk, dk], v [B, T, H, dv] (float32 or bfloat16, may be
+    strided slices with a contiguous last axis; H % Hk == 0), g None, [H] or [B, T, H] float32
+    (natural log of the decay), s0 [B, H, dk, dv] float32, lengths [B] int32.  Returns o
+    [B, T, H, dv] in v's type, or (o, s_final) with return_final (or when s_final is passed)."""
+    import torch
+    lib = load()
+    key, (B, T, H, dk, dv) = _la_key(q, k, v, g, s0, scale, lengths, False)
+    dims, need = _la_plan(key, False)
+    dev = v.device
+    with _on(dev, stream, (q, k, v, g, s0, lengths, o, s_final, workspace)):
+        if o is None:
+            o = torch.empty((B, T, H, dv), dtype=v.dtype, device=dev)
+        _check(o, "o", (B, T, H, dv), v.dtype, dev)
+        if return_final and s_final is None:
+            s_final = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
+        _check(s_final, "s_final", (B, H, dk, dv), torch.float32, dev)
+        if workspace is None and need > 0:
+            workspace = _bytes(need, dev)
+        wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        rc = lib.ss_la_fwd(dims, _addr(q), _addr(k), _addr(v), _addr(g), _addr(s0),
+                           _addr(lengths), _addr(o), _addr(s_final), _addr(workspace), wbytes,
+                           _raw_stream())
+    if rc != 0:
+        raise SSError(rc, lib)
+    return o if s_final is None else (o, s_final)
+
+
+def ss_la_bwd(q, k, v, do, g=None, s0=None, ds_final=None, *, scale=1.0, lengths=None,
+              workspace=None, out=None, stream=None):
+    """Gradients of ss_la_fwd through the C ABI: do [B, T, H, dv] in v's type, ds_final
+    [B, H, dk, dv] float32.  Returns a dict dq, dk, dv (the inputs' type), dg (float32, shaped
+    like g; None without decay), ds0 (None without s0)."""
+    import torch
+    lib = load()
+    key, (B, T, H, dk, dv) = _la_key(q, k, v, g, s0, scale, lengths, False)
+    dims, need = _la_plan(key, True)
+    dev, dt, f32 = v.device, v.dtype, torch.float32
+    _check(do, "do", (B, T, H, dv), dt, dev)
+    _check(ds_final, "ds_final", (B, H, dk, dv), f32, dev)
+    shapes = dict(dq=(tuple(q.shape), dt), dk=(tuple(q.shape), dt), dv=(tuple(v.shape), dt),
+                  dg=None if g is None else (tuple(g.shape), f32),
+                  ds0=None if s0 is None else ((B, H, dk, dv), f32))
+    r = {} if out is None else dict(out)
+    with _on(dev, stream, (q, k, v, do, g, s0, ds_final, lengths, workspace, *r.values())):
+        for name, want in shapes.items():
+            if want is None:
+                r[name] = None
+                continue
+            if r.get(name) is None:
+                r[name] = torch.empty(want[0], dtype=want[1], device=dev)
+            _check(r[name], name, want[0], want[1], dev)
+        if workspace is None and need > 0:
+            workspace = _bytes(need, dev)
+        wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        rc = lib.ss_la_bwd(dims, _addr(q), _addr(k), _addr(v), _addr(g), _addr(s0),
+                           _addr(lengths), _addr(do), _addr(ds_final), _addr(r["dq"]),
+                           _addr(r["dk"]), _addr(r["dv"]), _addr(r["dg"]), _addr(r["ds0"]),
+                           _addr(workspace), wbytes, _raw_stream())
+    if rc != 0:
+        raise SSError(rc, lib)
+    return r
+
+
+def ss_la_step(q, k, v, s, g=None, *, scale=1.0, s_out=None, o=None, stream=None):
+    """One token through the C ABI: q, k [B, Hk, dk], v [B, H, dv], g None, [H] or [B, H], s
+    [B, H, dk, dv] float32, the state before the token.  The state after it goes to s_out
+    (default: s itself, updated in place).  Returns o [B, H, dv] in v's type."""
+    import torch
+    lib = load()
+    key, (B, _, H, dk, dv) = _la_key(q, k, v, g, s, scale, None, True)
+    dims, _ = _la_plan(key, False)
+    dev = v.device
+    with _on(dev, stream, (q, k, v, g, s, s_out, o)):
+        if s_out is None:
+            s_out = s
+        else:
+            _check(s_out, "s_out", (B, H, dk, dv), torch.float32, dev)
+        if o is None:
+            o = torch.empty((B, H, dv), dtype=v.dtype, device=dev)
+        else:
+            _check(o, "o", (B, H, dv), v.dtype, dev)
+        rc = lib.ss_la_step(dims, _addr(q), _addr(k), _addr(v), _addr(g), _addr(s), _addr(s_out),
+                            _addr(o), _raw_stream())
+    if rc != 0:
+        raise SSError(rc, lib)
+    return o

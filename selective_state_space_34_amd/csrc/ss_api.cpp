@@ -30,12 +30,9 @@ namespace {
 
 thread_local int g_last_hip_error = 0;
 
-int hip_fail(hipError_t e) {
-    g_last_hip_error = int(e);
-    return SS_ERR_HIP;
-}
-
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+using ss::hip_fail;
 
 constexpr int kMaxDevices = 64;
 std::mutex g_scratch_mu;
@@ -80,6 +77,11 @@ ss::DtRows dt_rows(const ss::Plan& p) {
 }
 
 }  // namespace
+
+int ss::hip_fail(hipError_t e) {
+    g_last_hip_error = int(e);
+    return SS_ERR_HIP;
+}
 
 extern "C" {
 

@@ -154,4 +154,84 @@ hipError_t launch_gemm_bf16_nt(const void* A, const void* W, float* C0, float* C
 hipError_t launch_xproj(const float* x, const float* Wx, float* part, float* dt, float* Bm,
                         float* Cm, int64_t M, int64_t D, int N, hipStream_t s);
 
+// ---- linear attention with a decay for each head (ss_la*.hip) -----------------------------------
+
+// Rows of one operand: element (b, t, head, i) at p + b·sb + t·st + (head / rep)·sh + i elements.
+struct LaOperand {
+    const void* p;
+    int64_t sb, st, sh;
+    int64_t rep;       // value heads that share a row
+    int dim;           // width
+    int vec;           // every row starts on 16 bytes and holds whole 16-byte pieces
+};
+
+// One sweep (ss_la_sweep.h).
+struct LaSweep {
+    LaOperand a, b, c, e;      // e: with dots
+    const float* g;            // nullable; log decays [B, T, H] or [H]
+    int decay_token;
+    const int32_t* lengths;    // nullable [B]
+    void* out;                 // [B, T, H, dC]; the operands' type, or float32 with out_f32
+    int out_f32;
+    const float* s_in;         // nullable; element (i, j) of row-head bh, segment s at
+    int64_t s_in_sz, s_in_i, s_in_j;   // (bh·in_seg + s)·s_in_sz + i·s_in_i + j·s_in_j
+    int64_t in_seg;
+    float* s_out;              // nullable [B, H, dA, dC]; state_only: [B, H, nseg, dA, dC]
+    int64_t s_out_sz;
+    float* dots;               // nullable [tiles, B, H, T]
+    float* seg_decay;          // state_only: [B, H, nseg]
+    int64_t B, T, H;
+    int tiles, nseg, grid_seg, seg0;   // the grid covers segments [seg0, seg0 + grid_seg)
+    int64_t seg_chunks;
+    int reverse, state_only;
+    float alpha, in_scale, up_scale;   // of a·b; of the entering state in out; of c in the state
+    int pad_a, nt;
+};
+hipError_t launch_la_sweep_bf16(const LaSweep& p, hipStream_t s);
+hipError_t launch_la_sweep_f32(const LaSweep& p, hipStream_t s);
+
+// State entering each segment, in place over what each segment adds: state [BH, nseg, sz].
+// first: nullable, element i·dC + j of row-head bh at bh·sz + i·f_i + j·f_j.
+struct LaCarry {
+    float* state;
+    const float* decay;        // [BH, nseg]
+    const float* first;
+    int64_t BH, sz, dC, f_i, f_j;
+    int nseg, reverse;
+};
+hipError_t launch_la_carry(const LaCarry& p, hipStream_t s);
+
+// dg from the row and column sums: token [B, T, H] (dg), or one value a head [H] through
+// head_part [B, H].  ds, s_final: both or neither; ds [B, H, dk, dv], s_final [B, H, dv, dk].
+struct LaDecayGrad {
+    const float *row, *col;    // [row_tiles | col_tiles, B, H, T]
+    int tiles;
+    const float *ds, *s_final;
+    const int32_t* lengths;
+    float *dg, *head_part;
+    int64_t B, T, H, dk, dv;
+    int decay_token;
+};
+hipError_t launch_la_decay_grad(const LaDecayGrad& p, hipStream_t s);
+
+// out [BT, Hk, d] = sum of part [BT, Hk·rep, d] over the rep heads of each group, in order.
+hipError_t launch_la_group_sum(int bf16, const float* part, void* out, int64_t BT, int64_t Hk,
+                               int64_t rep, int64_t d, hipStream_t s);
+
+// One token: state [B, H, dk, dv] float32, s_out may be s_in.
+struct LaStep {
+    LaOperand q, k, v;         // st unused
+    const float* g;            // nullable; [B, H] or [H]
+    int decay_token;
+    const float* s_in;
+    float* s_out;
+    void* o;                   // [B, H, dv], the operands' type
+    int64_t B, H, dk, dv;
+    float scale;
+};
+hipError_t launch_la_step(int bf16, const LaStep& p, hipStream_t s);
+
+// Records a failed HIP call for ss_last_hip_error; returns SS_ERR_HIP.
+int hip_fail(hipError_t e);
+
 }  // namespace ss

@@ -1,0 +1,268 @@
+// Linear attention with a decay for each head, beside the sweep (ss_la_sweep.h): the state
+// carried across segments, the log decays' gradient, the sum of shared heads' gradients and
+// the single-token step.
+#include "ss_device.h"
+#include "ss_kernels.h"
+
+namespace ss {
+
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ bf16_t round_bf16(float v) {
+    union { __bf16 h; bf16_t b; } u;
+    u.h = __bf16(v);
+    return u.b;
+}
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(bf16_t* p, float v) { *p = round_bf16(v); }
+
+// S_{s+1} = decay_s·S_s + U_s over the segments, element by element: state holds U and gets S.
+__global__ __launch_bounds__(256) void la_carry_kernel(const LaCarry p) {
+    const int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    const int64_t bh = id / p.sz, x = id - bh * p.sz;
+    if (bh >= p.BH) return;
+    float s = 0.0f;
+    if (p.first) s = p.first[bh * p.sz + (x / p.dC) * p.f_i + (x % p.dC) * p.f_j];
+    float* st = p.state + bh * p.nseg * p.sz + x;
+    const float* dec = p.decay + bh * p.nseg;
+    const int step = p.reverse ? -1 : 1;
+    int seg = p.reverse ? p.nseg - 1 : 0;
+    float u = st[seg * p.sz];
+    for (int i = 0; i < p.nseg - 1; ++i, seg += step) {
+        const float next = i + 2 < p.nseg ? st[(seg + step) * p.sz] : 0.0f;
+        st[seg * p.sz] = s;
+        s = fmaf(dec[seg], s, u);
+        u = next;
+    }
+    st[seg * p.sz] = s;
+}
+
+// dg_t = Σ_{u>=t} (row_u - col_u) + <dS_T, S_T>.  One workgroup for each (row, head), 1024
+// tokens at a time from the end; the running sum is kept in 64 bits, so its own rounding does
+// not grow with the length.
+__global__ __launch_bounds__(256) void la_decay_grad_kernel(const LaDecayGrad p) {
+    __shared__ double part[4];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int64_t bh = blockIdx.x, b = bh / p.H, h = bh - b * p.H;
+    auto block_sum = [&](double v) {
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m, 64);
+        __syncthreads();
+        if (lane == 0) part[wave] = v;
+        __syncthreads();
+        return part[0] + part[1] + part[2] + part[3];
+    };
+    int64_t len = p.T;
+    if (p.lengths) {
+        len = p.lengths[b];
+        len = len < 0 ? 0 : len > p.T ? p.T : len;
+    }
+    double run = 0.0, total = 0.0;
+    if (p.ds) {
+        double v = 0.0;
+        const int64_t sz = p.dk * p.dv;
+        for (int64_t x = tid; x < sz; x += 256) {
+            const int64_t i = x / p.dv, j = x - i * p.dv;
+            v += double(p.ds[bh * sz + x]) * double(p.s_final[bh * sz + j * p.dk + i]);
+        }
+        run = block_sum(v);
+    }
+    const int64_t tiles = (p.T + 1023) / 1024, plane = p.B * p.H * p.T;
+    for (int64_t w = tiles - 1; w >= 0; --w) {
+        const int64_t t0 = w * 1024 + tid * 4;
+        double v[4];
+#pragma unroll
+        for (int i = 3; i >= 0; --i) {
+            double x = 0.0;
+            if (t0 + i < len)
+                for (int q = 0; q < p.tiles; ++q) {
+                    const int64_t at = q * plane + bh * p.T + t0 + i;
+                    x += double(p.row[at]) - double(p.col[at]);
+                }
+            v[i] = x + (i < 3 ? v[i + 1] : 0.0);  // suffix sums of the thread's four
+        }
+        double s = v[0];                          // suffix sum over the lanes behind this one
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) {
+            const double o = __shfl_down(s, m, 64);
+            if (lane + m < 64) s += o;
+        }
+        const double wave_sum = __shfl(s, 0, 64);
+        __syncthreads();
+        if (lane == 0) part[wave] = wave_sum;
+        __syncthreads();
+        double behind = run + (s - v[0]), all = 0.0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (q > wave) behind += part[q];
+            all += part[q];
+        }
+        run += all;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t t = t0 + i;
+            const double dg = t < len ? v[i] + behind : 0.0;
+            if (p.decay_token) {
+                if (t < p.T) p.dg[(b * p.T + t) * p.H + h] = float(dg);
+            } else {
+                total += dg;
+            }
+        }
+    }
+    if (!p.decay_token) {
+        total = block_sum(total);
+        if (tid == 0) p.head_part[bh] = float(total);
+    }
+}
+
+__global__ __launch_bounds__(256) void la_head_sum_kernel(const float* part, float* dg, int64_t B,
+                                                          int64_t H) {
+    const int64_t h = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    if (h >= H) return;
+    double v = 0.0;
+    for (int64_t b = 0; b < B; ++b) v += part[b * H + h];
+    dg[h] = float(v);
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void la_group_sum_kernel(const float* __restrict__ part,
+                                                           T* __restrict__ out, int64_t n,
+                                                           int64_t rep, int64_t d) {
+    const int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x;  // (token, key head, i)
+    if (id >= n) return;
+    const int64_t g = id / d, i = id - g * d;
+    const float* q = part + g * rep * d + i;
+    float v = 0.0f;
+    for (int64_t r = 0; r < rep; ++r) v += q[r * d];
+    put(out + id, v);
+}
+
+// One token.  S ← e^g S + k vᵀ, o = α Sᵀ q: every element of the state is read and written
+// once, and that traffic is all of the cost.  A workgroup takes CW·VW columns of one head's
+// state: CW threads across them, 256 / CW row groups, each thread its rows in batches of kRows
+// loads in flight.  Row groups meet in LDS for o.
+template <typename T, int CW, int VW>
+__global__ __launch_bounds__(256) void la_step_kernel(const LaStep p) {
+    constexpr int RG = 256 / CW, kRows = 8;
+    __shared__ float ql[256], kl[256];
+    __shared__ float red[RG][CW * VW];
+    const int tid = threadIdx.x, cw = tid % CW, rg = tid / CW;
+    const int64_t slabs = (p.dv + CW * VW - 1) / (CW * VW);
+    const int64_t bh = blockIdx.x / slabs, slab = blockIdx.x - bh * slabs;
+    const int64_t b = bh / p.H, h = bh - b * p.H;
+    const int64_t j = (slab * CW + cw) * VW;
+    const bool on = j < p.dv;                       // VW divides dv
+    const float* sp = p.s_in + bh * p.dk * p.dv + j;
+    float* so = p.s_out + bh * p.dk * p.dv + j;
+    auto row = [](const LaOperand& o, int64_t b, int64_t h) {
+        return static_cast<const T*>(o.p) + b * o.sb + (h / o.rep) * o.sh;
+    };
+    if (tid < p.dk) {
+        ql[tid] = p.scale * to_f32(row(p.q, b, h)[tid]);
+        kl[tid] = to_f32(row(p.k, b, h)[tid]);
+    }
+    float v[VW], acc[VW];
+#pragma unroll
+    for (int c = 0; c < VW; ++c) {
+        v[c] = on ? to_f32(row(p.v, b, h)[j + c]) : 0.0f;
+        acc[c] = 0.0f;
+    }
+    float a = 1.0f;
+    if (p.g) a = expf(p.g[p.decay_token ? bh : h]);
+    __syncthreads();
+    for (int64_t i0 = rg; i0 < p.dk; i0 += RG * kRows) {
+        float s[kRows][VW];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            const int64_t i = i0 + r * RG;
+            if (!on || i >= p.dk) continue;
+            if constexpr (VW == 4) {
+                const f32x4 x = *reinterpret_cast<const f32x4*>(sp + i * p.dv);
+#pragma unroll
+                for (int c = 0; c < VW; ++c) s[r][c] = x[c];
+            } else {
+                s[r][0] = sp[i * p.dv];
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            const int64_t i = i0 + r * RG;
+            if (!on || i >= p.dk) continue;
+            const float kk = kl[i], qq = ql[i];
+#pragma unroll
+            for (int c = 0; c < VW; ++c) {
+                s[r][c] = fmaf(a, s[r][c], kk * v[c]);
+                acc[c] = fmaf(qq, s[r][c], acc[c]);
+            }
+            if constexpr (VW == 4) {
+                *reinterpret_cast<f32x4*>(so + i * p.dv) = f32x4{s[r][0], s[r][1], s[r][2], s[r][3]};
+            } else {
+                so[i * p.dv] = s[r][0];
+            }
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < VW; ++c) red[rg][cw * VW + c] = acc[c];
+    __syncthreads();
+    if (tid < CW * VW) {
+        const int64_t col = slab * CW * VW + tid;
+        float o = 0.0f;
+#pragma unroll
+        for (int g = 0; g < RG; ++g) o += red[g][tid];
+        if (col < p.dv) put(static_cast<T*>(p.o) + bh * p.dv + col, o);
+    }
+}
+
+template <typename T, int CW, int VW>
+hipError_t launch_step_slab(const LaStep& p, hipStream_t s) {
+    const int64_t slabs = (p.dv + CW * VW - 1) / (CW * VW);
+    const dim3 grid{unsigned(p.B * p.H * slabs)};
+    hipLaunchKernelGGL((la_step_kernel<T, CW, VW>), grid, dim3(256), 0, s, p);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_step_type(const LaStep& p, hipStream_t s) {
+    // four columns a thread where rows keep 16-byte alignment
+    if (p.dv % 4 == 0) {
+        if (p.B * p.H >= 512) return launch_step_slab<T, 32, 4>(p, s);
+        return launch_step_slab<T, 8, 4>(p, s);
+    }
+    return launch_step_slab<T, 32, 1>(p, s);
+}
+
+}  // namespace
+
+hipError_t launch_la_carry(const LaCarry& p, hipStream_t s) {
+    const dim3 grid{unsigned((p.BH * p.sz + 255) / 256)};
+    hipLaunchKernelGGL(la_carry_kernel, grid, dim3(256), 0, s, p);
+    return hipGetLastError();
+}
+
+hipError_t launch_la_decay_grad(const LaDecayGrad& p, hipStream_t s) {
+    hipLaunchKernelGGL(la_decay_grad_kernel, dim3(unsigned(p.B * p.H)), dim3(256), 0, s, p);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.decay_token) return e;
+    hipLaunchKernelGGL(la_head_sum_kernel, dim3(unsigned((p.H + 255) / 256)), dim3(256), 0, s,
+                       p.head_part, p.dg, p.B, p.H);
+    return hipGetLastError();
+}
+
+hipError_t launch_la_group_sum(int bf16, const float* part, void* out, int64_t BT, int64_t Hk,
+                               int64_t rep, int64_t d, hipStream_t s) {
+    const int64_t n = BT * Hk * d;
+    const dim3 grid{unsigned((n + 255) / 256)};
+    if (bf16) hipLaunchKernelGGL(la_group_sum_kernel<bf16_t>, grid, dim3(256), 0, s, part,
+                                 static_cast<bf16_t*>(out), n, rep, d);
+    else hipLaunchKernelGGL(la_group_sum_kernel<float>, grid, dim3(256), 0, s, part,
+                            static_cast<float*>(out), n, rep, d);
+    return hipGetLastError();
+}
+
+hipError_t launch_la_step(int bf16, const LaStep& p, hipStream_t s) {
+    return bf16 ? launch_step_type<bf16_t>(p, s) : launch_step_type<float>(p, s);
+}
+
+}  // namespace ss

@@ -1,0 +1,265 @@
+// C ABI of the linear attention: validation, workspace carving and launches on the caller's
+// stream.  Declared in include/ss.h; nothing is launched before every argument is checked.
+#include "ss.h"
+
+#include <hip/hip_runtime.h>
+
+#include "ss_kernels.h"
+#include "ss_la_plan.h"
+
+namespace {
+
+using ss::hip_fail;
+using ss::LaOperand;
+using ss::LaPlan;
+using ss::LaSweep;
+
+bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Row layout of a [B, T, heads, dim] tensor, dense where no stride is given.
+LaOperand operand(const LaPlan& p, const void* ptr, const int64_t* stride, int64_t heads,
+                  int64_t dim) {
+    LaOperand o{};
+    o.p = ptr;
+    o.sb = p.T * heads * dim; o.st = heads * dim; o.sh = dim;
+    if (stride && (stride[0] || stride[1] || stride[2])) {
+        o.sb = stride[0]; o.st = stride[1]; o.sh = stride[2];
+    }
+    o.rep = p.H / heads;
+    o.dim = int(dim);
+    const int64_t v = p.in_dtype == SS_BF16 ? 8 : 4;
+    o.vec = aligned(ptr, 16) && o.sb % v == 0 && o.st % v == 0 && o.sh % v == 0 && dim % v == 0;
+    return o;
+}
+
+struct Inputs {
+    LaOperand q, k, v;
+};
+
+// Checks what the three entry points share.
+int check(const ss_la_dims* d, bool backward, const void* q, const void* k, const void* v,
+          const float* g, const int32_t* lengths, LaPlan* p) {
+    const int rc = ss::make_la_plan(*d, backward, p);
+    if (rc != SS_OK) return rc;
+    if (!q || !k || !v || ((p->decay != SS_LA_DECAY_NONE) != (g != nullptr))) return SS_ERR_NULL;
+    const size_t el = p->in_dtype == SS_BF16 ? 2 : 4;
+    if (!aligned(q, el) || !aligned(k, el) || !aligned(v, el) || !aligned(g, 4) ||
+        !aligned(lengths, 4))
+        return SS_ERR_ALIGN;
+    return SS_OK;
+}
+
+Inputs inputs(const ss_la_dims* d, const LaPlan& p, const void* q, const void* k, const void* v) {
+    return Inputs{operand(p, q, d->q_stride, p.Hk, p.dk), operand(p, k, d->k_stride, p.Hk, p.dk),
+                  operand(p, v, d->v_stride, p.H, p.dv)};
+}
+
+hipError_t sweep(const LaPlan& p, const LaSweep& s, hipStream_t stream) {
+    return p.in_dtype == SS_BF16 ? ss::launch_la_sweep_bf16(s, stream)
+                                 : ss::launch_la_sweep_f32(s, stream);
+}
+
+LaSweep base(const LaPlan& p, const float* g, const int32_t* lengths, int reverse) {
+    LaSweep s{};
+    s.g = g; s.decay_token = p.decay == SS_LA_DECAY_TOKEN; s.lengths = lengths;
+    s.B = p.B; s.T = p.T; s.H = p.H;
+    s.nseg = int(p.nseg); s.seg_chunks = p.seg_chunks;
+    s.reverse = reverse;
+    // forward: the scale goes into out; reverse: the state collects scale·q doᵀ, so that dS_T
+    // enters it as it is
+    s.alpha = p.scale;
+    s.in_scale = reverse ? 1.0f : p.scale;
+    s.up_scale = reverse ? p.scale : 1.0f;
+    return s;
+}
+
+void shape(LaSweep* s, const ss::LaShape& f) {
+    s->pad_a = f.pad_a; s->nt = f.nt; s->tiles = f.tiles;
+}
+
+// States entering every segment, [B, H, nseg, dA, dC], from the operands b, c of `s` and the
+// state that enters the whole sequence (element (i, j) at i·f_i + j·f_j; nullable).
+hipError_t segment_states(const LaPlan& p, LaSweep s, const ss::LaShape& f, const float* first,
+                          int64_t f_i, int64_t f_j, float* state, float* decay,
+                          hipStream_t stream) {
+    const int64_t sz = p.dk * p.dv;
+    shape(&s, f);
+    s.state_only = 1;
+    s.a = s.b; s.e = s.b;
+    s.grid_seg = s.nseg - 1; s.seg0 = s.reverse ? 1 : 0;
+    s.s_in = nullptr; s.in_seg = 1; s.s_in_sz = sz;
+    s.s_out = state; s.s_out_sz = sz; s.seg_decay = decay;
+    s.dots = nullptr; s.out = nullptr;
+    const hipError_t e = sweep(p, s, stream);
+    if (e != hipSuccess) return e;
+    ss::LaCarry c{};
+    c.state = state; c.decay = decay; c.first = first; c.BH = p.B * p.H; c.sz = sz;
+    c.dC = s.c.dim; c.f_i = f_i; c.f_j = f_j; c.nseg = s.nseg; c.reverse = s.reverse;
+    return ss::launch_la_carry(c, stream);
+}
+
+// The whole sweep: state [dA, dC] enters each segment from `state` (nseg > 1) or from `first`;
+// strides as element (i, j).
+hipError_t full_sweep(const LaPlan& p, LaSweep s, const ss::LaShape& f, const float* first,
+                      int64_t f_i, int64_t f_j, const float* state, int64_t s_i, int64_t s_j,
+                      hipStream_t stream) {
+    shape(&s, f);
+    s.grid_seg = s.nseg; s.seg0 = 0;
+    s.s_in_sz = p.dk * p.dv;
+    s.s_out_sz = p.dk * p.dv;
+    if (s.nseg > 1) {
+        s.s_in = state; s.in_seg = s.nseg; s.s_in_i = s_i; s.s_in_j = s_j;
+    } else {
+        s.s_in = first; s.in_seg = 1; s.s_in_i = f_i; s.s_in_j = f_j;
+    }
+    return sweep(p, s, stream);
+}
+
+int workspace_size(const ss_la_dims* dims, bool backward, size_t* bytes) {
+    if (!dims || !bytes) return SS_ERR_NULL;
+    LaPlan p;
+    const int rc = ss::make_la_plan(*dims, backward, &p);
+    if (rc != SS_OK) return rc;
+    *bytes = p.total;
+    return SS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ss_la_fwd_workspace_size(const ss_la_dims* dims, size_t* bytes) {
+    return workspace_size(dims, false, bytes);
+}
+
+int ss_la_bwd_workspace_size(const ss_la_dims* dims, size_t* bytes) {
+    return workspace_size(dims, true, bytes);
+}
+
+int ss_la_fwd(const ss_la_dims* dims, const void* q, const void* k, const void* v, const float* g,
+              const float* s0, const int32_t* lengths, void* o, float* s_final,
+              void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (!dims) return SS_ERR_NULL;
+    LaPlan p;
+    const int rc = check(dims, false, q, k, v, g, lengths, &p);
+    if (rc != SS_OK) return rc;
+    if (!o) return SS_ERR_NULL;
+    if (!aligned(o, 16) || !aligned(s0, 16) || !aligned(s_final, 16)) return SS_ERR_ALIGN;
+    if (p.total > 0 && (!workspace || workspace_bytes < p.total)) return SS_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return SS_ERR_ALIGN;
+    char* ws = static_cast<char*>(workspace);
+    float* state = reinterpret_cast<float*>(ws + p.off_state);
+    const Inputs in = inputs(dims, p, q, k, v);
+    LaSweep s = base(p, g, lengths, 0);
+    s.a = in.q; s.b = in.k; s.c = in.v; s.e = in.v;
+    hipError_t e;
+    if (p.nseg > 1) {
+        e = segment_states(p, s, p.fwd, s0, p.dv, 1, state,
+                           reinterpret_cast<float*>(ws + p.off_decay), stream);
+        if (e != hipSuccess) return hip_fail(e);
+    }
+    s.out = o; s.s_out = s_final;
+    e = full_sweep(p, s, p.fwd, s0, p.dv, 1, state, p.dv, 1, stream);
+    return e == hipSuccess ? SS_OK : hip_fail(e);
+}
+
+int ss_la_bwd(const ss_la_dims* dims, const void* q, const void* k, const void* v, const float* g,
+              const float* s0, const int32_t* lengths, const void* dO, const float* ds_final,
+              void* dq, void* dk, void* dv, float* dg, float* ds0,
+              void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (!dims) return SS_ERR_NULL;
+    LaPlan p;
+    const int rc = check(dims, true, q, k, v, g, lengths, &p);
+    if (rc != SS_OK) return rc;
+    if (!dO || !dq || !dk || !dv) return SS_ERR_NULL;
+    if ((g != nullptr) != (dg != nullptr) || (s0 != nullptr) != (ds0 != nullptr)) return SS_ERR_NULL;
+    const void* ptrs[] = {s0, dO, ds_final, dq, dk, dv, dg, ds0};
+    for (const void* x : ptrs)
+        if (!aligned(x, 16)) return SS_ERR_ALIGN;
+    if (p.total > 0 && (!workspace || workspace_bytes < p.total)) return SS_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return SS_ERR_ALIGN;
+    char* ws = static_cast<char*>(workspace);
+    auto at = [ws](size_t off) { return reinterpret_cast<float*>(ws + off); };
+    float* state = at(p.off_state);
+    float* decay = at(p.off_decay);
+    float* part = p.Hk < p.H ? at(p.off_part) : nullptr;
+    float* s_final = g && ds_final ? at(p.off_final) : nullptr;
+    const int bf16 = p.in_dtype == SS_BF16;
+    const Inputs in = inputs(dims, p, q, k, v);
+    const LaOperand od = operand(p, dO, nullptr, p.H, p.dv);
+    hipError_t e;
+
+    // 1. dq: forward sweep of (dO, v, k), state S_tᵀ [dv, dk]
+    LaSweep s = base(p, g, lengths, 0);
+    s.a = od; s.b = in.v; s.c = in.k; s.e = in.q;
+    if (p.nseg > 1) {
+        e = segment_states(p, s, p.rev, s0, 1, p.dv, state, decay, stream);
+        if (e != hipSuccess) return hip_fail(e);
+    }
+    s.out = part ? static_cast<void*>(part) : dq; s.out_f32 = part != nullptr;
+    s.dots = g ? at(p.off_row) : nullptr;
+    s.s_out = s_final;
+    e = full_sweep(p, s, p.rev, s0, 1, p.dv, state, p.dk, 1, stream);
+    if (e != hipSuccess) return hip_fail(e);
+    if (part) {
+        e = ss::launch_la_group_sum(bf16, part, dq, p.B * p.T, p.Hk, p.H / p.Hk, p.dk, stream);
+        if (e != hipSuccess) return hip_fail(e);
+    }
+
+    // 2. dv: reverse sweep of (k, q, dO), state dS_t [dk, dv]; its segments' states serve dk too
+    s = base(p, g, lengths, 1);
+    s.a = in.k; s.b = in.q; s.c = od; s.e = od;
+    if (p.nseg > 1) {
+        e = segment_states(p, s, p.fwd, ds_final, p.dv, 1, state, decay, stream);
+        if (e != hipSuccess) return hip_fail(e);
+    }
+    s.out = dv;
+    s.s_out = ds0;
+    e = full_sweep(p, s, p.fwd, ds_final, p.dv, 1, state, p.dv, 1, stream);
+    if (e != hipSuccess) return hip_fail(e);
+
+    // 3. dk: reverse sweep of (v, dO, q), state dS_tᵀ [dv, dk], read transposed
+    s = base(p, g, lengths, 1);
+    s.a = in.v; s.b = od; s.c = in.q; s.e = in.k;
+    s.out = part ? static_cast<void*>(part) : dk; s.out_f32 = part != nullptr;
+    s.dots = g ? at(p.off_col) : nullptr;
+    e = full_sweep(p, s, p.rev, ds_final, 1, p.dv, state, 1, p.dv, stream);
+    if (e != hipSuccess) return hip_fail(e);
+    if (part) {
+        e = ss::launch_la_group_sum(bf16, part, dk, p.B * p.T, p.Hk, p.H / p.Hk, p.dk, stream);
+        if (e != hipSuccess) return hip_fail(e);
+    }
+
+    // 4. dg from the row and column sums
+    if (g) {
+        ss::LaDecayGrad d{};
+        d.row = at(p.off_row); d.col = at(p.off_col); d.tiles = p.rev.tiles;
+        d.ds = ds_final; d.s_final = s_final; d.lengths = lengths;
+        d.dg = dg; d.head_part = at(p.off_head);
+        d.B = p.B; d.T = p.T; d.H = p.H; d.dk = p.dk; d.dv = p.dv;
+        d.decay_token = p.decay == SS_LA_DECAY_TOKEN;
+        e = ss::launch_la_decay_grad(d, stream);
+        if (e != hipSuccess) return hip_fail(e);
+    }
+    return SS_OK;
+}
+
+int ss_la_step(const ss_la_dims* dims, const void* q, const void* k, const void* v, const float* g,
+               const float* s_in, float* s_out, void* o, hipStream_t stream) {
+    if (!dims) return SS_ERR_NULL;
+    if (dims->seqlen != 1) return SS_ERR_DIMS;
+    LaPlan p;
+    const int rc = check(dims, false, q, k, v, g, nullptr, &p);
+    if (rc != SS_OK) return rc;
+    if (!s_in || !s_out || !o) return SS_ERR_NULL;
+    if (!aligned(s_in, 16) || !aligned(s_out, 16) || !aligned(o, 16)) return SS_ERR_ALIGN;
+    const Inputs in = inputs(dims, p, q, k, v);
+    ss::LaStep s{};
+    s.q = in.q; s.k = in.k; s.v = in.v; s.g = g; s.decay_token = p.decay == SS_LA_DECAY_TOKEN;
+    s.s_in = s_in; s.s_out = s_out; s.o = o;
+    s.B = p.B; s.H = p.H; s.dk = p.dk; s.dv = p.dv; s.scale = p.scale;
+    const hipError_t e = ss::launch_la_step(p.in_dtype == SS_BF16, s, stream);
+    return e == hipSuccess ? SS_OK : hip_fail(e);
+}
+
+}  // extern "C"
