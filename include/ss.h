@@ -313,6 +313,60 @@ int ss_la_bwd(const ss_la_dims* dims, const void* q, const void* k, const void* 
 int ss_la_step(const ss_la_dims* dims, const void* q, const void* k, const void* v, const float* g,
                const float* s_in, float* s_out, void* o, hipStream_t stream);
 
+/* ---- Root-mean-square norm with the residual's addition ------------------------------------
+ *
+ *   r = x + res (or x)       y = r / sqrt(mean(r²) + eps) · w        over rows of `dim` elements
+ * x [rows, dim] in_dtype; res and r [rows, dim] res_dtype (float32, or bfloat16 with bfloat16 x);
+ * w [dim] float32.  y is formed from the unrounded sum and has in_dtype, or with dims.q8 it is
+ * in 8 bits with one float32 scale a row: y ≈ code · y_scale, y_scale = max|y| / 448 (e4m3) or
+ * / 127 (int8).  A row with max|y| <= 1e-35 has zero codes.  A row that holds a NaN has a NaN
+ * scale. */
+typedef enum { SS_Q8_NONE = 0, SS_Q8_FP8 = 1, SS_Q8_INT8 = 2 } ss_q8;
+
+typedef struct ss_rms_dims {
+    int64_t rows;       /* >= 1 */
+    int64_t dim;        /* 1 .. 32768 */
+    int32_t in_dtype;   /* ss_dtype of x, y, dy */
+    int32_t res_dtype;  /* ss_dtype of res, r, dr, dx (float32 where in_dtype is) */
+    int32_t q8;         /* ss_q8 of y (backward: SS_Q8_NONE) */
+    float eps;          /* finite, >= 0 */
+} ss_rms_dims;
+
+/* res NULL: no residual, and r must be NULL; else r is required and may equal res.  y_scale
+ * [rows] is required iff q8 is set.  Needs no workspace. */
+int ss_rms_fwd(const ss_rms_dims* dims, const void* x, const void* res, const float* w, void* r,
+               void* y, float* y_scale, hipStream_t stream);
+
+/* Gradients from dy [rows, dim] (in_dtype), r as the forward stored it (its input where there
+ * was no residual) and, where r goes on beside the norm, that path's gradient dr (else NULL):
+ * dx [rows, dim] (res_dtype; the gradient of x and of res alike; may equal dr), dw [dim]
+ * float32, summed in a fixed order. */
+int ss_rms_bwd_workspace_size(const ss_rms_dims* dims, size_t* bytes);
+int ss_rms_bwd(const ss_rms_dims* dims, const void* dy, const void* r, const float* w,
+               const void* dr, void* dx, float* dw, void* workspace, size_t workspace_bytes,
+               hipStream_t stream);
+
+/* ---- Products with 4-bit weights ------------------------------------------------------------
+ *
+ *   y[m, i] = x_scale[m] · Σ_j x[m, j] · scales[i, j / group] · (u[i, j] - zeros[i, j / group])
+ * for the few rows of a decode step (any number is taken; 16 at a time, 5 of float32).
+ *   wq     [n, k / 2] bytes: u[i, 2j] in the low half of byte j of row i, u[i, 2j+1] in the high
+ *   scales [n, ceil(k / group)] bfloat16
+ *   zeros  [n, ceil(k / group)] bytes; NULL: 8
+ *   x      [rows, k] in_dtype, or 8-bit codes (x_q8) with x_scale [rows] float32
+ *   y      [rows, n] y_dtype, rounded once; sums are float32
+ * Needs no workspace. */
+typedef struct ss_q4_dims {
+    int64_t rows, n, k;   /* k a multiple of 32 */
+    int32_t group;        /* 32, 64 or 128; the last group may be short */
+    int32_t in_dtype;     /* ss_dtype of x (not used with x_q8) */
+    int32_t x_q8;         /* ss_q8 of x */
+    int32_t y_dtype;      /* ss_dtype of y */
+} ss_q4_dims;
+
+int ss_q4_mv(const ss_q4_dims* dims, const void* x, const float* x_scale, const void* wq,
+             const void* scales, const void* zeros, void* y, hipStream_t stream);
+
 /* Static description of a return code. */
 const char* ss_strerror(int code);
 

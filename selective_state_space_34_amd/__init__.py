@@ -13,6 +13,10 @@ PyTorch fallback: if the compiled library is missing, ``load()`` raises.
     o = ss_la_fwd(q, k, v, g=None, s0=None, scale=1.0)      # linear attention, decay per head
     grads = ss_la_bwd(q, k, v, do, g=None, s0=None, ds_final=None, scale=1.0)
     o_t = ss_la_step(q_t, k_t, v_t, s, g_t=None, scale=1.0)                  # s updated in place
+    y, r = ss_rms_fwd(x, w, res)                 # RMS norm after the residual's addition
+    y8, y_scale, r = ss_rms_fwd(x, w, res, q8=SS_Q8_FP8)                     # ... in 8 bits
+    dx, dw = ss_rms_bwd(dy, r, w, dr=None)
+    y = ss_q4_mv(x, wq, scales, zeros=None, x_scale=None)                    # 4-bit weights
 
 Layouts: x, dt_raw, z, y [B, D, L]; Bm, Cm [B, N, L]; A [D, N]; dt_bias, Dskip [D];
 h0, h_final [B, D, N]; h_ckpt [B, D, ceil(L/16), N] (state entering every 16th step).  x, dt_raw, z, Bm, Cm are float32 or bfloat16 (all the same);
@@ -32,6 +36,7 @@ SS_DISC_EULER, SS_DISC_ZOH = 0, 1
 SS_ORDER_BDL, SS_ORDER_BLD = 0, 1
 SS_DT_FULL, SS_DT_SHARED = 0, 1
 SS_LA_DECAY_NONE, SS_LA_DECAY_HEAD, SS_LA_DECAY_TOKEN = 0, 1, 2
+SS_Q8_NONE, SS_Q8_FP8, SS_Q8_INT8 = 0, 1, 2
 
 ERRORS = {0: "SS_OK", -1: "SS_ERR_NULL", -2: "SS_ERR_DIMS", -3: "SS_ERR_DTYPE", -4: "SS_ERR_ALIGN",
           -5: "SS_ERR_WORKSPACE", -6: "SS_ERR_HIP", -7: "SS_ERR_UNSUPPORTED", -8: "SS_ERR_SCRATCH"}
@@ -40,7 +45,8 @@ EXPORTS = ("ss_fwd", "ss_bwd", "ss_step", "ss_fwd_workspace_size", "ss_bwd_works
            "ss_block_fwd", "ss_block_fwd_workspace_size", "ss_in_proj", "ss_strerror",
            "ss_last_hip_error", "ss_version", "ss_build_id", "ss_fwd_noalloc",
            "ss_la_fwd", "ss_la_bwd", "ss_la_step", "ss_la_fwd_workspace_size",
-           "ss_la_bwd_workspace_size")
+           "ss_la_bwd_workspace_size", "ss_rms_fwd", "ss_rms_bwd", "ss_rms_bwd_workspace_size",
+           "ss_q4_mv")
 
 
 class ss_dims(ctypes.Structure):
@@ -62,6 +68,17 @@ class ss_la_dims(ctypes.Structure):
                 ("q_stride", ctypes.c_int64 * 3), ("k_stride", ctypes.c_int64 * 3),
                 ("v_stride", ctypes.c_int64 * 3), ("in_dtype", ctypes.c_int32),
                 ("decay", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class ss_rms_dims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("dim", ctypes.c_int64), ("in_dtype", ctypes.c_int32),
+                ("res_dtype", ctypes.c_int32), ("q8", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class ss_q4_dims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("group", ctypes.c_int32), ("in_dtype", ctypes.c_int32), ("x_q8", ctypes.c_int32),
+                ("y_dtype", ctypes.c_int32)]
 
 
 class SSError(RuntimeError):
@@ -124,6 +141,15 @@ def load(path: str = LIB, expect: str = None):
     for f in ("ss_la_fwd_workspace_size", "ss_la_bwd_workspace_size"):
         getattr(lib, f).argtypes = [LD, ctypes.POINTER(ctypes.c_size_t)]
         getattr(lib, f).restype = ctypes.c_int
+    RD = ctypes.POINTER(ss_rms_dims)
+    lib.ss_rms_fwd.argtypes = [RD] + [P] * 7
+    lib.ss_rms_fwd.restype = ctypes.c_int
+    lib.ss_rms_bwd.argtypes = [RD] + [P] * 7 + [ctypes.c_size_t, P]
+    lib.ss_rms_bwd.restype = ctypes.c_int
+    lib.ss_rms_bwd_workspace_size.argtypes = [RD, ctypes.POINTER(ctypes.c_size_t)]
+    lib.ss_rms_bwd_workspace_size.restype = ctypes.c_int
+    lib.ss_q4_mv.argtypes = [ctypes.POINTER(ss_q4_dims)] + [P] * 7
+    lib.ss_q4_mv.restype = ctypes.c_int
     lib.ss_strerror.argtypes = [ctypes.c_int]
     lib.ss_strerror.restype = ctypes.c_char_p
     lib.ss_last_hip_error.restype = ctypes.c_int
@@ -675,3 +701,160 @@ def ss_la_step(q, k, v, s, g=None, *, scale=1.0, s_out=None, o=None, stream=None
     if rc != 0:
         raise SSError(rc, lib)
     return o
+
+
+# ---- root-mean-square norm with the residual's addition, in 8 bits where asked -----------------
+
+def make_rms_dims(rows, dim, in_dtype=SS_BF16, res_dtype=SS_BF16, q8=SS_Q8_NONE, eps=1e-5):
+    return ss_rms_dims(rows, dim, in_dtype, res_dtype, q8, eps)
+
+
+def rms_workspace_size(dims) -> int:
+    lib = load()
+    n = ctypes.c_size_t(0)
+    rc = lib.ss_rms_bwd_workspace_size(ctypes.byref(dims), ctypes.byref(n))
+    if rc != 0:
+        raise SSError(rc, lib)
+    return n.value
+
+
+@functools.lru_cache(maxsize=512)
+def _rms_plan(key, backward):
+    dims = make_rms_dims(*key)
+    return dims, rms_workspace_size(dims) if backward else 0
+
+
+def _rows_of(x, name):
+    if x.dim() < 1 or x.numel() == 0:
+        raise ValueError(f"{name} must have rows and a width, got shape {tuple(x.shape)}")
+    D = x.shape[-1]
+    return x.numel() // D, D
+
+
+def ss_rms_fwd(x, w, res=None, *, eps=1e-5, q8=SS_Q8_NONE, y=None, y_scale=None, r=None,
+               stream=None):
+    """y = r / sqrt(mean(r²) + eps) · w with r = x + res, over the last axis, through the C ABI.
+    x [..., D] float32 or bfloat16; res like x, or float32; w [D] float32.  y has x's type, or
+    with q8 = SS_Q8_FP8 / SS_Q8_INT8 it holds float8_e4m3fn / int8 codes with y_scale [...]
+    float32, y ≈ code · y_scale.  r (default new; may be res) takes the sum, in res's type.
+    Returns y, followed by y_scale with q8 and by r with res."""
+    import torch
+    lib = load()
+    M, D = _rows_of(x, "x")
+    dev, shape, f32 = x.device, tuple(x.shape), torch.float32
+    dt = _in_dtype(x, "x")
+    _check(x, "x", shape, x.dtype, dev)
+    _check(w, "w", (D,), f32, dev)
+    rdt = x.dtype if res is None else res.dtype
+    _check(res, "res", shape, rdt, dev)
+    dims, _ = _rms_plan((M, D, dt, dt if res is None else _in_dtype(res, "res"), q8, float(eps)), False)
+    with _on(dev, stream, (x, w, res, y, y_scale, r)):
+        yt = {SS_Q8_FP8: torch.float8_e4m3fn, SS_Q8_INT8: torch.int8}.get(q8, x.dtype)
+        if y is None:
+            y = torch.empty(shape, dtype=yt, device=dev)
+        else:
+            _check(y, "y", shape, yt, dev)
+        if q8 != SS_Q8_NONE:
+            if y_scale is None:
+                y_scale = torch.empty(shape[:-1], dtype=f32, device=dev)
+            else:
+                _check(y_scale, "y_scale", shape[:-1], f32, dev)
+        if res is not None:
+            if r is None:
+                r = torch.empty(shape, dtype=rdt, device=dev)
+            else:
+                _check(r, "r", shape, rdt, dev)
+        rc = lib.ss_rms_fwd(dims, _addr(x), _addr(res), _addr(w), _addr(r), _addr(y),
+                            _addr(y_scale), _raw_stream())
+    if rc != 0:
+        raise SSError(rc, lib)
+    out = (y,) if q8 == SS_Q8_NONE else (y, y_scale)
+    if res is not None:
+        out += (r,)
+    return out if len(out) > 1 else y
+
+
+def ss_rms_bwd(dy, r, w, dr=None, *, eps=1e-5, dx=None, dw=None, workspace=None, stream=None):
+    """Gradients of ss_rms_fwd through the C ABI: dy [..., D] (the forward's x's type), r [..., D]
+    the sum the forward returned (its x without a residual), dr like r, the gradient of r where
+    it goes on beside the norm.  Returns dx (like r: the gradient of x and of res) and dw [D]
+    float32."""
+    import torch
+    lib = load()
+    M, D = _rows_of(r, "r")
+    dev, shape, f32 = r.device, tuple(r.shape), torch.float32
+    _check(r, "r", shape, r.dtype, dev)
+    _check(dy, "dy", shape, dy.dtype, dev)
+    _check(w, "w", (D,), f32, dev)
+    _check(dr, "dr", shape, r.dtype, dev)
+    dims, need = _rms_plan((M, D, _in_dtype(dy, "dy"), _in_dtype(r, "r"), SS_Q8_NONE, float(eps)), True)
+    with _on(dev, stream, (dy, r, w, dr, dx, dw, workspace)):
+        if dx is None:
+            dx = torch.empty(shape, dtype=r.dtype, device=dev)
+        else:
+            _check(dx, "dx", shape, r.dtype, dev)
+        if dw is None:
+            dw = torch.empty((D,), dtype=f32, device=dev)
+        else:
+            _check(dw, "dw", (D,), f32, dev)
+        if workspace is None:
+            workspace = _bytes(need, dev)
+        wbytes = workspace.numel() * workspace.element_size()
+        rc = lib.ss_rms_bwd(dims, _addr(dy), _addr(r), _addr(w), _addr(dr), _addr(dx), _addr(dw),
+                            _addr(workspace), wbytes, _raw_stream())
+    if rc != 0:
+        raise SSError(rc, lib)
+    return dx, dw
+
+
+# ---- products with 4-bit weights ---------------------------------------------------------------
+
+def make_q4_dims(rows, n, k, group=128, in_dtype=SS_BF16, x_q8=SS_Q8_NONE, y_dtype=SS_BF16):
+    return ss_q4_dims(rows, n, k, group, in_dtype, x_q8, y_dtype)
+
+
+@functools.lru_cache(maxsize=512)
+def _q4_plan(key):
+    return make_q4_dims(*key)
+
+
+def ss_q4_mv(x, wq, scales, zeros=None, *, group=128, x_scale=None, y=None, y_dtype=None,
+             stream=None):
+    """y = x · Wᵀ with W[i, j] = scales[i, j // group] · (u[i, j] - zeros[i, j // group]) through
+    the C ABI.  x [..., K] float32 or bfloat16, or float8_e4m3fn or int8 with x_scale [...]
+    float32; wq [N, K / 2] uint8, two codes a byte, the first in the low half; scales
+    [N, ceil(K / group)] bfloat16; zeros the same in uint8 (None: 8).  Returns y [..., N], in
+    y_dtype (default: float32 for float32 x, else bfloat16)."""
+    import torch
+    lib = load()
+    M, K = _rows_of(x, "x")
+    dev, lead = x.device, tuple(x.shape[:-1])
+    q8 = {torch.float8_e4m3fn: SS_Q8_FP8, torch.int8: SS_Q8_INT8}.get(x.dtype, SS_Q8_NONE)
+    dt = SS_BF16 if q8 else _in_dtype(x, "x")
+    if (x_scale is not None) != (q8 != SS_Q8_NONE):
+        raise ValueError("x_scale goes with 8-bit x, and only with it")
+    if y is not None:
+        y_dtype = y.dtype
+    elif y_dtype is None:
+        y_dtype = torch.float32 if x.dtype == torch.float32 else torch.bfloat16
+    if wq.dim() != 2 or group <= 0:
+        raise ValueError(f"wq must be [N, K / 2] and group positive, got {tuple(wq.shape)}, {group}")
+    N, ng = wq.shape[0], -(-K // group)
+    _check(x, "x", (*lead, K), x.dtype, dev)
+    _check(wq, "wq", (N, K // 2), torch.uint8, dev)
+    _check(scales, "scales", (N, ng), torch.bfloat16, dev)
+    _check(zeros, "zeros", (N, ng), torch.uint8, dev)
+    _check(x_scale, "x_scale", lead, torch.float32, dev)
+    if y_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"y dtype must be float32 or bfloat16, got {y_dtype}")
+    dims = _q4_plan((M, N, K, group, dt, q8, SS_F32 if y_dtype == torch.float32 else SS_BF16))
+    with _on(dev, stream, (x, wq, scales, zeros, x_scale, y)):
+        if y is None:
+            y = torch.empty((*lead, N), dtype=y_dtype, device=dev)
+        else:
+            _check(y, "y", (*lead, N), y_dtype, dev)
+        rc = lib.ss_q4_mv(dims, _addr(x), _addr(x_scale), _addr(wq), _addr(scales), _addr(zeros),
+                          _addr(y), _raw_stream())
+    if rc != 0:
+        raise SSError(rc, lib)
+    return y

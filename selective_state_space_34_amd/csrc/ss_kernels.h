@@ -6,6 +6,8 @@
 
 #include <type_traits>
 
+#include "ss.h"
+
 namespace ss {
 
 // Steps between the forward's state checkpoints (the backward's tile length).
@@ -230,6 +232,41 @@ struct LaStep {
     float scale;
 };
 hipError_t launch_la_step(int bf16, const LaStep& p, hipStream_t s);
+
+// ---- norm (ss_norm.hip) --------------------------------------------------------------------------
+
+// Forward: x [M, D] (in_dtype), res (nullable) and r [M, D] (res_dtype), y in in_dtype or 8-bit
+// codes with y_scale [M].  Backward: x is dy, res is r, r is dx; dr nullable; part [grid, D].
+struct RmsLaunch {
+    const void *x, *res, *dr;
+    const float* w;
+    void *r, *y;
+    float *y_scale, *part;
+    int64_t M, D;
+    float eps, inv_d;
+    int in_dtype, res_dtype, q8, vec;
+    int threads, pieces, grid;   // threads of a row, eight-element pieces of each, workgroups
+};
+hipError_t launch_rms_fwd(const RmsLaunch& p, hipStream_t s);
+hipError_t launch_rms_bwd(const RmsLaunch& p, float* dw, hipStream_t s);
+
+// ---- products with 4-bit weights (ss_q4.hip) -----------------------------------------------------
+
+constexpr int kQ4Lds = 57344;    // most bytes of x that a workgroup keeps in LDS (two a CU)
+
+struct Q4Launch {
+    const void* x;               // [M, K]
+    const float* x_scale;        // nullable [M]
+    const uint8_t* wq;           // [N, K / 2]
+    const uint16_t* scales;      // bf16 [N, groups]
+    const uint8_t* zeros;        // nullable [N, groups]
+    void* y;                     // [M, N]
+    int64_t M, N, K, groups;
+    int64_t slab;                // k of x in LDS at a time, a multiple of the group
+    int mb;                      // rows of x of a workgroup
+    int group, in_dtype, x_q8, y_dtype;
+};
+hipError_t launch_q4(const Q4Launch& p, hipStream_t s);
 
 // Records a failed HIP call for ss_last_hip_error; returns SS_ERR_HIP.
 int hip_fail(hipError_t e);

@@ -1,4 +1,4 @@
-// C ABI of the linear attention: validation, workspace carving and launches on the caller's
+// C ABI of the linear attention, the norm and the 4-bit products: validation, workspace carving and launches on the caller's
 // stream.  Declared in include/ss.h; nothing is launched before every argument is checked.
 #include "ss.h"
 
@@ -122,6 +122,14 @@ int workspace_size(const ss_la_dims* dims, bool backward, size_t* bytes) {
     if (rc != SS_OK) return rc;
     *bytes = p.total;
     return SS_OK;
+}
+
+ss::RmsLaunch rms_launch(const ss_rms_dims& d, const ss::RmsPlan& p) {
+    ss::RmsLaunch l{};
+    l.M = p.M; l.D = p.D; l.eps = d.eps; l.inv_d = float(1.0 / double(p.D));
+    l.in_dtype = d.in_dtype; l.res_dtype = d.res_dtype; l.vec = p.vec;
+    l.threads = p.threads; l.pieces = p.pieces; l.grid = p.grid;
+    return l;
 }
 
 }  // namespace
@@ -259,6 +267,73 @@ int ss_la_step(const ss_la_dims* dims, const void* q, const void* k, const void*
     s.s_in = s_in; s.s_out = s_out; s.o = o;
     s.B = p.B; s.H = p.H; s.dk = p.dk; s.dv = p.dv; s.scale = p.scale;
     const hipError_t e = ss::launch_la_step(p.in_dtype == SS_BF16, s, stream);
+    return e == hipSuccess ? SS_OK : hip_fail(e);
+}
+
+int ss_rms_fwd(const ss_rms_dims* dims, const void* x, const void* res, const float* w, void* r,
+               void* y, float* y_scale, hipStream_t stream) {
+    if (!dims) return SS_ERR_NULL;
+    ss::RmsPlan p;
+    const int rc = ss::make_rms_plan(*dims, false, &p);
+    if (rc != SS_OK) return rc;
+    if (!x || !w || !y || ((res != nullptr) != (r != nullptr)) ||
+        ((dims->q8 != SS_Q8_NONE) != (y_scale != nullptr)))
+        return SS_ERR_NULL;
+    const void* ptrs[] = {x, res, w, r, y, y_scale};
+    for (const void* q : ptrs)
+        if (!aligned(q, 16)) return SS_ERR_ALIGN;
+    ss::RmsLaunch l = rms_launch(*dims, p);
+    l.x = x; l.res = res; l.w = w; l.r = r; l.y = y; l.y_scale = y_scale; l.q8 = dims->q8;
+    const hipError_t e = ss::launch_rms_fwd(l, stream);
+    return e == hipSuccess ? SS_OK : hip_fail(e);
+}
+
+int ss_rms_bwd_workspace_size(const ss_rms_dims* dims, size_t* bytes) {
+    if (!dims || !bytes) return SS_ERR_NULL;
+    ss::RmsPlan p;
+    const int rc = ss::make_rms_plan(*dims, true, &p);
+    if (rc != SS_OK) return rc;
+    *bytes = p.total;
+    return SS_OK;
+}
+
+int ss_rms_bwd(const ss_rms_dims* dims, const void* dy, const void* r, const float* w,
+               const void* dr, void* dx, float* dw, void* workspace, size_t workspace_bytes,
+               hipStream_t stream) {
+    if (!dims) return SS_ERR_NULL;
+    ss::RmsPlan p;
+    const int rc = ss::make_rms_plan(*dims, true, &p);
+    if (rc != SS_OK) return rc;
+    if (!dy || !r || !w || !dx || !dw) return SS_ERR_NULL;
+    const void* ptrs[] = {dy, r, w, dr, dx, dw};
+    for (const void* q : ptrs)
+        if (!aligned(q, 16)) return SS_ERR_ALIGN;
+    if (!workspace || workspace_bytes < p.total) return SS_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return SS_ERR_ALIGN;
+    ss::RmsLaunch l = rms_launch(*dims, p);
+    l.x = dy; l.res = r; l.w = w; l.dr = dr; l.r = dx; l.part = static_cast<float*>(workspace);
+    const hipError_t e = ss::launch_rms_bwd(l, dw, stream);
+    return e == hipSuccess ? SS_OK : hip_fail(e);
+}
+
+int ss_q4_mv(const ss_q4_dims* dims, const void* x, const float* x_scale, const void* wq,
+             const void* scales, const void* zeros, void* y, hipStream_t stream) {
+    if (!dims) return SS_ERR_NULL;
+    ss::Q4Plan p;
+    const int rc = ss::make_q4_plan(*dims, ss::kQ4Lds, &p);
+    if (rc != SS_OK) return rc;
+    if (!x || !wq || !scales || !y || ((dims->x_q8 != SS_Q8_NONE) != (x_scale != nullptr)))
+        return SS_ERR_NULL;
+    const void* ptrs[] = {x, x_scale, wq, scales, zeros, y};
+    for (const void* q : ptrs)
+        if (!aligned(q, 16)) return SS_ERR_ALIGN;
+    ss::Q4Launch l{};
+    l.x = x; l.x_scale = x_scale; l.wq = static_cast<const uint8_t*>(wq);
+    l.scales = static_cast<const uint16_t*>(scales); l.zeros = static_cast<const uint8_t*>(zeros);
+    l.y = y; l.M = dims->rows; l.N = dims->n; l.K = dims->k;
+    l.groups = p.groups; l.slab = p.slab; l.mb = p.mb; l.group = dims->group;
+    l.in_dtype = dims->in_dtype; l.x_q8 = dims->x_q8; l.y_dtype = dims->y_dtype;
+    const hipError_t e = ss::launch_q4(l, stream);
     return e == hipSuccess ? SS_OK : hip_fail(e);
 }
 

@@ -109,4 +109,78 @@ inline int make_la_plan(const ss_la_dims& d, bool backward, LaPlan* out) {
     return SS_OK;
 }
 
+// Norm: how many threads share a row and how many eight-element pieces each holds.
+struct RmsPlan {
+    int64_t M, D;
+    int threads, pieces, grid, vec;
+    size_t total;                // backward: part [grid, D] float32
+};
+
+constexpr int64_t kRmsMaxDim = 32768;
+
+inline int make_rms_plan(const ss_rms_dims& d, bool backward, RmsPlan* out) {
+    if (d.rows <= 0 || d.dim <= 0 || d.dim > kRmsMaxDim) return SS_ERR_DIMS;
+    if (!mul_ok(d.rows, d.dim, int64_t(1) << 40)) return SS_ERR_DIMS;
+    if (d.in_dtype != SS_F32 && d.in_dtype != SS_BF16) return SS_ERR_DTYPE;
+    if (d.res_dtype != SS_F32 && d.res_dtype != SS_BF16) return SS_ERR_DTYPE;
+    if (d.in_dtype == SS_F32 && d.res_dtype != SS_F32) return SS_ERR_DTYPE;
+    if (d.q8 < SS_Q8_NONE || d.q8 > SS_Q8_INT8 || (backward && d.q8 != SS_Q8_NONE))
+        return SS_ERR_DTYPE;
+    if (!(d.eps >= 0.0f) || !(d.eps - d.eps == 0.0f)) return SS_ERR_DIMS;
+    RmsPlan p{};
+    p.M = d.rows; p.D = d.dim;
+    p.vec = d.dim % 8 == 0;
+    const int64_t D = d.dim;
+    // a wave a row up to six pieces where there are rows enough to fill the part; wider rows,
+    // and few rows, take a workgroup
+    if (D <= 512 || (D <= 64 * 8 * 6 && d.rows >= 1024)) {
+        p.threads = 64;
+        p.pieces = D <= 512 ? 1 : D <= 1024 ? 2 : D <= 2048 ? 4 : 6;
+    } else if (D <= 256 * 8 * 4) {
+        p.threads = 256;
+        p.pieces = D <= 2048 ? 1 : D <= 4096 ? 2 : 4;
+    } else {
+        p.threads = 1024;
+        p.pieces = D <= 16384 ? 2 : 4;
+    }
+    const int64_t wg_rows = p.threads >= 256 ? 1 : 256 / p.threads;
+    const int64_t need = (d.rows + wg_rows - 1) / wg_rows;
+    // workgroups take rows in turn: enough of them to fill the 256 CUs
+    const int64_t most = p.threads == 1024 ? 512 : backward ? 512 : 2048;
+    p.grid = int(need < most ? need : most);
+    p.total = backward ? align256(size_t(p.grid) * size_t(D) * sizeof(float)) : 0;
+    *out = p;
+    return SS_OK;
+}
+
+// 4-bit products: rows of x a workgroup takes, and how much of them stays in LDS at a time.
+struct Q4Plan {
+    int64_t groups, slab;
+    int mb;
+};
+
+inline int make_q4_plan(const ss_q4_dims& d, int64_t lds, Q4Plan* out) {
+    if (d.rows <= 0 || d.n <= 0 || d.k <= 0 || d.k % 32 != 0) return SS_ERR_DIMS;
+    if (d.group != 32 && d.group != 64 && d.group != 128) return SS_ERR_DIMS;
+    if (d.in_dtype != SS_F32 && d.in_dtype != SS_BF16) return SS_ERR_DTYPE;
+    if (d.y_dtype != SS_F32 && d.y_dtype != SS_BF16) return SS_ERR_DTYPE;
+    if (d.x_q8 < SS_Q8_NONE || d.x_q8 > SS_Q8_INT8) return SS_ERR_DTYPE;
+    const int64_t lim = int64_t(1) << 38;
+    if (!mul_ok(d.rows, d.k, lim) || !mul_ok(d.n, d.k, lim) || !mul_ok(d.rows, d.n, lim))
+        return SS_ERR_DIMS;
+    Q4Plan p{};
+    const int terms = d.x_q8 == SS_Q8_NONE && d.in_dtype == SS_F32 ? 3 : 1;
+    p.mb = 16 / terms;
+    if (d.rows < p.mb) p.mb = int(d.rows);
+    if ((d.rows + p.mb - 1) / p.mb > kMaxGridYZ) return SS_ERR_DIMS;
+    p.groups = (d.k + d.group - 1) / d.group;
+    // rows are padded by 8 elements in LDS
+    int64_t most = lds / 2 / (p.mb * terms) - 8;
+    most = most / (4 * d.group) * (4 * d.group);   // whole rounds of the four waves
+    const int64_t all = p.groups * d.group;
+    p.slab = all < most ? all : most;
+    *out = p;
+    return SS_OK;
+}
+
 }  // namespace ss

@@ -1,0 +1,345 @@
+// Root-mean-square norm with the residual's addition, its 8-bit output and its gradients, for
+// gfx950.
+//
+//   r = x + res                      (kept unrounded for y; stored in the residual's type)
+//   y = r·c·w,  c = 1/sqrt(mean(r²) + eps)
+//   8 bits: scale = max|y| / top, codes = y·(top / max|y|), top 448 (e4m3) or 127 (int8)
+//   dx = dr + c·(w·dy) - r·(c³/D)·Σ(w·dy·r)        dw = Σ_rows dy·r·c
+//
+// The work is traffic: every element is read once and written once, a row staying in registers
+// between the sums and the result.  A row belongs to P threads (64, 256 or 1024, by its length
+// and by how many rows there are), eight consecutive elements of it to each thread at a time,
+// NV such pieces a thread; sums meet by shuffles, across waves through LDS.  Workgroups take
+// rows in turn, so that in the gradient the columns' sums stay in registers over a workgroup's
+// rows; the sums of dw over workgroups are added by a second kernel in a fixed order.  w is
+// read for every row (it stays in the CU's cache): holding it too would cost 8·NV registers
+// and with them the waves that keep loads in flight.
+#include "ss_device.h"
+#include "ss_kernels.h"
+
+namespace ss {
+
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// Eight consecutive elements from col, zeros beyond the width; vec: whole aligned pieces.
+template <typename T>
+__device__ __forceinline__ void get8(const T* row, int64_t col, int64_t dim, int vec, float (&o)[8]) {
+    if (vec) {
+        if (col < dim) {
+            load8(row + col, o);
+            return;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = col + e < dim ? to_f32(row[col + e]) : 0.0f;
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = 0.0f;
+}
+
+__device__ __forceinline__ void put8(float* row, int64_t col, int64_t dim, int vec, const float (&v)[8]) {
+    if (vec) {
+        if (col < dim) store8(row + col, v);
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (col + e < dim) row[col + e] = v[e];
+}
+__device__ __forceinline__ void put8(bf16_t* row, int64_t col, int64_t dim, int vec, const float (&v)[8]) {
+    bf16x8 h;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = __bf16(v[e]);
+    __bf16* p = reinterpret_cast<__bf16*>(row);
+    if (vec) {
+        if (col < dim) *reinterpret_cast<bf16x8*>(p + col) = h;
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (col + e < dim) p[col + e] = h[e];
+}
+
+// Eight codes of v·inv: e4m3 (round to nearest even; |v·inv| <= 448, so none overflows) or
+// int8 in [-127, 127].
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv, int q8) {
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        float a[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a[e] = v[4 * i + e] * inv;
+        if (q8 == SS_Q8_FP8) {
+            int x = __builtin_amdgcn_cvt_pk_fp8_f32(a[0], a[1], 0, false);
+            w[i] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(a[2], a[3], x, true));
+        } else {
+            w[i] = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int c = int(rintf(fminf(fmaxf(a[e], -127.0f), 127.0f)));
+                w[i] |= uint32_t(c & 255) << (8 * e);
+            }
+        }
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+// Sums (or maxima of bit patterns) over the P threads of a row.  P > 64: one row a workgroup;
+// two slots alternate so that one barrier a call is enough.
+template <int P>
+struct RowSum {
+    float* slots;   // [2][16], LDS
+    int at = 0;
+    __device__ __forceinline__ float sum(float v) {
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m, 64);
+        if constexpr (P > 64) {
+            float* s = slots + 16 * at;
+            at ^= 1;
+            if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+            __syncthreads();
+            v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < P / 64; ++w) v += s[w];
+        }
+        return v;
+    }
+    __device__ __forceinline__ uint32_t max(uint32_t v) {
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) {
+            const uint32_t o = uint32_t(__shfl_xor(int(v), m, 64));
+            v = v > o ? v : o;
+        }
+        if constexpr (P > 64) {
+            uint32_t* s = reinterpret_cast<uint32_t*>(slots) + 16 * at;
+            at ^= 1;
+            if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+            __syncthreads();
+            v = 0;
+#pragma unroll
+            for (int w = 0; w < P / 64; ++w) v = v > s[w] ? v : s[w];
+        }
+        return v;
+    }
+};
+
+template <typename Tx, typename Tr, int P, int NV>
+__global__ __launch_bounds__(P > 256 ? P : 256) void rms_fwd_kernel(const RmsLaunch p) {
+    constexpr int kRowsWG = P >= 256 ? 1 : 256 / P;
+    __shared__ float slots[32];
+    RowSum<P> rs{slots};
+    const int tid = threadIdx.x % P;
+    const int64_t D = p.D, step = int64_t(gridDim.x) * kRowsWG;
+    for (int64_t row = int64_t(blockIdx.x) * kRowsWG + threadIdx.x / P; row < p.M; row += step) {
+        const Tx* x = static_cast<const Tx*>(p.x) + row * D;
+        float v[NV][8], sq = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) get8(x, (int64_t(j) * P + tid) * 8, D, p.vec, v[j]);
+        if (p.res) {
+            const Tr* res = static_cast<const Tr*>(p.res) + row * D;
+            Tr* r = static_cast<Tr*>(p.r) + row * D;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int64_t col = (int64_t(j) * P + tid) * 8;
+                float a[8];
+                get8(res, col, D, p.vec, a);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[j][e] += a[e];
+                put8(r, col, D, p.vec, v[j]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sq = fmaf(v[j][e], v[j][e], sq);
+        sq = rs.sum(sq);
+        const float c = rsqrtf(sq * p.inv_d + p.eps);
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            float w[8];
+            get8(p.w, (int64_t(j) * P + tid) * 8, D, p.vec, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                v[j][e] = v[j][e] * c * w[e];
+                // bit patterns of magnitudes order like the magnitudes, NaN above all
+                const uint32_t m = __float_as_uint(v[j][e]) & 0x7fffffffu;
+                top = top > m ? top : m;
+            }
+        }
+        if (p.q8 == SS_Q8_NONE) {
+            Tx* y = static_cast<Tx*>(p.y) + row * D;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) put8(y, (int64_t(j) * P + tid) * 8, D, p.vec, v[j]);
+        } else {
+            const float amax = __uint_as_float(rs.max(top));
+            const float full = p.q8 == SS_Q8_FP8 ? 448.0f : 127.0f;
+            // below 1e-35 the reciprocal would leave float32: such a row is all zero codes
+            const float inv = amax > 1e-35f ? full / amax : 0.0f;
+            uint8_t* y = static_cast<uint8_t*>(p.y) + row * D;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int64_t col = (int64_t(j) * P + tid) * 8;
+                if (col >= D) continue;
+                // a row that is not finite keeps NaN codes where e4m3 has them
+                const uint2 q = codes8(v[j], amax != amax ? amax : inv, p.q8);
+                if (p.vec) {
+                    *reinterpret_cast<uint2*>(y + col) = q;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (col + e < D) y[col + e] = uint8_t((e < 4 ? q.x : q.y) >> (8 * (e & 3)));
+                }
+            }
+            if (tid == 0) p.y_scale[row] = amax / full;
+        }
+    }
+}
+
+// dx of each row; the workgroup's sum of dy·r·c over its rows goes to part [gridDim.x, D].
+template <typename Tx, typename Tr, int P, int NV>
+__global__ __launch_bounds__(P > 256 ? P : 256) void rms_bwd_kernel(const RmsLaunch p) {
+    constexpr int kRowsWG = P >= 256 ? 1 : 256 / P;
+    __shared__ float slots[32];
+    __shared__ float fold[kRowsWG > 1 ? P * 8 : 1];
+    RowSum<P> rs{slots};
+    const int tid = threadIdx.x % P, sub = threadIdx.x / P;
+    const int64_t D = p.D, step = int64_t(gridDim.x) * kRowsWG;
+    float dw[NV][8];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dw[j][e] = 0.0f;
+    for (int64_t row = int64_t(blockIdx.x) * kRowsWG + sub; row < p.M; row += step) {
+        const Tr* rr = static_cast<const Tr*>(p.res) + row * D;
+        const Tx* dyr = static_cast<const Tx*>(p.x) + row * D;
+        float r[NV][8], dy[NV][8], sq = 0.0f, dot = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int64_t col = (int64_t(j) * P + tid) * 8;
+            get8(rr, col, D, p.vec, r[j]);
+            get8(dyr, col, D, p.vec, dy[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            float w[8];
+            get8(p.w, (int64_t(j) * P + tid) * 8, D, p.vec, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                sq = fmaf(r[j][e], r[j][e], sq);
+                dot = fmaf(dy[j][e] * w[e], r[j][e], dot);
+            }
+        }
+        sq = rs.sum(sq);
+        dot = rs.sum(dot);
+        const float c = rsqrtf(sq * p.inv_d + p.eps);
+        const float k = c * c * c * (dot * p.inv_d);
+        Tr* dx = static_cast<Tr*>(p.r) + row * D;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int64_t col = (int64_t(j) * P + tid) * 8;
+            float o[8], w[8];
+            get8(p.w, col, D, p.vec, w);
+            if (p.dr) get8(static_cast<const Tr*>(p.dr) + row * D, col, D, p.vec, o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float g = fmaf(c * w[e], dy[j][e], -k * r[j][e]);
+                dw[j][e] = fmaf(dy[j][e], r[j][e] * c, dw[j][e]);
+                o[e] = p.dr ? o[e] + g : g;
+            }
+            put8(dx, col, D, p.vec, o);
+        }
+    }
+    float* part = p.part + int64_t(blockIdx.x) * D;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int64_t col = (int64_t(j) * P + tid) * 8;
+        if constexpr (kRowsWG > 1) {
+            // the workgroup's row slots one after the other
+            for (int s = 0; s < kRowsWG; ++s) {
+                __syncthreads();
+                if (sub == s)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        fold[e * P + tid] = (s ? fold[e * P + tid] : 0.0f) + dw[j][e];
+            }
+            __syncthreads();
+            if (sub == 0) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) dw[j][e] = fold[e * P + tid];
+                put8(part, col, D, p.vec, dw[j]);
+            }
+        } else {
+            put8(part, col, D, p.vec, dw[j]);
+        }
+    }
+}
+
+// dw = Σ over the workgroups' partial sums: 64 columns a workgroup, 16 groups of partials.
+__global__ __launch_bounds__(1024) void rms_dw_kernel(const float* __restrict__ part,
+                                                      float* __restrict__ dw, int64_t D, int n) {
+    __shared__ float red[16][64];
+    const int lane = threadIdx.x & 63, grp = threadIdx.x >> 6;
+    const int64_t col = int64_t(blockIdx.x) * 64 + lane;
+    float v = 0.0f;
+    if (col < D)
+#pragma unroll 8
+        for (int i = grp; i < n; i += 16) v += part[int64_t(i) * D + col];
+    red[grp][lane] = v;
+    __syncthreads();
+    if (grp == 0 && col < D) {
+        v = 0.0f;
+#pragma unroll
+        for (int g = 0; g < 16; ++g) v += red[g][lane];
+        dw[col] = v;
+    }
+}
+
+template <typename Tx, typename Tr, int P, int NV>
+hipError_t launch_t(const RmsLaunch& p, bool backward, hipStream_t s) {
+    const dim3 block(P > 256 ? P : 256), grid{unsigned(p.grid)};
+    if (backward) hipLaunchKernelGGL((rms_bwd_kernel<Tx, Tr, P, NV>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((rms_fwd_kernel<Tx, Tr, P, NV>), grid, block, 0, s, p);
+    return hipGetLastError();
+}
+
+template <typename Tx, typename Tr>
+hipError_t launch_shape(const RmsLaunch& p, bool backward, hipStream_t s) {
+    switch (p.threads * 10 + p.pieces) {
+        case 641: return launch_t<Tx, Tr, 64, 1>(p, backward, s);
+        case 642: return launch_t<Tx, Tr, 64, 2>(p, backward, s);
+        case 644: return launch_t<Tx, Tr, 64, 4>(p, backward, s);
+        case 646: return launch_t<Tx, Tr, 64, 6>(p, backward, s);
+        case 2561: return launch_t<Tx, Tr, 256, 1>(p, backward, s);
+        case 2562: return launch_t<Tx, Tr, 256, 2>(p, backward, s);
+        case 2564: return launch_t<Tx, Tr, 256, 4>(p, backward, s);
+        case 10242: return launch_t<Tx, Tr, 1024, 2>(p, backward, s);
+        case 10244: return launch_t<Tx, Tr, 1024, 4>(p, backward, s);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+hipError_t launch(const RmsLaunch& p, bool backward, hipStream_t s) {
+    if (p.in_dtype == SS_F32) return launch_shape<float, float>(p, backward, s);
+    return p.res_dtype == SS_F32 ? launch_shape<bf16_t, float>(p, backward, s)
+                                 : launch_shape<bf16_t, bf16_t>(p, backward, s);
+}
+
+}  // namespace
+
+hipError_t launch_rms_fwd(const RmsLaunch& p, hipStream_t s) { return launch(p, false, s); }
+
+hipError_t launch_rms_bwd(const RmsLaunch& p, float* dw, hipStream_t s) {
+    hipError_t e = launch(p, true, s);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(rms_dw_kernel, dim3(unsigned((p.D + 63) / 64)), dim3(1024), 0, s, p.part, dw,
+                       p.D, p.grid);
+    return hipGetLastError();
+}
+
+}  // namespace ss
