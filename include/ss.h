@@ -277,7 +277,7 @@ typedef struct ss_la_dims {
     int64_t seqlen;       /* T >= 1 */
     int64_t heads;        /* H: value heads */
     int64_t kheads;       /* Hk: query and key heads, H % Hk == 0 */
-    int64_t dk, dv;       /* 1 .. 256 */
+    int64_t dk, dv;       /* 1 .. 256; H · max(dk, dv) < 2^22 */
     int64_t q_stride[3];  /* batch row, token, head; all 0: dense */
     int64_t k_stride[3];
     int64_t v_stride[3];

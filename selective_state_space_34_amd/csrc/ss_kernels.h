@@ -164,7 +164,8 @@ struct LaOperand {
     int64_t sb, st, sh;
     int64_t rep;       // value heads that share a row
     int dim;           // width
-    int vec;           // every row starts on 16 bytes and holds whole 16-byte pieces
+    int vec;           // every row starts on 16 bytes and holds whole 16-byte pieces, and a
+                       // chunk's rows lie within 2^30 bytes
 };
 
 // One sweep (ss_la_sweep.h).
@@ -180,17 +181,20 @@ struct LaSweep {
     int64_t in_seg;
     float* s_out;              // nullable [B, H, dA, dC]; state_only: [B, H, nseg, dA, dC]
     int64_t s_out_sz;
-    float* dots;               // nullable [tiles, B, H, T]
+    double* dots;              // nullable [tiles, B, H, T]
     float* seg_decay;          // state_only: [B, H, nseg]
     int64_t B, T, H;
     int tiles, nseg, grid_seg, seg0;   // the grid covers segments [seg0, seg0 + grid_seg)
     int64_t seg_chunks;
     int reverse, state_only;
     float alpha, in_scale, up_scale;   // of a·b; of the entering state in out; of c in the state
-    int pad_a, nt;
+    int pad_a, waves;
 };
+// all operands of aligned rows; any rows
 hipError_t launch_la_sweep_bf16(const LaSweep& p, hipStream_t s);
+hipError_t launch_la_sweep_bf16_any(const LaSweep& p, hipStream_t s);
 hipError_t launch_la_sweep_f32(const LaSweep& p, hipStream_t s);
+hipError_t launch_la_sweep_f32_any(const LaSweep& p, hipStream_t s);
 
 // State entering each segment, in place over what each segment adds: state [BH, nseg, sz].
 // first: nullable, element i·dC + j of row-head bh at bh·sz + i·f_i + j·f_j.
@@ -206,7 +210,7 @@ hipError_t launch_la_carry(const LaCarry& p, hipStream_t s);
 // dg from the row and column sums: token [B, T, H] (dg), or one value a head [H] through
 // head_part [B, H].  ds, s_final: both or neither; ds [B, H, dk, dv], s_final [B, H, dv, dk].
 struct LaDecayGrad {
-    const float *row, *col;    // [row_tiles | col_tiles, B, H, T]
+    const double *row, *col;   // [tiles, B, H, T]
     int tiles;
     const float *ds, *s_final;
     const int32_t* lengths;

@@ -79,7 +79,7 @@ __global__ __launch_bounds__(256) void la_decay_grad_kernel(const LaDecayGrad p)
             if (t0 + i < len)
                 for (int q = 0; q < p.tiles; ++q) {
                     const int64_t at = q * plane + bh * p.T + t0 + i;
-                    x += double(p.row[at]) - double(p.col[at]);
+                    x += p.row[at] - p.col[at];
                 }
             v[i] = x + (i < 3 ? v[i + 1] : 0.0);  // suffix sums of the thread's four
         }

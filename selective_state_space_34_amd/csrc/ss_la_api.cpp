@@ -28,7 +28,8 @@ LaOperand operand(const LaPlan& p, const void* ptr, const int64_t* stride, int64
     o.rep = p.H / heads;
     o.dim = int(dim);
     const int64_t v = p.in_dtype == SS_BF16 ? 8 : 4;
-    o.vec = aligned(ptr, 16) && o.sb % v == 0 && o.st % v == 0 && o.sh % v == 0 && dim % v == 0;
+    o.vec = aligned(ptr, 16) && o.sb % v == 0 && o.st % v == 0 && o.sh % v == 0 && dim % v == 0 &&
+            o.st < (int64_t(1) << 22);
     return o;
 }
 
@@ -55,8 +56,10 @@ Inputs inputs(const ss_la_dims* d, const LaPlan& p, const void* q, const void* k
 }
 
 hipError_t sweep(const LaPlan& p, const LaSweep& s, hipStream_t stream) {
-    return p.in_dtype == SS_BF16 ? ss::launch_la_sweep_bf16(s, stream)
-                                 : ss::launch_la_sweep_f32(s, stream);
+    const bool vec = s.a.vec && s.b.vec && s.c.vec && s.e.vec;
+    if (p.in_dtype == SS_BF16)
+        return vec ? ss::launch_la_sweep_bf16(s, stream) : ss::launch_la_sweep_bf16_any(s, stream);
+    return vec ? ss::launch_la_sweep_f32(s, stream) : ss::launch_la_sweep_f32_any(s, stream);
 }
 
 LaSweep base(const LaPlan& p, const float* g, const int32_t* lengths, int reverse) {
@@ -74,7 +77,7 @@ LaSweep base(const LaPlan& p, const float* g, const int32_t* lengths, int revers
 }
 
 void shape(LaSweep* s, const ss::LaShape& f) {
-    s->pad_a = f.pad_a; s->nt = f.nt; s->tiles = f.tiles;
+    s->pad_a = f.pad_a; s->waves = f.waves; s->tiles = f.tiles;
 }
 
 // States entering every segment, [B, H, nseg, dA, dC], from the operands b, c of `s` and the
@@ -191,6 +194,7 @@ int ss_la_bwd(const ss_la_dims* dims, const void* q, const void* k, const void* 
     float* state = at(p.off_state);
     float* decay = at(p.off_decay);
     float* part = p.Hk < p.H ? at(p.off_part) : nullptr;
+    auto dots = [ws](size_t off) { return reinterpret_cast<double*>(ws + off); };
     float* s_final = g && ds_final ? at(p.off_final) : nullptr;
     const int bf16 = p.in_dtype == SS_BF16;
     const Inputs in = inputs(dims, p, q, k, v);
@@ -205,7 +209,7 @@ int ss_la_bwd(const ss_la_dims* dims, const void* q, const void* k, const void* 
         if (e != hipSuccess) return hip_fail(e);
     }
     s.out = part ? static_cast<void*>(part) : dq; s.out_f32 = part != nullptr;
-    s.dots = g ? at(p.off_row) : nullptr;
+    s.dots = g ? dots(p.off_row) : nullptr;
     s.s_out = s_final;
     e = full_sweep(p, s, p.rev, s0, 1, p.dv, state, p.dk, 1, stream);
     if (e != hipSuccess) return hip_fail(e);
@@ -230,7 +234,7 @@ int ss_la_bwd(const ss_la_dims* dims, const void* q, const void* k, const void* 
     s = base(p, g, lengths, 1);
     s.a = in.v; s.b = od; s.c = in.q; s.e = in.k;
     s.out = part ? static_cast<void*>(part) : dk; s.out_f32 = part != nullptr;
-    s.dots = g ? at(p.off_col) : nullptr;
+    s.dots = g ? dots(p.off_col) : nullptr;
     e = full_sweep(p, s, p.rev, ds_final, 1, p.dv, state, 1, p.dv, stream);
     if (e != hipSuccess) return hip_fail(e);
     if (part) {
@@ -241,7 +245,7 @@ int ss_la_bwd(const ss_la_dims* dims, const void* q, const void* k, const void* 
     // 4. dg from the row and column sums
     if (g) {
         ss::LaDecayGrad d{};
-        d.row = at(p.off_row); d.col = at(p.off_col); d.tiles = p.rev.tiles;
+        d.row = dots(p.off_row); d.col = dots(p.off_col); d.tiles = p.rev.tiles;
         d.ds = ds_final; d.s_final = s_final; d.lengths = lengths;
         d.dg = dg; d.head_part = at(p.off_head);
         d.B = p.B; d.T = p.T; d.H = p.H; d.dk = p.dk; d.dv = p.dv;

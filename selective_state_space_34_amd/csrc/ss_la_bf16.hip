@@ -1,8 +1,8 @@
-// The bf16 instances of the linear-attention sweep.
+// The bf16 instances of the linear-attention sweep for rows of aligned 16-byte pieces.
 #include "ss_la_sweep.h"
 
 namespace ss {
 hipError_t launch_la_sweep_bf16(const LaSweep& p, hipStream_t s) {
-    return la::launch_sweep_type<bf16_t>(p, s);
+    return la::launch_sweep_type<bf16_t, true>(p, s);
 }
 }  // namespace ss

@@ -1,0 +1,8 @@
+// The bf16 instances of the linear-attention sweep for rows of any alignment and width.
+#include "ss_la_sweep.h"
+
+namespace ss {
+hipError_t launch_la_sweep_bf16_any(const LaSweep& p, hipStream_t s) {
+    return la::launch_sweep_type<bf16_t, false>(p, s);
+}
+}  // namespace ss

@@ -1,8 +1,8 @@
-// The float32 instances of the linear-attention sweep.
+// The float32 instances of the linear-attention sweep for rows of aligned 16-byte pieces.
 #include "ss_la_sweep.h"
 
 namespace ss {
 hipError_t launch_la_sweep_f32(const LaSweep& p, hipStream_t s) {
-    return la::launch_sweep_type<float>(p, s);
+    return la::launch_sweep_type<float, true>(p, s);
 }
 }  // namespace ss

@@ -10,26 +10,27 @@ namespace ss {
 // and dC (the output's columns, and the state's).
 struct LaShape {
     int pad_a;   // dA padded to the kernel's 64, 128 or 256
-    int nt;      // 16-column tiles of each of a workgroup's four waves
+    int waves;   // of a workgroup, 16 columns each: 4 or 8
     int tiles;   // workgroups over dC
 };
 
 inline LaShape la_shape(int64_t dA, int64_t dC) {
     LaShape s;
     s.pad_a = dA <= 64 ? 64 : dA <= 128 ? 128 : 256;
-    // 256 state rows leave registers for one 16-column tile a wave
-    s.nt = dC <= 64 || s.pad_a == 256 ? 1 : 2;
-    s.tiles = int((dC + 64 * s.nt - 1) / (64 * s.nt));
+    s.waves = dC <= 64 ? 4 : 8;
+    s.tiles = int((dC + 16 * s.waves - 1) / (16 * s.waves));
     return s;
 }
 
 constexpr int64_t kLaMaxDim = 256;
 inline int64_t la_chunk(int in_dtype) { return in_dtype == SS_BF16 ? 64 : 32; }
 
-// Segments of a sequence that are swept side by side: enough for two workgroups on each of
-// the 256 CUs, none shorter than two chunks.
+// Segments of a sequence that are swept side by side: as many as keep all workgroups resident
+// at once, two on each of the 256 CUs (a few more than that would take a second round as long
+// as the first: a sweep over 13 segments of 40 heads measured 369 us, over 12 it measured 281), none shorter than
+// two chunks.
 inline int64_t la_segments(int64_t rows, int64_t nchunk) {
-    int64_t n = (512 + rows - 1) / rows;
+    int64_t n = 512 / rows;
     if (n > nchunk / 2) n = nchunk / 2;
     if (n < 1) n = 1;
     const int64_t len = (nchunk + n - 1) / n;
@@ -45,7 +46,7 @@ struct LaPlan {
     int64_t nseg, seg_chunks;
     // forward: off_state [B, H, nseg, dk·dv], off_decay [B, H, nseg] (nseg > 1)
     // backward: the same (used by one direction after the other), and
-    //   off_row, off_col   [rev.tiles, B, H, T] row and column sums behind dg
+    //   off_row, off_col   [rev.tiles, B, H, T] row and column sums behind dg (64 bits)
     //   off_final          [B, H, dv·dk] S_Tᵀ
     //   off_head           [B, H] dg of each (row, head) summed over tokens (one decay a head)
     //   off_part           [B, T, H, dk] float32 dq, then dk, of each value head (Hk < H)
@@ -66,6 +67,8 @@ inline int make_la_plan(const ss_la_dims& d, bool backward, LaPlan* out) {
     if (d.dk > kLaMaxDim || d.dv > kLaMaxDim || d.heads % d.kheads != 0) return SS_ERR_DIMS;
     if (d.in_dtype != SS_F32 && d.in_dtype != SS_BF16) return SS_ERR_DTYPE;
     if (d.decay < SS_LA_DECAY_NONE || d.decay > SS_LA_DECAY_TOKEN) return SS_ERR_DTYPE;
+    // a chunk's rows of an output lie within 2^30 bytes
+    if (d.heads >= (int64_t(1) << 22) / (d.dk > d.dv ? d.dk : d.dv)) return SS_ERR_DIMS;
     if (!(d.scale - d.scale == 0.0f)) return SS_ERR_DIMS;   // not finite
     if (!la_strides_ok(d.q_stride) || !la_strides_ok(d.k_stride) || !la_strides_ok(d.v_stride))
         return SS_ERR_DIMS;
@@ -96,7 +99,7 @@ inline int make_la_plan(const ss_la_dims& d, bool backward, LaPlan* out) {
     p.off_decay = off;
     if (p.nseg > 1) off = align256(off + size_t(bh * p.nseg) * f);
     if (backward) {
-        const size_t dots = size_t(p.rev.tiles) * size_t(bh) * size_t(p.T) * f;
+        const size_t dots = size_t(p.rev.tiles) * size_t(bh) * size_t(p.T) * sizeof(double);
         p.off_row = off; off = align256(off + dots);
         p.off_col = off; off = align256(off + dots);
         p.off_final = off; off = align256(off + state);

@@ -18,8 +18,8 @@
 // that a row or column sum holds is also held by some dg near it, so the running sum loses
 // nothing to cancellation.
 //
-// A workgroup of four waves takes one head's rows chunk by chunk (64 tokens of bf16, 32 of
-// float32) with the state in registers: wave w holds all dA rows of its 16·NT columns, in the
+// A workgroup of four or eight waves takes one head's rows chunk by chunk (64 tokens of bf16,
+// 32 of float32) with the state in registers: a wave holds all dA rows of 16 columns, in the
 // accumulator layout of v_mfma_f32_16x16x32_bf16 (lane l: column l % 16, rows 4·(l/16) + r).
 // Inside a chunk:
 //   P  = (a bᵀ) ⊙ decay: 16 x 16 tiles dealt to the waves, only those the mask leaves, through LDS
@@ -29,8 +29,8 @@
 //   S  = e^{G_C} S + bᵀ(w ⊙ c)   (transposed operands: ds_read_b64_tr_b16)
 // The next chunk's rows are loaded into registers meanwhile.
 //
-// Numerics.  Log decays are summed in 64 bits and kept as an integer and a fraction in base 2,
-// so a weight is ldexp(2^fraction, integer) of an exact difference: no error grows with the
+// Numerics.  Log decays are summed as 64-bit integers with 32 fraction bits, in base 2, so a
+// weight is ldexp(2^fraction, integer) of an exact difference: no error grows with the
 // length, and a token that decays by e^{-inf} cuts the sequence exactly.  P, and S where it
 // feeds out, are rounded to bf16 once (the operand the matrix cores take; out is bf16 too).
 // The state's own sums are float32: c's weight w is not a bf16 value, so w·c is fed as three
@@ -92,24 +92,24 @@ struct Mma<bf16_t> {
         for (int e = 0; e < 8; ++e) f[e] = Elem(v[e]);
         return f;
     }
-    // v as kTerms bf16 terms that sum to it (relative error below 2^-24).  An infinite value
-    // is its first term alone.
-    static __device__ __forceinline__ void split(const float (&v)[8], Frag (&f)[kTerms]) {
-        float r[8], probe = 0.0f;
+    // v as kTerms bf16 terms that sum to it (relative error below 2^-24).  keep: all ones, or
+    // zero where v may hold an infinity, which is then its first term alone.
+    static __device__ __forceinline__ void split(const float (&v)[8], unsigned keep, Frag (&f)[kTerms]) {
+        float r[8];
         f[0] = round8(v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            r[e] = v[e] - float(f[0][e]);
-            probe = fmaf(r[e], 0.0f, probe);
-        }
-        if (__any(probe != probe)) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) r[e] = r[e] != r[e] ? 0.0f : r[e];
-        }
-        f[1] = round8(r);
+        for (int e = 0; e < 8; ++e) r[e] = v[e] - float(f[0][e]);
+        f[1] = masked(round8(r), keep);
 #pragma unroll
         for (int e = 0; e < 8; ++e) r[e] -= float(f[1][e]);
-        f[2] = round8(r);
+        f[2] = masked(round8(r), keep);
+    }
+    static __device__ __forceinline__ Frag masked(Frag f, unsigned keep) {
+        union { Frag f; unsigned w[4]; } u;
+        u.f = f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u.w[i] &= keep;
+        return u.f;
     }
 };
 
@@ -149,7 +149,7 @@ struct Mma<float> {
         for (int e = 0; e < 8; ++e) f[e] = v[e];
         return f;
     }
-    static __device__ __forceinline__ void split(const float (&v)[8], Frag (&f)[kTerms]) {
+    static __device__ __forceinline__ void split(const float (&v)[8], unsigned, Frag (&f)[kTerms]) {
         f[0] = round8(v);
     }
 };
@@ -166,33 +166,85 @@ __device__ __forceinline__ typename Mma<T>::Frag col_frag(const typename Mma<T>:
     }
 }
 
-// Rows of one operand of one (batch row, head).
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+
+// Rows of one operand of one (batch row, head), and this thread's place in them: the same
+// columns in every one of its 16-byte pieces.
 template <typename T>
 struct Rows {
     const T* p;
-    int64_t st;  // elements from token to token
-    int dim, vec;
+    int64_t st;       // elements from token to token
+    int dim;
+    int tok, col;     // of the thread's first piece
+    unsigned at;      // its byte offset from a chunk's first row; beyond any row where col >= dim
 };
 
+constexpr unsigned kNowhere = 0x80000000u;
+constexpr int kRsrcFlags = 0x00020000;   // raw buffer, 32-bit elements
+
 template <typename T>
-__device__ __forceinline__ Rows<T> rows_of(const LaOperand& o, int64_t b, int64_t h) {
-    return Rows<T>{static_cast<const T*>(o.p) + b * o.sb + (h / o.rep) * o.sh, o.st, o.dim, o.vec};
+__device__ __forceinline__ Rows<T> rows_of(const LaOperand& o, int64_t b, int64_t h, int tok,
+                                           int col) {
+    Rows<T> r{static_cast<const T*>(o.p) + b * o.sb + (h / o.rep) * o.sh, o.st, o.dim, tok, col,
+              kNowhere};
+    if (col < o.dim) r.at = unsigned((tok * int(o.st) + col) * int(sizeof(T)));
+    return r;
 }
 
-// 16 bytes of token t, elements [col, col + kVec); zeros outside the token range and the width.
+// A 16-byte load that needs only the elements' alignment.
 template <typename T>
-__device__ __forceinline__ uint4 load16(const Rows<T>& r, int64_t t, int64_t end, int col) {
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (t >= end || col >= r.dim) return v;
-    const T* q = r.p + t * r.st + col;
-    if (r.vec) return *reinterpret_cast<const uint4*>(q);
-    constexpr int kVec = Mma<T>::kVec;
-    union { uint4 v; T e[kVec]; } u;
-    u.v = v;
+__device__ __forceinline__ u32x4 load_unaligned(const T* p) {
+    u32x4 v;
+    __builtin_memcpy(&v, p, 16);
+    return v;
+}
+
+// N pieces of a chunk (nv of its tokens exist), STEP tokens apart; zeros outside the tokens and
+// the width.  Aligned rows (kVec) go through a buffer descriptor that ends with the chunk's last
+// row, so the bounds cost nothing.  For others a piece that would pass the row's end starts
+// earlier, at the row's last 16 bytes, and is shifted into place; rows shorter than a piece are
+// put together element by element.
+template <typename T, bool kVec, int N, int STEP>
+__device__ __forceinline__ void load_pieces(const Rows<T>& r, int64_t t0, int nv, u32x4 (&v)[N]) {
+    constexpr int V = Mma<T>::kVec, kBits = 8 * int(sizeof(T));
+    const T* base = r.p + t0 * r.st;
+    if constexpr (kVec) {
+        const int bytes = nv > 0 ? (int(r.st) * (nv - 1) + r.dim) * int(sizeof(T)) : 0;
+        const __amdgpu_buffer_rsrc_t d =
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(base), 0, bytes, kRsrcFlags);
 #pragma unroll
-    for (int i = 0; i < kVec; ++i)
-        if (col + i < r.dim) u.e[i] = q[i];
-    return u.v;
+        for (int x = 0; x < N; ++x)
+            v[x] = __builtin_amdgcn_raw_buffer_load_b128(d, int(r.at), x * STEP * int(r.st) * int(sizeof(T)), 0);
+    } else {
+        const bool some = r.col < r.dim;
+        const int back = r.col + V > r.dim ? r.col + V - r.dim : 0;   // elements it starts early
+#pragma unroll
+        for (int x = 0; x < N; ++x) {
+            v[x] = u32x4{0, 0, 0, 0};
+            const int t = r.tok + x * STEP;
+            if (!some || t >= nv) continue;
+            const T* q = base + int64_t(t) * r.st + r.col;
+            uint64_t lo = 0, hi = 0;
+            if (r.dim >= V) {
+                union { u32x4 v; uint64_t w[2]; } u;
+                u.v = load_unaligned(q - back);
+                const int bits = back * kBits;
+                lo = bits >= 64 ? u.w[1] >> (bits - 64)
+                   : bits > 0 ? (u.w[0] >> bits) | (u.w[1] << (64 - bits)) : u.w[0];
+                hi = bits >= 64 ? 0 : u.w[1] >> bits;
+            } else {
+                for (int i = r.dim - 1; i >= 0; --i) {
+                    uint64_t e;
+                    if constexpr (sizeof(T) == 2) e = reinterpret_cast<const uint16_t*>(q)[i];
+                    else e = reinterpret_cast<const uint32_t*>(q)[i];
+                    hi = (hi << kBits) | (lo >> (64 - kBits));
+                    lo = (lo << kBits) | e;
+                }
+            }
+            v[x] = u32x4{unsigned(lo), unsigned(lo >> 32), unsigned(hi), unsigned(hi >> 32)};
+        }
+    }
 }
 
 // The log decays of a chunk in base 2 and the weights made of them.
@@ -210,87 +262,146 @@ __device__ __forceinline__ float exp2_parts(float frac, int whole) {
     return __builtin_amdgcn_ldexpf(exp2_hw(frac), whole);
 }
 
-// 2^d of a 64-bit exponent
-__device__ __forceinline__ float exp2_wide(double d) {
-    const double n = __builtin_rint(d);
-    return exp2_parts(float(d - n), int(n));
+// A log decay (natural) in base 2 with 32 fraction bits, bounded so that sums stay exact:
+// 2^±1024 is 0 or inf in float32 either way.  (NaN is kept apart, by its lane.)
+__device__ __forceinline__ int64_t decay_fixed(float g) {
+    double x = double(g) * 1.4426950408889634074;
+    x = fmin(fmax(x, -1024.0), 1024.0);
+    const double n = __builtin_floor(x);
+    return (int64_t(int(n)) << 32) + int64_t(uint32_t((x - n) * 4294967296.0));
 }
 
-// Per-token log decays (natural) to base 2, bounded so that sums stay exact: 2^±1024 is 0 or
-// inf in float32 either way.  NaN stays NaN.
-__device__ __forceinline__ double decay_log2(float g) {
-    double x = double(g) * 1.4426950408889634074;
-    x = x < -1024.0 ? -1024.0 : x;
-    return x > 1024.0 ? 1024.0 : x;
+__device__ __forceinline__ float fraction_of(int64_t v) { return float(uint32_t(v)) * 2.3283064365386963e-10f; }
+__device__ __forceinline__ float exp2_fixed(int64_t v) { return exp2_parts(fraction_of(v), int(v >> 32)); }
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int64_t add_moved(int64_t v) {
+    const int lo = __builtin_amdgcn_update_dpp(0, int(v), CTRL, ROWS, 0xf, true);
+    const int hi = __builtin_amdgcn_update_dpp(0, int(v >> 32), CTRL, ROWS, 0xf, true);
+    return v + ((int64_t(hi) << 32) | uint32_t(lo));
 }
 
 // One wave: lane t holds token t's log decay (0 beyond the rows' end and for lanes >= C).
-// Returns the chunk's sum.
+// Running sums by lane moves inside 16 lanes, then across.  Returns the chunk's sum.
 template <int C>
-__device__ __forceinline__ double decay_prepare(double x, int lane, int reverse, float in_scale,
-                                                float up_scale, Decay<C>& d) {
-    double sum = x;
-#pragma unroll
-    for (int m = 1; m < C; m <<= 1) {
-        const double o = __shfl_up(sum, m, 64);
-        if (lane >= m) sum += o;
-    }
-    const double total = __shfl(sum, C - 1, 64);
+__device__ __forceinline__ int64_t decay_prepare(float g, int lane, int reverse, float in_scale,
+                                                 float up_scale, Decay<C>& d) {
+    int64_t sum = decay_fixed(g);
+    sum = add_moved<0x111, 0xf>(sum);
+    sum = add_moved<0x112, 0xf>(sum);
+    sum = add_moved<0x114, 0xf>(sum);
+    sum = add_moved<0x118, 0xf>(sum);
+    sum = add_moved<0x142, 0xa>(sum);   // row 0's last lane to row 1, row 2's to row 3
+    sum = add_moved<0x143, 0xc>(sum);   // lane 31 to rows 2 and 3
+    const int64_t total = (int64_t(__builtin_amdgcn_readlane(int(sum >> 32), 63)) << 32) |
+                          uint32_t(__builtin_amdgcn_readlane(int(sum), 63));
+    // from the first NaN on every sum is one
+    const uint64_t bad = __ballot(g != g);
+    const float mark = (bad << (63 - lane)) ? __builtin_nanf("") : 0.0f;
+    const float mark_all = bad ? __builtin_nanf("") : 0.0f;
     if (lane < C) {
-        const double n = __builtin_rint(sum);
-        d.whole[lane] = int(n);
-        d.frac[lane] = float(sum - n);
-        const float fwd = exp2_wide(sum), bwd = exp2_wide(total - sum);
+        d.whole[lane] = int(sum >> 32);
+        d.frac[lane] = fraction_of(sum) + mark;
+        const float fwd = exp2_fixed(sum) + mark, bwd = exp2_fixed(total - sum) + mark_all;
         d.in[lane] = in_scale * (reverse ? bwd : fwd);
         d.up[lane] = up_scale * (reverse ? fwd : bwd);
-        if (lane == 0) d.all = exp2_wide(total);
+        if (lane == 0) d.all = exp2_fixed(total) + mark_all;
     }
-    return total;
+    return bad ? INT64_MIN : total;
+}
+
+// Whether a fragment holds an infinity or NaN: bit 31 of the result, or bit 15 for bf16.
+__device__ __forceinline__ uint32_t not_finite(bf16x8 f, uint32_t seen) {
+    union { bf16x8 f; uint32_t w[4]; } u;
+    u.f = f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) seen |= (u.w[i] & 0x7f807f80u) + 0x00800080u;
+    return seen;
+}
+__device__ __forceinline__ uint32_t not_finite(f32x8 f, uint32_t seen) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        seen |= ((__float_as_uint(f[i]) & 0x7fffffffu) + 0x00800000u) & 0x80000000u;
+    return seen;
+}
+
+// Waves a SIMD that the registers are to allow: four (two workgroups of eight waves on a CU)
+// where the state, the rows in flight and the products fit 128 registers without spilling.
+constexpr int sweep_occupancy(bool vec, int DA, int NW, bool dot, bool state) {
+    if (DA == 256 && NW == 4 && !state) return 1;
+    if (DA == 256 || dot || !vec) return 2;
+    return DA == 128 && NW == 4 && !state ? 2 : 4;
 }
 
 // kState: only the state that a segment adds from zero, and the segment's decay (the first of
 // the two passes over a sequence that is split into segments).  kDot: also e_t·out_t without
-// the diagonal, in float32.
-template <typename T, int DA, int NT, bool kDot, bool kState>
-__global__ __launch_bounds__(256) void sweep_kernel(const LaSweep p) {
+// the diagonal.  Its pairs are summed in 64 bits: a pair's value has the same bits in the row
+// sums and in the column sums, so what enters one and leaves the other cancels exactly in the
+// running sum of dg.
+template <typename T, bool kVec, int DA, int NW, bool kDot, bool kState>
+__global__ __launch_bounds__(64 * NW, sweep_occupancy(kVec, DA, NW, kDot, kState)) void sweep_kernel(const LaSweep p) {
     using M = Mma<T>;
     using Frag = typename M::Frag;
     using Elem = typename M::Elem;
     constexpr int C = M::kChunk, V = M::kVec, KT = M::kTerms;
-    constexpr int DC = 64 * NT;                     // columns of a workgroup
+    constexpr int NT = 64 * NW;                     // threads
+    constexpr int DC = 16 * NW;                     // columns of a workgroup
     constexpr int kPad = 16 / int(sizeof(Elem));    // rows start 16 bytes (four banks) apart
-    constexpr int LA = DA + kPad, LC = DC + kPad, LP = C + kPad;
-    constexpr int NA = C * DA / V / 256, NC = C * DC / V / 256;  // 16-byte loads of a thread
+    constexpr int LA = DA + kPad, LC = DC + kPad;
+    constexpr int NA = C * DA / V / NT, NC = C * DC / V / NT;    // 16-byte pieces of a thread
+    constexpr int SA = NT * V / DA, SC = NT * V / DC;            // tokens between them
     constexpr int TB = C / 16, KS = C / 32, IB = DA / 32;
     constexpr int kTiles = TB * (TB + 1) / 2;
 
     __shared__ __attribute__((aligned(16))) Elem lb[C * LA];
     __shared__ __attribute__((aligned(16))) Elem lc[C * LC];
-    __shared__ __attribute__((aligned(16))) Elem lall[kState ? 1 : C * LA];
-    __shared__ __attribute__((aligned(16))) Elem lp[kState ? 1 : C * LP];
-    __shared__ __attribute__((aligned(16))) Elem le[kDot ? C * LC : 1];
-    __shared__ Decay<C> dec[2];
-    __shared__ float dot_tile[kDot ? TB * TB * 16 : 1];
-    __shared__ float dot_wave[kDot ? 4 * C : 1];
-    Elem* const la_ = lall;
+    __shared__ __attribute__((aligned(16))) Elem la_[kState ? 8 : C * LA];
+    __shared__ __attribute__((aligned(16))) Elem lp[kState ? 8 : C * C];
+    __shared__ __attribute__((aligned(16))) Elem le[kDot ? C * DC : 8];
+    __shared__ __attribute__((aligned(16))) Decay<C> dec[2];
+    __shared__ double dot_tile[kDot ? kTiles * 16 : 1];
+    __shared__ float dot_wave[kDot ? NW * C : 1];
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int l16 = lane & 15, lg = lane >> 4;
+    // P and e lie in LDS without padding, their 16-byte pieces exchanged by row instead
+    auto p_at = [](int t, int s) { return t * C + (((s / V) ^ (t & (C / V - 1))) * V) + s % V; };
+    auto e_at = [](int t, int j) { return t * DC + (((j / V) ^ (t & (DC / V - 1))) * V) + j % V; };
+    auto p_row = [&](int t, int s) {   // eight consecutive values
+        if constexpr (sizeof(T) == 2) return M::row(&lp[p_at(t, s)]);
+        else {
+            const f32x4 lo = *reinterpret_cast<const f32x4*>(&lp[p_at(t, s)]);
+            const f32x4 hi = *reinterpret_cast<const f32x4*>(&lp[p_at(t, s + 4)]);
+            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+    };
+    auto e_row = [&](int t, int j) {
+        if constexpr (sizeof(T) == 2) return M::row(&le[e_at(t, j)]);
+        else {
+            const f32x4 lo = *reinterpret_cast<const f32x4*>(&le[e_at(t, j)]);
+            const f32x4 hi = *reinterpret_cast<const f32x4*>(&le[e_at(t, j + 4)]);
+            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+    };
     // blocks: column tile fastest, then head, then segment, then batch row
-    int64_t blk = blockIdx.x;
-    const int tile = int(blk % p.tiles);
-    blk /= p.tiles;
-    const int64_t h = blk % p.H;
-    blk /= p.H;
-    const int seg = int(blk % p.grid_seg) + p.seg0;
-    const int64_t b = blk / p.grid_seg;
+    unsigned blk = blockIdx.x;
+    const int tile = int(blk % unsigned(p.tiles));
+    blk /= unsigned(p.tiles);
+    const int64_t h = blk % unsigned(p.H);
+    blk /= unsigned(p.H);
+    const int seg = int(blk % unsigned(p.grid_seg)) + p.seg0;
+    const int64_t b = blk / unsigned(p.grid_seg);
     const int64_t bh = b * p.H + h;
     const int c0 = tile * DC;                       // first column
-    const int jw = wave * 16 * NT;                  // the wave's first column in the tile
+    const int jw = wave * 16;                       // the wave's first column in the tile
 
-    const Rows<T> rb = rows_of<T>(p.b, b, h), rc = rows_of<T>(p.c, b, h);
-    const Rows<T> ra = kState ? rb : rows_of<T>(p.a, b, h);
-    const Rows<T> re = kDot ? rows_of<T>(p.e, b, h) : rb;
+    const int tok_a = tid / (DA / V), col_a = (tid % (DA / V)) * V;
+    const int tok_c = tid / (DC / V), col_c = (tid % (DC / V)) * V;
+    const Rows<T> rb = rows_of<T>(p.b, b, h, tok_a, col_a);
+    const Rows<T> rc = rows_of<T>(p.c, b, h, tok_c, c0 + col_c);
+    const Rows<T> ra = kState ? rb : rows_of<T>(p.a, b, h, tok_a, col_a);
+    const Rows<T> re = kDot ? rows_of<T>(p.e, b, h, tok_c, c0 + col_c) : rc;
     int64_t len = p.T;
     if (p.lengths) {
         len = p.lengths[b];
@@ -304,64 +415,66 @@ __global__ __launch_bounds__(256) void sweep_kernel(const LaSweep p) {
     const int rev = p.reverse;
 
     // ---- the state this segment starts from --------------------------------------------------
-    f32x4 S[IB][2][NT];
+    f32x4 S[IB][2];
 #pragma unroll
     for (int ib = 0; ib < IB; ++ib)
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < 2; ++u) S[ib][u] = f32x4{0, 0, 0, 0};
+    if (!kState && p.s_in) {
+        const float* si = p.s_in + (bh * p.in_seg + (p.in_seg > 1 ? seg : 0)) * p.s_in_sz;
+        const int sti = int(p.s_in_i), stj = int(p.s_in_j);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                f32x4 s = {0, 0, 0, 0};
-                if (!kState && p.s_in) {
-                    const int j = c0 + jw + 16 * nt + l16;
+        for (int ib = 0; ib < IB; ++ib)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int i = 32 * ib + 8 * lg + 4 * u + r;
-                        if (i < p.b.dim && j < p.c.dim)
-                            s[r] = p.s_in[(bh * p.in_seg + (p.in_seg > 1 ? seg : 0)) * p.s_in_sz +
-                                          i * p.s_in_i + j * p.s_in_j];
-                    }
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int i = 32 * ib + 8 * lg + 4 * u + r, j = c0 + jw + l16;
+                    if (i < p.b.dim && j < p.c.dim) S[ib][u][r] = si[i * sti + j * stj];
                 }
-                S[ib][u][nt] = s;
-            }
+    }
 
-    uint4 va[kState ? 1 : NA], vb[NA], vc[NC], ve[kDot ? NC : 1];
+    u32x4 va[kState ? 1 : NA], vb[NA], vc[NC], ve[kDot ? NC : 1];
     float vg = 0.0f;
-    // chunk number of step i, in the sweep's direction
-    auto chunk_of = [&](int i) { return rev ? ch_hi - 1 - i : ch_lo + i; };
+    // first token of step i, in the sweep's direction, and how many tokens its chunk has
+    auto first_of = [&](int i) { return (rev ? ch_hi - 1 - i : ch_lo + i) * C; };
+    auto tokens_at = [](int64_t t0, int64_t end) {
+        const int64_t m = end - t0;
+        return int(m < 0 ? 0 : m < C ? m : C);
+    };
     auto load_rows = [&](int i) {
-        const int64_t t0 = chunk_of(i) * C;
-#pragma unroll
-        for (int x = 0; x < NA; ++x) {
-            const int id = x * 256 + tid, t = id / (DA / V), col = (id % (DA / V)) * V;
-            vb[x] = load16(rb, t0 + t, len, col);
-            if constexpr (!kState) va[x] = load16(ra, t0 + t, len, col);
-        }
-#pragma unroll
-        for (int x = 0; x < NC; ++x) {
-            const int id = x * 256 + tid, t = id / (DC / V), col = c0 + (id % (DC / V)) * V;
-            vc[x] = load16(rc, t0 + t, len, col);
-            if constexpr (kDot) ve[x] = load16(re, t0 + t, len, col);
-        }
+        const int64_t t0 = first_of(i);
+        const int nv = tokens_at(t0, len);
+        load_pieces<T, kVec, NA, SA>(rb, t0, nv, vb);
+        if constexpr (!kState) load_pieces<T, kVec, NA, SA>(ra, t0, nv, va);
+        load_pieces<T, kVec, NC, SC>(rc, t0, nv, vc);
+        if constexpr (kDot) load_pieces<T, kVec, NC, SC>(re, t0, nv, ve);
     };
     auto load_g = [&](int i) {  // the last wave prepares the decays
+        if (wave != NW - 1) return;
         vg = 0.0f;
-        const int64_t t = chunk_of(i) * C + lane;
-        if (wave == 3 && p.g && lane < C && t < len)
-            vg = p.g[p.decay_token ? (b * p.T + t) * p.H + h : h];
+        const int64_t t0 = first_of(i);
+        if (p.g && lane < tokens_at(t0, len))
+            vg = p.decay_token ? p.g[(b * p.T + t0 + lane) * p.H + h] : p.g[h];
     };
-    double seg_sum = 0.0;
+    int64_t seg_sum = 0;
+    bool seg_nan = false;
     auto prepare = [&](int i) {
-        if (wave == 3)
-            seg_sum += decay_prepare<C>(decay_log2(vg), lane, rev, p.in_scale, p.up_scale, dec[i & 1]);
+        if (wave != NW - 1) return;
+        const int64_t sum = decay_prepare<C>(vg, lane, rev, p.in_scale, p.up_scale, dec[i & 1]);
+        if (sum == INT64_MIN) {
+            seg_nan = true;
+        } else {
+            // beyond ±2^17 the decay is 0 or inf in any case, and the sum must not wrap
+            const int64_t most = int64_t(1) << 49;
+            seg_sum += sum;
+            seg_sum = seg_sum < -most ? -most : seg_sum > most ? most : seg_sum;
+        }
     };
 
-    if constexpr (!kState) {
-        // tiles of P that the mask empties are read in 32-wide steps but never written again
-        for (int i = tid; i < C * LP; i += 256) lp[i] = M::from(0.0f);
-        if constexpr (kDot)
-            for (int i = tid; i < TB * TB * 16; i += 256) dot_tile[i] = 0.0f;
-    }
+    if constexpr (!kState)
+        // tiles of P that the mask empties are read but never written again
+        for (int i = tid; i < C * C; i += NT) lp[i] = M::from(0.0f);
     if (n > 0) {
         load_g(0);
         load_rows(0);
@@ -369,19 +482,19 @@ __global__ __launch_bounds__(256) void sweep_kernel(const LaSweep p) {
         if (n > 1) load_g(1);
     }
     for (int it = 0; it < n; ++it) {
-        const int64_t t0 = chunk_of(it) * C;
+        const int64_t t0 = first_of(it);
+        const int nv = tokens_at(t0, len);
         __syncthreads();  // the last chunk's readers are done
 #pragma unroll
         for (int x = 0; x < NA; ++x) {
-            const int id = x * 256 + tid, at = (id / (DA / V)) * LA + (id % (DA / V)) * V;
-            *reinterpret_cast<uint4*>(&lb[at]) = vb[x];
-            if constexpr (!kState) *reinterpret_cast<uint4*>(&la_[at]) = va[x];
+            const int at = (tok_a + x * SA) * LA + col_a;
+            *reinterpret_cast<u32x4*>(&lb[at]) = vb[x];
+            if constexpr (!kState) *reinterpret_cast<u32x4*>(&la_[at]) = va[x];
         }
 #pragma unroll
         for (int x = 0; x < NC; ++x) {
-            const int id = x * 256 + tid, at = (id / (DC / V)) * LC + (id % (DC / V)) * V;
-            *reinterpret_cast<uint4*>(&lc[at]) = vc[x];
-            if constexpr (kDot) *reinterpret_cast<uint4*>(&le[at]) = ve[x];
+            *reinterpret_cast<u32x4*>(&lc[(tok_c + x * SC) * LC + col_c]) = vc[x];
+            if constexpr (kDot) *reinterpret_cast<u32x4*>(&le[e_at(tok_c + x * SC, col_c)]) = ve[x];
         }
         __syncthreads();
         if (it + 1 < n) {
@@ -392,99 +505,102 @@ __global__ __launch_bounds__(256) void sweep_kernel(const LaSweep p) {
         const Decay<C>& d = dec[it & 1];
 
         // columns of c, transposed: the operand of out and of the state
-        Frag cf[KS][NT];
+        Frag cf[KS];
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                cf[ks][nt] = col_frag<T>(&lc[32 * ks * LC], LC, lane, jw + 16 * nt, 4);
+        for (int ks = 0; ks < KS; ++ks) cf[ks] = col_frag<T>(&lc[32 * ks * LC], LC, lane, jw, 4);
 
+        // whether something in the wave's columns of c is not finite
+        uint32_t seen = 0;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) seen = not_finite(cf[ks], seen);
+        const unsigned keep = (seen & 0x80008000u) ? 0u : ~0u;
+        const bool bad = __any(keep == 0);
         if constexpr (!kState) {
             // ---- P, transposed tiles: lane's column is token t, its rows four tokens s ----------
-            for (int x = wave; x < kTiles; x += 4) {
-                int hi = 0, lo = x;
-                while (lo > hi) lo -= ++hi;  // row hi of the triangle, 0 <= lo <= hi
+            for (int x = wave; x < kTiles; x += NW) {
+                const int hi = (x >= 1) + (x >= 3) + (x >= 6), lo = x - hi * (hi + 1) / 2;
                 const int tb = rev ? lo : hi, sb = rev ? hi : lo;
                 f32x4 acc = {0, 0, 0, 0}, ec = {0, 0, 0, 0};
+                const Elem* brow = &lb[(16 * sb + l16) * LA + 8 * lg];
+                const Elem* arow = &la_[(16 * tb + l16) * LA + 8 * lg];
 #pragma unroll
-                for (int k = 0; k < IB; ++k)
-                    acc = M::mma(M::row(&lb[(16 * sb + l16) * LA + 32 * k + 8 * lg]),
-                                 M::row(&la_[(16 * tb + l16) * LA + 32 * k + 8 * lg]), acc);
+                for (int k = 0; k < IB; ++k) acc = M::mma(M::row(brow + 32 * k), M::row(arow + 32 * k), acc);
                 if constexpr (kDot) {
+                    const Elem* crow = &lc[(16 * sb + l16) * LC + 8 * lg];
 #pragma unroll
                     for (int k = 0; k < DC / 32; ++k)
-                        ec = M::mma(M::row(&lc[(16 * sb + l16) * LC + 32 * k + 8 * lg]),
-                                    M::row(&le[(16 * tb + l16) * LC + 32 * k + 8 * lg]), ec);
+                        ec = M::mma(M::row(crow + 32 * k), e_row(16 * tb + l16, 32 * k + 8 * lg), ec);
                 }
                 const int t = 16 * tb + l16, s0 = 16 * sb + 4 * lg;
                 const float ft = d.frac[t];
                 const int wt = d.whole[t];
-                float dot = 0.0f;
-                Elem out[4];
+                const f32x4 fs = *reinterpret_cast<const f32x4*>(&d.frac[s0]);
+                const int4 ws = *reinterpret_cast<const int4*>(&d.whole[s0]);
+                const int wsa[4] = {ws.x, ws.y, ws.z, ws.w};
+                float v[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const int s = s0 + r;
-                    const float df = rev ? d.frac[s] - ft : ft - d.frac[s];
-                    const int dw = rev ? d.whole[s] - wt : wt - d.whole[s];
-                    float v = acc[r] * (p.alpha * exp2_parts(df, dw));
-                    // the mask selects: what a masked place holds reaches nothing
-                    v = ((rev ? s >= t : s <= t) && t0 + s < len) ? v : 0.0f;
-                    if (kDot && s != t && (rev ? s >= t : s <= t) && t0 + s < len)
-                        dot = fmaf(v, ec[r], dot);
-                    out[r] = M::from(v);
+                    const float df = ft - fs[r];
+                    const int dw = wt - wsa[r];
+                    v[r] = acc[r] * (p.alpha * exp2_parts(rev ? -df : df, rev ? -dw : dw));
                 }
+                if (tb == sb || nv < C) {
+                    // the mask selects: what a masked place holds reaches nothing
 #pragma unroll
-                for (int r = 0; r < 4; ++r) lp[t * LP + s0 + r] = out[r];
+                    for (int r = 0; r < 4; ++r) {
+                        const int s = s0 + r;
+                        v[r] = (rev ? s >= t : s <= t) && s < nv ? v[r] : 0.0f;
+                    }
+                }
                 if constexpr (kDot) {
+                    double dot = 0.0;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int s = s0 + r;
+                        const bool off = (rev ? s > t : s < t) && s < nv;
+                        dot += off ? double(v[r]) * double(ec[r]) : 0.0;
+                    }
                     dot += __shfl_xor(dot, 16, 64);
                     dot += __shfl_xor(dot, 32, 64);
-                    if (lg == 0) dot_tile[(tb * TB + sb) * 16 + l16] = dot;
+                    if (lg == 0) dot_tile[x * 16 + l16] = dot;
+                }
+                if constexpr (sizeof(T) == 2) {
+                    bf16x4 o;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) o[r] = __bf16(v[r]);
+                    *reinterpret_cast<bf16x4*>(&lp[p_at(t, s0)]) = o;
+                } else {
+                    *reinterpret_cast<f32x4*>(&lp[p_at(t, s0)]) = f32x4{v[0], v[1], v[2], v[3]};
                 }
             }
             // ---- out, transposed: the entering state's part ---------------------------------------
-            f32x4 O[TB][NT];
-            auto entering = [&]() {
+            f32x4 O[TB];
 #pragma unroll
-                for (int tb = 0; tb < TB; ++tb)
+            for (int tb = 0; tb < TB; ++tb) O[tb] = f32x4{0, 0, 0, 0};
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) O[tb][nt] = f32x4{0, 0, 0, 0};
+            for (int ib = 0; ib < IB; ++ib) {
+                Frag sf[kDot ? KT : 1];
+                float v[8];
 #pragma unroll
-                for (int ib = 0; ib < IB; ++ib) {
-                    Frag sf[NT][kDot ? KT : 1];
+                for (int e = 0; e < 8; ++e) v[e] = S[ib][e >> 2][e & 3];
+                if constexpr (kDot) M::split(v, ~0u, sf);
+                else sf[0] = M::round8(v);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        float v[8];
+                for (int tb = 0; tb < TB; ++tb) {
+                    const Frag af = M::row(&la_[(16 * tb + l16) * LA + 32 * ib + 8 * lg]);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] = S[ib][e >> 2][nt][e & 3];
-                        if constexpr (kDot) M::split(v, sf[nt]);
-                        else sf[nt][0] = M::round8(v);
-                    }
-#pragma unroll
-                    for (int tb = 0; tb < TB; ++tb) {
-                        const Frag af = M::row(&la_[(16 * tb + l16) * LA + 32 * ib + 8 * lg]);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int q = 0; q < (kDot ? KT : 1); ++q)
-                                O[tb][nt] = M::mma(sf[nt][q], af, O[tb][nt]);
-                    }
+                    for (int q = 0; q < (kDot ? KT : 1); ++q) O[tb] = M::mma(sf[q], af, O[tb]);
                 }
+            }
 #pragma unroll
-                for (int tb = 0; tb < TB; ++tb)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) O[tb][nt] *= d.in[16 * tb + l16];
-            };
-            entering();
+            for (int tb = 0; tb < TB; ++tb) O[tb] *= d.in[16 * tb + l16];
             if constexpr (kDot) {
 #pragma unroll
                 for (int tb = 0; tb < TB; ++tb) {
                     float dot = 0.0f;
+                    const Elem* q = &le[e_at(16 * tb + l16, jw + 4 * lg)];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            dot = fmaf(float(le[(16 * tb + l16) * LC + jw + 16 * nt + 4 * lg + r]),
-                                       O[tb][nt][r], dot);
+                    for (int r = 0; r < 4; ++r) dot = fmaf(float(q[r]), O[tb][r], dot);
                     dot += __shfl_xor(dot, 16, 64);
                     dot += __shfl_xor(dot, 32, 64);
                     if (lg == 0) dot_wave[wave * C + 16 * tb + l16] = dot;
@@ -493,84 +609,84 @@ __global__ __launch_bounds__(256) void sweep_kernel(const LaSweep p) {
             __syncthreads();  // P is whole
             if constexpr (kDot) {
                 if (tid < C && t0 + tid < p.T) {
-                    float dot = 0.0f;
+                    double dot = 0.0;
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) dot += dot_wave[w * C + tid];
-#pragma unroll
-                    for (int sb = 0; sb < TB; ++sb) dot += dot_tile[((tid >> 4) * TB + sb) * 16 + (tid & 15)];
-                    p.dots[(int64_t(tile) * p.B * p.H + bh) * p.T + t0 + tid] = t0 + tid < len ? dot : 0.0f;
+                    for (int w = 0; w < NW; ++w) dot += double(dot_wave[w * C + tid]);
+                    const int tb = tid >> 4;
+                    for (int x = 0; x < kTiles; ++x) {
+                        const int hi = (x >= 1) + (x >= 3) + (x >= 6), lo = x - hi * (hi + 1) / 2;
+                        if ((rev ? lo : hi) == tb) dot += dot_tile[x * 16 + (tid & 15)];
+                    }
+                    p.dots[(int64_t(tile) * p.B * p.H + bh) * p.T + t0 + tid] = tid < nv ? dot : 0.0;
                 }
             }
             // ---- the chunk's own part ---------------------------------------------------------------
-            float probe = 0.0f;
+            // All of P, the tiles that the mask empties too (zeros): a branch around a product is
+            // avoided, since the compiler (ROCm 7.2's) has left too few wait states before the
+            // use of a product's result on a path that jumps over a block behind the product.
+            if (!bad) {
 #pragma unroll
-            for (int tb = 0; tb < TB; ++tb) {
+                for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    if (rev ? ks < tb / 2 : ks > tb / 2) continue;
-                    const Frag pf = M::row(&lp[(16 * tb + l16) * LP + 32 * ks + 8 * lg]);
+                    for (int ks = 0; ks < KS; ++ks)
+                        O[tb] = M::mma(cf[ks], p_row(16 * tb + l16, 32 * ks + 8 * lg), O[tb]);
+            } else {
+                // A masked weight is 0, and its product with an infinity would be NaN: the
+                // allowed pairs alone, one by one.
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) O[tb][nt] = M::mma(cf[ks][nt], pf, O[tb][nt]);
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) probe = fmaf(O[tb][nt][r], 0.0f, probe);
-            }
-            // A masked weight is 0, and 0·inf in the product above is NaN: where something not
-            // finite came out, the products are formed again from the allowed pairs alone.
-            if (__any(probe != probe)) {
-                entering();
                 for (int tb = 0; tb < TB; ++tb) {
                     const int t = 16 * tb + l16;
-                    for (int s = 0; s < C; ++s) {
-                        if ((rev ? s < t : s > t) || t0 + s >= len) continue;
-                        const float w = float(lp[t * LP + s]);
+#pragma unroll 1
+                    for (int s = 0; s < nv; ++s) {
+                        if (rev ? s < t : s > t) continue;
+                        const float w = float(lp[p_at(t, s)]);
 #pragma unroll
-                        for (int q = 0; q < TB; ++q)
-                            if (q == tb)
-#pragma unroll
-                                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                    for (int r = 0; r < 4; ++r)
-                                        O[q][nt][r] = fmaf(w, float(lc[s * LC + jw + 16 * nt + 4 * lg + r]), O[q][nt][r]);
+                        for (int r = 0; r < 4; ++r)
+                            O[tb][r] = fmaf(w, float(lc[s * LC + jw + 4 * lg + r]), O[tb][r]);
                     }
                 }
             }
             // ---- store: four consecutive columns of one token a lane ------------------------------------
+            if (nv < C) {
 #pragma unroll
-            for (int tb = 0; tb < TB; ++tb) {
-                const int64_t t = t0 + 16 * tb + l16;
-                if (t >= p.T) continue;
+                for (int tb = 0; tb < TB; ++tb)
+                    if (16 * tb + l16 >= nv) O[tb] = f32x4{0, 0, 0, 0};
+            }
+            const int rows = tokens_at(t0, p.T), dim = p.c.dim;
+            const int64_t first = ((b * p.T + t0) * p.H + h) * dim;
+            const bool wide = sizeof(T) == 4 || p.out_f32;
+            const int st = int(p.H) * dim, el = wide ? 4 : 2;
+            // the descriptor ends with the chunk's last row: tokens beyond are dropped
+            const __amdgpu_buffer_rsrc_t od = __builtin_amdgcn_make_buffer_rsrc(
+                static_cast<char*>(p.out) + first * el, 0, ((rows - 1) * st + dim) * el, kRsrcFlags);
+            const int j = c0 + jw + 4 * lg;
+            const unsigned at = j < dim ? unsigned((l16 * st + j) * el) : kNowhere;
+            if (dim % 4 == 0) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const int j = c0 + jw + 16 * nt + 4 * lg;
-                    const int left = p.c.dim - j;
-                    if (left <= 0) continue;
-                    f32x4 v = O[tb][nt];
-                    if (t >= len) v = f32x4{0, 0, 0, 0};
-                    const int64_t at = ((b * p.T + t) * p.H + h) * p.c.dim + j;
-                    if (sizeof(T) == 4 || p.out_f32) {
-                        float* o = static_cast<float*>(p.out) + at;
-                        if (left >= 4 && p.c.dim % 4 == 0) {
-                            *reinterpret_cast<f32x4*>(o) = v;
-                        } else {
-#pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                if (r < left) o[r] = v[r];
-                        }
+                for (int tb = 0; tb < TB; ++tb) {
+                    if (wide) {
+                        union { f32x4 f; u32x4 u; } w;
+                        w.f = O[tb];
+                        __builtin_amdgcn_raw_buffer_store_b128(w.u, od, int(at), 16 * tb * st * el, 0);
                     } else {
-                        __bf16* o = static_cast<__bf16*>(p.out) + at;
-                        bf16x4 w;
+                        union { bf16x4 f; u32x2 u; } w;
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) w[r] = __bf16(v[r]);
-                        if (left >= 4 && p.c.dim % 4 == 0) {
-                            *reinterpret_cast<bf16x4*>(o) = w;
-                        } else {
+                        for (int r = 0; r < 4; ++r) w.f[r] = __bf16(O[tb][r]);
+                        __builtin_amdgcn_raw_buffer_store_b64(w.u, od, int(at), 16 * tb * st * el, 0);
+                    }
+                }
+            } else {
 #pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                if (r < left) o[r] = w[r];
-                        }
+                for (int r = 0; r < 4; ++r) {
+                    const unsigned to = j + r < dim ? at + unsigned(r * el) : kNowhere;
+#pragma unroll
+                    for (int tb = 0; tb < TB; ++tb) {
+                        union { float f; unsigned u; } w;
+                        union { __bf16 f; unsigned short u; } x;
+                        w.f = O[tb][r];
+                        x.f = __bf16(O[tb][r]);
+                        if (wide) __builtin_amdgcn_raw_buffer_store_b32(w.u, od, int(to), 16 * tb * st * el, 0);
+                        else __builtin_amdgcn_raw_buffer_store_b16(x.u, od, int(to), 16 * tb * st * el, 0);
                     }
                 }
             }
@@ -581,28 +697,23 @@ __global__ __launch_bounds__(256) void sweep_kernel(const LaSweep p) {
 #pragma unroll
         for (int ib = 0; ib < IB; ++ib)
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) S[ib][u][nt] *= all;
+            for (int u = 0; u < 2; ++u) S[ib][u] *= all;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-            Frag wf[NT][KT];
+            Frag wf[KT];
+            const f32x4 u0 = *reinterpret_cast<const f32x4*>(&d.up[32 * ks + 8 * lg]);
+            const f32x4 u1 = *reinterpret_cast<const f32x4*>(&d.up[32 * ks + 8 * lg + 4]);
+            float v[8];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float v[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = M::get(cf[ks][nt], e) * d.up[32 * ks + 8 * lg + e];
-                M::split(v, wf[nt]);
-            }
+            for (int e = 0; e < 8; ++e) v[e] = M::get(cf[ks], e) * (e < 4 ? u0[e & 3] : u1[e & 3]);
+            M::split(v, keep, wf);
 #pragma unroll
             for (int ib = 0; ib < IB; ++ib)
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const Frag bf = col_frag<T>(&lb[32 * ks * LA], LA, lane, 32 * ib + 4 * u, 8);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int q = KT - 1; q >= 0; --q) S[ib][u][nt] = M::mma(bf, wf[nt][q], S[ib][u][nt]);
+                    for (int q = KT - 1; q >= 0; --q) S[ib][u] = M::mma(bf, wf[q], S[ib][u]);
                 }
         }
     }
@@ -616,38 +727,36 @@ __global__ __launch_bounds__(256) void sweep_kernel(const LaSweep p) {
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const int j = c0 + jw + 16 * nt + l16;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int i = 32 * ib + 8 * lg + 4 * u + r;
-                        if (i < p.b.dim && j < p.c.dim) so[int64_t(i) * p.c.dim + j] = S[ib][u][nt][r];
-                    }
+                for (int r = 0; r < 4; ++r) {
+                    const int i = 32 * ib + 8 * lg + 4 * u + r, j = c0 + jw + l16;
+                    if (i < p.b.dim && j < p.c.dim) so[i * p.c.dim + j] = S[ib][u][r];
                 }
     }
-    if (kState && tile == 0 && tid == 192) p.seg_decay[bh * p.nseg + seg] = exp2_wide(seg_sum);
+    if (kState && tile == 0 && tid == NT - 64)
+        p.seg_decay[bh * p.nseg + seg] = seg_nan ? __builtin_nanf("") : exp2_fixed(seg_sum);
 }
 
-template <typename T, int DA, int NT>
+template <typename T, bool kVec, int DA, int NW>
 hipError_t launch_sweep_t(const LaSweep& p, hipStream_t s) {
     const int64_t blocks = int64_t(p.tiles) * p.H * p.grid_seg * p.B;
     if (blocks <= 0) return hipSuccess;
-    const dim3 grid{unsigned(blocks)}, block(256);
-    if (p.state_only) hipLaunchKernelGGL((sweep_kernel<T, DA, NT, false, true>), grid, block, 0, s, p);
-    else if (p.dots) hipLaunchKernelGGL((sweep_kernel<T, DA, NT, true, false>), grid, block, 0, s, p);
-    else hipLaunchKernelGGL((sweep_kernel<T, DA, NT, false, false>), grid, block, 0, s, p);
+    const dim3 grid{unsigned(blocks)}, block(64 * NW);
+    if (p.state_only) hipLaunchKernelGGL((sweep_kernel<T, kVec, DA, NW, false, true>), grid, block, 0, s, p);
+    else if (p.dots) hipLaunchKernelGGL((sweep_kernel<T, kVec, DA, NW, true, false>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((sweep_kernel<T, kVec, DA, NW, false, false>), grid, block, 0, s, p);
     return hipGetLastError();
 }
 
-template <typename T>
+template <typename T, bool kVec>
 hipError_t launch_sweep_type(const LaSweep& p, hipStream_t s) {
-    const int key = p.pad_a * 10 + p.nt;
+    const int key = p.pad_a * 10 + p.waves;
     switch (key) {
-        case 641: return launch_sweep_t<T, 64, 1>(p, s);
-        case 642: return launch_sweep_t<T, 64, 2>(p, s);
-        case 1281: return launch_sweep_t<T, 128, 1>(p, s);
-        case 1282: return launch_sweep_t<T, 128, 2>(p, s);
-        case 2561: return launch_sweep_t<T, 256, 1>(p, s);
+        case 644: return launch_sweep_t<T, kVec, 64, 4>(p, s);
+        case 648: return launch_sweep_t<T, kVec, 64, 8>(p, s);
+        case 1284: return launch_sweep_t<T, kVec, 128, 4>(p, s);
+        case 1288: return launch_sweep_t<T, kVec, 128, 8>(p, s);
+        case 2564: return launch_sweep_t<T, kVec, 256, 4>(p, s);
+        case 2568: return launch_sweep_t<T, kVec, 256, 8>(p, s);
         default: return hipErrorInvalidValue;
     }
 }
