@@ -34,7 +34,7 @@
 // length, and a token that decays by e^{-inf} cuts the sequence exactly.  P, and S where it
 // feeds out, are rounded to bf16 once (the operand the matrix cores take; out is bf16 too).
 // The state's own sums are float32: c's weight w is not a bf16 value, so w·c is fed as three
-// bf16 terms (24 bits).  The products behind dg (P, e·c, e·(Sᵀa)) are kept in float32 the same
+// bf16 terms (24 bits, all of it).  The products behind dg (P, e·c, e·(Sᵀa)) are kept in float32 the same
 // way, since dg is float32.  With float32 rows the matrix cores' float32 form runs on the same
 // layouts and nothing is rounded.
 #pragma once
@@ -70,15 +70,17 @@ struct Mma<bf16_t> {
     static __device__ __forceinline__ Frag row(const Elem* p) {
         return *reinterpret_cast<const Frag*>(p);
     }
-    // Transposed: eight consecutive rows (tokens) of one column.  In a group of 16 lanes,
-    // lane λ of ds_read_b64_tr_b16 names four consecutive elements (row λ / 4, piece λ % 4 of
-    // 16 columns) and receives column λ of the four rows.  p: row 0 of the 32 tokens; col(q):
-    // the first column of piece q.
+    // Transposed: one column of eight tokens, 4·(l / 16) .. + 3 and the same 16 tokens on (the
+    // order of tokens along k is free; in this one the eight rows that 32 lanes read together
+    // lie next to each other, in different banks).  In a group of 16 lanes, lane λ of
+    // ds_read_b64_tr_b16 names four consecutive elements (row λ / 4, piece λ % 4 of 16 columns)
+    // and receives column λ of the four rows.  p: row 0 of the 32 tokens; piece_col: the first
+    // column of piece λ % 4.
     static __device__ __forceinline__ Frag col(const Elem* p, int ld, int lane, int piece_col) {
-        const Elem* q = p + (8 * (lane >> 4) + ((lane >> 2) & 3)) * ld + piece_col;
+        const Elem* q = p + (4 * (lane >> 4) + ((lane >> 2) & 3)) * ld + piece_col;
         typedef __attribute__((address_space(3))) s16x4* Lds;
         const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(q));
-        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(q + 4 * ld));
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(q + 16 * ld));
         union { s16x4 h[2]; Frag f; } u;
         u.h[0] = lo;
         u.h[1] = hi;
@@ -92,24 +94,29 @@ struct Mma<bf16_t> {
         for (int e = 0; e < 8; ++e) f[e] = Elem(v[e]);
         return f;
     }
-    // v as kTerms bf16 terms that sum to it (relative error below 2^-24).  keep: all ones, or
-    // zero where v may hold an infinity, which is then its first term alone.
+    // v as kTerms bf16 terms that sum to it exactly: each takes the upper eight significant bits
+    // of what is left.  keep 0 (else all ones) where v may hold an infinity, which is then its
+    // first term alone.
     static __device__ __forceinline__ void split(const float (&v)[8], unsigned keep, Frag (&f)[kTerms]) {
-        float r[8];
-        f[0] = round8(v);
+        const unsigned upper = 0x07060302u, rest = keep ? upper : 0x0c0c0c0cu;
+        union { Frag f; unsigned w[4]; } t[3];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) r[e] = v[e] - float(f[0][e]);
-        f[1] = masked(round8(r), keep);
+        for (int i = 0; i < 4; ++i) {
+            unsigned x[2][3];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) r[e] -= float(f[1][e]);
-        f[2] = masked(round8(r), keep);
-    }
-    static __device__ __forceinline__ Frag masked(Frag f, unsigned keep) {
-        union { Frag f; unsigned w[4]; } u;
-        u.f = f;
+            for (int y = 0; y < 2; ++y) {
+                const float a = v[2 * i + y];
+                x[y][0] = __float_as_uint(a);
+                const float b = a - __uint_as_float(x[y][0] & 0xffff0000u);
+                x[y][1] = __float_as_uint(b);
+                x[y][2] = __float_as_uint(b - __uint_as_float(x[y][1] & 0xffff0000u));
+            }
+            t[0].w[i] = __builtin_amdgcn_perm(x[1][0], x[0][0], upper);
+            t[1].w[i] = __builtin_amdgcn_perm(x[1][1], x[0][1], rest);
+            t[2].w[i] = __builtin_amdgcn_perm(x[1][2], x[0][2], rest);
+        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) u.w[i] &= keep;
-        return u.f;
+        for (int q = 0; q < 3; ++q) f[q] = t[q].f;
     }
 };
 
@@ -135,10 +142,10 @@ struct Mma<float> {
     // piece_col as above: lane λ's own column is that of piece λ / 4, element λ % 4, which the
     // caller's formula gives for the lane whose λ % 4 is that piece
     static __device__ __forceinline__ Frag col_at(const Elem* p, int ld, int lane, int column) {
-        const Elem* q = p + 8 * (lane >> 4) * ld + column;
+        const Elem* q = p + 4 * (lane >> 4) * ld + column;
         Frag f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = q[e * ld];
+        for (int e = 0; e < 8; ++e) f[e] = q[(e < 4 ? e : 12 + e) * ld];
         return f;
     }
     static __device__ __forceinline__ float get(Frag f, int e) { return f[e]; }
@@ -347,13 +354,14 @@ __global__ __launch_bounds__(64 * NW, sweep_occupancy(kVec, DA, NW, kDot, kState
     constexpr int NT = 64 * NW;                     // threads
     constexpr int DC = 16 * NW;                     // columns of a workgroup
     constexpr int kPad = 16 / int(sizeof(Elem));    // rows start 16 bytes (four banks) apart
-    constexpr int LA = DA + kPad, LC = DC + kPad;
+    constexpr int LA = DA + kPad;                   // read by rows of 16 bytes
+    constexpr int LB = DA + 2 * kPad, LC = DC + 2 * kPad;   // read transposed, 32 bytes a row
     constexpr int NA = C * DA / V / NT, NC = C * DC / V / NT;    // 16-byte pieces of a thread
     constexpr int SA = NT * V / DA, SC = NT * V / DC;            // tokens between them
     constexpr int TB = C / 16, KS = C / 32, IB = DA / 32;
     constexpr int kTiles = TB * (TB + 1) / 2;
 
-    __shared__ __attribute__((aligned(16))) Elem lb[C * LA];
+    __shared__ __attribute__((aligned(16))) Elem lb[C * LB];
     __shared__ __attribute__((aligned(16))) Elem lc[C * LC];
     __shared__ __attribute__((aligned(16))) Elem la_[kState ? 8 : C * LA];
     __shared__ __attribute__((aligned(16))) Elem lp[kState ? 8 : C * C];
@@ -365,8 +373,9 @@ __global__ __launch_bounds__(64 * NW, sweep_occupancy(kVec, DA, NW, kDot, kState
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int l16 = lane & 15, lg = lane >> 4;
-    // P and e lie in LDS without padding, their 16-byte pieces exchanged by row instead
-    auto p_at = [](int t, int s) { return t * C + (((s / V) ^ (t & (C / V - 1))) * V) + s % V; };
+    // P and e lie in LDS without padding, their 16-byte pieces exchanged by row instead; P with
+    // the tokens s of each 32 in the order of the transposed operands
+    auto p_at = [](int t, int s) { return t * C + (((s / V) ^ ((t >> 1) & (C / V - 1))) * V) + s % V; };
     auto e_at = [](int t, int j) { return t * DC + (((j / V) ^ (t & (DC / V - 1))) * V) + j % V; };
     auto p_row = [&](int t, int s) {   // eight consecutive values
         if constexpr (sizeof(T) == 2) return M::row(&lp[p_at(t, s)]);
@@ -384,8 +393,11 @@ __global__ __launch_bounds__(64 * NW, sweep_occupancy(kVec, DA, NW, kDot, kState
             return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
         }
     };
-    // blocks: column tile fastest, then head, then segment, then batch row
-    unsigned blk = blockIdx.x;
+    // Work items: column tile fastest, then head, then segment, then batch row.  Workgroups go
+    // round the eight XCDs in turn, so each XCD is given a run of consecutive items: the tiles
+    // of a head, and the heads that share q and k, find each other's rows in their L2.
+    const unsigned xcd = blockIdx.x % 8, each = gridDim.x / 8, more = gridDim.x % 8;
+    unsigned blk = xcd * each + (xcd < more ? xcd : more) + blockIdx.x / 8;
     const int tile = int(blk % unsigned(p.tiles));
     blk /= unsigned(p.tiles);
     const int64_t h = blk % unsigned(p.H);
@@ -487,9 +499,9 @@ __global__ __launch_bounds__(64 * NW, sweep_occupancy(kVec, DA, NW, kDot, kState
         __syncthreads();  // the last chunk's readers are done
 #pragma unroll
         for (int x = 0; x < NA; ++x) {
-            const int at = (tok_a + x * SA) * LA + col_a;
-            *reinterpret_cast<u32x4*>(&lb[at]) = vb[x];
-            if constexpr (!kState) *reinterpret_cast<u32x4*>(&la_[at]) = va[x];
+            const int t = tok_a + x * SA;
+            *reinterpret_cast<u32x4*>(&lb[t * LB + col_a]) = vb[x];
+            if constexpr (!kState) *reinterpret_cast<u32x4*>(&la_[t * LA + col_a]) = va[x];
         }
 #pragma unroll
         for (int x = 0; x < NC; ++x) {
@@ -521,7 +533,7 @@ __global__ __launch_bounds__(64 * NW, sweep_occupancy(kVec, DA, NW, kDot, kState
                 const int hi = (x >= 1) + (x >= 3) + (x >= 6), lo = x - hi * (hi + 1) / 2;
                 const int tb = rev ? lo : hi, sb = rev ? hi : lo;
                 f32x4 acc = {0, 0, 0, 0}, ec = {0, 0, 0, 0};
-                const Elem* brow = &lb[(16 * sb + l16) * LA + 8 * lg];
+                const Elem* brow = &lb[(16 * sb + l16) * LB + 8 * lg];
                 const Elem* arow = &la_[(16 * tb + l16) * LA + 8 * lg];
 #pragma unroll
                 for (int k = 0; k < IB; ++k) acc = M::mma(M::row(brow + 32 * k), M::row(arow + 32 * k), acc);
@@ -532,6 +544,7 @@ __global__ __launch_bounds__(64 * NW, sweep_occupancy(kVec, DA, NW, kDot, kState
                         ec = M::mma(M::row(crow + 32 * k), e_row(16 * tb + l16, 32 * k + 8 * lg), ec);
                 }
                 const int t = 16 * tb + l16, s0 = 16 * sb + 4 * lg;
+                const int sp = 32 * (sb / 2) + 8 * lg + 4 * (sb & 1);   // s0's place in P
                 const float ft = d.frac[t];
                 const int wt = d.whole[t];
                 const f32x4 fs = *reinterpret_cast<const f32x4*>(&d.frac[s0]);
@@ -568,9 +581,9 @@ __global__ __launch_bounds__(64 * NW, sweep_occupancy(kVec, DA, NW, kDot, kState
                     bf16x4 o;
 #pragma unroll
                     for (int r = 0; r < 4; ++r) o[r] = __bf16(v[r]);
-                    *reinterpret_cast<bf16x4*>(&lp[p_at(t, s0)]) = o;
+                    *reinterpret_cast<bf16x4*>(&lp[p_at(t, sp)]) = o;
                 } else {
-                    *reinterpret_cast<f32x4*>(&lp[p_at(t, s0)]) = f32x4{v[0], v[1], v[2], v[3]};
+                    *reinterpret_cast<f32x4*>(&lp[p_at(t, sp)]) = f32x4{v[0], v[1], v[2], v[3]};
                 }
             }
             // ---- out, transposed: the entering state's part ---------------------------------------
@@ -639,7 +652,8 @@ __global__ __launch_bounds__(64 * NW, sweep_occupancy(kVec, DA, NW, kDot, kState
 #pragma unroll 1
                     for (int s = 0; s < nv; ++s) {
                         if (rev ? s < t : s > t) continue;
-                        const float w = float(lp[p_at(t, s)]);
+                        const int sp = (s & ~31) + 8 * ((s >> 2) & 3) + 4 * ((s >> 4) & 1) + (s & 3);
+                        const float w = float(lp[p_at(t, sp)]);
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
                             O[tb][r] = fmaf(w, float(lc[s * LC + jw + 4 * lg + r]), O[tb][r]);
@@ -701,8 +715,8 @@ __global__ __launch_bounds__(64 * NW, sweep_occupancy(kVec, DA, NW, kDot, kState
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
             Frag wf[KT];
-            const f32x4 u0 = *reinterpret_cast<const f32x4*>(&d.up[32 * ks + 8 * lg]);
-            const f32x4 u1 = *reinterpret_cast<const f32x4*>(&d.up[32 * ks + 8 * lg + 4]);
+            const f32x4 u0 = *reinterpret_cast<const f32x4*>(&d.up[32 * ks + 4 * lg]);
+            const f32x4 u1 = *reinterpret_cast<const f32x4*>(&d.up[32 * ks + 16 + 4 * lg]);
             float v[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = M::get(cf[ks], e) * (e < 4 ? u0[e & 3] : u1[e & 3]);
@@ -711,7 +725,7 @@ __global__ __launch_bounds__(64 * NW, sweep_occupancy(kVec, DA, NW, kDot, kState
             for (int ib = 0; ib < IB; ++ib)
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const Frag bf = col_frag<T>(&lb[32 * ks * LA], LA, lane, 32 * ib + 4 * u, 8);
+                    const Frag bf = col_frag<T>(&lb[32 * ks * LB], LB, lane, 32 * ib + 4 * u, 8);
 #pragma unroll
                     for (int q = KT - 1; q >= 0; --q) S[ib][u] = M::mma(bf, wf[q], S[ib][u]);
                 }
