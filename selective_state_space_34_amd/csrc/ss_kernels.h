@@ -248,15 +248,13 @@ struct RmsLaunch {
     float *y_scale, *part;
     int64_t M, D;
     float eps, inv_d;
-    int in_dtype, res_dtype, q8, vec;
+    int in_dtype, res_dtype, q8;
     int threads, pieces, grid;   // threads of a row, eight-element pieces of each, workgroups
 };
 hipError_t launch_rms_fwd(const RmsLaunch& p, hipStream_t s);
 hipError_t launch_rms_bwd(const RmsLaunch& p, float* dw, hipStream_t s);
 
 // ---- products with 4-bit weights (ss_q4.hip) -----------------------------------------------------
-
-constexpr int kQ4Lds = 57344;    // most bytes of x that a workgroup keeps in LDS (two a CU)
 
 struct Q4Launch {
     const void* x;               // [M, K]
@@ -266,8 +264,7 @@ struct Q4Launch {
     const uint8_t* zeros;        // nullable [N, groups]
     void* y;                     // [M, N]
     int64_t M, N, K, groups;
-    int64_t slab;                // k of x in LDS at a time, a multiple of the group
-    int mb;                      // rows of x of a workgroup
+    int mb, tiles;               // of a workgroup: rows of x, 16-row tiles of weights
     int group, in_dtype, x_q8, y_dtype;
 };
 hipError_t launch_q4(const Q4Launch& p, hipStream_t s);

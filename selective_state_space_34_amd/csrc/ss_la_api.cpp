@@ -130,7 +130,7 @@ int workspace_size(const ss_la_dims* dims, bool backward, size_t* bytes) {
 ss::RmsLaunch rms_launch(const ss_rms_dims& d, const ss::RmsPlan& p) {
     ss::RmsLaunch l{};
     l.M = p.M; l.D = p.D; l.eps = d.eps; l.inv_d = float(1.0 / double(p.D));
-    l.in_dtype = d.in_dtype; l.res_dtype = d.res_dtype; l.vec = p.vec;
+    l.in_dtype = d.in_dtype; l.res_dtype = d.res_dtype;
     l.threads = p.threads; l.pieces = p.pieces; l.grid = p.grid;
     return l;
 }
@@ -324,7 +324,7 @@ int ss_q4_mv(const ss_q4_dims* dims, const void* x, const float* x_scale, const 
              const void* scales, const void* zeros, void* y, hipStream_t stream) {
     if (!dims) return SS_ERR_NULL;
     ss::Q4Plan p;
-    const int rc = ss::make_q4_plan(*dims, ss::kQ4Lds, &p);
+    const int rc = ss::make_q4_plan(*dims, &p);
     if (rc != SS_OK) return rc;
     if (!x || !wq || !scales || !y || ((dims->x_q8 != SS_Q8_NONE) != (x_scale != nullptr)))
         return SS_ERR_NULL;
@@ -335,7 +335,7 @@ int ss_q4_mv(const ss_q4_dims* dims, const void* x, const float* x_scale, const 
     l.x = x; l.x_scale = x_scale; l.wq = static_cast<const uint8_t*>(wq);
     l.scales = static_cast<const uint16_t*>(scales); l.zeros = static_cast<const uint8_t*>(zeros);
     l.y = y; l.M = dims->rows; l.N = dims->n; l.K = dims->k;
-    l.groups = p.groups; l.slab = p.slab; l.mb = p.mb; l.group = dims->group;
+    l.groups = p.groups; l.mb = p.mb; l.tiles = p.tiles; l.group = dims->group;
     l.in_dtype = dims->in_dtype; l.x_q8 = dims->x_q8; l.y_dtype = dims->y_dtype;
     const hipError_t e = ss::launch_q4(l, stream);
     return e == hipSuccess ? SS_OK : hip_fail(e);

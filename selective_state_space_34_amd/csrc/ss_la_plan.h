@@ -115,7 +115,7 @@ inline int make_la_plan(const ss_la_dims& d, bool backward, LaPlan* out) {
 // Norm: how many threads share a row and how many eight-element pieces each holds.
 struct RmsPlan {
     int64_t M, D;
-    int threads, pieces, grid, vec;
+    int threads, pieces, grid;
     size_t total;                // backward: part [grid, D] float32
 };
 
@@ -132,37 +132,48 @@ inline int make_rms_plan(const ss_rms_dims& d, bool backward, RmsPlan* out) {
     if (!(d.eps >= 0.0f) || !(d.eps - d.eps == 0.0f)) return SS_ERR_DIMS;
     RmsPlan p{};
     p.M = d.rows; p.D = d.dim;
-    p.vec = d.dim % 8 == 0;
     const int64_t D = d.dim;
-    // a wave a row up to six pieces where there are rows enough to fill the part; wider rows,
-    // and few rows, take a workgroup
-    if (D <= 512 || (D <= 64 * 8 * 6 && d.rows >= 1024)) {
+    // The fewest threads that hold a row in one or two pieces each, so that many rows are in
+    // flight on a CU.  In between, 2048 < D <= 64·8·6, the forward over many rows is faster with
+    // a wave a row and no barrier (D = 2560, 16384 rows, bf16, 8-bit output: 56 us against 61;
+    // odd width 2563: 75 against 96), the gradient, with three rows and dw to hold, is not
+    // (97 us against 83).
+    if (D <= 64 * 8 * 2) {
         p.threads = 64;
-        p.pieces = D <= 512 ? 1 : D <= 1024 ? 2 : D <= 2048 ? 4 : 6;
-    } else if (D <= 256 * 8 * 4) {
+        p.pieces = D <= 64 * 8 ? 1 : 2;
+    } else if (!backward && D > 256 * 8 && D <= 64 * 8 * 6 && d.rows >= 1024) {
+        p.threads = 64;
+        p.pieces = 6;
+    } else if (D <= 256 * 8 * 2) {
         p.threads = 256;
-        p.pieces = D <= 2048 ? 1 : D <= 4096 ? 2 : 4;
+        p.pieces = D <= 256 * 8 ? 1 : 2;
+    } else if (D <= 512 * 8 * 2) {
+        p.threads = 512;
+        p.pieces = 2;
     } else {
         p.threads = 1024;
-        p.pieces = D <= 16384 ? 2 : 4;
+        p.pieces = D <= 1024 * 8 * 2 ? 2 : 4;
     }
     const int64_t wg_rows = p.threads >= 256 ? 1 : 256 / p.threads;
     const int64_t need = (d.rows + wg_rows - 1) / wg_rows;
-    // workgroups take rows in turn: enough of them to fill the 256 CUs
-    const int64_t most = p.threads == 1024 ? 512 : backward ? 512 : 2048;
+    // Workgroups take rows in turn.  Two on each CU where one holds much or leaves a row of
+    // partial sums (gradient, D = 2560: 1024 workgroups 81 us, 2048 86; D = 5120: 512 146 us,
+    // 1024 153), else eight.
+    const int64_t most = p.threads >= 512 || p.pieces == 6 ? 512
+                       : backward ? (p.threads == 256 ? 1024 : 512) : 2048;
     p.grid = int(need < most ? need : most);
     p.total = backward ? align256(size_t(p.grid) * size_t(D) * sizeof(float)) : 0;
     *out = p;
     return SS_OK;
 }
 
-// 4-bit products: rows of x a workgroup takes, and how much of them stays in LDS at a time.
+// 4-bit products: rows of x a workgroup takes, and its 16-row tiles of weights.
 struct Q4Plan {
-    int64_t groups, slab;
-    int mb;
+    int64_t groups;
+    int mb, tiles;
 };
 
-inline int make_q4_plan(const ss_q4_dims& d, int64_t lds, Q4Plan* out) {
+inline int make_q4_plan(const ss_q4_dims& d, Q4Plan* out) {
     if (d.rows <= 0 || d.n <= 0 || d.k <= 0 || d.k % 32 != 0) return SS_ERR_DIMS;
     if (d.group != 32 && d.group != 64 && d.group != 128) return SS_ERR_DIMS;
     if (d.in_dtype != SS_F32 && d.in_dtype != SS_BF16) return SS_ERR_DTYPE;
@@ -177,11 +188,12 @@ inline int make_q4_plan(const ss_q4_dims& d, int64_t lds, Q4Plan* out) {
     if (d.rows < p.mb) p.mb = int(d.rows);
     if ((d.rows + p.mb - 1) / p.mb > kMaxGridYZ) return SS_ERR_DIMS;
     p.groups = (d.k + d.group - 1) / d.group;
-    // rows are padded by 8 elements in LDS
-    int64_t most = lds / 2 / (p.mb * terms) - 8;
-    most = most / (4 * d.group) * (4 * d.group);   // whole rounds of the four waves
-    const int64_t all = p.groups * d.group;
-    p.slab = all < most ? all : most;
+    // A workgroup's eight waves share the groups of its rows of weights.  Two tiles of rows share the
+    // work on x where that leaves a workgroup for every CU (bf16, us: 16 x 2560 by 10240 11 with
+    // two tiles, 12.5 with one; 1 x 8192 by 16384 24 against 27); with fewer, one tile keeps
+    // more CUs busy (16 x 5120 in 8 bits by 2560 11 against 17).
+    const int64_t wgs = (d.n + 15) / 16 * ((d.rows + p.mb - 1) / p.mb);
+    p.tiles = wgs >= 512 ? 2 : 1;
     *out = p;
     return SS_OK;
 }

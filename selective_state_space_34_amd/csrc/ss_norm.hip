@@ -7,7 +7,7 @@
 //   dx = dr + c·(w·dy) - r·(c³/D)·Σ(w·dy·r)        dw = Σ_rows dy·r·c
 //
 // The work is traffic: every element is read once and written once, a row staying in registers
-// between the sums and the result.  A row belongs to P threads (64, 256 or 1024, by its length
+// between the sums and the result.  A row belongs to P threads (64 to 1024, by its length
 // and by how many rows there are), eight consecutive elements of it to each thread at a time,
 // NV such pieces a thread; sums meet by shuffles, across waves through LDS.  Workgroups take
 // rows in turn, so that in the gradient the columns' sums stay in registers over a workgroup's
@@ -25,44 +25,64 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-// Eight consecutive elements from col, zeros beyond the width; vec: whole aligned pieces.
-template <typename T>
-__device__ __forceinline__ void get8(const T* row, int64_t col, int64_t dim, int vec, float (&o)[8]) {
-    if (vec) {
-        if (col < dim) {
-            load8(row + col, o);
-            return;
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = col + e < dim ? to_f32(row[col + e]) : 0.0f;
-        return;
+// Eight consecutive elements as they lie in memory; 16-byte accesses that need only the
+// elements' alignment (rows of odd widths start anywhere).
+template <typename T> struct Piece;
+template <> struct Piece<bf16_t> {
+    u32x4 w;
+    __device__ __forceinline__ float get(int e) const {
+        return __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
     }
+    __device__ __forceinline__ void load(const bf16_t* p) { __builtin_memcpy(&w, p, 16); }
+    __device__ __forceinline__ void clear() { w = u32x4{0, 0, 0, 0}; }
+    __device__ __forceinline__ void set(int e, bf16_t v) { w[e / 2] |= uint32_t(v.bits) << (16 * (e & 1)); }
+};
+template <> struct Piece<float> {
+    f32x4 v[2];
+    __device__ __forceinline__ float get(int e) const { return v[e / 4][e & 3]; }
+    __device__ __forceinline__ void load(const float* p) { __builtin_memcpy(&v, p, 32); }
+    __device__ __forceinline__ void clear() { v[0] = v[1] = f32x4{0, 0, 0, 0}; }
+    __device__ __forceinline__ void set(int e, float x) { v[e / 4][e & 3] = x; }
+};
+
+// The row's piece at col, zeros beyond the width.
+template <typename T>
+__device__ __forceinline__ Piece<T> get8(const T* row, int64_t col, int64_t dim) {
+    Piece<T> o;
+    if (col + 8 <= dim) {
+        o.load(row + col);
+        return o;
+    }
+    o.clear();
+    if (col < dim) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = 0.0f;
+        for (int e = 0; e < 7; ++e)
+            if (col + e < dim) o.set(e, row[col + e]);
+    }
+    return o;
 }
 
-__device__ __forceinline__ void put8(float* row, int64_t col, int64_t dim, int vec, const float (&v)[8]) {
-    if (vec) {
-        if (col < dim) store8(row + col, v);
-        return;
-    }
+__device__ __forceinline__ void put8(float* row, int64_t col, int64_t dim, const float (&v)[8]) {
+    if (col + 8 <= dim) {
+        __builtin_memcpy(row + col, v, 32);
+    } else if (col < dim) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (col + e < dim) row[col + e] = v[e];
+        for (int e = 0; e < 7; ++e)
+            if (col + e < dim) row[col + e] = v[e];
+    }
 }
-__device__ __forceinline__ void put8(bf16_t* row, int64_t col, int64_t dim, int vec, const float (&v)[8]) {
+__device__ __forceinline__ void put8(bf16_t* row, int64_t col, int64_t dim, const float (&v)[8]) {
     bf16x8 h;
 #pragma unroll
     for (int e = 0; e < 8; ++e) h[e] = __bf16(v[e]);
-    __bf16* p = reinterpret_cast<__bf16*>(row);
-    if (vec) {
-        if (col < dim) *reinterpret_cast<bf16x8*>(p + col) = h;
-        return;
-    }
+    if (col + 8 <= dim) {
+        __builtin_memcpy(row + col, &h, 16);
+    } else if (col < dim) {
+        __bf16* p = reinterpret_cast<__bf16*>(row);
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (col + e < dim) p[col + e] = h[e];
+        for (int e = 0; e < 7; ++e)
+            if (col + e < dim) p[col + e] = h[e];
+    }
 }
 
 // Eight codes of v·inv: e4m3 (round to nearest even; |v·inv| <= 448, so none overflows) or
@@ -93,13 +113,13 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv, int q8) 
 // two slots alternate so that one barrier a call is enough.
 template <int P>
 struct RowSum {
-    float* slots;   // [2][16], LDS
+    float* slots;   // [2][32], LDS
     int at = 0;
     __device__ __forceinline__ float sum(float v) {
 #pragma unroll
         for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m, 64);
         if constexpr (P > 64) {
-            float* s = slots + 16 * at;
+            float* s = slots + 32 * at;
             at ^= 1;
             if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
             __syncthreads();
@@ -109,6 +129,28 @@ struct RowSum {
         }
         return v;
     }
+    __device__ __forceinline__ void sum2(float& a, float& b) {
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) {
+            a += __shfl_xor(a, m, 64);
+            b += __shfl_xor(b, m, 64);
+        }
+        if constexpr (P > 64) {
+            float* s = slots + 32 * at;
+            at ^= 1;
+            if ((threadIdx.x & 63) == 0) {
+                s[threadIdx.x >> 6] = a;
+                s[16 + (threadIdx.x >> 6)] = b;
+            }
+            __syncthreads();
+            a = b = 0.0f;
+#pragma unroll
+            for (int w = 0; w < P / 64; ++w) {
+                a += s[w];
+                b += s[16 + w];
+            }
+        }
+    }
     __device__ __forceinline__ uint32_t max(uint32_t v) {
 #pragma unroll
         for (int m = 1; m < 64; m <<= 1) {
@@ -116,7 +158,7 @@ struct RowSum {
             v = v > o ? v : o;
         }
         if constexpr (P > 64) {
-            uint32_t* s = reinterpret_cast<uint32_t*>(slots) + 16 * at;
+            uint32_t* s = reinterpret_cast<uint32_t*>(slots) + 32 * at;
             at ^= 1;
             if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
             __syncthreads();
@@ -131,42 +173,43 @@ struct RowSum {
 template <typename Tx, typename Tr, int P, int NV>
 __global__ __launch_bounds__(P > 256 ? P : 256) void rms_fwd_kernel(const RmsLaunch p) {
     constexpr int kRowsWG = P >= 256 ? 1 : 256 / P;
-    __shared__ float slots[32];
+    __shared__ float slots[64];
     RowSum<P> rs{slots};
     const int tid = threadIdx.x % P;
     const int64_t D = p.D, step = int64_t(gridDim.x) * kRowsWG;
     for (int64_t row = int64_t(blockIdx.x) * kRowsWG + threadIdx.x / P; row < p.M; row += step) {
         const Tx* x = static_cast<const Tx*>(p.x) + row * D;
+        const Tr* res = static_cast<const Tr*>(p.res) + (p.res ? row * D : 0);
+        Piece<Tx> px[NV];
+        Piece<Tr> pr[NV];
         float v[NV][8], sq = 0.0f;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) get8(x, (int64_t(j) * P + tid) * 8, D, p.vec, v[j]);
-        if (p.res) {
-            const Tr* res = static_cast<const Tr*>(p.res) + row * D;
-            Tr* r = static_cast<Tr*>(p.r) + row * D;
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int64_t col = (int64_t(j) * P + tid) * 8;
-                float a[8];
-                get8(res, col, D, p.vec, a);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[j][e] += a[e];
-                put8(r, col, D, p.vec, v[j]);
-            }
+        for (int j = 0; j < NV; ++j) {
+            const int64_t col = (int64_t(j) * P + tid) * 8;
+            px[j] = get8(x, col, D);
+            if (p.res) pr[j] = get8(res, col, D);
         }
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+        for (int j = 0; j < NV; ++j) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[j][e] = px[j].get(e);
+            if (p.res) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[j][e] += pr[j].get(e);
+                put8(static_cast<Tr*>(p.r) + row * D, (int64_t(j) * P + tid) * 8, D, v[j]);
+            }
 #pragma unroll
             for (int e = 0; e < 8; ++e) sq = fmaf(v[j][e], v[j][e], sq);
+        }
         sq = rs.sum(sq);
         const float c = rsqrtf(sq * p.inv_d + p.eps);
         uint32_t top = 0;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            float w[8];
-            get8(p.w, (int64_t(j) * P + tid) * 8, D, p.vec, w);
+            const Piece<float> w = get8(p.w, (int64_t(j) * P + tid) * 8, D);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                v[j][e] = v[j][e] * c * w[e];
+                v[j][e] = v[j][e] * c * w.get(e);
                 // bit patterns of magnitudes order like the magnitudes, NaN above all
                 const uint32_t m = __float_as_uint(v[j][e]) & 0x7fffffffu;
                 top = top > m ? top : m;
@@ -175,7 +218,7 @@ __global__ __launch_bounds__(P > 256 ? P : 256) void rms_fwd_kernel(const RmsLau
         if (p.q8 == SS_Q8_NONE) {
             Tx* y = static_cast<Tx*>(p.y) + row * D;
 #pragma unroll
-            for (int j = 0; j < NV; ++j) put8(y, (int64_t(j) * P + tid) * 8, D, p.vec, v[j]);
+            for (int j = 0; j < NV; ++j) put8(y, (int64_t(j) * P + tid) * 8, D, v[j]);
         } else {
             const float amax = __uint_as_float(rs.max(top));
             const float full = p.q8 == SS_Q8_FP8 ? 448.0f : 127.0f;
@@ -185,14 +228,13 @@ __global__ __launch_bounds__(P > 256 ? P : 256) void rms_fwd_kernel(const RmsLau
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int64_t col = (int64_t(j) * P + tid) * 8;
-                if (col >= D) continue;
                 // a row that is not finite keeps NaN codes where e4m3 has them
                 const uint2 q = codes8(v[j], amax != amax ? amax : inv, p.q8);
-                if (p.vec) {
-                    *reinterpret_cast<uint2*>(y + col) = q;
-                } else {
+                if (col + 8 <= D) {
+                    __builtin_memcpy(y + col, &q, 8);
+                } else if (col < D) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
+                    for (int e = 0; e < 7; ++e)
                         if (col + e < D) y[col + e] = uint8_t((e < 4 ? q.x : q.y) >> (8 * (e & 3)));
                 }
             }
@@ -205,7 +247,7 @@ __global__ __launch_bounds__(P > 256 ? P : 256) void rms_fwd_kernel(const RmsLau
 template <typename Tx, typename Tr, int P, int NV>
 __global__ __launch_bounds__(P > 256 ? P : 256) void rms_bwd_kernel(const RmsLaunch p) {
     constexpr int kRowsWG = P >= 256 ? 1 : 256 / P;
-    __shared__ float slots[32];
+    __shared__ float slots[64];
     __shared__ float fold[kRowsWG > 1 ? P * 8 : 1];
     RowSum<P> rs{slots};
     const int tid = threadIdx.x % P, sub = threadIdx.x / P;
@@ -218,41 +260,42 @@ __global__ __launch_bounds__(P > 256 ? P : 256) void rms_bwd_kernel(const RmsLau
     for (int64_t row = int64_t(blockIdx.x) * kRowsWG + sub; row < p.M; row += step) {
         const Tr* rr = static_cast<const Tr*>(p.res) + row * D;
         const Tx* dyr = static_cast<const Tx*>(p.x) + row * D;
-        float r[NV][8], dy[NV][8], sq = 0.0f, dot = 0.0f;
+        Piece<Tr> r[NV], g[NV];
+        Piece<Tx> dy[NV];
+        float sq = 0.0f, dot = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int64_t col = (int64_t(j) * P + tid) * 8;
-            get8(rr, col, D, p.vec, r[j]);
-            get8(dyr, col, D, p.vec, dy[j]);
+            r[j] = get8(rr, col, D);
+            dy[j] = get8(dyr, col, D);
+            if (p.dr) g[j] = get8(static_cast<const Tr*>(p.dr) + row * D, col, D);
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            float w[8];
-            get8(p.w, (int64_t(j) * P + tid) * 8, D, p.vec, w);
+            const Piece<float> w = get8(p.w, (int64_t(j) * P + tid) * 8, D);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                sq = fmaf(r[j][e], r[j][e], sq);
-                dot = fmaf(dy[j][e] * w[e], r[j][e], dot);
+                sq = fmaf(r[j].get(e), r[j].get(e), sq);
+                dot = fmaf(dy[j].get(e) * w.get(e), r[j].get(e), dot);
             }
         }
-        sq = rs.sum(sq);
-        dot = rs.sum(dot);
+        rs.sum2(sq, dot);
         const float c = rsqrtf(sq * p.inv_d + p.eps);
         const float k = c * c * c * (dot * p.inv_d);
         Tr* dx = static_cast<Tr*>(p.r) + row * D;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int64_t col = (int64_t(j) * P + tid) * 8;
-            float o[8], w[8];
-            get8(p.w, col, D, p.vec, w);
-            if (p.dr) get8(static_cast<const Tr*>(p.dr) + row * D, col, D, p.vec, o);
+            const Piece<float> w = get8(p.w, col, D);
+            float o[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float g = fmaf(c * w[e], dy[j][e], -k * r[j][e]);
-                dw[j][e] = fmaf(dy[j][e], r[j][e] * c, dw[j][e]);
-                o[e] = p.dr ? o[e] + g : g;
+                const float x = r[j].get(e), y = dy[j].get(e);
+                o[e] = fmaf(c * w.get(e), y, -k * x);
+                dw[j][e] = fmaf(y, x * c, dw[j][e]);
+                if (p.dr) o[e] += g[j].get(e);
             }
-            put8(dx, col, D, p.vec, o);
+            put8(dx, col, D, o);
         }
     }
     float* part = p.part + int64_t(blockIdx.x) * D;
@@ -272,10 +315,10 @@ __global__ __launch_bounds__(P > 256 ? P : 256) void rms_bwd_kernel(const RmsLau
             if (sub == 0) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) dw[j][e] = fold[e * P + tid];
-                put8(part, col, D, p.vec, dw[j]);
+                put8(part, col, D, dw[j]);
             }
         } else {
-            put8(part, col, D, p.vec, dw[j]);
+            put8(part, col, D, dw[j]);
         }
     }
 }
@@ -303,8 +346,8 @@ __global__ __launch_bounds__(1024) void rms_dw_kernel(const float* __restrict__ 
 template <typename Tx, typename Tr, int P, int NV>
 hipError_t launch_t(const RmsLaunch& p, bool backward, hipStream_t s) {
     const dim3 block(P > 256 ? P : 256), grid{unsigned(p.grid)};
-    if (backward) hipLaunchKernelGGL((rms_bwd_kernel<Tx, Tr, P, NV>), grid, block, 0, s, p);
-    else hipLaunchKernelGGL((rms_fwd_kernel<Tx, Tr, P, NV>), grid, block, 0, s, p);
+    if (!backward) hipLaunchKernelGGL((rms_fwd_kernel<Tx, Tr, P, NV>), grid, block, 0, s, p);
+    else if constexpr (NV < 6) hipLaunchKernelGGL((rms_bwd_kernel<Tx, Tr, P, NV>), grid, block, 0, s, p);
     return hipGetLastError();
 }
 
@@ -313,11 +356,10 @@ hipError_t launch_shape(const RmsLaunch& p, bool backward, hipStream_t s) {
     switch (p.threads * 10 + p.pieces) {
         case 641: return launch_t<Tx, Tr, 64, 1>(p, backward, s);
         case 642: return launch_t<Tx, Tr, 64, 2>(p, backward, s);
-        case 644: return launch_t<Tx, Tr, 64, 4>(p, backward, s);
         case 646: return launch_t<Tx, Tr, 64, 6>(p, backward, s);
         case 2561: return launch_t<Tx, Tr, 256, 1>(p, backward, s);
         case 2562: return launch_t<Tx, Tr, 256, 2>(p, backward, s);
-        case 2564: return launch_t<Tx, Tr, 256, 4>(p, backward, s);
+        case 5122: return launch_t<Tx, Tr, 512, 2>(p, backward, s);
         case 10242: return launch_t<Tx, Tr, 1024, 2>(p, backward, s);
         case 10244: return launch_t<Tx, Tr, 1024, 4>(p, backward, s);
         default: return hipErrorInvalidValue;

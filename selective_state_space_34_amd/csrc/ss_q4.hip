@@ -3,17 +3,21 @@
 // u the 4-bit codes of row n, two a byte, low half first; z 8 where no zeros are given; xs the
 // rows' scales where x is in 8 bits, else 1.
 //
-// What bounds it is reading the codes, so they go from memory to the matrix cores with the
-// fewest instructions.  A lane reads G/8 bytes of one row (16 rows a wave, the four 16-lane
-// groups side by side: one group of G codes a row), and turns eight codes of 32 bits into the
-// eight bf16 values of one v_mfma_f32_16x16x32_bf16 operand with four shifts and four
-// and-ors: a code in the upper mantissa bits of 16.0 is exactly 16 + u.  The products of one
-// group are summed on the matrix cores, Σ x of the group by one more product with ones, and
+// What bounds it is reading the codes (a decode step's matrices are a few MB: mostly the time
+// until the first of them arrive), so all loads of a wave are in flight at once and the codes go
+// from registers to the matrix cores with the fewest instructions.  A lane reads G/8 bytes of
+// one row (16 rows a wave, the four 16-lane groups side by side: one group of G codes a row),
+// and turns eight codes of 32 bits into the eight bf16 values of one v_mfma_f32_16x16x32_bf16
+// operand with four shifts and four and-ors: a code in the upper mantissa bits of 16.0 is
+// exactly 16 + u.  The products of one group are summed on the matrix cores, Σ x of the group by
+// one more product with ones, and
 //   acc += s·(Σ x(16 + u) - (16 + z)·Σ x)
 // in float32, so every scale is applied exactly.  The codes of a word come out in the order
-// 0 4 1 5 2 6 3 7; x is put into LDS in that order, as bf16.  Float32 rows are three bf16 rows
-// there (24 bits), which the products' unused rows hold for nothing; 8-bit rows are bf16
-// exactly.  A workgroup's four waves take the groups of 16 rows in turn and meet in LDS.
+// 0 4 1 5 2 6 3 7, and x, read by its lane straight from memory (each wave needs other k, so
+// LDS would be a detour: with it 27 us at 16 x 5120 in 8 bits by 2560, without 11), is put
+// into that order.  A float32 row takes three of the product's 16 rows, one for each bf16 term
+// (exact: eight significant bits each); 8-bit values are bf16 exactly.  The waves of a workgroup
+// take the groups of 16 rows in turn and meet in LDS.
 #include "ss_device.h"
 #include "ss_kernels.h"
 
@@ -23,6 +27,7 @@ namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 
 template <int W> struct Words;
 template <> struct Words<1> { using type = uint32_t; };
@@ -40,124 +45,188 @@ __device__ __forceinline__ bf16x8 widen(uint32_t d) {
     return o.f;
 }
 
-// eight elements of x as float32
-__device__ __forceinline__ void read8(const float* p, float (&o)[8]) { load8(p, o); }
-__device__ __forceinline__ void read8(const bf16_t* p, float (&o)[8]) { load8(p, o); }
 struct fp8_t { uint8_t b; };
 struct int8_q { int8_t b; };
-__device__ __forceinline__ void read8(const fp8_t* p, float (&o)[8]) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
+
+// eight values, exact in bf16, in the codes' order
+__device__ __forceinline__ bf16x8 ordered(const float (&v)[8]) {
+    bf16x8 o;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int w = int(i ? v.y : v.x);
-        o[4 * i] = __builtin_amdgcn_cvt_f32_fp8(w, 0);
-        o[4 * i + 1] = __builtin_amdgcn_cvt_f32_fp8(w, 1);
-        o[4 * i + 2] = __builtin_amdgcn_cvt_f32_fp8(w, 2);
-        o[4 * i + 3] = __builtin_amdgcn_cvt_f32_fp8(w, 3);
-    }
-}
-__device__ __forceinline__ void read8(const int8_q* p, float (&o)[8]) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = float(int8_t((e < 4 ? v.x : v.y) >> (8 * (e & 3))));
+    for (int e = 0; e < 8; ++e) o[(e & 3) * 2 + (e >> 2)] = __bf16(v[e]);
+    return o;
 }
 
-// W: 32-bit words of codes a lane reads of each group (G = 32·W codes).
-template <typename Tx, int W>
-__global__ __launch_bounds__(256) void q4_kernel(const Q4Launch p) {
+// Eight elements of x as they lie in memory, and as an operand; term: which bf16 term of
+// float32 values.
+template <typename T> struct Eight;
+template <> struct Eight<bf16_t> {
+    u32x4 w = {0, 0, 0, 0};
+    __device__ __forceinline__ void load(const bf16_t* p) { w = *reinterpret_cast<const u32x4*>(p); }
+    __device__ __forceinline__ bf16x8 get(int) const {
+        union { uint32_t w[4]; bf16x8 f; } o;
+        o.w[0] = __builtin_amdgcn_perm(w[2], w[0], 0x05040100u);
+        o.w[1] = __builtin_amdgcn_perm(w[2], w[0], 0x07060302u);
+        o.w[2] = __builtin_amdgcn_perm(w[3], w[1], 0x05040100u);
+        o.w[3] = __builtin_amdgcn_perm(w[3], w[1], 0x07060302u);
+        return o.f;
+    }
+};
+template <> struct Eight<fp8_t> {
+    uint2 w = {0, 0};
+    __device__ __forceinline__ void load(const fp8_t* p) { w = *reinterpret_cast<const uint2*>(p); }
+    __device__ __forceinline__ bf16x8 get(int) const {
+        float v[8];
+        v[0] = __builtin_amdgcn_cvt_f32_fp8(int(w.x), 0);
+        v[1] = __builtin_amdgcn_cvt_f32_fp8(int(w.x), 1);
+        v[2] = __builtin_amdgcn_cvt_f32_fp8(int(w.x), 2);
+        v[3] = __builtin_amdgcn_cvt_f32_fp8(int(w.x), 3);
+        v[4] = __builtin_amdgcn_cvt_f32_fp8(int(w.y), 0);
+        v[5] = __builtin_amdgcn_cvt_f32_fp8(int(w.y), 1);
+        v[6] = __builtin_amdgcn_cvt_f32_fp8(int(w.y), 2);
+        v[7] = __builtin_amdgcn_cvt_f32_fp8(int(w.y), 3);
+        return ordered(v);
+    }
+};
+template <> struct Eight<int8_q> {
+    uint2 w = {0, 0};
+    __device__ __forceinline__ void load(const int8_q* p) { w = *reinterpret_cast<const uint2*>(p); }
+    __device__ __forceinline__ bf16x8 get(int) const {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = float(int8_t((e < 4 ? w.x : w.y) >> (8 * (e & 3))));
+        return ordered(v);
+    }
+};
+template <> struct Eight<float> {
+    f32x4 v[2] = {};
+    __device__ __forceinline__ void load(const float* p) {
+        v[0] = *reinterpret_cast<const f32x4*>(p);
+        v[1] = *reinterpret_cast<const f32x4*>(p + 4);
+    }
+    // the upper eight significant bits, the next eight of what is left, or the rest
+    __device__ __forceinline__ uint32_t part(float a, int term) const {
+        const uint32_t first = term >= 1 ? 0xffff0000u : 0u, second = term == 2 ? 0xffff0000u : 0u;
+        a -= __uint_as_float(__float_as_uint(a) & first);
+        a -= __uint_as_float(__float_as_uint(a) & second);
+        return __float_as_uint(a);
+    }
+    __device__ __forceinline__ bf16x8 get(int term) const {
+        union { uint32_t w[4]; bf16x8 f; } o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            o.w[i] = __builtin_amdgcn_perm(part(v[1][i], term), part(v[0][i], term), 0x07060302u);
+        return o.f;
+    }
+};
+
+// W: 32-bit words of codes a lane reads of each group (G = 32·W codes); NW: waves; NT: tiles of
+// 16 rows of weights of a workgroup, which share what is done to x.
+template <typename Tx, int W, int NW, int NT>
+__global__ __launch_bounds__(64 * NW) void q4_kernel(const Q4Launch p) {
     constexpr int G = 32 * W;
-    constexpr int kTerms = sizeof(Tx) == 4 ? 3 : 1;  // bf16 rows of one row of x
-    constexpr int kAhead = 4;                        // groups whose loads are in flight
-    extern __shared__ __attribute__((aligned(16))) char lds[];
-    __bf16* const xl = reinterpret_cast<__bf16*>(lds);
-    __shared__ float red[4][16][17];
+    constexpr int kTerms = sizeof(Tx) == 4 ? 3 : 1;       // product rows of one row of x
+    // groups whose loads are in flight, by the registers that one takes
+    constexpr int kRegs = W * (NT + int(sizeof(Eight<Tx>)) / 4) + 2 * NT;
+    constexpr int kAhead = 72 / kRegs < 2 ? 2 : 72 / kRegs > 6 ? 6 : 72 / kRegs;
+    __shared__ float red[NW][16][16 * NT + 1];
     using Word = typename Words<W>::type;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int l16 = lane & 15, lg = lane >> 4;
     const int64_t m0 = int64_t(blockIdx.y) * p.mb;
-    const int rows = int(p.M - m0 < p.mb ? p.M - m0 : p.mb), xrows = rows * kTerms;
-    const int64_t n = int64_t(blockIdx.x) * 16 + l16;
-    const int64_t nr = n < p.N ? n : p.N - 1;        // rows behind the end repeat the last one
-    const uint8_t* wq = p.wq + nr * (p.K / 2) + lg * 4 * W;
-    const uint16_t* sc = p.scales + nr * p.groups;
-    const uint8_t* zr = p.zeros ? p.zeros + nr * p.groups : nullptr;
-    const int ld = int(p.slab) + 8;                  // rows of x in LDS start 4 banks apart
-    const int xrow = (l16 < xrows ? l16 : xrows - 1) * ld + lg * 8 * W;
+    const int rows = int(p.M - m0 < p.mb ? p.M - m0 : p.mb);
+    const int xm = l16 / kTerms, term = l16 - xm * kTerms;
+    const bool has_x = xm < rows;                         // else a row of zeros
+    const int64_t kl = lg * 8 * W;                        // the lane's first code of a group
+    const uint8_t* wq[NT];
+    const uint16_t* sc[NT];
+    const uint8_t* zr[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int64_t n = int64_t(blockIdx.x) * 16 * NT + 16 * t + l16;
+        const int64_t nr = n < p.N ? n : p.N - 1;         // rows behind the end repeat the last one
+        wq[t] = p.wq + nr * (p.K / 2) + kl / 2;
+        sc[t] = p.scales + nr * p.groups;
+        zr[t] = p.zeros ? p.zeros + nr * p.groups : nullptr;
+    }
+    const Tx* xp = static_cast<const Tx*>(p.x) + (m0 + (has_x ? xm : 0)) * p.K + kl;
+    bf16x8 ones;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ones[e] = __bf16(1.0f);
 
-    f32x4 acc = {0, 0, 0, 0};
-    for (int64_t k0 = 0; k0 < p.K; k0 += p.slab) {
-        const int64_t kn = p.K - k0 < p.slab ? p.K - k0 : p.slab;
-        const int64_t kpad = (kn + G - 1) / G * G;
-        if (k0) __syncthreads();
-        for (int64_t i = tid; i < rows * (kpad / 8); i += 256) {
-            const int r = int(i / (kpad / 8));
-            const int64_t k = (i - r * (kpad / 8)) * 8;
-            float v[8];
+    f32x4 acc[NT];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-            if (k < kn) read8(static_cast<const Tx*>(p.x) + (m0 + r) * p.K + k0 + k, v);
+    for (int t = 0; t < NT; ++t) acc[t] = f32x4{0, 0, 0, 0};
+    Word d[kAhead][NT];
+    Eight<Tx> x[kAhead][W];
+    uint32_t s[kAhead][NT], z[kAhead][NT];
+    auto load = [&](int a, int64_t g) {
+        const int64_t k = g * G;
+        // a short last group ends between lanes: 8·W codes divide 32, which divides K
+        const bool on = k + kl < p.K;
 #pragma unroll
-            for (int t = 0; t < kTerms; ++t) {
-                bf16x8 o;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const __bf16 h = __bf16(v[e]);
-                    o[(e & 3) * 2 + (e >> 2)] = h;
-                    // an infinite value is its first term alone
-                    const float left = v[e] - float(h);
-                    v[e] = left == left ? left : 0.0f;
-                }
-                *reinterpret_cast<bf16x8*>(&xl[(r * kTerms + t) * ld + k]) = o;
-            }
+        for (int t = 0; t < NT; ++t) {
+            d[a][t] = Word{};
+            if (on) d[a][t] = *reinterpret_cast<const Word*>(wq[t] + k / 2);
+            s[a][t] = sc[t][g];
+            z[a][t] = p.zeros ? zr[t][g] : 8;
         }
-        __syncthreads();
-        const int64_t g0 = k0 / G, gn = kpad / G;
-        for (int64_t gb = wave; gb < gn; gb += 4 * kAhead) {
-            Word d[kAhead];
-            uint32_t s[kAhead], z[kAhead];
 #pragma unroll
-            for (int a = 0; a < kAhead; ++a) {
-                const int64_t g = gb + 4 * a;
-                if (g >= gn) break;
-                d[a] = Word{};
-                // a short last group ends between lanes: 8·W codes divide 32, which divides K
-                if (g * G + lg * 8 * W < kn) d[a] = *reinterpret_cast<const Word*>(wq + (k0 + g * G) / 2);
-                s[a] = sc[g0 + g];
-                z[a] = zr ? zr[g0 + g] : 8;
-            }
+        for (int i = 0; i < W; ++i) {
+            x[a][i] = Eight<Tx>{};
+            if (on && has_x) x[a][i].load(xp + k + 8 * i);
+        }
+    };
 #pragma unroll
-            for (int a = 0; a < kAhead; ++a) {
-                const int64_t g = gb + 4 * a;
-                if (g >= gn) break;
-                const uint32_t* q = reinterpret_cast<const uint32_t*>(&d[a]);
-                f32x4 t = {0, 0, 0, 0}, u = {0, 0, 0, 0};
-                bf16x8 ones;
+    for (int a = 0; a < kAhead; ++a)
+        if (wave + NW * a < p.groups) load(a, wave + NW * a);
+    for (int64_t gb = wave; gb < p.groups; gb += NW * kAhead) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) ones[e] = __bf16(1.0f);
+        for (int a = 0; a < kAhead; ++a) {
+            const int64_t g = gb + NW * a;
+            if (g >= p.groups) break;
+            f32x4 v[NT], u = {0, 0, 0, 0};
 #pragma unroll
-                for (int i = 0; i < W; ++i) {
-                    const bf16x8 xf = *reinterpret_cast<const bf16x8*>(&xl[xrow + g * G + 8 * i]);
-                    t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, widen(q[i]), t, 0, 0, 0);
-                    u = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, ones, u, 0, 0, 0);
+            for (int t = 0; t < NT; ++t) v[t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                const bf16x8 xf = x[a][i].get(term);
+                u = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, ones, u, 0, 0, 0);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const uint32_t* q = reinterpret_cast<const uint32_t*>(&d[a][t]);
+                    v[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, widen(q[i]), v[t], 0, 0, 0);
                 }
-                const float sf = __uint_as_float(s[a] << 16), zf = 16.0f + float(z[a]);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) acc[r] = fmaf(sf, fmaf(-zf, u[r], t[r]), acc[r]);
             }
+            float sf[NT], zf[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                sf[t] = __uint_as_float(s[a][t] << 16);
+                zf[t] = 16.0f + float(z[a][t]);
+            }
+            if (g + NW * kAhead < p.groups) load(a, g + NW * kAhead);
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    acc[t][r] = fmaf(sf[t], fmaf(-zf[t], u[r], v[t][r]), acc[t][r]);
         }
     }
-    // lane: column n = l16, rows 4·lg + r of x in LDS
+    // lane: column l16 of each tile, product rows 4·lg + r
 #pragma unroll
-    for (int r = 0; r < 4; ++r) red[wave][4 * lg + r][l16] = acc[r];
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) red[wave][4 * lg + r][16 * t + l16] = acc[t][r];
     __syncthreads();
-    const int m = tid >> 4, c = tid & 15;
-    const int64_t col = int64_t(blockIdx.x) * 16 + c;
-    if (m < rows && col < p.N) {
+    for (int i = tid; i < rows * 16 * NT; i += 64 * NW) {
+        const int m = i / (16 * NT), c = i % (16 * NT);
+        const int64_t col = int64_t(blockIdx.x) * 16 * NT + c;
+        if (col >= p.N) continue;
         float v = 0.0f;
 #pragma unroll
         for (int t = 0; t < kTerms; ++t)
 #pragma unroll
-            for (int w = 0; w < 4; ++w) v += red[w][m * kTerms + (kTerms - 1 - t)][c];
+            for (int w = 0; w < NW; ++w) v += red[w][m * kTerms + (kTerms - 1 - t)][c];
         if (p.x_scale) v *= p.x_scale[m0 + m];
         const int64_t at = (m0 + m) * p.N + col;
         if (p.y_dtype == SS_BF16) static_cast<__bf16*>(p.y)[at] = __bf16(v);
@@ -165,17 +234,26 @@ __global__ __launch_bounds__(256) void q4_kernel(const Q4Launch p) {
     }
 }
 
+template <typename Tx, int W, int NW, int NT>
+hipError_t launch_tiles(const Q4Launch& p, hipStream_t s) {
+    const dim3 grid{unsigned((p.N + 16 * NT - 1) / (16 * NT)), unsigned((p.M + p.mb - 1) / p.mb)};
+    hipLaunchKernelGGL((q4_kernel<Tx, W, NW, NT>), grid, dim3(64 * NW), 0, s, p);
+    return hipGetLastError();
+}
+
+template <typename Tx, int W>
+hipError_t launch_words(const Q4Launch& p, hipStream_t s) {
+    return p.tiles == 2 ? launch_tiles<Tx, W, 8, 2>(p, s) : launch_tiles<Tx, W, 8, 1>(p, s);
+}
+
 template <typename Tx>
 hipError_t launch_x(const Q4Launch& p, hipStream_t s) {
-    const dim3 grid{unsigned((p.N + 15) / 16), unsigned((p.M + p.mb - 1) / p.mb)};
-    const unsigned lds = unsigned(p.mb * (sizeof(Tx) == 4 ? 3 : 1) * (p.slab + 8) * 2);
     switch (p.group) {
-        case 32: hipLaunchKernelGGL((q4_kernel<Tx, 1>), grid, dim3(256), lds, s, p); break;
-        case 64: hipLaunchKernelGGL((q4_kernel<Tx, 2>), grid, dim3(256), lds, s, p); break;
-        case 128: hipLaunchKernelGGL((q4_kernel<Tx, 4>), grid, dim3(256), lds, s, p); break;
+        case 32: return launch_words<Tx, 1>(p, s);
+        case 64: return launch_words<Tx, 2>(p, s);
+        case 128: return launch_words<Tx, 4>(p, s);
         default: return hipErrorInvalidValue;
     }
-    return hipGetLastError();
 }
 
 }  // namespace
