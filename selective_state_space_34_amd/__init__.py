@@ -180,9 +180,14 @@ def _ptr(t):
 
 
 def _check(t, name, shape, dtype, device):
-    import torch
     if t is None:
         return
+    try:  # what is right passes with the fewest steps: a call's checks are most of its host time
+        if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != device:
@@ -528,9 +533,11 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _raw_stream():
+def _raw_stream(device):
+    """Handle of the device's current stream (without the Stream object where torch gives it)."""
     import torch
-    return torch.cuda.current_stream().cuda_stream
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return torch.cuda.current_stream(device).cuda_stream if get is None else get(device.index)
 
 
 def _in_dtype(x, name):
@@ -636,7 +643,7 @@ def ss_la_fwd(q, k, v, g=None, s0=None, *, scale=1.0, lengths=None, return_final
         wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         rc = lib.ss_la_fwd(dims, _addr(q), _addr(k), _addr(v), _addr(g), _addr(s0),
                            _addr(lengths), _addr(o), _addr(s_final), _addr(workspace), wbytes,
-                           _raw_stream())
+                           _raw_stream(dev))
     if rc != 0:
         raise SSError(rc, lib)
     return o if s_final is None else (o, s_final)
@@ -672,7 +679,7 @@ def ss_la_bwd(q, k, v, do, g=None, s0=None, ds_final=None, *, scale=1.0, lengths
         rc = lib.ss_la_bwd(dims, _addr(q), _addr(k), _addr(v), _addr(g), _addr(s0),
                            _addr(lengths), _addr(do), _addr(ds_final), _addr(r["dq"]),
                            _addr(r["dk"]), _addr(r["dv"]), _addr(r["dg"]), _addr(r["ds0"]),
-                           _addr(workspace), wbytes, _raw_stream())
+                           _addr(workspace), wbytes, _raw_stream(dev))
     if rc != 0:
         raise SSError(rc, lib)
     return r
@@ -697,7 +704,7 @@ def ss_la_step(q, k, v, s, g=None, *, scale=1.0, s_out=None, o=None, stream=None
         else:
             _check(o, "o", (B, H, dv), v.dtype, dev)
         rc = lib.ss_la_step(dims, _addr(q), _addr(k), _addr(v), _addr(g), _addr(s), _addr(s_out),
-                            _addr(o), _raw_stream())
+                            _addr(o), _raw_stream(dev))
     if rc != 0:
         raise SSError(rc, lib)
     return o
@@ -765,7 +772,7 @@ def ss_rms_fwd(x, w, res=None, *, eps=1e-5, q8=SS_Q8_NONE, y=None, y_scale=None,
             else:
                 _check(r, "r", shape, rdt, dev)
         rc = lib.ss_rms_fwd(dims, _addr(x), _addr(res), _addr(w), _addr(r), _addr(y),
-                            _addr(y_scale), _raw_stream())
+                            _addr(y_scale), _raw_stream(dev))
     if rc != 0:
         raise SSError(rc, lib)
     out = (y,) if q8 == SS_Q8_NONE else (y, y_scale)
@@ -801,7 +808,7 @@ def ss_rms_bwd(dy, r, w, dr=None, *, eps=1e-5, dx=None, dw=None, workspace=None,
             workspace = _bytes(need, dev)
         wbytes = workspace.numel() * workspace.element_size()
         rc = lib.ss_rms_bwd(dims, _addr(dy), _addr(r), _addr(w), _addr(dr), _addr(dx), _addr(dw),
-                            _addr(workspace), wbytes, _raw_stream())
+                            _addr(workspace), wbytes, _raw_stream(dev))
     if rc != 0:
         raise SSError(rc, lib)
     return dx, dw
@@ -854,7 +861,7 @@ def ss_q4_mv(x, wq, scales, zeros=None, *, group=128, x_scale=None, y=None, y_dt
         else:
             _check(y, "y", (*lead, N), y_dtype, dev)
         rc = lib.ss_q4_mv(dims, _addr(x), _addr(x_scale), _addr(wq), _addr(scales), _addr(zeros),
-                          _addr(y), _raw_stream())
+                          _addr(y), _raw_stream(dev))
     if rc != 0:
         raise SSError(rc, lib)
     return y
