@@ -180,7 +180,6 @@ struct LaSweep {
     int64_t s_in_sz, s_in_i, s_in_j;   // (bh·in_seg + s)·s_in_sz + i·s_in_i + j·s_in_j
     int64_t in_seg;
     float* s_out;              // nullable [B, H, dA, dC]; state_only: [B, H, nseg, dA, dC]
-    int64_t s_out_sz;
     double* dots;              // nullable [tiles, B, H, T]
     float* seg_decay;          // state_only: [B, H, nseg]
     int64_t B, T, H;

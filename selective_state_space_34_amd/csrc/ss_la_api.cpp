@@ -91,7 +91,7 @@ hipError_t segment_states(const LaPlan& p, LaSweep s, const ss::LaShape& f, cons
     s.a = s.b; s.e = s.b;
     s.grid_seg = s.nseg - 1; s.seg0 = s.reverse ? 1 : 0;
     s.s_in = nullptr; s.in_seg = 1; s.s_in_sz = sz;
-    s.s_out = state; s.s_out_sz = sz; s.seg_decay = decay;
+    s.s_out = state; s.seg_decay = decay;
     s.dots = nullptr; s.out = nullptr;
     const hipError_t e = sweep(p, s, stream);
     if (e != hipSuccess) return e;
@@ -109,7 +109,6 @@ hipError_t full_sweep(const LaPlan& p, LaSweep s, const ss::LaShape& f, const fl
     shape(&s, f);
     s.grid_seg = s.nseg; s.seg0 = 0;
     s.s_in_sz = p.dk * p.dv;
-    s.s_out_sz = p.dk * p.dv;
     if (s.nseg > 1) {
         s.s_in = state; s.in_seg = s.nseg; s.s_in_i = s_i; s.s_in_j = s_j;
     } else {

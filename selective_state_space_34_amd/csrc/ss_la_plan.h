@@ -25,12 +25,17 @@ inline LaShape la_shape(int64_t dA, int64_t dC) {
 constexpr int64_t kLaMaxDim = 256;
 inline int64_t la_chunk(int in_dtype) { return in_dtype == SS_BF16 ? 64 : 32; }
 
-// Segments of a sequence that are swept side by side: as many as keep all workgroups resident
-// at once, two on each of the 256 CUs (a few more than that would take a second round as long
-// as the first: a sweep over 13 segments of 40 heads measured 369 us, over 12 it measured 281), none shorter than
-// two chunks.
-inline int64_t la_segments(int64_t rows, int64_t nchunk) {
-    int64_t n = 512 / rows;
+// Workgroups of a sweep that the 256 CUs hold at once, by the waves a SIMD that its registers
+// allow; dots: the sweeps that also give the sums behind dg.
+inline int64_t la_round(const LaShape& s, bool dots) {
+    const int waves = s.pad_a == 64 && !dots ? 4 : s.pad_a == 256 && s.waves == 4 ? 1 : 2;
+    return 256 * (4 * waves / s.waves);
+}
+
+// Segments of a sequence that are swept side by side: as many as are resident at once (a few
+// more would take a second round as long as the first: a sweep over 13 segments of 40 heads
+// measured 369 us, over 12 it measured 281), none shorter than two chunks.
+inline int64_t la_segments(int64_t n, int64_t nchunk) {
     if (n > nchunk / 2) n = nchunk / 2;
     if (n < 1) n = 1;
     const int64_t len = (nchunk + n - 1) / n;
@@ -84,9 +89,13 @@ inline int make_la_plan(const ss_la_dims& d, bool backward, LaPlan* out) {
     p.fwd = la_shape(p.dk, p.dv);
     p.rev = la_shape(p.dv, p.dk);
     const int64_t bh = p.B * p.H;
-    const int tiles = backward && p.rev.tiles < p.fwd.tiles ? p.rev.tiles : p.fwd.tiles;
     const int most = p.rev.tiles > p.fwd.tiles ? p.rev.tiles : p.fwd.tiles;
-    p.nseg = la_segments(bh * tiles, p.nchunk);
+    int64_t n = la_round(p.fwd, false) / (bh * p.fwd.tiles);
+    if (backward) {
+        const int64_t r = la_round(p.rev, p.decay != SS_LA_DECAY_NONE) / (bh * p.rev.tiles);
+        n = r < n ? r : n;
+    }
+    p.nseg = la_segments(n, p.nchunk);
     p.seg_chunks = (p.nchunk + p.nseg - 1) / p.nseg;
     // one workgroup for each (column tile, row, head, segment), and the row-wise kernels
     const int64_t grid = int64_t(1) << 31;

@@ -264,6 +264,15 @@ struct Decay {
     float all;       // decay of the state over the chunk
 };
 
+// Lets products finish before a branch.  Where a block behind a product may be jumped over, the
+// compiler (ROCm 7.2's) has counted the wait states before the use of the product's result along
+// the longer path alone, and the use read registers not yet written.
+__device__ __forceinline__ void settle() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_nop 11");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
 // 2^x for x given as whole + frac
 __device__ __forceinline__ float exp2_parts(float frac, int whole) {
     return __builtin_amdgcn_ldexpf(exp2_hw(frac), whole);
@@ -332,12 +341,14 @@ __device__ __forceinline__ uint32_t not_finite(f32x8 f, uint32_t seen) {
     return seen;
 }
 
-// Waves a SIMD that the registers are to allow: four (two workgroups of eight waves on a CU)
-// where the state, the rows in flight and the products fit 128 registers without spilling.
+// Waves a SIMD that the registers are to allow (la_round in ss_la_plan.h counts on them).  Four
+// where the state, the rows in flight and the products fit 128 registers; at 128 state rows they
+// would spill 18 of them, and two workgroups a CU were no faster than one after the other
+// (B = 4, T = 2048, H = 16, 128 x 128: 47 us with four waves, 44 with two on half the segments).
 constexpr int sweep_occupancy(bool vec, int DA, int NW, bool dot, bool state) {
     if (DA == 256 && NW == 4 && !state) return 1;
-    if (DA == 256 || dot || !vec) return 2;
-    return DA == 128 && NW == 4 && !state ? 2 : 4;
+    if (state) return DA == 256 ? 2 : 4;
+    return DA > 64 || dot || !vec ? 2 : 4;
 }
 
 // kState: only the state that a segment adds from zero, and the segment's decay (the first of
@@ -432,18 +443,25 @@ __global__ __launch_bounds__(64 * NW, sweep_occupancy(kVec, DA, NW, kDot, kState
     for (int ib = 0; ib < IB; ++ib)
 #pragma unroll
         for (int u = 0; u < 2; ++u) S[ib][u] = f32x4{0, 0, 0, 0};
+    // element (i, j) of a lane's register r; descriptors again stand for the bounds, so that all
+    // of a lane's accesses are in flight at once
+    const int state_bytes = int(p.s_in_sz) * 4;
+    auto state_at = [&](int ib, int u, int r, int sti, int stj) {
+        const int i = 32 * ib + 8 * lg + 4 * u + r, j = c0 + jw + l16;
+        return i < p.b.dim && j < p.c.dim ? (i * sti + j * stj) * 4 : int(kNowhere);
+    };
     if (!kState && p.s_in) {
         const float* si = p.s_in + (bh * p.in_seg + (p.in_seg > 1 ? seg : 0)) * p.s_in_sz;
-        const int sti = int(p.s_in_i), stj = int(p.s_in_j);
+        const __amdgpu_buffer_rsrc_t d =
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(si), 0, state_bytes, kRsrcFlags);
 #pragma unroll
         for (int ib = 0; ib < IB; ++ib)
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int i = 32 * ib + 8 * lg + 4 * u + r, j = c0 + jw + l16;
-                    if (i < p.b.dim && j < p.c.dim) S[ib][u][r] = si[i * sti + j * stj];
-                }
+                for (int r = 0; r < 4; ++r)
+                    S[ib][u][r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+                        d, state_at(ib, u, r, int(p.s_in_i), int(p.s_in_j)), 0, 0));
     }
 
     u32x4 va[kState ? 1 : NA], vb[NA], vc[NC], ve[kDot ? NC : 1];
@@ -634,15 +652,14 @@ __global__ __launch_bounds__(64 * NW, sweep_occupancy(kVec, DA, NW, kDot, kState
                 }
             }
             // ---- the chunk's own part ---------------------------------------------------------------
-            // All of P, the tiles that the mask empties too (zeros): a branch around a product is
-            // avoided, since the compiler (ROCm 7.2's) has left too few wait states before the
-            // use of a product's result on a path that jumps over a block behind the product.
+            // All of P, the tiles that the mask empties too (zeros).
             if (!bad) {
 #pragma unroll
                 for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks)
                         O[tb] = M::mma(cf[ks], p_row(16 * tb + l16, 32 * ks + 8 * lg), O[tb]);
+                settle();
             } else {
                 // A masked weight is 0, and its product with an infinity would be NaN: the
                 // allowed pairs alone, one by one.
@@ -735,16 +752,16 @@ __global__ __launch_bounds__(64 * NW, sweep_occupancy(kVec, DA, NW, kDot, kState
     // ---- the state this segment leaves ---------------------------------------------------------------
     const bool last = kState || (rev ? seg == 0 : seg == p.nseg - 1);
     if (p.s_out && last) {
-        float* so = p.s_out + (bh * (kState ? p.nseg : 1) + (kState ? seg : 0)) * p.s_out_sz;
+        float* so = p.s_out + (bh * (kState ? p.nseg : 1) + (kState ? seg : 0)) * p.s_in_sz;
+        const __amdgpu_buffer_rsrc_t d = __builtin_amdgcn_make_buffer_rsrc(so, 0, state_bytes, kRsrcFlags);
 #pragma unroll
         for (int ib = 0; ib < IB; ++ib)
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int i = 32 * ib + 8 * lg + 4 * u + r, j = c0 + jw + l16;
-                    if (i < p.b.dim && j < p.c.dim) so[i * p.c.dim + j] = S[ib][u][r];
-                }
+                for (int r = 0; r < 4; ++r)
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[ib][u][r]), d,
+                                                          state_at(ib, u, r, p.c.dim, 1), 0, 0);
     }
     if (kState && tile == 0 && tid == NT - 64)
         p.seg_decay[bh * p.nseg + seg] = seg_nan ? __builtin_nanf("") : exp2_fixed(seg_sum);
