@@ -206,15 +206,21 @@ struct LaCarry {
 };
 hipError_t launch_la_carry(const LaCarry& p, hipStream_t s);
 
-// dg from the row and column sums: token [B, T, H] (dg), or one value a head [H] through
-// head_part [B, H].  ds, s_final: both or neither; ds [B, H, dk, dv], s_final [B, H, dv, dk].
+// dg from the row and column sums and the states at the segments' borders: token [B, T, H]
+// (dg), or one value a head [H] through head_part [B, H, nseg].
 struct LaDecayGrad {
     const double *row, *col;   // [tiles, B, H, T]
     int tiles;
-    const float *ds, *s_final;
+    const float *fwd_state, *rev_state;   // [B, H, nseg, dv·dk] and [.., dk·dv]: the states that
+                                          // enter each segment from the left, from the right
+    const float *s0, *ds0, *ds, *s_final; // nullable; s_final [B, H, dv, dk], the others [.., dk, dv]
+    double* border;            // [B, H, nseg + 1]
     const int32_t* lengths;
-    float *dg, *head_part;
+    float* dg;
+    double* head_part;
     int64_t B, T, H, dk, dv;
+    int nseg;
+    int64_t seg_tokens;
     int decay_token;
 };
 hipError_t launch_la_decay_grad(const LaDecayGrad& p, hipStream_t s);

@@ -39,50 +39,93 @@ __global__ __launch_bounds__(256) void la_carry_kernel(const LaCarry p) {
     st[seg * p.sz] = s;
 }
 
-// dg_t = Σ_{u>=t} (row_u - col_u) + <dS_T, S_T>.  One workgroup for each (row, head), 1024
-// tokens at a time from the end; the running sum is kept in 64 bits, so its own rounding does
-// not grow with the length.
+// Sum over the 256 threads of a workgroup; part: four doubles in LDS.
+__device__ __forceinline__ double block_sum(double v, double* part) {
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m, 64);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return part[0] + part[1] + part[2] + part[3];
+}
+
+// E at the segments' borders: <adjoint of the state, state> there, which is dg of the first
+// token behind the border.  Border 0: dS_0 and S_0; border nseg: dS_T and S_T (0 where either is
+// not given); between them the states that enter the segments from either side.
+__global__ __launch_bounds__(256) void la_border_kernel(const LaDecayGrad p) {
+    __shared__ double part[4];
+    __shared__ float tile[64][65];
+    const int64_t bh = blockIdx.x / (p.nseg + 1);
+    const int k = int(blockIdx.x - bh * (p.nseg + 1));
+    const int64_t sz = p.dk * p.dv;
+    const int tid = threadIdx.x, dk = int(p.dk), dv = int(p.dv);
+    double v = 0.0;
+    if (k == 0) {
+        if (p.ds0 && p.s0)
+            for (int64_t x = tid; x < sz; x += 256)
+                v += double(p.ds0[bh * sz + x]) * double(p.s0[bh * sz + x]);
+    } else if (k < p.nseg || (p.ds && p.s_final)) {
+        const float* r = k < p.nseg ? p.rev_state + (bh * p.nseg + k - 1) * sz : p.ds + bh * sz;
+        const float* s = k < p.nseg ? p.fwd_state + (bh * p.nseg + k) * sz : p.s_final + bh * sz;
+        // r is [dk, dv], s [dv, dk]: s by way of a tile in LDS, so that both are read by rows
+        for (int i0 = 0; i0 < dk; i0 += 64)
+            for (int j0 = 0; j0 < dv; j0 += 64) {
+                __syncthreads();
+#pragma unroll 4
+                for (int x = tid; x < 64 * 64; x += 256) {
+                    const int j = x / 64, i = x % 64;
+                    tile[j][i] = j0 + j < dv && i0 + i < dk ? s[(j0 + j) * dk + i0 + i] : 0.0f;
+                }
+                __syncthreads();
+#pragma unroll 4
+                for (int x = tid; x < 64 * 64; x += 256) {
+                    const int i = x / 64, j = x % 64;
+                    if (i0 + i < dk && j0 + j < dv)
+                        v += double(r[(i0 + i) * dv + j0 + j]) * double(tile[j][i]);
+                }
+            }
+    }
+    v = block_sum(v, part);
+    if (tid == 0) p.border[blockIdx.x] = v;
+}
+
+// dg_t = Σ_{u>=t} (row_u - col_u) + E at the segment's end, u inside the segment.  A sum over the
+// whole sequence would hold the rounding of every row and column sum behind t, which grows with
+// the length and, summed again for one decay a head, is all that is left where dg is small; so
+// each segment starts from the exact value at its end, and what it misses at its beginning,
+// where the exact value is known too, is taken off in proportion to the way.  One workgroup a
+// segment, 1024 tokens at a time from its end, in 64 bits.
 __global__ __launch_bounds__(256) void la_decay_grad_kernel(const LaDecayGrad p) {
     __shared__ double part[4];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int64_t bh = blockIdx.x, b = bh / p.H, h = bh - b * p.H;
-    auto block_sum = [&](double v) {
-#pragma unroll
-        for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m, 64);
-        __syncthreads();
-        if (lane == 0) part[wave] = v;
-        __syncthreads();
-        return part[0] + part[1] + part[2] + part[3];
-    };
+    const int64_t bh = blockIdx.x / p.nseg, b = bh / p.H, h = bh - b * p.H;
+    const int seg = int(blockIdx.x - bh * p.nseg);
     int64_t len = p.T;
     if (p.lengths) {
         len = p.lengths[b];
         len = len < 0 ? 0 : len > p.T ? p.T : len;
     }
-    double run = 0.0, total = 0.0;
-    if (p.ds) {
-        double v = 0.0;
-        const int64_t sz = p.dk * p.dv;
-        for (int64_t x = tid; x < sz; x += 256) {
-            const int64_t i = x / p.dv, j = x - i * p.dv;
-            v += double(p.ds[bh * sz + x]) * double(p.s_final[bh * sz + j * p.dk + i]);
-        }
-        run = block_sum(v);
-    }
-    const int64_t tiles = (p.T + 1023) / 1024, plane = p.B * p.H * p.T;
-    for (int64_t w = tiles - 1; w >= 0; --w) {
-        const int64_t t0 = w * 1024 + tid * 4;
+    const int64_t lo = seg * p.seg_tokens;
+    const int64_t hi = lo + p.seg_tokens < p.T ? lo + p.seg_tokens : p.T;
+    const int64_t plane = p.B * p.H * p.T;
+    auto diff = [&](int64_t t) {
+        double x = 0.0;
+        if (t < hi && t < len)
+            for (int q = 0; q < p.tiles; ++q) {
+                const int64_t at = q * plane + bh * p.T + t;
+                x += p.row[at] - p.col[at];
+            }
+        return x;
+    };
+    double miss = 0.0, run = p.border[bh * (p.nseg + 1) + seg + 1], total = 0.0;
+    for (int64_t t = lo + tid; t < hi; t += 256) miss += diff(t);
+    miss = run + block_sum(miss, part) - p.border[bh * (p.nseg + 1) + seg];
+    const double slope = miss / double(hi - lo);
+    for (int64_t w = (hi - lo + 1023) / 1024 - 1; w >= 0; --w) {
+        const int64_t t0 = lo + w * 1024 + tid * 4;
         double v[4];
 #pragma unroll
-        for (int i = 3; i >= 0; --i) {
-            double x = 0.0;
-            if (t0 + i < len)
-                for (int q = 0; q < p.tiles; ++q) {
-                    const int64_t at = q * plane + bh * p.T + t0 + i;
-                    x += p.row[at] - p.col[at];
-                }
-            v[i] = x + (i < 3 ? v[i + 1] : 0.0);  // suffix sums of the thread's four
-        }
+        for (int i = 3; i >= 0; --i) v[i] = diff(t0 + i) + (i < 3 ? v[i + 1] : 0.0);
         double s = v[0];                          // suffix sum over the lanes behind this one
 #pragma unroll
         for (int m = 1; m < 64; m <<= 1) {
@@ -103,27 +146,29 @@ __global__ __launch_bounds__(256) void la_decay_grad_kernel(const LaDecayGrad p)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int64_t t = t0 + i;
-            const double dg = t < len ? v[i] + behind : 0.0;
-            if (p.decay_token) {
-                if (t < p.T) p.dg[(b * p.T + t) * p.H + h] = float(dg);
-            } else {
-                total += dg;
-            }
+            if (t >= hi) continue;
+            const double dg = t < len ? v[i] + behind - slope * double(hi - t) : 0.0;
+            if (p.decay_token) p.dg[(b * p.T + t) * p.H + h] = float(dg);
+            else total += dg;
         }
     }
     if (!p.decay_token) {
-        total = block_sum(total);
-        if (tid == 0) p.head_part[bh] = float(total);
+        total = block_sum(total, part);
+        if (tid == 0) p.head_part[blockIdx.x] = total;
     }
 }
 
-__global__ __launch_bounds__(256) void la_head_sum_kernel(const float* part, float* dg, int64_t B,
-                                                          int64_t H) {
-    const int64_t h = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    if (h >= H) return;
+// One wave a head: the sums of its rows and segments.
+__global__ __launch_bounds__(64) void la_head_sum_kernel(const LaDecayGrad p) {
+    const int64_t h = blockIdx.x, n = p.B * p.nseg;
     double v = 0.0;
-    for (int64_t b = 0; b < B; ++b) v += part[b * H + h];
-    dg[h] = float(v);
+    for (int64_t x = threadIdx.x; x < n; x += 64) {
+        const int64_t b = x / p.nseg, seg = x - b * p.nseg;
+        v += p.head_part[(b * p.H + h) * p.nseg + seg];
+    }
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m, 64);
+    if (threadIdx.x == 0) p.dg[h] = float(v);
 }
 
 template <typename T>
@@ -242,11 +287,14 @@ hipError_t launch_la_carry(const LaCarry& p, hipStream_t s) {
 }
 
 hipError_t launch_la_decay_grad(const LaDecayGrad& p, hipStream_t s) {
-    hipLaunchKernelGGL(la_decay_grad_kernel, dim3(unsigned(p.B * p.H)), dim3(256), 0, s, p);
+    const int64_t bh = p.B * p.H;
+    hipLaunchKernelGGL(la_border_kernel, dim3(unsigned(bh * (p.nseg + 1))), dim3(256), 0, s, p);
     hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(la_decay_grad_kernel, dim3(unsigned(bh * p.nseg)), dim3(256), 0, s, p);
+    e = hipGetLastError();
     if (e != hipSuccess || p.decay_token) return e;
-    hipLaunchKernelGGL(la_head_sum_kernel, dim3(unsigned((p.H + 255) / 256)), dim3(256), 0, s,
-                       p.head_part, p.dg, p.B, p.H);
+    hipLaunchKernelGGL(la_head_sum_kernel, dim3(unsigned(p.H)), dim3(64), 0, s, p);
     return hipGetLastError();
 }
 

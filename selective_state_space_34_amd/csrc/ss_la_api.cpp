@@ -218,15 +218,16 @@ int ss_la_bwd(const ss_la_dims* dims, const void* q, const void* k, const void* 
     }
 
     // 2. dv: reverse sweep of (k, q, dO), state dS_t [dk, dv]; its segments' states serve dk too
+    float* rstate = at(p.off_rstate);
     s = base(p, g, lengths, 1);
     s.a = in.k; s.b = in.q; s.c = od; s.e = od;
     if (p.nseg > 1) {
-        e = segment_states(p, s, p.fwd, ds_final, p.dv, 1, state, decay, stream);
+        e = segment_states(p, s, p.fwd, ds_final, p.dv, 1, rstate, decay, stream);
         if (e != hipSuccess) return hip_fail(e);
     }
     s.out = dv;
     s.s_out = ds0;
-    e = full_sweep(p, s, p.fwd, ds_final, p.dv, 1, state, p.dv, 1, stream);
+    e = full_sweep(p, s, p.fwd, ds_final, p.dv, 1, rstate, p.dv, 1, stream);
     if (e != hipSuccess) return hip_fail(e);
 
     // 3. dk: reverse sweep of (v, dO, q), state dS_tᵀ [dv, dk], read transposed
@@ -234,20 +235,23 @@ int ss_la_bwd(const ss_la_dims* dims, const void* q, const void* k, const void* 
     s.a = in.v; s.b = od; s.c = in.q; s.e = in.k;
     s.out = part ? static_cast<void*>(part) : dk; s.out_f32 = part != nullptr;
     s.dots = g ? dots(p.off_col) : nullptr;
-    e = full_sweep(p, s, p.rev, ds_final, 1, p.dv, state, 1, p.dv, stream);
+    e = full_sweep(p, s, p.rev, ds_final, 1, p.dv, rstate, 1, p.dv, stream);
     if (e != hipSuccess) return hip_fail(e);
     if (part) {
         e = ss::launch_la_group_sum(bf16, part, dk, p.B * p.T, p.Hk, p.H / p.Hk, p.dk, stream);
         if (e != hipSuccess) return hip_fail(e);
     }
 
-    // 4. dg from the row and column sums
+    // 4. dg from the row and column sums and the states at the segments' borders
     if (g) {
         ss::LaDecayGrad d{};
         d.row = dots(p.off_row); d.col = dots(p.off_col); d.tiles = p.rev.tiles;
-        d.ds = ds_final; d.s_final = s_final; d.lengths = lengths;
-        d.dg = dg; d.head_part = at(p.off_head);
+        d.fwd_state = state; d.rev_state = rstate;
+        d.s0 = s0; d.ds0 = ds0; d.ds = ds_final; d.s_final = s_final;
+        d.border = dots(p.off_border); d.head_part = dots(p.off_head);
+        d.lengths = lengths; d.dg = dg;
         d.B = p.B; d.T = p.T; d.H = p.H; d.dk = p.dk; d.dv = p.dv;
+        d.nseg = int(p.nseg); d.seg_tokens = p.seg_chunks * ss::la_chunk(p.in_dtype);
         d.decay_token = p.decay == SS_LA_DECAY_TOKEN;
         e = ss::launch_la_decay_grad(d, stream);
         if (e != hipSuccess) return hip_fail(e);

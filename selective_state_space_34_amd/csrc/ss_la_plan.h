@@ -34,9 +34,9 @@ inline int64_t la_round(const LaShape& s, bool dots) {
 
 // Segments of a sequence that are swept side by side: as many as are resident at once (a few
 // more would take a second round as long as the first: a sweep over 13 segments of 40 heads
-// measured 369 us, over 12 it measured 281), none shorter than two chunks.
-inline int64_t la_segments(int64_t n, int64_t nchunk) {
-    if (n > nchunk / 2) n = nchunk / 2;
+// measured 369 us, over 12 it measured 281), none shorter than `least` chunks.
+inline int64_t la_segments(int64_t n, int64_t nchunk, int64_t least) {
+    if (n > nchunk / least) n = nchunk / least;
     if (n < 1) n = 1;
     const int64_t len = (nchunk + n - 1) / n;
     return (nchunk + len - 1) / len;
@@ -50,12 +50,15 @@ struct LaPlan {
     LaShape fwd, rev;           // sweeps whose state is [dk, dv]; [dv, dk]
     int64_t nseg, seg_chunks;
     // forward: off_state [B, H, nseg, dk·dv], off_decay [B, H, nseg] (nseg > 1)
-    // backward: the same (used by one direction after the other), and
+    // backward: the same for the forward direction, and
+    //   off_rstate         [B, H, nseg, dk·dv] of the reverse direction (nseg > 1)
     //   off_row, off_col   [rev.tiles, B, H, T] row and column sums behind dg (64 bits)
     //   off_final          [B, H, dv·dk] S_Tᵀ
-    //   off_head           [B, H] dg of each (row, head) summed over tokens (one decay a head)
+    //   off_border         [B, H, nseg + 1] (64 bits) <adjoint, state> at the segments' borders
+    //   off_head           [B, H, nseg] (64 bits) dg summed over a segment (one decay a head)
     //   off_part           [B, T, H, dk] float32 dq, then dk, of each value head (Hk < H)
-    size_t off_state, off_decay, off_row, off_col, off_final, off_head, off_part, total;
+    size_t off_state, off_decay, off_rstate, off_row, off_col, off_final, off_border, off_head, off_part,
+        total;
 };
 
 // q, k, v strides: all zero means dense; otherwise each must be >= 0.
@@ -95,11 +98,12 @@ inline int make_la_plan(const ss_la_dims& d, bool backward, LaPlan* out) {
         const int64_t r = la_round(p.rev, p.decay != SS_LA_DECAY_NONE) / (bh * p.rev.tiles);
         n = r < n ? r : n;
     }
-    p.nseg = la_segments(n, p.nchunk);
+    // the gradient's borders are exact, so there short segments are a gain in themselves
+    p.nseg = la_segments(n, p.nchunk, backward ? 1 : 2);
     p.seg_chunks = (p.nchunk + p.nseg - 1) / p.nseg;
     // one workgroup for each (column tile, row, head, segment), and the row-wise kernels
     const int64_t grid = int64_t(1) << 31;
-    if (!mul_ok(bh, p.nseg * most, grid - 1)) return SS_ERR_DIMS;
+    if (!mul_ok(bh, (p.nseg + 1) * most, grid - 1)) return SS_ERR_DIMS;
     const size_t f = sizeof(float);
     const size_t state = size_t(bh) * size_t(p.dk * p.dv) * f;
     size_t off = 0;
@@ -108,11 +112,14 @@ inline int make_la_plan(const ss_la_dims& d, bool backward, LaPlan* out) {
     p.off_decay = off;
     if (p.nseg > 1) off = align256(off + size_t(bh * p.nseg) * f);
     if (backward) {
+        p.off_rstate = off;
+        if (p.nseg > 1) off = align256(off + size_t(p.nseg) * state);
         const size_t dots = size_t(p.rev.tiles) * size_t(bh) * size_t(p.T) * sizeof(double);
         p.off_row = off; off = align256(off + dots);
         p.off_col = off; off = align256(off + dots);
         p.off_final = off; off = align256(off + state);
-        p.off_head = off; off = align256(off + size_t(bh) * f);
+        p.off_border = off; off = align256(off + size_t(bh * (p.nseg + 1)) * sizeof(double));
+        p.off_head = off; off = align256(off + size_t(bh * p.nseg) * sizeof(double));
         p.off_part = off;
         if (p.Hk < p.H) off = align256(off + size_t(bh) * size_t(p.T) * size_t(p.dk) * f);
     }

@@ -14,9 +14,8 @@
 // The log decays' gradient needs only the products A_ts = α e^{G_t-G_s} (q_t·k_s)(do_t·v_s):
 //   dg_t = Σ_{u>=t} (row_u - col_u) + <dS_T, S_T>, row_u = Σ_{s<u} A_us + (S_0's part),
 // and likewise col_u = Σ_{t>u} A_tu + (dS_T's part): row_u is e_u·out_u of the dq sweep with
-// e = q and the diagonal left out, col_u that of the dk sweep with e = k (kDot).  Every pair
-// that a row or column sum holds is also held by some dg near it, so the running sum loses
-// nothing to cancellation.
+// e = q and the diagonal left out, col_u that of the dk sweep with e = k (kDot).  (The running
+// sum starts anew at every segment, ss_la.hip.)
 //
 // A workgroup of four or eight waves takes one head's rows chunk by chunk (64 tokens of bf16,
 // 32 of float32) with the state in registers: a wave holds all dA rows of 16 columns, in the
@@ -371,11 +370,12 @@ __global__ __launch_bounds__(64 * NW, sweep_occupancy(kVec, DA, NW, kDot, kState
     constexpr int SA = NT * V / DA, SC = NT * V / DC;            // tokens between them
     constexpr int TB = C / 16, KS = C / 32, IB = DA / 32;
     constexpr int kTiles = TB * (TB + 1) / 2;
+    constexpr int PT = sizeof(T) == 2 ? 2 : 1;      // terms of P
 
     __shared__ __attribute__((aligned(16))) Elem lb[C * LB];
     __shared__ __attribute__((aligned(16))) Elem lc[C * LC];
     __shared__ __attribute__((aligned(16))) Elem la_[kState ? 8 : C * LA];
-    __shared__ __attribute__((aligned(16))) Elem lp[kState ? 8 : C * C];
+    __shared__ __attribute__((aligned(16))) Elem lp[kState ? 8 : PT * C * C];
     __shared__ __attribute__((aligned(16))) Elem le[kDot ? C * DC : 8];
     __shared__ __attribute__((aligned(16))) Decay<C> dec[2];
     __shared__ double dot_tile[kDot ? kTiles * 16 : 1];
@@ -388,8 +388,8 @@ __global__ __launch_bounds__(64 * NW, sweep_occupancy(kVec, DA, NW, kDot, kState
     // the tokens s of each 32 in the order of the transposed operands
     auto p_at = [](int t, int s) { return t * C + (((s / V) ^ ((t >> 1) & (C / V - 1))) * V) + s % V; };
     auto e_at = [](int t, int j) { return t * DC + (((j / V) ^ (t & (DC / V - 1))) * V) + j % V; };
-    auto p_row = [&](int t, int s) {   // eight consecutive values
-        if constexpr (sizeof(T) == 2) return M::row(&lp[p_at(t, s)]);
+    auto p_row = [&](int t, int s, int term) {   // eight consecutive values
+        if constexpr (sizeof(T) == 2) return M::row(&lp[term * C * C + p_at(t, s)]);
         else {
             const f32x4 lo = *reinterpret_cast<const f32x4*>(&lp[p_at(t, s)]);
             const f32x4 hi = *reinterpret_cast<const f32x4*>(&lp[p_at(t, s + 4)]);
@@ -504,7 +504,7 @@ __global__ __launch_bounds__(64 * NW, sweep_occupancy(kVec, DA, NW, kDot, kState
 
     if constexpr (!kState)
         // tiles of P that the mask empties are read but never written again
-        for (int i = tid; i < C * C; i += NT) lp[i] = M::from(0.0f);
+        for (int i = tid; i < PT * C * C; i += NT) lp[i] = M::from(0.0f);
     if (n > 0) {
         load_g(0);
         load_rows(0);
@@ -596,10 +596,16 @@ __global__ __launch_bounds__(64 * NW, sweep_occupancy(kVec, DA, NW, kDot, kState
                     if (lg == 0) dot_tile[x * 16 + l16] = dot;
                 }
                 if constexpr (sizeof(T) == 2) {
-                    bf16x4 o;
+                    bf16x4 o[PT];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) o[r] = __bf16(v[r]);
-                    *reinterpret_cast<bf16x4*>(&lp[p_at(t, sp)]) = o;
+                    for (int r = 0; r < 4; ++r) {
+                        o[0][r] = __bf16(v[r]);
+                        const float left = v[r] - float(o[0][r]);
+                        o[1][r] = __bf16(left == left ? left : 0.0f);
+                    }
+#pragma unroll
+                    for (int q = 0; q < PT; ++q)
+                        *reinterpret_cast<bf16x4*>(&lp[q * C * C + p_at(t, sp)]) = o[q];
                 } else {
                     *reinterpret_cast<f32x4*>(&lp[p_at(t, sp)]) = f32x4{v[0], v[1], v[2], v[3]};
                 }
@@ -658,7 +664,9 @@ __global__ __launch_bounds__(64 * NW, sweep_occupancy(kVec, DA, NW, kDot, kState
                 for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks)
-                        O[tb] = M::mma(cf[ks], p_row(16 * tb + l16, 32 * ks + 8 * lg), O[tb]);
+#pragma unroll
+                        for (int q = 0; q < PT; ++q)
+                            O[tb] = M::mma(cf[ks], p_row(16 * tb + l16, 32 * ks + 8 * lg, q), O[tb]);
                 settle();
             } else {
                 // A masked weight is 0, and its product with an infinity would be NaN: the
@@ -670,7 +678,8 @@ __global__ __launch_bounds__(64 * NW, sweep_occupancy(kVec, DA, NW, kDot, kState
                     for (int s = 0; s < nv; ++s) {
                         if (rev ? s < t : s > t) continue;
                         const int sp = (s & ~31) + 8 * ((s >> 2) & 3) + 4 * ((s >> 4) & 1) + (s & 3);
-                        const float w = float(lp[p_at(t, sp)]);
+                        float w = float(lp[p_at(t, sp)]);
+                        if (PT == 2) w += float(lp[(PT - 1) * C * C + p_at(t, sp)]);
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
                             O[tb][r] = fmaf(w, float(lc[s * LC + jw + 4 * lg + r]), O[tb][r]);
