@@ -70,18 +70,23 @@ __global__ __launch_bounds__(256) void la_border_kernel(const LaDecayGrad p) {
         // r is [dk, dv], s [dv, dk]: s by way of a tile in LDS, so that both are read by rows
         for (int i0 = 0; i0 < dk; i0 += 64)
             for (int j0 = 0; j0 < dv; j0 += 64) {
-                __syncthreads();
-#pragma unroll 4
-                for (int x = tid; x < 64 * 64; x += 256) {
-                    const int j = x / 64, i = x % 64;
-                    tile[j][i] = j0 + j < dv && i0 + i < dk ? s[(j0 + j) * dk + i0 + i] : 0.0f;
+                float a[16], c[16];
+                const int low = tid & 63, high = tid >> 6;
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {   // all in flight; what is outside is not used
+                    const int y = high + 4 * x;
+                    a[x] = s[min(j0 + y, dv - 1) * dk + min(i0 + low, dk - 1)];
+                    c[x] = r[min(i0 + y, dk - 1) * dv + min(j0 + low, dv - 1)];
                 }
                 __syncthreads();
-#pragma unroll 4
-                for (int x = tid; x < 64 * 64; x += 256) {
-                    const int i = x / 64, j = x % 64;
-                    if (i0 + i < dk && j0 + j < dv)
-                        v += double(r[(i0 + i) * dv + j0 + j]) * double(tile[j][i]);
+#pragma unroll
+                for (int x = 0; x < 16; ++x) tile[high + 4 * x][low] = a[x];
+                __syncthreads();
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                    const int i = high + 4 * x;
+                    const double y = double(c[x]) * double(tile[low][i]);
+                    v += i0 + i < dk && j0 + low < dv ? y : 0.0;
                 }
             }
     }

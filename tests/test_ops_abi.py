@@ -1,0 +1,197 @@
+"""C ABI of the linear attention, the norm and the 4-bit products: bad arguments are refused with
+the documented codes before anything is launched (no GPU needed: every call here fails first),
+and the workspaces of a sweep of shapes are carved without overlap."""
+import ctypes
+
+import pytest
+
+import selective_state_space_34_amd as ss
+from selective_state_space_34_amd import _build
+
+FAKE = 0x10000   # 16-byte aligned, never dereferenced
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if _build.stale():
+        _build.build()
+    return ss.load()
+
+
+def la(B=2, T=300, H=4, Hk=2, dk=64, dv=64, **kw):
+    return ss.make_la_dims(B, T, H, Hk, dk, dv, **kw)
+
+
+BAD_DIMS = [la(B=0), la(T=0), la(H=0), la(Hk=0), la(dk=0), la(dv=0), la(dk=257), la(dv=300),
+            la(H=5), la(scale=float("inf")), la(scale=float("nan")), la(q_stride=(1, -2, 3)),
+            la(v_stride=(1 << 41, 1, 1)), la(B=1 << 30, T=1 << 20), la(H=1 << 20, Hk=1, dk=1, dv=8)]
+
+
+def test_la_fwd(lib):
+    # q k v g | s0 lengths | o s_final
+    good = [FAKE] * 4 + [None, None, FAKE, None]
+
+    def call(d, a, ws=None, n=0):
+        return lib.ss_la_fwd(d, *a, ws, n, None)
+    assert call(None, good) == -1
+    for d in BAD_DIMS:
+        assert call(d, good) == -2
+    assert call(la(in_dtype=2), good) == -3
+    assert call(la(decay=3), good) == -3
+    assert call(la(decay=-1), good) == -3
+    for i in (0, 1, 2, 3, 6):
+        a = list(good)
+        a[i] = None
+        assert call(la(), a) == -1, i
+    assert call(la(decay=ss.SS_LA_DECAY_NONE), good) == -1       # g without a decay
+    full = [FAKE] * 8
+    for i, off in ((0, 1), (1, 1), (2, 1), (3, 2), (4, 4), (5, 2), (6, 8), (7, 4)):
+        a = list(full)
+        a[i] = FAKE + off
+        assert call(la(), a) == -4, i
+    need = ss.la_workspace_size(la())
+    assert need > 0
+    assert call(la(), full) == -5
+    assert call(la(), full, FAKE, need - 1) == -5
+    assert call(la(), full, FAKE + 8, need) == -4
+    # element alignment is enough for q, k, v: the call goes on to the workspace
+    a = list(full)
+    a[0] = a[1] = a[2] = FAKE + 2
+    assert call(la(), a) == -5
+
+
+def test_la_bwd(lib):
+    # q k v g s0 lengths | dO ds_final | dq dk dv dg ds0
+    good = [FAKE] * 13
+
+    def call(d, a, ws=None, n=0):
+        return lib.ss_la_bwd(d, *a, ws, n, None)
+    assert call(None, good) == -1
+    for d in BAD_DIMS:
+        assert call(d, good) == -2
+    for i in (0, 1, 2, 3, 6, 8, 9, 10, 11):
+        a = list(good)
+        a[i] = None
+        assert call(la(), a) == -1, i
+    for i in (4, 12):                                            # s0 and ds0: both or neither
+        a = list(good)
+        a[i] = None
+        assert call(la(), a) == -1, i
+    none = list(good)
+    none[3] = None
+    assert call(la(decay=ss.SS_LA_DECAY_NONE), none) == -1       # dg without a decay
+    none[11] = None
+    assert call(la(decay=ss.SS_LA_DECAY_NONE), none) == -5
+    for i in (4, 6, 7, 8, 9, 10, 11, 12):
+        a = list(good)
+        a[i] = FAKE + 4
+        assert call(la(), a) == -4, i
+    need = ss.la_workspace_size(la(), backward=True)
+    assert call(la(), good) == -5
+    assert call(la(), good, FAKE, need - 1) == -5
+    assert call(la(), good, FAKE + 4, need) == -4
+
+
+def test_la_step(lib):
+    # q k v g | s_in s_out o
+    good = [FAKE] * 7
+
+    def call(d, a):
+        return lib.ss_la_step(d, *a, None)
+    assert call(None, good) == -1
+    assert call(la(T=2), good) == -2
+    for i in range(7):
+        a = list(good)
+        a[i] = None
+        assert call(la(T=1), a) == -1, i
+    for i, off in ((0, 1), (3, 2), (4, 4), (5, 8), (6, 2)):
+        a = list(good)
+        a[i] = FAKE + off
+        assert call(la(T=1), a) == -4, i
+
+
+def test_rms(lib):
+    def fwd(d, a):
+        return lib.ss_rms_fwd(d, *a, None)
+    r = ss.make_rms_dims
+    good = [FAKE] * 5 + [None]           # x res w r y | y_scale
+    assert fwd(None, good) == -1
+    for d in (r(0, 8), r(8, 0), r(1, 32769), r(1 << 40, 1 << 12), r(4, 8, eps=-1.0),
+              r(4, 8, eps=float("nan")), r(4, 8, eps=float("inf"))):
+        assert fwd(d, good) == -2
+    for d in (r(4, 8, in_dtype=5), r(4, 8, res_dtype=-1), r(4, 8, in_dtype=0, res_dtype=1), r(4, 8, q8=3)):
+        assert fwd(d, good) == -3
+    for i in (0, 1, 2, 3, 4):            # res and r go together
+        a = list(good)
+        a[i] = None
+        assert fwd(r(4, 8), a) == -1, i
+    assert fwd(r(4, 8, q8=1), good) == -1
+    assert fwd(r(4, 8), [FAKE] * 6) == -1
+    for i in range(6):
+        a = [FAKE] * 6
+        a[i] = FAKE + 8
+        assert fwd(r(4, 8, q8=2), a) == -4, i
+    # dy r w dr dx dw
+    back = [FAKE] * 6
+
+    def bwd(d, a, ws=None, n=0):
+        return lib.ss_rms_bwd(d, *a, ws, n, None)
+    assert bwd(r(4, 8, q8=1), back) == -3
+    for i in (0, 1, 2, 4, 5):
+        a = list(back)
+        a[i] = None
+        assert bwd(r(4, 8), a) == -1, i
+    need = ss.rms_workspace_size(r(4, 8))
+    assert bwd(r(4, 8), back) == -5
+    assert bwd(r(4, 8), back, FAKE, need - 1) == -5
+    assert bwd(r(4, 8), back, FAKE + 4, need) == -4
+
+
+def test_q4(lib):
+    # x x_scale wq scales zeros y
+    good = [FAKE, None, FAKE, FAKE, None, FAKE]
+
+    def call(d, a):
+        return lib.ss_q4_mv(d, *a, None)
+    q = ss.make_q4_dims
+    assert call(None, good) == -1
+    for d in (q(0, 8, 64), q(1, 0, 64), q(1, 8, 0), q(1, 8, 48), q(1, 8, 64, group=16),
+              q(1, 8, 64, group=256), q(1 << 30, 8, 1 << 20), q(16 * 65536, 8, 32)):
+        assert call(d, good) == -2
+    for d in (q(1, 8, 64, in_dtype=2), q(1, 8, 64, y_dtype=2), q(1, 8, 64, x_q8=3)):
+        assert call(d, good) == -3
+    for i in (0, 2, 3, 5):
+        a = list(good)
+        a[i] = None
+        assert call(q(1, 8, 64), a) == -1, i
+    assert call(q(1, 8, 64, x_q8=1), good) == -1                 # 8-bit rows without scales
+    assert call(q(1, 8, 64), [FAKE] * 6) == -1                   # scales without 8-bit rows
+    for i in range(6):
+        a = [FAKE] * 6
+        a[i] = FAKE + 8
+        assert call(q(1, 8, 64, x_q8=2), a) == -4, i
+
+
+def test_workspaces(lib):
+    """Sizes follow the formulas of the parts they hold."""
+    a256 = lambda n: (n + 255) // 256 * 256  # noqa: E731
+    assert ss.la_workspace_size(la(T=64)) == 0                   # one chunk: nothing to carry
+    for B, T, H, Hk, dk, dv in ((1, 4096, 2, 2, 64, 64), (4, 2048, 16, 16, 128, 128), (3, 200, 5, 1, 17, 90),
+                                (2, 1000, 4, 4, 200, 256), (700, 640, 1, 1, 16, 16)):
+        d = la(B=B, T=T, H=H, Hk=Hk, dk=dk, dv=dv)
+        state = B * H * dk * dv * 4
+        f, b = ss.la_workspace_size(d), ss.la_workspace_size(d, backward=True)
+        assert f == 0 or any(f == a256(n * state) + a256(B * H * n * 4) for n in range(2, 1025))
+        tiles = -(-dk // (64 if dk <= 64 else 128))
+        part = a256(B * H * T * dk * 4) if Hk < H else 0
+        fixed = 2 * a256(tiles * B * H * T * 8) + a256(state) + part
+
+        def whole(n):
+            seg = 2 * a256(n * state) + a256(B * H * n * 4) if n > 1 else 0
+            return fixed + seg + a256(B * H * (n + 1) * 8) + a256(B * H * n * 8)
+        assert any(b == whole(n) for n in range(1, 1025)), (B, T, H, dk, dv)
+        n = ctypes.c_size_t()
+        assert lib.ss_la_fwd_workspace_size(None, ctypes.byref(n)) == -1
+        assert lib.ss_la_bwd_workspace_size(d, None) == -1
+    d = ss.make_rms_dims(100000, 2560)
+    assert ss.rms_workspace_size(d) % (2560 * 4) == 0
