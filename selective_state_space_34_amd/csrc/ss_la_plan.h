@@ -155,7 +155,7 @@ inline int make_rms_plan(const ss_rms_dims& d, bool backward, RmsPlan* out) {
     // odd width 2563: 75 against 96), the gradient, with three rows and dw to hold, is not
     // (97 us against 83).
     if (D <= 64 * 8 * 2) {
-        p.threads = 64;
+        p.threads = D <= 8 * 8 ? 8 : D <= 32 * 8 ? 32 : 64;
         p.pieces = D <= 64 * 8 ? 1 : 2;
     } else if (!backward && D > 256 * 8 && D <= 64 * 8 * 6 && d.rows >= 1024) {
         p.threads = 64;
@@ -172,11 +172,10 @@ inline int make_rms_plan(const ss_rms_dims& d, bool backward, RmsPlan* out) {
     }
     const int64_t wg_rows = p.threads >= 256 ? 1 : 256 / p.threads;
     const int64_t need = (d.rows + wg_rows - 1) / wg_rows;
-    // Workgroups take rows in turn.  Two on each CU where one holds much or leaves a row of
-    // partial sums (gradient, D = 2560: 1024 workgroups 81 us, 2048 86; D = 5120: 512 146 us,
-    // 1024 153), else eight.
-    const int64_t most = p.threads >= 512 || p.pieces == 6 ? 512
-                       : backward ? (p.threads == 256 ? 1024 : 512) : 2048;
+    // Workgroups take rows in turn.  Two on each CU where one holds much, four where each leaves
+    // a row of partial sums (gradient, D = 2560: 1024 workgroups 81 us, 2048 86; D = 5120: 512
+    // 146 us, 1024 153), else eight.
+    const int64_t most = p.threads >= 512 || p.pieces == 6 ? 512 : backward ? 1024 : 2048;
     p.grid = int(need < most ? need : most);
     p.total = backward ? align256(size_t(p.grid) * size_t(D) * sizeof(float)) : 0;
     *out = p;

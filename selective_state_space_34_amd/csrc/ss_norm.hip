@@ -7,7 +7,7 @@
 //   dx = dr + c·(w·dy) - r·(c³/D)·Σ(w·dy·r)        dw = Σ_rows dy·r·c
 //
 // The work is traffic: every element is read once and written once, a row staying in registers
-// between the sums and the result.  A row belongs to P threads (64 to 1024, by its length
+// between the sums and the result.  A row belongs to P threads (8 to 1024, by its length
 // and by how many rows there are), eight consecutive elements of it to each thread at a time,
 // NV such pieces a thread; sums meet by shuffles, across waves through LDS.  Workgroups take
 // rows in turn, so that in the gradient the columns' sums stay in registers over a workgroup's
@@ -85,6 +85,21 @@ __device__ __forceinline__ void put8(bf16_t* row, int64_t col, int64_t dim, cons
     }
 }
 
+// Where the piece at col is taken from.  A row that ends inside a piece would be read and written
+// there element by element; where one wave holds a row, the last piece is the row's last eight
+// elements instead, and `twice` of them, its neighbour's too, are left out of the sums.  (All
+// loads of a wave come before its stores, so this holds in place as well; between waves it would
+// not.)
+struct Span {
+    int64_t at;
+    int twice;
+};
+template <int P>
+__device__ __forceinline__ Span span_of(int64_t col, int64_t dim) {
+    if (P <= 64 && dim >= 8 && col < dim && col + 8 > dim) return Span{dim - 8, int(col + 8 - dim)};
+    return Span{col, 0};
+}
+
 // Eight codes of v·inv: e4m3 (round to nearest even; |v·inv| <= 448, so none overflows) or
 // int8 in [-127, 127].
 __device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv, int q8) {
@@ -115,9 +130,10 @@ template <int P>
 struct RowSum {
     float* slots;   // [2][32], LDS
     int at = 0;
+    static constexpr int kLanes = P < 64 ? P : 64;
     __device__ __forceinline__ float sum(float v) {
 #pragma unroll
-        for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m, 64);
+        for (int m = 1; m < kLanes; m <<= 1) v += __shfl_xor(v, m, 64);
         if constexpr (P > 64) {
             float* s = slots + 32 * at;
             at ^= 1;
@@ -131,7 +147,7 @@ struct RowSum {
     }
     __device__ __forceinline__ void sum2(float& a, float& b) {
 #pragma unroll
-        for (int m = 1; m < 64; m <<= 1) {
+        for (int m = 1; m < kLanes; m <<= 1) {
             a += __shfl_xor(a, m, 64);
             b += __shfl_xor(b, m, 64);
         }
@@ -153,7 +169,7 @@ struct RowSum {
     }
     __device__ __forceinline__ uint32_t max(uint32_t v) {
 #pragma unroll
-        for (int m = 1; m < 64; m <<= 1) {
+        for (int m = 1; m < kLanes; m <<= 1) {
             const uint32_t o = uint32_t(__shfl_xor(int(v), m, 64));
             v = v > o ? v : o;
         }
@@ -185,28 +201,32 @@ __global__ __launch_bounds__(P > 256 ? P : 256) void rms_fwd_kernel(const RmsLau
         float v[NV][8], sq = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int64_t col = (int64_t(j) * P + tid) * 8;
-            px[j] = get8(x, col, D);
-            if (p.res) pr[j] = get8(res, col, D);
+            const Span c = span_of<P>((int64_t(j) * P + tid) * 8, D);
+            px[j] = get8(x, c.at, D);
+            if (p.res) pr[j] = get8(res, c.at, D);
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
+            const Span c = span_of<P>((int64_t(j) * P + tid) * 8, D);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[j][e] = px[j].get(e);
             if (p.res) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[j][e] += pr[j].get(e);
-                put8(static_cast<Tr*>(p.r) + row * D, (int64_t(j) * P + tid) * 8, D, v[j]);
+                put8(static_cast<Tr*>(p.r) + row * D, c.at, D, v[j]);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sq = fmaf(v[j][e], v[j][e], sq);
+            for (int e = 0; e < 8; ++e) {
+                const float x = e >= c.twice ? v[j][e] : 0.0f;
+                sq = fmaf(x, x, sq);
+            }
         }
         sq = rs.sum(sq);
         const float c = rsqrtf(sq * p.inv_d + p.eps);
         uint32_t top = 0;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const Piece<float> w = get8(p.w, (int64_t(j) * P + tid) * 8, D);
+            const Piece<float> w = get8(p.w, span_of<P>((int64_t(j) * P + tid) * 8, D).at, D);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 v[j][e] = v[j][e] * c * w.get(e);
@@ -218,7 +238,8 @@ __global__ __launch_bounds__(P > 256 ? P : 256) void rms_fwd_kernel(const RmsLau
         if (p.q8 == SS_Q8_NONE) {
             Tx* y = static_cast<Tx*>(p.y) + row * D;
 #pragma unroll
-            for (int j = 0; j < NV; ++j) put8(y, (int64_t(j) * P + tid) * 8, D, v[j]);
+            for (int j = 0; j < NV; ++j)
+                put8(y, span_of<P>((int64_t(j) * P + tid) * 8, D).at, D, v[j]);
         } else {
             const float amax = __uint_as_float(rs.max(top));
             const float full = p.q8 == SS_Q8_FP8 ? 448.0f : 127.0f;
@@ -227,7 +248,7 @@ __global__ __launch_bounds__(P > 256 ? P : 256) void rms_fwd_kernel(const RmsLau
             uint8_t* y = static_cast<uint8_t*>(p.y) + row * D;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                const int64_t col = (int64_t(j) * P + tid) * 8;
+                const int64_t col = span_of<P>((int64_t(j) * P + tid) * 8, D).at;
                 // a row that is not finite keeps NaN codes where e4m3 has them
                 const uint2 q = codes8(v[j], amax != amax ? amax : inv, p.q8);
                 if (col + 8 <= D) {
@@ -265,18 +286,20 @@ __global__ __launch_bounds__(P > 256 ? P : 256) void rms_bwd_kernel(const RmsLau
         float sq = 0.0f, dot = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int64_t col = (int64_t(j) * P + tid) * 8;
+            const int64_t col = span_of<P>((int64_t(j) * P + tid) * 8, D).at;
             r[j] = get8(rr, col, D);
             dy[j] = get8(dyr, col, D);
             if (p.dr) g[j] = get8(static_cast<const Tr*>(p.dr) + row * D, col, D);
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const Piece<float> w = get8(p.w, (int64_t(j) * P + tid) * 8, D);
+            const Span c = span_of<P>((int64_t(j) * P + tid) * 8, D);
+            const Piece<float> w = get8(p.w, c.at, D);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                sq = fmaf(r[j].get(e), r[j].get(e), sq);
-                dot = fmaf(dy[j].get(e) * w.get(e), r[j].get(e), dot);
+                const float x = e >= c.twice ? r[j].get(e) : 0.0f;
+                sq = fmaf(x, x, sq);
+                dot = fmaf(dy[j].get(e) * w.get(e), x, dot);
             }
         }
         rs.sum2(sq, dot);
@@ -285,23 +308,32 @@ __global__ __launch_bounds__(P > 256 ? P : 256) void rms_bwd_kernel(const RmsLau
         Tr* dx = static_cast<Tr*>(p.r) + row * D;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int64_t col = (int64_t(j) * P + tid) * 8;
-            const Piece<float> w = get8(p.w, col, D);
+            const Span at = span_of<P>((int64_t(j) * P + tid) * 8, D);
+            const Piece<float> w = get8(p.w, at.at, D);
             float o[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float x = r[j].get(e), y = dy[j].get(e);
                 o[e] = fmaf(c * w.get(e), y, -k * x);
-                dw[j][e] = fmaf(y, x * c, dw[j][e]);
+                dw[j][e] = fmaf(y, e >= at.twice ? x * c : 0.0f, dw[j][e]);
                 if (p.dr) o[e] += g[j].get(e);
             }
-            put8(dx, col, D, o);
+            put8(dx, at.at, D, o);
         }
     }
     float* part = p.part + int64_t(blockIdx.x) * D;
+    auto put_own = [&](const Span& c, const float (&v)[8]) {
+        if (c.twice == 0) {
+            put8(part, c.at, D, v);
+        } else {
+#pragma unroll
+            for (int e = 1; e < 8; ++e)
+                if (e >= c.twice) part[c.at + e] = v[e];
+        }
+    };
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int64_t col = (int64_t(j) * P + tid) * 8;
+        const Span c = span_of<P>((int64_t(j) * P + tid) * 8, D);
         if constexpr (kRowsWG > 1) {
             // the workgroup's row slots one after the other
             for (int s = 0; s < kRowsWG; ++s) {
@@ -315,10 +347,10 @@ __global__ __launch_bounds__(P > 256 ? P : 256) void rms_bwd_kernel(const RmsLau
             if (sub == 0) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) dw[j][e] = fold[e * P + tid];
-                put8(part, col, D, dw[j]);
+                put_own(c, dw[j]);
             }
         } else {
-            put8(part, col, D, dw[j]);
+            put_own(c, dw[j]);
         }
     }
 }
@@ -354,6 +386,8 @@ hipError_t launch_t(const RmsLaunch& p, bool backward, hipStream_t s) {
 template <typename Tx, typename Tr>
 hipError_t launch_shape(const RmsLaunch& p, bool backward, hipStream_t s) {
     switch (p.threads * 10 + p.pieces) {
+        case 81: return launch_t<Tx, Tr, 8, 1>(p, backward, s);
+        case 321: return launch_t<Tx, Tr, 32, 1>(p, backward, s);
         case 641: return launch_t<Tx, Tr, 64, 1>(p, backward, s);
         case 642: return launch_t<Tx, Tr, 64, 2>(p, backward, s);
         case 646: return launch_t<Tx, Tr, 64, 6>(p, backward, s);

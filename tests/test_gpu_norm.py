@@ -173,6 +173,24 @@ def test_in_place_stream_and_graph(gpu):
         torch.randn(1 << 20, device="cuda").sum().item()
 
 
+@pytest.mark.parametrize("D", [9, 76, 311, 918, 1025, 2563, 4099])
+@pytest.mark.parametrize("types", TYPES, ids="/".join)
+def test_in_place_where_rows_end_inside_a_piece(gpu, types, D):
+    """The stream updated in place: every element read before it is written, also where two
+    threads read it."""
+    import torch
+    x, rs, w = data(D, 1200, D, types, True)
+    note(f"rms in place {types} {D}")
+    y, r = gpu.ss_rms_fwd(x, w, rs)
+    own = rs.clone()
+    y2, _ = gpu.ss_rms_fwd(x, w, own, r=own)
+    assert torch.equal(y, y2) and torch.equal(r, own)
+    dx, dw = gpu.ss_rms_bwd(y, r, w, rs)
+    own = rs.clone()
+    dx2, dw2 = gpu.ss_rms_bwd(y, r, w, own, dx=own)
+    assert torch.equal(dx, own) and dx2 is own and torch.equal(dw, dw2)
+
+
 def test_refusals(gpu):
     import torch
     x, rs, w = data(10, 4, 64, ("bf16", "bf16"), True)
