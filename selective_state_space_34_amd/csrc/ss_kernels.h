@@ -179,7 +179,8 @@ struct LaSweep {
     const float* s_in;         // nullable; element (i, j) of row-head bh, segment s at
     int64_t s_in_sz, s_in_i, s_in_j;   // (bh·in_seg + s)·s_in_sz + i·s_in_i + j·s_in_j
     int64_t in_seg;
-    float* s_out;              // nullable [B, H, dA, dC]; state_only: [B, H, nseg, dA, dC]
+    float* s_out;              // nullable [B, H, dA, dC] (s_out_t, with dots: [B, H, dC, dA]);
+    int s_out_t;               // state_only: [B, H, nseg, dA, dC]
     double* dots;              // nullable [tiles, B, H, T]
     float* seg_decay;          // state_only: [B, H, nseg]
     int64_t B, T, H;
@@ -189,11 +190,17 @@ struct LaSweep {
     float alpha, in_scale, up_scale;   // of a·b; of the entering state in out; of c in the state
     int pad_a, waves;
 };
+// n = 1 or 2 sweeps in one launch; two differ in operands, results and direction only, and
+// neither reads what the other writes.
+struct LaSweeps {
+    LaSweep p[2];
+    int n;
+};
 // all operands of aligned rows; any rows
-hipError_t launch_la_sweep_bf16(const LaSweep& p, hipStream_t s);
-hipError_t launch_la_sweep_bf16_any(const LaSweep& p, hipStream_t s);
-hipError_t launch_la_sweep_f32(const LaSweep& p, hipStream_t s);
-hipError_t launch_la_sweep_f32_any(const LaSweep& p, hipStream_t s);
+hipError_t launch_la_sweep_bf16(const LaSweeps& p, hipStream_t s);
+hipError_t launch_la_sweep_bf16_any(const LaSweeps& p, hipStream_t s);
+hipError_t launch_la_sweep_f32(const LaSweeps& p, hipStream_t s);
+hipError_t launch_la_sweep_f32_any(const LaSweeps& p, hipStream_t s);
 
 // State entering each segment, in place over what each segment adds: state [BH, nseg, sz].
 // first: nullable, element i·dC + j of row-head bh at bh·sz + i·f_i + j·f_j.
@@ -204,16 +211,20 @@ struct LaCarry {
     int64_t BH, sz, dC, f_i, f_j;
     int nseg, reverse;
 };
-hipError_t launch_la_carry(const LaCarry& p, hipStream_t s);
+struct LaCarries {             // n = 1 or 2 of the same sizes
+    LaCarry p[2];
+    int n;
+};
+hipError_t launch_la_carry(const LaCarries& p, hipStream_t s);
 
 // dg from the row and column sums and the states at the segments' borders: token [B, T, H]
 // (dg), or one value a head [H] through head_part [B, H, nseg].
 struct LaDecayGrad {
     const double *row, *col;   // [tiles, B, H, T]
     int tiles;
-    const float *fwd_state, *rev_state;   // [B, H, nseg, dv·dk] and [.., dk·dv]: the states that
-                                          // enter each segment from the left, from the right
-    const float *s0, *ds0, *ds, *s_final; // nullable; s_final [B, H, dv, dk], the others [.., dk, dv]
+    const float *fwd_state, *rev_state;   // [B, H, nseg, dv, dk]: the states that enter each
+                                          // segment from the left, from the right
+    const float *s0, *ds0, *ds, *s_final; // nullable [B, H, dk, dv]
     double* border;            // [B, H, nseg + 1]
     const int32_t* lengths;
     float* dg;
@@ -225,9 +236,14 @@ struct LaDecayGrad {
 };
 hipError_t launch_la_decay_grad(const LaDecayGrad& p, hipStream_t s);
 
-// out [BT, Hk, d] = sum of part [BT, Hk·rep, d] over the rep heads of each group, in order.
-hipError_t launch_la_group_sum(int bf16, const float* part, void* out, int64_t BT, int64_t Hk,
-                               int64_t rep, int64_t d, hipStream_t s);
+// Gradients of the shared key heads, dq and dk in turn: sums over the value heads of each,
+// part[x] [tokens, key heads, rep, d] float32 into out[x], n = tokens·key heads·d elements.
+struct LaGroupSum {
+    const float* part[2];
+    void* out[2];
+    int64_t n, rep, d;
+};
+hipError_t launch_la_group_sum(int bf16, const LaGroupSum& p, hipStream_t s);
 
 // One token: state [B, H, dk, dv] float32, s_out may be s_in.
 struct LaStep {

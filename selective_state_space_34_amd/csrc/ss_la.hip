@@ -19,7 +19,8 @@ __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(bf16_t* p, float v) { *p = round_bf16(v); }
 
 // S_{s+1} = decay_s·S_s + U_s over the segments, element by element: state holds U and gets S.
-__global__ __launch_bounds__(256) void la_carry_kernel(const LaCarry p) {
+__global__ __launch_bounds__(256) void la_carry_kernel(const LaCarries carries) {
+    const LaCarry& p = carries.p[blockIdx.y];
     const int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x;
     const int64_t bh = id / p.sz, x = id - bh * p.sz;
     if (bh >= p.BH) return;
@@ -54,41 +55,32 @@ __device__ __forceinline__ double block_sum(double v, double* part) {
 // not given); between them the states that enter the segments from either side.
 __global__ __launch_bounds__(256) void la_border_kernel(const LaDecayGrad p) {
     __shared__ double part[4];
-    __shared__ float tile[64][65];
     const int64_t bh = blockIdx.x / (p.nseg + 1);
     const int k = int(blockIdx.x - bh * (p.nseg + 1));
-    const int64_t sz = p.dk * p.dv;
-    const int tid = threadIdx.x, dk = int(p.dk), dv = int(p.dv);
+    const int sz = int(p.dk * p.dv), tid = threadIdx.x;
+    const float *r = p.ds0, *s = p.s0;
+    int64_t at_r = bh, at_s = bh;
+    if (k > 0 && k < p.nseg) {
+        r = p.rev_state; at_r = bh * p.nseg + k - 1;
+        s = p.fwd_state; at_s = bh * p.nseg + k;
+    } else if (k > 0) {
+        r = p.ds; s = p.s_final;
+    }
     double v = 0.0;
-    if (k == 0) {
-        if (p.ds0 && p.s0)
-            for (int64_t x = tid; x < sz; x += 256)
-                v += double(p.ds0[bh * sz + x]) * double(p.s0[bh * sz + x]);
-    } else if (k < p.nseg || (p.ds && p.s_final)) {
-        const float* r = k < p.nseg ? p.rev_state + (bh * p.nseg + k - 1) * sz : p.ds + bh * sz;
-        const float* s = k < p.nseg ? p.fwd_state + (bh * p.nseg + k) * sz : p.s_final + bh * sz;
-        // r is [dk, dv], s [dv, dk]: s by way of a tile in LDS, so that both are read by rows
-        for (int i0 = 0; i0 < dk; i0 += 64)
-            for (int j0 = 0; j0 < dv; j0 += 64) {
-                float a[16], c[16];
-                const int low = tid & 63, high = tid >> 6;
+    if (r && s) {
+        r += at_r * sz; s += at_s * sz;
+        for (int x0 = tid; x0 < sz; x0 += 16 * 256) {
+            float a[16], c[16];
 #pragma unroll
-                for (int x = 0; x < 16; ++x) {   // all in flight; what is outside is not used
-                    const int y = high + 4 * x;
-                    a[x] = s[min(j0 + y, dv - 1) * dk + min(i0 + low, dk - 1)];
-                    c[x] = r[min(i0 + y, dk - 1) * dv + min(j0 + low, dv - 1)];
-                }
-                __syncthreads();
-#pragma unroll
-                for (int x = 0; x < 16; ++x) tile[high + 4 * x][low] = a[x];
-                __syncthreads();
-#pragma unroll
-                for (int x = 0; x < 16; ++x) {
-                    const int i = high + 4 * x;
-                    const double y = double(c[x]) * double(tile[low][i]);
-                    v += i0 + i < dk && j0 + low < dv ? y : 0.0;
-                }
+            for (int i = 0; i < 16; ++i) {       // all in flight; what is outside is not used
+                const int x = min(x0 + i * 256, sz - 1);
+                a[i] = s[x];
+                c[i] = r[x];
             }
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                v += x0 + i * 256 < sz ? double(a[i]) * double(c[i]) : 0.0;
+        }
     }
     v = block_sum(v, part);
     if (tid == 0) p.border[blockIdx.x] = v;
@@ -177,16 +169,14 @@ __global__ __launch_bounds__(64) void la_head_sum_kernel(const LaDecayGrad p) {
 }
 
 template <typename T>
-__global__ __launch_bounds__(256) void la_group_sum_kernel(const float* __restrict__ part,
-                                                           T* __restrict__ out, int64_t n,
-                                                           int64_t rep, int64_t d) {
+__global__ __launch_bounds__(256) void la_group_sum_kernel(const LaGroupSum p) {
     const int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x;  // (token, key head, i)
-    if (id >= n) return;
-    const int64_t g = id / d, i = id - g * d;
-    const float* q = part + g * rep * d + i;
+    if (id >= p.n) return;
+    const int64_t g = id / p.d, i = id - g * p.d;
+    const float* q = p.part[blockIdx.y] + g * p.rep * p.d + i;
     float v = 0.0f;
-    for (int64_t r = 0; r < rep; ++r) v += q[r * d];
-    put(out + id, v);
+    for (int64_t r = 0; r < p.rep; ++r) v += q[r * p.d];
+    put(static_cast<T*>(p.out[blockIdx.y]) + id, v);
 }
 
 // One token.  S ← e^g S + k vᵀ, o = α Sᵀ q: every element of the state is read and written
@@ -285,8 +275,8 @@ hipError_t launch_step_type(const LaStep& p, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_la_carry(const LaCarry& p, hipStream_t s) {
-    const dim3 grid{unsigned((p.BH * p.sz + 255) / 256)};
+hipError_t launch_la_carry(const LaCarries& p, hipStream_t s) {
+    const dim3 grid{unsigned((p.p[0].BH * p.p[0].sz + 255) / 256), unsigned(p.n)};
     hipLaunchKernelGGL(la_carry_kernel, grid, dim3(256), 0, s, p);
     return hipGetLastError();
 }
@@ -303,14 +293,10 @@ hipError_t launch_la_decay_grad(const LaDecayGrad& p, hipStream_t s) {
     return hipGetLastError();
 }
 
-hipError_t launch_la_group_sum(int bf16, const float* part, void* out, int64_t BT, int64_t Hk,
-                               int64_t rep, int64_t d, hipStream_t s) {
-    const int64_t n = BT * Hk * d;
-    const dim3 grid{unsigned((n + 255) / 256)};
-    if (bf16) hipLaunchKernelGGL(la_group_sum_kernel<bf16_t>, grid, dim3(256), 0, s, part,
-                                 static_cast<bf16_t*>(out), n, rep, d);
-    else hipLaunchKernelGGL(la_group_sum_kernel<float>, grid, dim3(256), 0, s, part,
-                            static_cast<float*>(out), n, rep, d);
+hipError_t launch_la_group_sum(int bf16, const LaGroupSum& p, hipStream_t s) {
+    const dim3 grid{unsigned((p.n + 255) / 256), 2};
+    if (bf16) hipLaunchKernelGGL(la_group_sum_kernel<bf16_t>, grid, dim3(256), 0, s, p);
+    else hipLaunchKernelGGL(la_group_sum_kernel<float>, grid, dim3(256), 0, s, p);
     return hipGetLastError();
 }
 

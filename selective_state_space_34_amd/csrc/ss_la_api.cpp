@@ -13,6 +13,7 @@ using ss::hip_fail;
 using ss::LaOperand;
 using ss::LaPlan;
 using ss::LaSweep;
+using ss::LaSweeps;
 
 bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -55,8 +56,10 @@ Inputs inputs(const ss_la_dims* d, const LaPlan& p, const void* q, const void* k
                   operand(p, v, d->v_stride, p.H, p.dv)};
 }
 
-hipError_t sweep(const LaPlan& p, const LaSweep& s, hipStream_t stream) {
-    const bool vec = s.a.vec && s.b.vec && s.c.vec && s.e.vec;
+hipError_t sweep(const LaPlan& p, const LaSweeps& s, hipStream_t stream) {
+    bool vec = true;
+    for (int i = 0; i < s.n; ++i)
+        vec = vec && s.p[i].a.vec && s.p[i].b.vec && s.p[i].c.vec && s.p[i].e.vec;
     if (p.in_dtype == SS_BF16)
         return vec ? ss::launch_la_sweep_bf16(s, stream) : ss::launch_la_sweep_bf16_any(s, stream);
     return vec ? ss::launch_la_sweep_f32(s, stream) : ss::launch_la_sweep_f32_any(s, stream);
@@ -80,41 +83,51 @@ void shape(LaSweep* s, const ss::LaShape& f) {
     s->pad_a = f.pad_a; s->waves = f.waves; s->tiles = f.tiles;
 }
 
-// States entering every segment, [B, H, nseg, dA, dC], from the operands b, c of `s` and the
-// state that enters the whole sequence (element (i, j) at i·f_i + j·f_j; nullable).
-hipError_t segment_states(const LaPlan& p, LaSweep s, const ss::LaShape& f, const float* first,
-                          int64_t f_i, int64_t f_j, float* state, float* decay,
+// States entering every segment, [B, H, nseg, dA, dC] from where[i].state on, from the operands
+// b, c of each sweep and the state that enters the whole sequence (element (i, j) at
+// i·f_i + j·f_j; nullable).
+struct Entering {
+    float* state;
+    float* decay;
+    const float* first;
+    int64_t f_i, f_j;
+};
+hipError_t segment_states(const LaPlan& p, LaSweeps w, const ss::LaShape& f, const Entering* where,
                           hipStream_t stream) {
     const int64_t sz = p.dk * p.dv;
-    shape(&s, f);
-    s.state_only = 1;
-    s.a = s.b; s.e = s.b;
-    s.grid_seg = s.nseg - 1; s.seg0 = s.reverse ? 1 : 0;
-    s.s_in = nullptr; s.in_seg = 1; s.s_in_sz = sz;
-    s.s_out = state; s.seg_decay = decay;
-    s.dots = nullptr; s.out = nullptr;
-    const hipError_t e = sweep(p, s, stream);
-    if (e != hipSuccess) return e;
-    ss::LaCarry c{};
-    c.state = state; c.decay = decay; c.first = first; c.BH = p.B * p.H; c.sz = sz;
-    c.dC = s.c.dim; c.f_i = f_i; c.f_j = f_j; c.nseg = s.nseg; c.reverse = s.reverse;
-    return ss::launch_la_carry(c, stream);
+    ss::LaCarries c{};
+    c.n = w.n;
+    for (int i = 0; i < w.n; ++i) {
+        LaSweep& s = w.p[i];
+        const Entering& e = where[i];
+        shape(&s, f);
+        s.state_only = 1;
+        s.a = s.b; s.e = s.b;
+        s.grid_seg = s.nseg - 1; s.seg0 = s.reverse ? 1 : 0;
+        s.s_in = nullptr; s.in_seg = 1; s.s_in_sz = sz;
+        s.s_out = e.state;
+        s.seg_decay = e.decay;
+        s.dots = nullptr; s.out = nullptr;
+        ss::LaCarry& t = c.p[i];
+        t.state = e.state; t.decay = e.decay; t.first = e.first; t.BH = p.B * p.H; t.sz = sz;
+        t.dC = s.c.dim; t.f_i = e.f_i; t.f_j = e.f_j; t.nseg = s.nseg; t.reverse = s.reverse;
+    }
+    const hipError_t e = sweep(p, w, stream);
+    return e == hipSuccess ? ss::launch_la_carry(c, stream) : e;
 }
 
-// The whole sweep: state [dA, dC] enters each segment from `state` (nseg > 1) or from `first`;
-// strides as element (i, j).
-hipError_t full_sweep(const LaPlan& p, LaSweep s, const ss::LaShape& f, const float* first,
-                      int64_t f_i, int64_t f_j, const float* state, int64_t s_i, int64_t s_j,
-                      hipStream_t stream) {
-    shape(&s, f);
-    s.grid_seg = s.nseg; s.seg0 = 0;
-    s.s_in_sz = p.dk * p.dv;
-    if (s.nseg > 1) {
-        s.s_in = state; s.in_seg = s.nseg; s.s_in_i = s_i; s.s_in_j = s_j;
+// What is common to whole sweeps: the state [dA, dC] enters each segment from `state` (nseg > 1)
+// or from `first`; strides as element (i, j).
+void whole(const LaPlan& p, LaSweep* s, const ss::LaShape& f, const float* first, int64_t f_i,
+           int64_t f_j, const float* state, int64_t s_i, int64_t s_j) {
+    shape(s, f);
+    s->grid_seg = s->nseg; s->seg0 = 0;
+    s->s_in_sz = p.dk * p.dv;
+    if (s->nseg > 1) {
+        s->s_in = state; s->in_seg = s->nseg; s->s_in_i = s_i; s->s_in_j = s_j;
     } else {
-        s.s_in = first; s.in_seg = 1; s.s_in_i = f_i; s.s_in_j = f_j;
+        s->s_in = first; s->in_seg = 1; s->s_in_i = f_i; s->s_in_j = f_j;
     }
-    return sweep(p, s, stream);
 }
 
 int workspace_size(const ss_la_dims* dims, bool backward, size_t* bytes) {
@@ -160,16 +173,20 @@ int ss_la_fwd(const ss_la_dims* dims, const void* q, const void* k, const void* 
     char* ws = static_cast<char*>(workspace);
     float* state = reinterpret_cast<float*>(ws + p.off_state);
     const Inputs in = inputs(dims, p, q, k, v);
-    LaSweep s = base(p, g, lengths, 0);
+    LaSweeps w{};
+    w.n = 1;
+    LaSweep& s = w.p[0];
+    s = base(p, g, lengths, 0);
     s.a = in.q; s.b = in.k; s.c = in.v; s.e = in.v;
     hipError_t e;
     if (p.nseg > 1) {
-        e = segment_states(p, s, p.fwd, s0, p.dv, 1, state,
-                           reinterpret_cast<float*>(ws + p.off_decay), stream);
+        const Entering where{state, reinterpret_cast<float*>(ws + p.off_decay), s0, p.dv, 1};
+        e = segment_states(p, w, p.fwd, &where, stream);
         if (e != hipSuccess) return hip_fail(e);
     }
     s.out = o; s.s_out = s_final;
-    e = full_sweep(p, s, p.fwd, s0, p.dv, 1, state, p.dv, 1, stream);
+    whole(p, &s, p.fwd, s0, p.dv, 1, state, p.dv, 1);
+    e = sweep(p, w, stream);
     return e == hipSuccess ? SS_OK : hip_fail(e);
 }
 
@@ -198,49 +215,50 @@ int ss_la_bwd(const ss_la_dims* dims, const void* q, const void* k, const void* 
     const int bf16 = p.in_dtype == SS_BF16;
     const Inputs in = inputs(dims, p, q, k, v);
     const LaOperand od = operand(p, dO, nullptr, p.H, p.dv);
+    float* part2 = p.Hk < p.H ? at(p.off_part2) : nullptr;
+    float* rstate = at(p.off_rstate);
     hipError_t e;
 
-    // 1. dq: forward sweep of (dO, v, k), state S_tᵀ [dv, dk]
-    LaSweep s = base(p, g, lengths, 0);
-    s.a = od; s.b = in.v; s.c = in.k; s.e = in.q;
+    // 1. the segments' states, S_tᵀ forward and dS_tᵀ reverse, both [dv, dk]
+    LaSweeps w{};
+    w.n = 2;
+    LaSweep &f = w.p[0], &r = w.p[1];
+    f = base(p, g, lengths, 0);
+    f.a = od; f.b = in.v; f.c = in.k; f.e = in.q;
+    r = base(p, g, lengths, 1);
+    r.a = in.v; r.b = od; r.c = in.q; r.e = in.k;
     if (p.nseg > 1) {
-        e = segment_states(p, s, p.rev, s0, 1, p.dv, state, decay, stream);
-        if (e != hipSuccess) return hip_fail(e);
-    }
-    s.out = part ? static_cast<void*>(part) : dq; s.out_f32 = part != nullptr;
-    s.dots = g ? dots(p.off_row) : nullptr;
-    s.s_out = s_final;
-    e = full_sweep(p, s, p.rev, s0, 1, p.dv, state, p.dk, 1, stream);
-    if (e != hipSuccess) return hip_fail(e);
-    if (part) {
-        e = ss::launch_la_group_sum(bf16, part, dq, p.B * p.T, p.Hk, p.H / p.Hk, p.dk, stream);
+        const Entering where[2] = {{state, decay, s0, 1, p.dv},
+                                   {rstate, at(p.off_rdecay), ds_final, 1, p.dv}};
+        e = segment_states(p, w, p.rev, where, stream);
         if (e != hipSuccess) return hip_fail(e);
     }
 
-    // 2. dv: reverse sweep of (k, q, dO), state dS_t [dk, dv]; its segments' states serve dk too
-    float* rstate = at(p.off_rstate);
+    // 2. dq: forward sweep of (dO, v, k); dk: reverse sweep of (v, dO, q)
+    f.out = part ? static_cast<void*>(part) : dq; f.out_f32 = part != nullptr;
+    f.dots = g ? dots(p.off_row) : nullptr;
+    f.s_out = s_final; f.s_out_t = 1;
+    whole(p, &f, p.rev, s0, 1, p.dv, state, p.dk, 1);
+    r.out = part2 ? static_cast<void*>(part2) : dk; r.out_f32 = part2 != nullptr;
+    r.dots = g ? dots(p.off_col) : nullptr;
+    whole(p, &r, p.rev, ds_final, 1, p.dv, rstate, p.dk, 1);
+    e = sweep(p, w, stream);
+    if (e != hipSuccess) return hip_fail(e);
+    if (part) {
+        const ss::LaGroupSum gs{{part, part2}, {dq, dk}, p.B * p.T * p.Hk * p.dk, p.H / p.Hk, p.dk};
+        e = ss::launch_la_group_sum(bf16, gs, stream);
+        if (e != hipSuccess) return hip_fail(e);
+    }
+
+    // 3. dv: reverse sweep of (k, q, dO) with the state transposed, dS_t [dk, dv]
+    w.n = 1;
+    LaSweep& s = w.p[0];
     s = base(p, g, lengths, 1);
     s.a = in.k; s.b = in.q; s.c = od; s.e = od;
-    if (p.nseg > 1) {
-        e = segment_states(p, s, p.fwd, ds_final, p.dv, 1, rstate, decay, stream);
-        if (e != hipSuccess) return hip_fail(e);
-    }
-    s.out = dv;
-    s.s_out = ds0;
-    e = full_sweep(p, s, p.fwd, ds_final, p.dv, 1, rstate, p.dv, 1, stream);
+    s.out = dv; s.s_out = ds0;
+    whole(p, &s, p.fwd, ds_final, p.dv, 1, rstate, 1, p.dk);
+    e = sweep(p, w, stream);
     if (e != hipSuccess) return hip_fail(e);
-
-    // 3. dk: reverse sweep of (v, dO, q), state dS_tᵀ [dv, dk], read transposed
-    s = base(p, g, lengths, 1);
-    s.a = in.v; s.b = od; s.c = in.q; s.e = in.k;
-    s.out = part ? static_cast<void*>(part) : dk; s.out_f32 = part != nullptr;
-    s.dots = g ? dots(p.off_col) : nullptr;
-    e = full_sweep(p, s, p.rev, ds_final, 1, p.dv, rstate, 1, p.dv, stream);
-    if (e != hipSuccess) return hip_fail(e);
-    if (part) {
-        e = ss::launch_la_group_sum(bf16, part, dk, p.B * p.T, p.Hk, p.H / p.Hk, p.dk, stream);
-        if (e != hipSuccess) return hip_fail(e);
-    }
 
     // 4. dg from the row and column sums and the states at the segments' borders
     if (g) {

@@ -2,7 +2,7 @@
 #include "ss_la_sweep.h"
 
 namespace ss {
-hipError_t launch_la_sweep_bf16_any(const LaSweep& p, hipStream_t s) {
+hipError_t launch_la_sweep_bf16_any(const LaSweeps& p, hipStream_t s) {
     return la::launch_sweep_type<bf16_t, false>(p, s);
 }
 }  // namespace ss

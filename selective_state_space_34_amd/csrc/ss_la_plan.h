@@ -26,9 +26,11 @@ constexpr int64_t kLaMaxDim = 256;
 inline int64_t la_chunk(int in_dtype) { return in_dtype == SS_BF16 ? 64 : 32; }
 
 // Workgroups of a sweep that the 256 CUs hold at once, by the waves a SIMD that its registers
-// allow; dots: the sweeps that also give the sums behind dg.
-inline int64_t la_round(const LaShape& s, bool dots) {
-    const int waves = s.pad_a == 64 && !dots ? 4 : s.pad_a == 256 && s.waves == 4 ? 1 : 2;
+// and LDS allow (four workgroups of four waves would need 188 KB of it in bf16); dots: the
+// sweeps that also give the sums behind dg.
+inline int64_t la_round(const LaShape& s, bool dots, int in_dtype) {
+    const int small = in_dtype == SS_BF16 && s.waves == 4 ? 3 : 4;
+    const int waves = s.pad_a == 64 && !dots ? small : s.pad_a == 256 && s.waves == 4 ? 1 : 2;
     return 256 * (4 * waves / s.waves);
 }
 
@@ -51,14 +53,14 @@ struct LaPlan {
     int64_t nseg, seg_chunks;
     // forward: off_state [B, H, nseg, dk·dv], off_decay [B, H, nseg] (nseg > 1)
     // backward: the same for the forward direction, and
-    //   off_rstate         [B, H, nseg, dk·dv] of the reverse direction (nseg > 1)
+    //   off_rstate, off_rdecay   the same of the reverse direction (nseg > 1)
     //   off_row, off_col   [rev.tiles, B, H, T] row and column sums behind dg (64 bits)
-    //   off_final          [B, H, dv·dk] S_Tᵀ
+    //   off_final          [B, H, dk, dv] S_T
     //   off_border         [B, H, nseg + 1] (64 bits) <adjoint, state> at the segments' borders
     //   off_head           [B, H, nseg] (64 bits) dg summed over a segment (one decay a head)
-    //   off_part           [B, T, H, dk] float32 dq, then dk, of each value head (Hk < H)
-    size_t off_state, off_decay, off_rstate, off_row, off_col, off_final, off_border, off_head, off_part,
-        total;
+    //   off_part, off_part2      [B, T, H, dk] float32 dq and dk of each value head (Hk < H)
+    size_t off_state, off_decay, off_rstate, off_rdecay, off_row, off_col, off_final, off_border,
+        off_head, off_part, off_part2, total;
 };
 
 // q, k, v strides: all zero means dense; otherwise each must be >= 0.
@@ -93,9 +95,9 @@ inline int make_la_plan(const ss_la_dims& d, bool backward, LaPlan* out) {
     p.rev = la_shape(p.dv, p.dk);
     const int64_t bh = p.B * p.H;
     const int most = p.rev.tiles > p.fwd.tiles ? p.rev.tiles : p.fwd.tiles;
-    int64_t n = la_round(p.fwd, false) / (bh * p.fwd.tiles);
+    int64_t n = la_round(p.fwd, false, p.in_dtype) / (bh * p.fwd.tiles);
     if (backward) {
-        const int64_t r = la_round(p.rev, p.decay != SS_LA_DECAY_NONE) / (bh * p.rev.tiles);
+        const int64_t r = la_round(p.rev, p.decay != SS_LA_DECAY_NONE, p.in_dtype) / (bh * p.rev.tiles);
         n = r < n ? r : n;
     }
     // the gradient's borders are exact, so there short segments are a gain in themselves
@@ -114,14 +116,17 @@ inline int make_la_plan(const ss_la_dims& d, bool backward, LaPlan* out) {
     if (backward) {
         p.off_rstate = off;
         if (p.nseg > 1) off = align256(off + size_t(p.nseg) * state);
+        p.off_rdecay = off;
+        if (p.nseg > 1) off = align256(off + size_t(bh * p.nseg) * f);
         const size_t dots = size_t(p.rev.tiles) * size_t(bh) * size_t(p.T) * sizeof(double);
         p.off_row = off; off = align256(off + dots);
         p.off_col = off; off = align256(off + dots);
         p.off_final = off; off = align256(off + state);
         p.off_border = off; off = align256(off + size_t(bh * (p.nseg + 1)) * sizeof(double));
         p.off_head = off; off = align256(off + size_t(bh * p.nseg) * sizeof(double));
-        p.off_part = off;
-        if (p.Hk < p.H) off = align256(off + size_t(bh) * size_t(p.T) * size_t(p.dk) * f);
+        const size_t part = p.Hk < p.H ? size_t(bh) * size_t(p.T) * size_t(p.dk) * f : 0;
+        p.off_part = off; off = align256(off + part);
+        p.off_part2 = off; off = align256(off + part);
     }
     p.total = off;
     *out = p;

@@ -344,10 +344,10 @@ __device__ __forceinline__ uint32_t not_finite(f32x8 f, uint32_t seen) {
 // where the state, the rows in flight and the products fit 128 registers; at 128 state rows they
 // would spill 18 of them, and two workgroups a CU were no faster than one after the other
 // (B = 4, T = 2048, H = 16, 128 x 128: 47 us with four waves, 44 with two on half the segments).
-constexpr int sweep_occupancy(bool vec, int DA, int NW, bool dot, bool state) {
+constexpr int sweep_occupancy(int el, bool vec, int DA, int NW, bool dot, bool state) {
     if (DA == 256 && NW == 4 && !state) return 1;
     if (state) return DA == 256 ? 2 : 4;
-    return DA > 64 || dot || !vec ? 2 : 4;
+    return DA > 64 || dot || !vec ? 2 : el == 2 && NW == 4 ? 3 : 4;
 }
 
 // kState: only the state that a segment adds from zero, and the segment's decay (the first of
@@ -356,7 +356,8 @@ constexpr int sweep_occupancy(bool vec, int DA, int NW, bool dot, bool state) {
 // sums and in the column sums, so what enters one and leaves the other cancels exactly in the
 // running sum of dg.
 template <typename T, bool kVec, int DA, int NW, bool kDot, bool kState>
-__global__ __launch_bounds__(64 * NW, sweep_occupancy(kVec, DA, NW, kDot, kState)) void sweep_kernel(const LaSweep p) {
+__global__ __launch_bounds__(64 * NW, sweep_occupancy(int(sizeof(T)), kVec, DA, NW, kDot, kState)) void sweep_kernel(const LaSweeps sweeps) {
+    const LaSweep& p = sweeps.p[blockIdx.y];
     using M = Mma<T>;
     using Frag = typename M::Frag;
     using Elem = typename M::Elem;
@@ -761,6 +762,7 @@ __global__ __launch_bounds__(64 * NW, sweep_occupancy(kVec, DA, NW, kDot, kState
     // ---- the state this segment leaves ---------------------------------------------------------------
     const bool last = kState || (rev ? seg == 0 : seg == p.nseg - 1);
     if (p.s_out && last) {
+        const int out_i = kDot && p.s_out_t ? 1 : p.c.dim, out_j = kDot && p.s_out_t ? p.b.dim : 1;
         float* so = p.s_out + (bh * (kState ? p.nseg : 1) + (kState ? seg : 0)) * p.s_in_sz;
         const __amdgpu_buffer_rsrc_t d = __builtin_amdgcn_make_buffer_rsrc(so, 0, state_bytes, kRsrcFlags);
 #pragma unroll
@@ -770,33 +772,34 @@ __global__ __launch_bounds__(64 * NW, sweep_occupancy(kVec, DA, NW, kDot, kState
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                     __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[ib][u][r]), d,
-                                                          state_at(ib, u, r, p.c.dim, 1), 0, 0);
+                                                          state_at(ib, u, r, out_i, out_j), 0, 0);
     }
     if (kState && tile == 0 && tid == NT - 64)
         p.seg_decay[bh * p.nseg + seg] = seg_nan ? __builtin_nanf("") : exp2_fixed(seg_sum);
 }
 
 template <typename T, bool kVec, int DA, int NW>
-hipError_t launch_sweep_t(const LaSweep& p, hipStream_t s) {
+hipError_t launch_sweep_t(const LaSweeps& w, hipStream_t s) {
+    const LaSweep& p = w.p[0];
     const int64_t blocks = int64_t(p.tiles) * p.H * p.grid_seg * p.B;
     if (blocks <= 0) return hipSuccess;
-    const dim3 grid{unsigned(blocks)}, block(64 * NW);
-    if (p.state_only) hipLaunchKernelGGL((sweep_kernel<T, kVec, DA, NW, false, true>), grid, block, 0, s, p);
-    else if (p.dots) hipLaunchKernelGGL((sweep_kernel<T, kVec, DA, NW, true, false>), grid, block, 0, s, p);
-    else hipLaunchKernelGGL((sweep_kernel<T, kVec, DA, NW, false, false>), grid, block, 0, s, p);
+    const dim3 grid{unsigned(blocks), unsigned(w.n)}, block(64 * NW);
+    if (p.state_only) hipLaunchKernelGGL((sweep_kernel<T, kVec, DA, NW, false, true>), grid, block, 0, s, w);
+    else if (p.dots) hipLaunchKernelGGL((sweep_kernel<T, kVec, DA, NW, true, false>), grid, block, 0, s, w);
+    else hipLaunchKernelGGL((sweep_kernel<T, kVec, DA, NW, false, false>), grid, block, 0, s, w);
     return hipGetLastError();
 }
 
 template <typename T, bool kVec>
-hipError_t launch_sweep_type(const LaSweep& p, hipStream_t s) {
-    const int key = p.pad_a * 10 + p.waves;
+hipError_t launch_sweep_type(const LaSweeps& w, hipStream_t s) {
+    const int key = w.p[0].pad_a * 10 + w.p[0].waves;
     switch (key) {
-        case 644: return launch_sweep_t<T, kVec, 64, 4>(p, s);
-        case 648: return launch_sweep_t<T, kVec, 64, 8>(p, s);
-        case 1284: return launch_sweep_t<T, kVec, 128, 4>(p, s);
-        case 1288: return launch_sweep_t<T, kVec, 128, 8>(p, s);
-        case 2564: return launch_sweep_t<T, kVec, 256, 4>(p, s);
-        case 2568: return launch_sweep_t<T, kVec, 256, 8>(p, s);
+        case 644: return launch_sweep_t<T, kVec, 64, 4>(w, s);
+        case 648: return launch_sweep_t<T, kVec, 64, 8>(w, s);
+        case 1284: return launch_sweep_t<T, kVec, 128, 4>(w, s);
+        case 1288: return launch_sweep_t<T, kVec, 128, 8>(w, s);
+        case 2564: return launch_sweep_t<T, kVec, 256, 4>(w, s);
+        case 2568: return launch_sweep_t<T, kVec, 256, 8>(w, s);
         default: return hipErrorInvalidValue;
     }
 }
