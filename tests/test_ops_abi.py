@@ -184,10 +184,10 @@ def test_workspaces(lib):
         assert f == 0 or any(f == a256(n * state) + a256(B * H * n * 4) for n in range(2, 1025))
         tiles = -(-dk // (64 if dk <= 64 else 128))
         part = a256(B * H * T * dk * 4) if Hk < H else 0
-        fixed = 2 * a256(tiles * B * H * T * 8) + a256(state) + part
+        fixed = 2 * a256(tiles * B * H * T * 8) + a256(state) + 2 * part
 
         def whole(n):
-            seg = 2 * a256(n * state) + a256(B * H * n * 4) if n > 1 else 0
+            seg = 2 * (a256(n * state) + a256(B * H * n * 4)) if n > 1 else 0
             return fixed + seg + a256(B * H * (n + 1) * 8) + a256(B * H * n * 8)
         assert any(b == whole(n) for n in range(1, 1025)), (B, T, H, dk, dv)
         n = ctypes.c_size_t()
