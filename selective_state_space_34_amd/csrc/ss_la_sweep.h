@@ -355,9 +355,9 @@ constexpr int sweep_occupancy(int el, bool vec, int DA, int NW, bool dot, bool s
 // the diagonal.  Its pairs are summed in 64 bits: a pair's value has the same bits in the row
 // sums and in the column sums, so what enters one and leaves the other cancels exactly in the
 // running sum of dg.
-template <typename T, bool kVec, int DA, int NW, bool kDot, bool kState>
+template <typename T, bool kVec, int DA, int NW, bool kDot, bool kState, bool kPair>
 __global__ __launch_bounds__(64 * NW, sweep_occupancy(int(sizeof(T)), kVec, DA, NW, kDot, kState)) void sweep_kernel(const LaSweeps sweeps) {
-    const LaSweep& p = sweeps.p[blockIdx.y];
+    const LaSweep& p = sweeps.p[kPair ? blockIdx.y : 0];
     using M = Mma<T>;
     using Frag = typename M::Frag;
     using Elem = typename M::Elem;
@@ -783,10 +783,23 @@ hipError_t launch_sweep_t(const LaSweeps& w, hipStream_t s) {
     const LaSweep& p = w.p[0];
     const int64_t blocks = int64_t(p.tiles) * p.H * p.grid_seg * p.B;
     if (blocks <= 0) return hipSuccess;
+    if (w.n == 2 && !p.state_only && !p.dots) {   // no pair instance: gradients without decays
+        LaSweeps one = w;
+        one.n = 1;
+        const hipError_t e = launch_sweep_t<T, kVec, DA, NW>(one, s);
+        if (e != hipSuccess) return e;
+        one.p[0] = w.p[1];
+        return launch_sweep_t<T, kVec, DA, NW>(one, s);
+    }
     const dim3 grid{unsigned(blocks), unsigned(w.n)}, block(64 * NW);
-    if (p.state_only) hipLaunchKernelGGL((sweep_kernel<T, kVec, DA, NW, false, true>), grid, block, 0, s, w);
-    else if (p.dots) hipLaunchKernelGGL((sweep_kernel<T, kVec, DA, NW, true, false>), grid, block, 0, s, w);
-    else hipLaunchKernelGGL((sweep_kernel<T, kVec, DA, NW, false, false>), grid, block, 0, s, w);
+    if (p.state_only && w.n == 2)
+        hipLaunchKernelGGL((sweep_kernel<T, kVec, DA, NW, false, true, true>), grid, block, 0, s, w);
+    else if (p.state_only)
+        hipLaunchKernelGGL((sweep_kernel<T, kVec, DA, NW, false, true, false>), grid, block, 0, s, w);
+    else if (p.dots)
+        hipLaunchKernelGGL((sweep_kernel<T, kVec, DA, NW, true, false, true>), grid, block, 0, s, w);
+    else
+        hipLaunchKernelGGL((sweep_kernel<T, kVec, DA, NW, false, false, false>), grid, block, 0, s, w);
     return hipGetLastError();
 }
 
