@@ -13,7 +13,10 @@
 // rows in turn, so that in the gradient the columns' sums stay in registers over a workgroup's
 // rows; the sums of dw over workgroups are added by a second kernel in a fixed order.  w is
 // read for every row (it stays in the CU's cache): holding it too would cost 8·NV registers
-// and with them the waves that keep loads in flight.
+// and with them the waves that keep loads in flight.  All loads of a row are issued before the
+// first is used, and kept as they lie until then: bf16, D = 2560, 16384 rows with a residual and
+// 8-bit output 89 us became 56 (5.2 TB/s, the rate of a copy).  The gradient of the same rows
+// takes 72 us and the sum of dw over workgroups 5.
 #include "ss_device.h"
 #include "ss_kernels.h"
 
