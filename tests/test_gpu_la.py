@@ -175,6 +175,33 @@ def test_backward(gpu, case, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(2, 700, 4, 2, 64, 128), (1, 500, 2, 2, 200, 72)])
+def test_segments_without_decays(gpu, shape, dtype):
+    """Several segments and no decays: dq and dk one launch each."""
+    c = make(23, *shape, dtype, "none", True)
+    note(f"la segments without decays {shape} {dtype}")
+    check_fwd(c, *run_fwd(gpu, c))
+    check_bwd(c, run_bwd(gpu, c))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("odd", ["q", "k", "v"])
+def test_one_operand_off_its_alignment(gpu, odd, dtype):
+    """One of q, k, v in rows that start anywhere, the others on 16 bytes, over segments."""
+    import torch
+    c = make(24, 2, 330, 2, 1, 64, 128, dtype, "token", True)
+    t = dev(c)
+    x = t[odd]
+    wide = torch.full((*x.shape[:3], x.shape[3] + 3), float("nan"), dtype=x.dtype, device=x.device)
+    wide[..., 1:-2] = x
+    t[odd] = wide[..., 1:-2]
+    note(f"la {odd} off its alignment {dtype}")
+    o, last = gpu.ss_la_fwd(t["q"], t["k"], t["v"], t["g"], t["s0"], scale=c["scale"], return_final=True)
+    check_fwd(c, o, last)
+    check_bwd(c, gpu.ss_la_bwd(t["q"], t["k"], t["v"], t["do"], t["g"], t["s0"], t["ds"], scale=c["scale"]))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_hard_decays(gpu, dtype):
     """Cuts (-inf, the lowest float32), no decay and underflowing steps inside every chunk."""
     c = make(5, 2, 261, 4, 2, 32, 48, dtype, "token", True, None, hard=True)
