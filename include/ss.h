@@ -265,7 +265,8 @@ int ss_step(const ss_dims* dims,
  *   lengths : NULL, or [B] int32 on the device: row b has lengths[b] tokens (clamped to
  *          [0, T]).  What the places behind hold is not used; o and the gradients are 0 there.
  * q, k and v may be strided: dims.*_stride are elements from batch row to batch row, token to
- * token and head to head (the last axis is contiguous); all three 0 means dense.  They need
+ * token and head to head (the last axis is contiguous); all three 0 means dense.  Rows may be
+ * shared (a stride of 0) or overlap; with one token its stride is not used.  They need
  * only their type's alignment, g and lengths 4 bytes; every other pointer 16 bytes.  Rows that
  * start on 16 bytes and hold whole 16-byte pieces load fastest.  States, sums and log decays
  * are kept in float32 or more; bfloat16 products round the scores and the state once where

@@ -26,11 +26,15 @@ LaOperand operand(const LaPlan& p, const void* ptr, const int64_t* stride, int64
     if (stride && (stride[0] || stride[1] || stride[2])) {
         o.sb = stride[0]; o.st = stride[1]; o.sh = stride[2];
     }
+    if (p.T == 1) o.st = dim;   // a single token's stride says nothing
     o.rep = p.H / heads;
     o.dim = int(dim);
+    // Tokens that share memory (an expanded or overlapping operand) take the rows whose loads ask
+    // for each token whether it exists: the other kind takes its bounds from the end of the chunk's
+    // last row, behind which the next tokens begin only where a row is no longer than its stride.
     const int64_t v = p.in_dtype == SS_BF16 ? 8 : 4;
     o.vec = aligned(ptr, 16) && o.sb % v == 0 && o.st % v == 0 && o.sh % v == 0 && dim % v == 0 &&
-            o.st < (int64_t(1) << 22);
+            o.st >= dim && o.st < (int64_t(1) << 22);
     return o;
 }
 
