@@ -269,8 +269,8 @@ int ss_step(const ss_dims* dims,
  * shared (a stride of 0) or overlap; with one token its stride is not used.  They need
  * only their type's alignment, g and lengths 4 bytes; every other pointer 16 bytes.  Rows that
  * start on 16 bytes and hold whole 16-byte pieces load fastest.  States, sums and log decays
- * are kept in float32 or more; bfloat16 products round the scores and the state once where
- * they feed o, dq, dk, dv (never where they feed s_final, ds0 or dg). */
+ * are kept in float32 or more; bfloat16 products hold scores and states to 16 bits where they feed
+ * o, dq, dk, dv (which are rounded to 8) and to all 24 where they feed s_final, ds0 or dg. */
 typedef enum { SS_LA_DECAY_NONE = 0, SS_LA_DECAY_HEAD = 1, SS_LA_DECAY_TOKEN = 2 } ss_la_decay;
 
 typedef struct ss_la_dims {
