@@ -278,7 +278,8 @@ typedef struct ss_la_dims {
     int64_t seqlen;       /* T >= 1 */
     int64_t heads;        /* H: value heads */
     int64_t kheads;       /* Hk: query and key heads, H % Hk == 0 */
-    int64_t dk, dv;       /* 1 .. 256; H · max(dk, dv) < 2^22 */
+    int64_t dk, dv;       /* 1 .. 256; H · max(dk, dv) < 2^22; B · H < 2^22, in the step with
+                             dv % 4 != 0 also B · H · ceil(dv / 32) < 2^24 */
     int64_t q_stride[3];  /* batch row, token, head; all 0: dense */
     int64_t k_stride[3];
     int64_t v_stride[3];
@@ -358,7 +359,7 @@ int ss_rms_bwd(const ss_rms_dims* dims, const void* dy, const void* r, const flo
  *   y      [rows, n] y_dtype, rounded once; sums are float32
  * Needs no workspace. */
 typedef struct ss_q4_dims {
-    int64_t rows, n, k;   /* k a multiple of 32 */
+    int64_t rows, n, k;   /* k a multiple of 32; n <= 2^28 - 32 */
     int32_t group;        /* 32, 64 or 128; the last group may be short */
     int32_t in_dtype;     /* ss_dtype of x (not used with x_q8) */
     int32_t x_q8;         /* ss_q8 of x */

@@ -255,6 +255,7 @@ struct LaStep {
     float* s_out;
     void* o;                   // [B, H, dv], the operands' type
     int64_t B, H, dk, dv;
+    int columns;               // of a workgroup: 128, 32
     float scale;
 };
 hipError_t launch_la_step(int bf16, const LaStep& p, hipStream_t s);

@@ -172,13 +172,14 @@ __global__ __launch_bounds__(64) void la_head_sum_kernel(const LaDecayGrad p) {
 
 template <typename T>
 __global__ __launch_bounds__(256) void la_group_sum_kernel(const LaGroupSum p) {
-    const int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x;  // (token, key head, i)
-    if (id >= p.n) return;
-    const int64_t g = id / p.d, i = id - g * p.d;
-    const float* q = p.part[blockIdx.y] + g * p.rep * p.d + i;
-    float v = 0.0f;
-    for (int64_t r = 0; r < p.rep; ++r) v += q[r * p.d];
-    put(static_cast<T*>(p.out[blockIdx.y]) + id, v);
+    const int64_t step = int64_t(gridDim.x) * 256;
+    for (int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x; id < p.n; id += step) {   // (token, key head, i)
+        const int64_t g = id / p.d, i = id - g * p.d;
+        const float* q = p.part[blockIdx.y] + g * p.rep * p.d + i;
+        float v = 0.0f;
+        for (int64_t r = 0; r < p.rep; ++r) v += q[r * p.d];
+        put(static_cast<T*>(p.out[blockIdx.y]) + id, v);
+    }
 }
 
 // One token.  S ← e^g S + k vᵀ, o = α Sᵀ q: every element of the state is read and written
@@ -268,12 +269,8 @@ hipError_t launch_step_slab(const LaStep& p, hipStream_t s) {
 
 template <typename T>
 hipError_t launch_step_type(const LaStep& p, hipStream_t s) {
-    // four columns a thread where rows keep 16-byte alignment
-    if (p.dv % 4 == 0) {
-        if (p.B * p.H >= 512) return launch_step_slab<T, 32, 4>(p, s);
-        return launch_step_slab<T, 8, 4>(p, s);
-    }
-    return launch_step_slab<T, 32, 1>(p, s);
+    if (p.columns == 128) return launch_step_slab<T, 32, 4>(p, s);
+    return p.dv % 4 == 0 ? launch_step_slab<T, 8, 4>(p, s) : launch_step_slab<T, 32, 1>(p, s);
 }
 
 }  // namespace
@@ -297,7 +294,9 @@ hipError_t launch_la_decay_grad(const LaDecayGrad& p, hipStream_t s) {
 }
 
 hipError_t launch_la_group_sum(int bf16, const LaGroupSum& p, hipStream_t s) {
-    const dim3 grid{unsigned((p.n + 255) / 256), 2};
+    // a launch takes fewer than 2^32 threads: beyond 2^31 elements each takes several
+    const int64_t need = (p.n + 255) / 256, most = int64_t(1) << 23;
+    const dim3 grid{unsigned(need < most ? need : most), 2};
     if (bf16) hipLaunchKernelGGL(la_group_sum_kernel<bf16_t>, grid, dim3(256), 0, s, p);
     else hipLaunchKernelGGL(la_group_sum_kernel<float>, grid, dim3(256), 0, s, p);
     return hipGetLastError();

@@ -288,13 +288,15 @@ int ss_la_step(const ss_la_dims* dims, const void* q, const void* k, const void*
     LaPlan p;
     const int rc = check(dims, false, q, k, v, g, nullptr, &p);
     if (rc != SS_OK) return rc;
+    const int columns = ss::la_step_columns(p.B * p.H, p.dv);
+    if (!ss::launch_ok(p.B * p.H * ((p.dv + columns - 1) / columns), 256)) return SS_ERR_DIMS;
     if (!s_in || !s_out || !o) return SS_ERR_NULL;
     if (!aligned(s_in, 16) || !aligned(s_out, 16) || !aligned(o, 16)) return SS_ERR_ALIGN;
     const Inputs in = inputs(dims, p, q, k, v);
     ss::LaStep s{};
     s.q = in.q; s.k = in.k; s.v = in.v; s.g = g; s.decay_token = p.decay == SS_LA_DECAY_TOKEN;
     s.s_in = s_in; s.s_out = s_out; s.o = o;
-    s.B = p.B; s.H = p.H; s.dk = p.dk; s.dv = p.dv; s.scale = p.scale;
+    s.B = p.B; s.H = p.H; s.dk = p.dk; s.dv = p.dv; s.columns = columns; s.scale = p.scale;
     const hipError_t e = ss::launch_la_step(p.in_dtype == SS_BF16, s, stream);
     return e == hipSuccess ? SS_OK : hip_fail(e);
 }

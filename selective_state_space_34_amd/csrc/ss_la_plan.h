@@ -6,6 +6,12 @@
 
 namespace ss {
 
+// Whether one launch takes the workgroups: the runtime counts its threads in 32 bits, and more of
+// them are cut off without an error.
+inline bool launch_ok(int64_t blocks, int threads) {
+    return blocks <= int64_t(0xffffffffu) / threads;
+}
+
 // Tiling of one sweep (ss_la_sweep.h) over rows of width dA (contracted, and the state's rows)
 // and dC (the output's columns, and the state's).
 struct LaShape {
@@ -94,7 +100,6 @@ inline int make_la_plan(const ss_la_dims& d, bool backward, LaPlan* out) {
     p.fwd = la_shape(p.dk, p.dv);
     p.rev = la_shape(p.dv, p.dk);
     const int64_t bh = p.B * p.H;
-    const int most = p.rev.tiles > p.fwd.tiles ? p.rev.tiles : p.fwd.tiles;
     int64_t n = la_round(p.fwd, false, p.in_dtype) / (bh * p.fwd.tiles);
     if (backward) {
         const int64_t r = la_round(p.rev, p.decay != SS_LA_DECAY_NONE, p.in_dtype) / (bh * p.rev.tiles);
@@ -103,9 +108,11 @@ inline int make_la_plan(const ss_la_dims& d, bool backward, LaPlan* out) {
     // the gradient's borders are exact, so there short segments are a gain in themselves
     p.nseg = la_segments(n, p.nchunk, backward ? 1 : 2);
     p.seg_chunks = (p.nchunk + p.nseg - 1) / p.nseg;
-    // one workgroup for each (column tile, row, head, segment), and the row-wise kernels
-    const int64_t grid = int64_t(1) << 31;
-    if (!mul_ok(bh, (p.nseg + 1) * most, grid - 1)) return SS_ERR_DIMS;
+    // one workgroup for each (column tile, row, head, segment), and for each border of a segment
+    if (!launch_ok(bh * p.nseg * p.fwd.tiles, 64 * p.fwd.waves)) return SS_ERR_DIMS;
+    if (backward && (!launch_ok(bh * p.nseg * p.rev.tiles, 64 * p.rev.waves) ||
+                     !launch_ok(bh * (p.nseg + 1), 256)))
+        return SS_ERR_DIMS;
     const size_t f = sizeof(float);
     const size_t state = size_t(bh) * size_t(p.dk * p.dv) * f;
     size_t off = 0;
@@ -131,6 +138,13 @@ inline int make_la_plan(const ss_la_dims& d, bool backward, LaPlan* out) {
     p.total = off;
     *out = p;
     return SS_OK;
+}
+
+// Single-token step: columns of a head's state that a workgroup of 256 threads takes, four a
+// thread where rows keep 16-byte alignment.
+inline int la_step_columns(int64_t bh, int64_t dv) {
+    if (dv % 4 == 0) return bh >= 512 ? 128 : 32;
+    return 32;
 }
 
 // Norm: how many threads share a row and how many eight-element pieces each holds.
@@ -214,6 +228,7 @@ inline int make_q4_plan(const ss_q4_dims& d, Q4Plan* out) {
     // more CUs busy (16 x 5120 in 8 bits by 2560 11 against 17).
     const int64_t wgs = (d.n + 15) / 16 * ((d.rows + p.mb - 1) / p.mb);
     p.tiles = wgs >= 512 ? 2 : 1;
+    if (!launch_ok((d.n + 16 * p.tiles - 1) / (16 * p.tiles), 512)) return SS_ERR_DIMS;
     *out = p;
     return SS_OK;
 }
