@@ -28,9 +28,11 @@
 //   S  = e^{G_C} S + bᵀ(w ⊙ c)   (transposed operands: ds_read_b64_tr_b16)
 // The next chunk's rows are loaded into registers meanwhile.
 //
-// Numerics.  Log decays are summed as 64-bit integers with 32 fraction bits, in base 2, so a
-// weight is ldexp(2^fraction, integer) of an exact difference: no error grows with the
-// length, and a token that decays by e^{-inf} cuts the sequence exactly.  P, and S where it
+// Numerics.  Log decays are summed as 64-bit integers with 44 fraction bits, in base 2, so a
+// weight is ldexp(2^fraction, integer) of an exact difference, however far the sum has come, and a
+// token that decays by e^{-inf} cuts the sequence exactly.  Over n tokens a sum is at most n·2^-45
+// off.  The state itself is float32: it takes one rounding of its decay and one of its product a
+// chunk (and a segment), as any recurrence in float32 does.  P, and S where it
 // feeds out, go to the matrix cores as two bf16 terms, 16 bits: with one, out was 2.0e-3 off
 // (root mean square against 64 bits) where its own rounding to bf16 is 1.7e-3.
 // The state's own sums are float32: c's weight w is not a bf16 value, so w·c is fed as three
@@ -289,17 +291,22 @@ __device__ __forceinline__ float exp2_parts(float frac, int whole) {
     return __builtin_amdgcn_ldexpf(exp2_hw(frac), whole);
 }
 
-// A log decay (natural) in base 2 with 32 fraction bits, bounded so that sums stay exact:
-// 2^±1024 is 0 or inf in float32 either way.  (NaN is kept apart, by its lane.)
+// A log decay (natural) in base 2 with 44 fraction bits, rounded to the nearest, and bounded so that
+// sums of 64 and their differences fit 64 bits: 2^±1024 is 0 or inf in float32 either way.  (NaN is
+// kept apart, by its lane.)  With 32 bits a segment of 2^18 tokens could be off by 4e-5.
+constexpr int kFracBits = 44;
 __device__ __forceinline__ int64_t decay_fixed(float g) {
     double x = double(g) * 1.4426950408889634074;
     x = fmin(fmax(x, -1024.0), 1024.0);
-    const double n = __builtin_floor(x);
-    return (int64_t(int(n)) << 32) + int64_t(uint32_t((x - n) * 4294967296.0));
+    return int64_t(__builtin_rint(x * double(int64_t(1) << kFracBits)));
 }
 
-__device__ __forceinline__ float fraction_of(int64_t v) { return float(uint32_t(v)) * 2.3283064365386963e-10f; }
-__device__ __forceinline__ float exp2_fixed(int64_t v) { return exp2_parts(fraction_of(v), int(v >> 32)); }
+__device__ __forceinline__ int whole_of(int64_t v) { return int(v >> kFracBits); }
+// the upper 32 of the fraction bits, in [0, 1]
+__device__ __forceinline__ float fraction_of(int64_t v) {
+    return float(uint32_t(v >> (kFracBits - 32))) * 2.3283064365386963e-10f;
+}
+__device__ __forceinline__ float exp2_fixed(int64_t v) { return exp2_parts(fraction_of(v), whole_of(v)); }
 
 template <int CTRL, int ROWS>
 __device__ __forceinline__ int64_t add_moved(int64_t v) {
@@ -327,7 +334,7 @@ __device__ __forceinline__ int64_t decay_prepare(float g, int lane, int reverse,
     const float mark = (bad << (63 - lane)) ? __builtin_nanf("") : 0.0f;
     const float mark_all = bad ? __builtin_nanf("") : 0.0f;
     if (lane < C) {
-        d.whole[lane] = int(sum >> 32);
+        d.whole[lane] = whole_of(sum);
         d.frac[lane] = fraction_of(sum) + mark;
         const float fwd = exp2_fixed(sum) + mark, bwd = exp2_fixed(total - sum) + mark_all;
         d.in[lane] = in_scale * (reverse ? bwd : fwd);
@@ -510,7 +517,7 @@ __global__ __launch_bounds__(64 * NW, sweep_occupancy(int(sizeof(T)), kVec, DA, 
             seg_nan = true;
         } else {
             // beyond ±2^17 the decay is 0 or inf in any case, and the sum must not wrap
-            const int64_t most = int64_t(1) << 49;
+            const int64_t most = int64_t(1) << (17 + kFracBits);
             seg_sum += sum;
             seg_sum = seg_sum < -most ? -most : seg_sum > most ? most : seg_sum;
         }
