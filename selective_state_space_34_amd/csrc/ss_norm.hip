@@ -4,7 +4,7 @@
 //   r = x + res                      (kept unrounded for y; stored in the residual's type)
 //   y = r·c·w,  c = 1/sqrt(mean(r²) + eps)
 //   8 bits: scale = max|y| / top, codes = y·(top / max|y|), top 448 (e4m3) or 127 (int8)
-//   dx = dr + c·(w·dy) - r·(c³/D)·Σ(w·dy·r)        dw = Σ_rows dy·r·c
+//   dx = dr + c·(w·dy) - (r·c)·(c·(c·Σ(w·dy·r)/D))        dw = Σ_rows dy·r·c
 //
 // The work is traffic: every element is read once and written once, a row staying in registers
 // between the sums and the result.  A row belongs to P threads (8 to 1024, by its length
@@ -307,7 +307,9 @@ __global__ __launch_bounds__(P > 256 ? P : 256) void rms_bwd_kernel(const RmsLau
         }
         rs.sum2(sq, dot);
         const float c = rsqrtf(sq * p.inv_d + p.eps);
-        const float k = c * c * c * (dot * p.inv_d);
+        // c²·(dot/D) first meets one c, then c·x: c³ would leave float32 for rows whose size is
+        // below 1e-13 or above 1e12, where each of these is of dx's own size or of 1
+        const float k = c * (c * (dot * p.inv_d));
         Tr* dx = static_cast<Tr*>(p.r) + row * D;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -317,8 +319,9 @@ __global__ __launch_bounds__(P > 256 ? P : 256) void rms_bwd_kernel(const RmsLau
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float x = r[j].get(e), y = dy[j].get(e);
-                o[e] = fmaf(c * w.get(e), y, -k * x);
-                dw[j][e] = fmaf(y, e >= at.twice ? x * c : 0.0f, dw[j][e]);
+                const float n = x * c;
+                o[e] = fmaf(c * w.get(e), y, -k * n);
+                dw[j][e] = fmaf(y, e >= at.twice ? n : 0.0f, dw[j][e]);
                 if (p.dr) o[e] += g[j].get(e);
             }
             put8(dx, at.at, D, o);
