@@ -356,7 +356,8 @@ int ss_rms_bwd(const ss_rms_dims* dims, const void* dy, const void* r, const flo
  *   scales [n, ceil(k / group)] bfloat16
  *   zeros  [n, ceil(k / group)] bytes; NULL: 8
  *   x      [rows, k] in_dtype, or 8-bit codes (x_q8) with x_scale [rows] float32
- *   y      [rows, n] y_dtype, rounded once; sums are float32
+ *   y      [rows, n] y_dtype, rounded once; sums are float32.  Infinities and NaN of x go where the
+ *          formula takes them, and stay in their row
  * Needs no workspace. */
 typedef struct ss_q4_dims {
     int64_t rows, n, k;   /* k a multiple of 32; n <= 2^28 - 32 */

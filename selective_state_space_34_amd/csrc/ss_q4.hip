@@ -47,6 +47,13 @@ __device__ __forceinline__ bf16x8 widen(uint32_t d) {
     return o.f;
 }
 
+// the same less by, exact where by is 16 and a zero
+__device__ __forceinline__ bf16x8 less(bf16x8 f, float by) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = __bf16(float(f[e]) - by);
+    return f;
+}
+
 struct fp8_t { uint8_t b; };
 struct int8_q { int8_t b; };
 
@@ -59,7 +66,8 @@ __device__ __forceinline__ bf16x8 ordered(const float (&v)[8]) {
 }
 
 // Eight elements of x as they lie in memory, and as an operand; term: which bf16 term of
-// float32 values.
+// float32 values.  get: for finite values (others give values that are not finite); get_any: for
+// any, as the product takes them.
 template <typename T> struct Eight;
 template <> struct Eight<bf16_t> {
     u32x4 w = {0, 0, 0, 0};
@@ -72,6 +80,7 @@ template <> struct Eight<bf16_t> {
         o.w[3] = __builtin_amdgcn_perm(w[3], w[1], 0x07060302u);
         return o.f;
     }
+    __device__ __forceinline__ bf16x8 get_any(int) const { return get(0); }
 };
 template <> struct Eight<fp8_t> {
     uint2 w = {0, 0};
@@ -88,6 +97,7 @@ template <> struct Eight<fp8_t> {
         v[7] = __builtin_amdgcn_cvt_f32_fp8(int(w.y), 3);
         return ordered(v);
     }
+    __device__ __forceinline__ bf16x8 get_any(int) const { return get(0); }
 };
 template <> struct Eight<int8_q> {
     uint2 w = {0, 0};
@@ -98,6 +108,7 @@ template <> struct Eight<int8_q> {
         for (int e = 0; e < 8; ++e) v[e] = float(int8_t((e < 4 ? w.x : w.y) >> (8 * (e & 3))));
         return ordered(v);
     }
+    __device__ __forceinline__ bf16x8 get_any(int) const { return get(0); }
 };
 template <> struct Eight<float> {
     f32x4 v[2] = {};
@@ -118,6 +129,18 @@ template <> struct Eight<float> {
         for (int i = 0; i < 4; ++i)
             o.w[i] = __builtin_amdgcn_perm(part(v[1][i], term), part(v[0][i], term), 0x07060302u);
         return o.f;
+    }
+    // an infinity is its first term alone (what is left of it would be NaN), a NaN is one in each
+    __device__ __forceinline__ bf16x8 get_any(int term) const {
+        Eight<float> f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float a = v[e / 4][e & 3];
+            if (__builtin_isinf(a) && term > 0) a = 0.0f;
+            if (a != a) a = __uint_as_float(0x7fc00000u);
+            f.v[e / 4][e & 3] = a;
+        }
+        return f.get(term);
     }
 };
 
@@ -212,6 +235,47 @@ __global__ __launch_bounds__(64 * NW) void q4_kernel(const Q4Launch p) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                     acc[t][r] = fmaf(sf[t], fmaf(-zf[t], u[r], v[t][r]), acc[t][r]);
+        }
+    }
+    // An infinity in x, or values whose sum with 16 added to the codes leaves float32, end in an acc
+    // that is not finite and stays so: those are formed once more, from weights u - z themselves
+    // (whole numbers of at most eight bits, exact in bf16).
+    bool finite = true;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) finite = finite && __builtin_isfinite(acc[t][r]);
+    if (__any(!finite)) {
+        int own = lane;
+        asm volatile("" : "+v"(own));   // nothing of what follows is kept in registers until here
+        const int c16 = own & 15, m = c16 / kTerms, part = c16 - m * kTerms;
+        const int64_t first = (own >> 4) * 8 * W;
+        const Tx* xr = static_cast<const Tx*>(p.x) + (m0 + (m < rows ? m : 0)) * p.K + first;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int64_t n = int64_t(blockIdx.x) * 16 * NT + 16 * t + c16, nr = n < p.N ? n : p.N - 1;
+            f32x4 again = {0, 0, 0, 0};
+#pragma unroll 1
+            for (int64_t g = wave; g < p.groups; g += NW) {
+                const bool on = g * G + first < p.K;
+                Word code{};
+                if (on) code = *reinterpret_cast<const Word*>(p.wq + nr * (p.K / 2) + (g * G + first) / 2);
+                const uint32_t* q = reinterpret_cast<const uint32_t*>(&code);
+                const float sf = __uint_as_float(uint32_t(p.scales[nr * p.groups + g]) << 16);
+                const float zf = 16.0f + (p.zeros ? float(p.zeros[nr * p.groups + g]) : 8.0f);
+                f32x4 v = {0, 0, 0, 0};
+#pragma unroll
+                for (int i = 0; i < W; ++i) {
+                    Eight<Tx> e;
+                    if (on && m < rows) e.load(xr + g * G + 8 * i);
+                    v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e.get_any(part), less(widen(q[i]), zf), v, 0, 0, 0);
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) again[r] = fmaf(sf, v[r], again[r]);
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (!__builtin_isfinite(acc[t][r])) acc[t][r] = again[r];
         }
     }
     // lane: column l16 of each tile, product rows 4·lg + r
