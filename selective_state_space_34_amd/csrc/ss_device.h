@@ -12,6 +12,16 @@
 
 namespace ss {
 
+// Lets products finish before a branch.  Where a block behind a product may be jumped over, the
+// compiler (ROCm 7.2's) has counted the wait states before the use of the product's result along
+// the longer path alone, and the use read registers not yet written.  tests/test_wait_states.py
+// walks every path of what was built.
+__device__ __forceinline__ void settle() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_nop 11");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 

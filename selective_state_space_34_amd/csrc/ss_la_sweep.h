@@ -277,15 +277,6 @@ struct Decay {
     float all;       // decay of the state over the chunk
 };
 
-// Lets products finish before a branch.  Where a block behind a product may be jumped over, the
-// compiler (ROCm 7.2's) has counted the wait states before the use of the product's result along
-// the longer path alone, and the use read registers not yet written.
-__device__ __forceinline__ void settle() {
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("s_nop 11");
-    __builtin_amdgcn_sched_barrier(0);
-}
-
 // 2^x for x given as whole + frac
 __device__ __forceinline__ float exp2_parts(float frac, int whole) {
     return __builtin_amdgcn_ldexpf(exp2_hw(frac), whole);

@@ -223,18 +223,15 @@ __global__ __launch_bounds__(64 * NW) void q4_kernel(const Q4Launch p) {
                     v[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, widen(q[i]), v[t], 0, 0, 0);
                 }
             }
-            float sf[NT], zf[NT];
+            // The sums before the next loads: between a product and the use of its result stands no
+            // branch (see settle() in ss_device.h).
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                sf[t] = __uint_as_float(s[a][t] << 16);
-                zf[t] = 16.0f + float(z[a][t]);
+                const float sf = __uint_as_float(s[a][t] << 16), zf = 16.0f + float(z[a][t]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[t][r] = fmaf(sf, fmaf(-zf, u[r], v[t][r]), acc[t][r]);
             }
             if (g + NW * kAhead < p.groups) load(a, g + NW * kAhead);
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    acc[t][r] = fmaf(sf[t], fmaf(-zf[t], u[r], v[t][r]), acc[t][r]);
         }
     }
     // An infinity in x, or values whose sum with 16 added to the codes leaves float32, end in an acc
