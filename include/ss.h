@@ -292,7 +292,8 @@ typedef struct ss_la_dims {
 int ss_la_fwd_workspace_size(const ss_la_dims* dims, size_t* bytes);
 int ss_la_bwd_workspace_size(const ss_la_dims* dims, size_t* bytes);
 
-/* Chunked form over T tokens.  s0, s_final, lengths optional; g as dims.decay says. */
+/* Chunked form over T tokens.  s0, s_final, lengths optional; g as dims.decay says.  s_final may
+ * equal s0 (a sequence continued in place); nothing else that is written may overlap anything. */
 int ss_la_fwd(const ss_la_dims* dims, const void* q, const void* k, const void* v, const float* g,
               const float* s0, const int32_t* lengths, void* o, float* s_final,
               void* workspace, size_t workspace_bytes, hipStream_t stream);
@@ -302,7 +303,8 @@ int ss_la_fwd(const ss_la_dims* dims, const void* q, const void* k, const void* 
  *   dq, dk [B, T, Hk, dk], dv [B, T, H, dv] (in_dtype, dense): required; a shared key head's
  *   gradients are summed over its value heads in float32, in order.
  *   dg : required unless there is no decay; shaped like g, float32.
- *   ds0: required iff s0 is given (else must be NULL). */
+ *   ds0: required iff s0 is given (else must be NULL); may equal ds_final.
+ * Nothing else that is written may overlap anything. */
 int ss_la_bwd(const ss_la_dims* dims, const void* q, const void* k, const void* v, const float* g,
               const float* s0, const int32_t* lengths, const void* dO, const float* ds_final,
               void* dq, void* dk, void* dv, float* dg, float* ds0,
@@ -335,7 +337,8 @@ typedef struct ss_rms_dims {
 } ss_rms_dims;
 
 /* res NULL: no residual, and r must be NULL; else r is required and may equal res.  y_scale
- * [rows] is required iff q8 is set.  Needs no workspace. */
+ * [rows] is required iff q8 is set.  Nothing else that is written may overlap anything.  Needs no
+ * workspace. */
 int ss_rms_fwd(const ss_rms_dims* dims, const void* x, const void* res, const float* w, void* r,
                void* y, float* y_scale, hipStream_t stream);
 

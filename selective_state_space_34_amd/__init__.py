@@ -625,7 +625,8 @@ def ss_la_fwd(q, k, v, g=None, s0=None, *, scale=1.0, lengths=None, return_final
     o_t = scale · S_tᵀ q_t.  q, k [B, T, Hk, dk], v [B, T, H, dv] (float32 or bfloat16, may be
     strided slices with a contiguous last axis; H % Hk == 0), g None, [H] or [B, T, H] float32
     (natural log of the decay), s0 [B, H, dk, dv] float32, lengths [B] int32.  Returns o
-    [B, T, H, dv] in v's type, or (o, s_final) with return_final (or when s_final is passed)."""
+    [B, T, H, dv] in v's type, or (o, s_final) with return_final (or when s_final is passed; it
+    may be s0, updated in place)."""
     import torch
     lib = load()
     key, (B, T, H, dk, dv) = _la_key(q, k, v, g, s0, scale, lengths, False)
@@ -653,7 +654,8 @@ def ss_la_bwd(q, k, v, do, g=None, s0=None, ds_final=None, *, scale=1.0, lengths
               workspace=None, out=None, stream=None):
     """Gradients of ss_la_fwd through the C ABI: do [B, T, H, dv] in v's type, ds_final
     [B, H, dk, dv] float32.  Returns a dict dq, dk, dv (the inputs' type), dg (float32, shaped
-    like g; None without decay), ds0 (None without s0)."""
+    like g; None without decay), ds0 (None without s0).  out: a dict of tensors to take them; its
+    ds0 may be ds_final."""
     import torch
     lib = load()
     key, (B, T, H, dk, dv) = _la_key(q, k, v, g, s0, scale, lengths, False)

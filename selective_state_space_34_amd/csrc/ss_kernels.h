@@ -227,6 +227,7 @@ struct LaDecayGrad {
                                           // segment from the left, from the right
     const float *s0, *ds0, *ds, *s_final; // nullable [B, H, dk, dv]
     double* border;            // [B, H, nseg + 1]
+    int border0, borders;      // launch_la_borders forms borders border0 .. border0 + borders - 1
     const int32_t* lengths;
     float* dg;
     double* head_part;
@@ -235,7 +236,8 @@ struct LaDecayGrad {
     int64_t seg_tokens;
     int decay_token;
 };
-hipError_t launch_la_decay_grad(const LaDecayGrad& p, hipStream_t s);
+hipError_t launch_la_borders(const LaDecayGrad& p, hipStream_t s);
+hipError_t launch_la_decay_grad(const LaDecayGrad& p, hipStream_t s);   // after all the borders
 
 // Gradients of the shared key heads, dq and dk in turn: sums over the value heads of each,
 // part[x] [tokens, key heads, rep, d] float32 into out[x], n = tokens·key heads·d elements.

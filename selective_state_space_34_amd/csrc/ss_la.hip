@@ -57,8 +57,8 @@ __device__ __forceinline__ double block_sum(double v, double* part) {
 // thread are in flight at once; 8 us for 64 heads' 4 segments of 128 x 128.
 __global__ __launch_bounds__(256) void la_border_kernel(const LaDecayGrad p) {
     __shared__ double part[4];
-    const int64_t bh = blockIdx.x / (p.nseg + 1);
-    const int k = int(blockIdx.x - bh * (p.nseg + 1));
+    const int64_t bh = blockIdx.x / p.borders;
+    const int k = p.border0 + int(blockIdx.x - bh * p.borders);
     const int sz = int(p.dk * p.dv), tid = threadIdx.x;
     const float *r = p.ds0, *s = p.s0;
     int64_t at_r = bh, at_s = bh;
@@ -85,7 +85,7 @@ __global__ __launch_bounds__(256) void la_border_kernel(const LaDecayGrad p) {
         }
     }
     v = block_sum(v, part);
-    if (tid == 0) p.border[blockIdx.x] = v;
+    if (tid == 0) p.border[bh * (p.nseg + 1) + k] = v;
 }
 
 // dg_t = Σ_{u>=t} (row_u - col_u) + E at the segment's end, u inside the segment.  A sum over the
@@ -281,13 +281,14 @@ hipError_t launch_la_carry(const LaCarries& p, hipStream_t s) {
     return hipGetLastError();
 }
 
+hipError_t launch_la_borders(const LaDecayGrad& p, hipStream_t s) {
+    hipLaunchKernelGGL(la_border_kernel, dim3(unsigned(p.B * p.H * p.borders)), dim3(256), 0, s, p);
+    return hipGetLastError();
+}
+
 hipError_t launch_la_decay_grad(const LaDecayGrad& p, hipStream_t s) {
-    const int64_t bh = p.B * p.H;
-    hipLaunchKernelGGL(la_border_kernel, dim3(unsigned(bh * (p.nseg + 1))), dim3(256), 0, s, p);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(la_decay_grad_kernel, dim3(unsigned(bh * p.nseg)), dim3(256), 0, s, p);
-    e = hipGetLastError();
+    hipLaunchKernelGGL(la_decay_grad_kernel, dim3(unsigned(p.B * p.H * p.nseg)), dim3(256), 0, s, p);
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.decay_token) return e;
     hipLaunchKernelGGL(la_head_sum_kernel, dim3(unsigned(p.H)), dim3(64), 0, s, p);
     return hipGetLastError();

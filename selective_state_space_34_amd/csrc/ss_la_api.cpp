@@ -254,6 +254,24 @@ int ss_la_bwd(const ss_la_dims* dims, const void* q, const void* k, const void* 
         if (e != hipSuccess) return hip_fail(e);
     }
 
+    // dg from the row and column sums and the states at the segments' borders
+    ss::LaDecayGrad d{};
+    d.row = dots(p.off_row); d.col = dots(p.off_col); d.tiles = p.rev.tiles;
+    d.fwd_state = state; d.rev_state = rstate;
+    d.s0 = s0; d.ds0 = ds0; d.ds = ds_final; d.s_final = s_final;
+    d.border = dots(p.off_border); d.head_part = dots(p.off_head);
+    d.lengths = lengths; d.dg = dg;
+    d.B = p.B; d.T = p.T; d.H = p.H; d.dk = p.dk; d.dv = p.dv;
+    d.nseg = int(p.nseg); d.seg_tokens = p.seg_chunks * ss::la_chunk(p.in_dtype);
+    d.decay_token = p.decay == SS_LA_DECAY_TOKEN;
+    d.borders = d.nseg + 1;
+    if (s_final && ds0 == ds_final) {   // in place: the last border before dS_0 replaces dS_T
+        d.border0 = d.nseg; d.borders = 1;
+        e = ss::launch_la_borders(d, stream);
+        if (e != hipSuccess) return hip_fail(e);
+        d.border0 = 0; d.borders = d.nseg;
+    }
+
     // 3. dv: reverse sweep of (k, q, dO) with the state transposed, dS_t [dk, dv]
     w.n = 1;
     LaSweep& s = w.p[0];
@@ -264,17 +282,10 @@ int ss_la_bwd(const ss_la_dims* dims, const void* q, const void* k, const void* 
     e = sweep(p, w, stream);
     if (e != hipSuccess) return hip_fail(e);
 
-    // 4. dg from the row and column sums and the states at the segments' borders
+    // 4. dg
     if (g) {
-        ss::LaDecayGrad d{};
-        d.row = dots(p.off_row); d.col = dots(p.off_col); d.tiles = p.rev.tiles;
-        d.fwd_state = state; d.rev_state = rstate;
-        d.s0 = s0; d.ds0 = ds0; d.ds = ds_final; d.s_final = s_final;
-        d.border = dots(p.off_border); d.head_part = dots(p.off_head);
-        d.lengths = lengths; d.dg = dg;
-        d.B = p.B; d.T = p.T; d.H = p.H; d.dk = p.dk; d.dv = p.dv;
-        d.nseg = int(p.nseg); d.seg_tokens = p.seg_chunks * ss::la_chunk(p.in_dtype);
-        d.decay_token = p.decay == SS_LA_DECAY_TOKEN;
+        e = ss::launch_la_borders(d, stream);
+        if (e != hipSuccess) return hip_fail(e);
         e = ss::launch_la_decay_grad(d, stream);
         if (e != hipSuccess) return hip_fail(e);
     }
