@@ -165,8 +165,8 @@ struct LaOperand {
     int64_t rep;       // value heads that share a row
     int dim;           // width
     int vec;           // every row starts on 16 bytes and holds whole 16-byte pieces, a token's
-                       // row ends before the next one's begins, and a chunk's rows lie within
-                       // 2^30 bytes
+                       // row ends before the next one's begins or all chunks are full, and a
+                       // chunk's rows lie within 2^30 bytes
 };
 
 // One sweep (ss_la_sweep.h).

@@ -222,7 +222,7 @@ __device__ __forceinline__ u32x4 load_unaligned(const T* p) {
 // N pieces of a chunk (nv of its tokens exist), STEP tokens apart; zeros outside the tokens and
 // the width.  Aligned rows (kVec) go through a buffer descriptor that ends with the chunk's last
 // row, so the bounds cost nothing; tokens behind it are outside because a row is no longer than the
-// stride.  For others a piece that would pass the row's end starts
+// stride (or there are none).  For others a piece that would pass the row's end starts
 // earlier, at the row's last 16 bytes, and is shifted into place; rows shorter than a piece are
 // put together element by element.
 template <typename T, bool kVec, int N, int STEP>

@@ -38,6 +38,22 @@ def test_rows_expanded_over_tokens(gpu, T, lengths, which, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [64, 128, 704])
+def test_expanded_rows_of_full_chunks(gpu, T, dtype):
+    """No token behind the end in any chunk: the same rows, with and without lengths."""
+    import torch
+    c = la.make(53 + T, 1, T, 4, 2, 64, 64, dtype, "token", True)
+    t = la.dev(c)
+    note(f"la expanded, full chunks T={T} {dtype}")
+    views = [t[n][:, :1].expand(-1, T, -1, -1) for n in "qkv"]
+    numpy_of(c, views)
+    call(gpu, c, t, views)
+    c["lengths"] = [T - 3]
+    t["lengths"] = torch.tensor([T - 3], dtype=torch.int32, device="cuda")
+    call(gpu, c, t, views)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("step", [8, 16, 48])
 def test_rows_that_overlap(gpu, step, dtype):
     """Token t starts `step` elements behind token t - 1, in rows of 64."""
