@@ -354,7 +354,8 @@ int ss_rms_bwd(const ss_rms_dims* dims, const void* dy, const void* r, const flo
 /* ---- Products with 4-bit weights ------------------------------------------------------------
  *
  *   y[m, i] = x_scale[m] · Σ_j x[m, j] · scales[i, j / group] · (u[i, j] - zeros[i, j / group])
- * for the few rows of a decode step (any number is taken; 16 at a time, 5 of float32).
+ * for the few rows of a decode step.  Any number is taken, but every 16 of them (5 of float32) read all
+ * weights again: from about 32 rows on a dense product of widened weights is faster.
  *   wq     [n, k / 2] bytes: u[i, 2j] in the low half of byte j of row i, u[i, 2j+1] in the high
  *   scales [n, ceil(k / group)] bfloat16
  *   zeros  [n, ceil(k / group)] bytes; NULL: 8

@@ -42,14 +42,16 @@
 //
 // What bounds it.  By its traffic a sweep is bound by memory, but with the state in registers a
 // CU holds eight or sixteen waves, and their chunk is a chain of barriers and dependent products:
-// vector ALUs and LDS are each busy for about 45% of the time, the matrix cores for 20%, and 40%
-// of the waves' time is waiting.  Measured, bf16, token decays: B = 4, T = 2048, H = 16,
-// 128 x 128 the states of 4 segments (kState) 22 us, the carry 7, the sweep 45 (3.0 TB/s);
-// B = 1, T = 32768, H = 40 on 8, 64 x 128 117, 8 and 244 us; gradient at B = 4, T = 4096, H = 16,
-// 128 x 128 states of both directions 62, carries 13, dq and dk 240, dv 85.  A sequence that is
+// at 128 x 128 vector ALUs are busy for 43% of the time, LDS for 33%, the matrix cores for 25%, and
+// 40% of the waves' time is waiting (64 x 128: 59, 43, 29 and 37%; dq and dk: 39, 34, 25 and 43%).
+// Measured, bf16, token decays: B = 4, T = 2048, H = 16, 128 x 128 the states of 4 segments
+// (kState) 23 us, the carry 7, the sweep 53 (2.9 TB/s); B = 1, T = 32768, H = 40 on 8, 64 x 128 130, 9
+// and 290 us; gradient at B = 4, T = 4096, H = 16, 128 x 128 states of both directions 61, carries
+// 12, dq and dk 233, dv 97.  Float32, B = 4, T = 2048, H = 16, 64 x 128: 113 us for all three, the
+// gradient 312.  A sequence that is
 // swept once instead, without segments, leaves most CUs idle where B·H is small; two chunks of rows
 // in flight instead of one cost more registers than they hid (59 us became 68), and out by way
-// of LDS in whole rows another barrier (235 us became 279).
+// of LDS in whole rows another barrier (235 us became 279).  (Both at one term of S.)
 #pragma once
 
 #include "ss_device.h"

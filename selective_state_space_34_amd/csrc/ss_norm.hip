@@ -7,7 +7,11 @@
 //   dx = dr + c·(w·dy) - (r·c)·(c·(c·Σ(w·dy·r)/D))        dw = Σ_rows dy·r·c
 //
 // The work is traffic: every element is read once and written once, a row staying in registers
-// between the sums and the result.  A row belongs to P threads (8 to 1024, by its length
+// between the sums and the result.  (Up to a width of 16384 forward and 8192 in the gradient, that
+// is.  Beyond, 1024 threads leave a thread 128 registers, and some of the row is kept in scratch:
+// 6 to 12 registers of the gradient up to 16384, above it 53 to 76 forward and 195 to 410 in the
+// gradient.  bf16, 67 MB of rows, forward and gradient: width 8192 44 and 59 us, 16384 48 and 71,
+// 32768 70 and 185.)  A row belongs to P threads (8 to 1024, by its length
 // and by how many rows there are), eight consecutive elements of it to each thread at a time,
 // NV such pieces a thread; sums meet by shuffles, across waves through LDS.  Workgroups take
 // rows in turn, so that in the gradient the columns' sums stay in registers over a workgroup's
@@ -15,8 +19,9 @@
 // read for every row (it stays in the CU's cache): holding it too would cost 8·NV registers
 // and with them the waves that keep loads in flight.  All loads of a row are issued before the
 // first is used, and kept as they lie until then: bf16, D = 2560, 16384 rows with a residual and
-// 8-bit output 89 us became 56 (5.2 TB/s, the rate of a copy).  The gradient of the same rows
-// takes 72 us and the sum of dw over workgroups 5.
+// 8-bit output 89 us became 57 (5.2 TB/s, the rate of a copy).  The gradient of the same rows
+// takes 75 us and the sum of dw over workgroups 6; at 26155 rows of 1472, where 184 of a row's 256
+// threads have work, 97 us for 308 MB.
 #include "ss_device.h"
 #include "ss_kernels.h"
 
