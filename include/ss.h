@@ -374,6 +374,122 @@ typedef struct ss_q4_dims {
 int ss_q4_mv(const ss_q4_dims* dims, const void* x, const float* x_scale, const void* wq,
              const void* scales, const void* zeros, void* y, hipStream_t stream);
 
+/* ---- Gated linear recurrence ----------------------------------------------------------------
+ *
+ * A recurrence of one number a channel whose decay is a gate of the token.  Per batch row b and
+ * channel d, with the rate c·softplus(lam[d]) >= 0:
+ *   a_t = exp(-c · softplus(lam) · σ(r_t))              (c = 8 is usual)
+ *   h_t = a_t h_{t-1} + sqrt(1 - a_t²) · σ(i_t) · x_t    y_t = h_t
+ * with h before the first token = h0[b,d] (or 0) and h_final[b,d] = h after the last one.
+ *   x, r, i : [B, T, D] (in_dtype), the input and the two gates before their sigmoids.  They may
+ *          be strided: dims.*_stride are elements from batch row to batch row and token to token
+ *          (the last axis is contiguous); both 0 means dense.  A token stride of less than D (an
+ *          expanded or overlapping operand) is taken too.  They need only their type's alignment.
+ *   y, and the gradients of x, r, i : [B, T, D] dense, in_dtype, each rounded once.
+ *   lam, dlam [D], h0, h_final, dh_final, dh0 [B, D], h_ckpt [B, ceil(T / SS_GR_CKPT), D] : float32.
+ *   lengths : NULL, or [B] int32 on the device: row b has lengths[b] tokens (clamped to [0, T]).
+ *          What the places behind hold is not used; y and the gradients are 0 there.
+ *   reset   : NULL, or [B, T] bytes on the device: a token with a byte other than 0 begins a
+ *          document: its a_t is 0 (and sqrt(1 - a_t²) is 1), nothing of the state before it, NaN
+ *          and infinities included, reaches it, and no gradient comes back.
+ * States, sums and gates are float32.  Where 1 - a_t² is below 1e-30 the gradient of the square
+ * root is taken as 0. */
+#define SS_GR_CKPT 64   /* tokens from one of h_ckpt's states to the next */
+
+typedef struct ss_gr_dims {
+    int64_t batch;        /* B >= 1 */
+    int64_t seqlen;       /* T >= 1 */
+    int64_t dim;          /* D >= 1 */
+    int64_t x_stride[2];  /* batch row, token; both 0: dense */
+    int64_t r_stride[2];
+    int64_t i_stride[2];
+    int32_t in_dtype;     /* ss_dtype of x, r, i, y, dy and the gradients of x, r, i */
+    float c;              /* finite, > 0 */
+} ss_gr_dims;
+
+/* Workspace bytes ss_gr_fwd / ss_gr_bwd need (the forward's may be 0); given_ckpt: whether ss_gr_bwd
+ * is called with h_ckpt. */
+int ss_gr_fwd_workspace_size(const ss_gr_dims* dims, size_t* bytes);
+int ss_gr_bwd_workspace_size(const ss_gr_dims* dims, int given_ckpt, size_t* bytes);
+
+/* Over T tokens.  h0, lengths, reset, h_final, h_ckpt optional.  h_ckpt: the states that enter
+ * tokens 0, SS_GR_CKPT, 2·SS_GR_CKPT, ..., which ss_gr_bwd can take instead of forming them once
+ * more.  h_final may equal h0; nothing else that is written may overlap anything. */
+int ss_gr_fwd(const ss_gr_dims* dims, const void* x, const void* r, const void* i, const float* lam,
+              const float* h0, const int32_t* lengths, const void* reset, void* y, float* h_final,
+              float* h_ckpt, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Gradients of sum(dy·y) + sum(dh_final·h_final).
+ *   dy [B, T, D] (in_dtype, dense); dh_final NULL = zero; h_ckpt NULL: the states are formed here,
+ *   else as ss_gr_fwd wrote it from the same inputs.
+ *   dx, dr, di (dense), dlam: required; dlam is summed in a fixed order.
+ *   dh0: required iff h0 is given (else must be NULL); may equal dh_final.
+ * Nothing else that is written may overlap anything. */
+int ss_gr_bwd(const ss_gr_dims* dims, const void* x, const void* r, const void* i, const float* lam,
+              const float* h0, const int32_t* lengths, const void* reset, const void* dy,
+              const float* dh_final, const float* h_ckpt, void* dx, void* dr, void* di, float* dlam,
+              float* dh0, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* One token: x, r, i, y [B, D]; dims.seqlen must be 1 (token strides are not used).  h_in [B, D] is
+ * the state before the token, h_out the state after it; h_out may equal h_in (updated in place),
+ * otherwise they must not overlap.  Needs no workspace. */
+int ss_gr_step(const ss_gr_dims* dims, const void* x, const void* r, const void* i, const float* lam,
+               const float* h_in, float* h_out, void* y, hipStream_t stream);
+
+/* ---- Layer norm with the residual's addition -------------------------------------------------
+ *
+ *   r = x + res (or x)     y = (r - mean(r)) / sqrt(mean((r - mean(r))²) + eps) · w + b
+ * over rows of `dim` elements; types, the 8-bit outputs and the rules of r and res as for
+ * ss_rms_fwd.  w, b [dim] float32; b NULL: none.  With q8 = SS_Q4_MX, y is in the blocks of
+ * ss_mx4_quant (dim a multiple of 32): codes [rows, dim / 2] and, in y_scale's place, exponents
+ * [rows, dim / 32] bytes. */
+enum { SS_Q4_MX = 3 };   /* ss_ln_dims.q8, beside ss_q8's values */
+
+typedef struct ss_ln_dims {
+    int64_t rows;       /* >= 1 */
+    int64_t dim;        /* 1 .. 32768 */
+    int32_t in_dtype;   /* ss_dtype of x, y, dy */
+    int32_t res_dtype;  /* ss_dtype of res, r, dr, dx (float32 where in_dtype is) */
+    int32_t q8;         /* ss_q8 of y, or SS_Q4_MX (backward: SS_Q8_NONE) */
+    float eps;          /* finite, >= 0 */
+} ss_ln_dims;
+
+int ss_ln_fwd(const ss_ln_dims* dims, const void* x, const void* res, const float* w, const float* b,
+              void* r, void* y, void* y_scale, hipStream_t stream);
+
+/* Gradients as of ss_rms_bwd: dx (may equal dr), dw [dim] and, unless NULL, db [dim] float32,
+ * summed in a fixed order. */
+int ss_ln_bwd_workspace_size(const ss_ln_dims* dims, size_t* bytes);
+int ss_ln_bwd(const ss_ln_dims* dims, const void* dy, const void* r, const float* w, const void* dr,
+              void* dx, float* dw, float* db, void* workspace, size_t workspace_bytes,
+              hipStream_t stream);
+
+/* ---- Microscaled 4-bit values and their products ------------------------------------------------
+ *
+ * 32 consecutive columns share a power of two: value = e2m1(code) · 2^(exponent - 127), e2m1 =
+ * 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives (bit 3 is the sign), two codes a byte, the first in
+ * the low half; exponent 255 makes a block NaN.
+ *   codes [rows, k / 2] bytes      exponents [rows, k / 32] bytes
+ * ss_mx4_quant rounds x [rows, k] (in_dtype) to it: the exponent is that of the block's largest
+ * magnitude less two (at least 1), codes go to the nearest value, ties to the even code, and
+ * values past 6 to 6.  A block that holds a NaN or an infinity has exponent 255 and zero codes. */
+typedef struct ss_mx4_dims {
+    int64_t rows, n, k;   /* k a multiple of 32; n is not used by ss_mx4_quant */
+    int32_t in_dtype;     /* ss_dtype of ss_mx4_quant's x */
+    int32_t x_q8;         /* ss_mx4_mm's x: SS_Q4_MX, or SS_Q8_FP8 */
+    int32_t y_dtype;      /* ss_dtype of y */
+} ss_mx4_dims;
+
+int ss_mx4_quant(const ss_mx4_dims* dims, const void* x, void* codes, void* exps, hipStream_t stream);
+
+/* y[m, i] = Σ_j x[m, j] · w[i, j], y [rows, n] y_dtype, rounded once; sums are float32.
+ *   w: codes wq [n, k / 2] and exponents w_exps [n, k / 32]
+ *   x: codes [rows, k / 2] with x_scale its exponents [rows, k / 32] bytes, or e4m3 [rows, k] with
+ *      x_scale [rows] float32, as the norms give them.
+ * Needs no workspace. */
+int ss_mx4_mm(const ss_mx4_dims* dims, const void* x, const void* x_scale, const void* wq,
+              const void* w_exps, void* y, hipStream_t stream);
+
 /* Static description of a return code. */
 const char* ss_strerror(int code);
 

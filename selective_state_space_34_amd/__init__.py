@@ -17,6 +17,14 @@ PyTorch fallback: if the compiled library is missing, ``load()`` raises.
     y8, y_scale, r = ss_rms_fwd(x, w, res, q8=SS_Q8_FP8)                     # ... in 8 bits
     dx, dw = ss_rms_bwd(dy, r, w, dr=None)
     y = ss_q4_mv(x, wq, scales, zeros=None, x_scale=None)                    # 4-bit weights
+    y = ss_gr_fwd(x, r, i, lam, h0=None)         # gated recurrence of one number a channel
+    y, h_ckpt = ss_gr_fwd(..., return_ckpt=True)
+    grads = ss_gr_bwd(x, r, i, lam, dy, h0=None, dh_final=None, h_ckpt=None)
+    y_t = ss_gr_step(x_t, r_t, i_t, lam, h)                                  # h updated in place
+    y, r = ss_ln_fwd(x, w, b, res)               # layer norm after the residual's addition
+    dx, dw, db = ss_ln_bwd(dy, r, w, dr=None)
+    codes, exps = ss_mx4_quant(x)                # 4-bit values, 32 to a power of two
+    y = ss_mx4_mm(codes, exps, wq, w_exps)       # their products, for one row or for many
 
 Layouts: x, dt_raw, z, y [B, D, L]; Bm, Cm [B, N, L]; A [D, N]; dt_bias, Dskip [D];
 h0, h_final [B, D, N]; h_ckpt [B, D, ceil(L/16), N] (state entering every 16th step).  x, dt_raw, z, Bm, Cm are float32 or bfloat16 (all the same);
@@ -37,6 +45,8 @@ SS_ORDER_BDL, SS_ORDER_BLD = 0, 1
 SS_DT_FULL, SS_DT_SHARED = 0, 1
 SS_LA_DECAY_NONE, SS_LA_DECAY_HEAD, SS_LA_DECAY_TOKEN = 0, 1, 2
 SS_Q8_NONE, SS_Q8_FP8, SS_Q8_INT8 = 0, 1, 2
+SS_Q4_MX = 3
+SS_GR_CKPT = 64
 
 ERRORS = {0: "SS_OK", -1: "SS_ERR_NULL", -2: "SS_ERR_DIMS", -3: "SS_ERR_DTYPE", -4: "SS_ERR_ALIGN",
           -5: "SS_ERR_WORKSPACE", -6: "SS_ERR_HIP", -7: "SS_ERR_UNSUPPORTED", -8: "SS_ERR_SCRATCH"}
@@ -46,7 +56,9 @@ EXPORTS = ("ss_fwd", "ss_bwd", "ss_step", "ss_fwd_workspace_size", "ss_bwd_works
            "ss_last_hip_error", "ss_version", "ss_build_id", "ss_fwd_noalloc",
            "ss_la_fwd", "ss_la_bwd", "ss_la_step", "ss_la_fwd_workspace_size",
            "ss_la_bwd_workspace_size", "ss_rms_fwd", "ss_rms_bwd", "ss_rms_bwd_workspace_size",
-           "ss_q4_mv")
+           "ss_q4_mv", "ss_gr_fwd", "ss_gr_bwd", "ss_gr_step", "ss_gr_fwd_workspace_size",
+           "ss_gr_bwd_workspace_size", "ss_ln_fwd", "ss_ln_bwd", "ss_ln_bwd_workspace_size",
+           "ss_mx4_quant", "ss_mx4_mm")
 
 
 class ss_dims(ctypes.Structure):
@@ -79,6 +91,22 @@ class ss_q4_dims(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
                 ("group", ctypes.c_int32), ("in_dtype", ctypes.c_int32), ("x_q8", ctypes.c_int32),
                 ("y_dtype", ctypes.c_int32)]
+
+
+class ss_gr_dims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("x_stride", ctypes.c_int64 * 2), ("r_stride", ctypes.c_int64 * 2),
+                ("i_stride", ctypes.c_int64 * 2), ("in_dtype", ctypes.c_int32),
+                ("c", ctypes.c_float)]
+
+
+class ss_ln_dims(ctypes.Structure):
+    _fields_ = list(ss_rms_dims._fields_)
+
+
+class ss_mx4_dims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("in_dtype", ctypes.c_int32), ("x_q8", ctypes.c_int32), ("y_dtype", ctypes.c_int32)]
 
 
 class SSError(RuntimeError):
@@ -150,6 +178,29 @@ def load(path: str = LIB, expect: str = None):
     lib.ss_rms_bwd_workspace_size.restype = ctypes.c_int
     lib.ss_q4_mv.argtypes = [ctypes.POINTER(ss_q4_dims)] + [P] * 7
     lib.ss_q4_mv.restype = ctypes.c_int
+    GD = ctypes.POINTER(ss_gr_dims)
+    lib.ss_gr_fwd.argtypes = [GD] + [P] * 11 + [ctypes.c_size_t, P]
+    lib.ss_gr_fwd.restype = ctypes.c_int
+    lib.ss_gr_bwd.argtypes = [GD] + [P] * 16 + [ctypes.c_size_t, P]
+    lib.ss_gr_bwd.restype = ctypes.c_int
+    lib.ss_gr_step.argtypes = [GD] + [P] * 8
+    lib.ss_gr_step.restype = ctypes.c_int
+    lib.ss_gr_fwd_workspace_size.argtypes = [GD, ctypes.POINTER(ctypes.c_size_t)]
+    lib.ss_gr_fwd_workspace_size.restype = ctypes.c_int
+    lib.ss_gr_bwd_workspace_size.argtypes = [GD, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]
+    lib.ss_gr_bwd_workspace_size.restype = ctypes.c_int
+    ND = ctypes.POINTER(ss_ln_dims)
+    lib.ss_ln_fwd.argtypes = [ND] + [P] * 8
+    lib.ss_ln_fwd.restype = ctypes.c_int
+    lib.ss_ln_bwd.argtypes = [ND] + [P] * 8 + [ctypes.c_size_t, P]
+    lib.ss_ln_bwd.restype = ctypes.c_int
+    lib.ss_ln_bwd_workspace_size.argtypes = [ND, ctypes.POINTER(ctypes.c_size_t)]
+    lib.ss_ln_bwd_workspace_size.restype = ctypes.c_int
+    MD = ctypes.POINTER(ss_mx4_dims)
+    lib.ss_mx4_quant.argtypes = [MD] + [P] * 4
+    lib.ss_mx4_quant.restype = ctypes.c_int
+    lib.ss_mx4_mm.argtypes = [MD] + [P] * 6
+    lib.ss_mx4_mm.restype = ctypes.c_int
     lib.ss_strerror.argtypes = [ctypes.c_int]
     lib.ss_strerror.restype = ctypes.c_char_p
     lib.ss_last_hip_error.restype = ctypes.c_int
@@ -864,6 +915,380 @@ def ss_q4_mv(x, wq, scales, zeros=None, *, group=128, x_scale=None, y=None, y_dt
             _check(y, "y", (*lead, N), y_dtype, dev)
         rc = lib.ss_q4_mv(dims, _addr(x), _addr(x_scale), _addr(wq), _addr(scales), _addr(zeros),
                           _addr(y), _raw_stream(dev))
+    if rc != 0:
+        raise SSError(rc, lib)
+    return y
+
+
+# ---- gated linear recurrence -------------------------------------------------------------------
+
+def make_gr_dims(batch, seqlen, dim, in_dtype=SS_BF16, c=8.0, x_stride=(0, 0), r_stride=(0, 0),
+                 i_stride=(0, 0)):
+    T2 = ctypes.c_int64 * 2
+    return ss_gr_dims(batch, seqlen, dim, T2(*x_stride), T2(*r_stride), T2(*i_stride), in_dtype, c)
+
+
+def gr_workspace_size(dims, backward=False, given_ckpt=False) -> int:
+    lib = load()
+    n = ctypes.c_size_t(0)
+    if backward:
+        rc = lib.ss_gr_bwd_workspace_size(ctypes.byref(dims), int(given_ckpt), ctypes.byref(n))
+    else:
+        rc = lib.ss_gr_fwd_workspace_size(ctypes.byref(dims), ctypes.byref(n))
+    if rc != 0:
+        raise SSError(rc, lib)
+    return n.value
+
+
+@functools.lru_cache(maxsize=512)
+def _gr_plan(key, backward, given_ckpt):
+    """The dims structure of a call's shapes and strides, and the workspace they need."""
+    dims = make_gr_dims(*key)
+    return dims, gr_workspace_size(dims, backward, given_ckpt)
+
+
+def _gr_rows(t, name, shape, dtype, device):
+    """Checks an operand [B, T, D] (the step's [B, D]) that may be strided; its strides of batch
+    row and token."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device or t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}, expected {dtype} "
+                         f"{tuple(shape)} on {device}")
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous, got strides {st}")
+    if not any(st[:-1]) and t.numel() > shape[-1]:
+        raise ValueError(f"{name}: one row broadcast over every axis is not taken")
+    return st[:2] if len(st) == 3 else (st[0], st[0])
+
+
+def _gr_key(x, r, i, lam, c, step):
+    """Checks the inputs that the three calls share; the key of their dims, and (B, T, D)."""
+    import torch
+    nd = 2 if step else 3
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    if x.dim() != nd or x.numel() == 0:
+        raise ValueError(f"x must be {nd}-D and hold something, got shape {tuple(x.shape)}")
+    dev, dt, shape = x.device, x.dtype, x.shape
+    D = shape[-1]
+    B, T = (shape[0], 1) if step else shape[:2]
+    key = (B, T, D, _in_dtype(x, "x"), float(c), _gr_rows(x, "x", shape, dt, dev),
+           _gr_rows(r, "r", shape, dt, dev), _gr_rows(i, "i", shape, dt, dev))
+    _check(lam, "lam", (D,), torch.float32, dev)
+    return key, (B, T, D)
+
+
+def _gr_marks(lengths, reset, B, T, device):
+    import torch
+    _check(lengths, "lengths", (B,), torch.int32, device)
+    if reset is not None:
+        if getattr(reset, "dtype", None) not in (torch.bool, torch.uint8):
+            raise ValueError("reset must be a bool or uint8 tensor")
+        _check(reset, "reset", (B, T), reset.dtype, device)
+
+
+def ss_gr_fwd(x, r, i, lam, h0=None, *, c=8.0, lengths=None, reset=None, return_final=False,
+              return_ckpt=False, y=None, h_final=None, h_ckpt=None, workspace=None, stream=None):
+    """Gated linear recurrence through the C ABI: a_t = exp(-c softplus(lam) sigmoid(r_t)),
+    h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t, y_t = h_t.  x, r, i [B, T, D] (float32 or
+    bfloat16, may be strided slices with a contiguous last axis), lam [D], h0 [B, D] float32,
+    lengths [B] int32, reset [B, T] bool or uint8 (tokens that begin a document).  Returns y
+    [B, T, D] in x's type, followed by h_final [B, D] with return_final (or when h_final is passed;
+    it may be h0, updated in place) and by h_ckpt [B, ceil(T / 64), D], the states that enter every
+    64th token, with return_ckpt (or when h_ckpt is passed)."""
+    import torch
+    lib = load()
+    key, (B, T, D) = _gr_key(x, r, i, lam, c, False)
+    dims, need = _gr_plan(key, False, False)
+    dev, f32 = x.device, torch.float32
+    _check(h0, "h0", (B, D), f32, dev)
+    _gr_marks(lengths, reset, B, T, dev)
+    with _on(dev, stream, (x, r, i, lam, h0, lengths, reset, y, h_final, h_ckpt, workspace)):
+        if y is None:
+            y = torch.empty((B, T, D), dtype=x.dtype, device=dev)
+        else:
+            _check(y, "y", (B, T, D), x.dtype, dev)
+        if return_final and h_final is None:
+            h_final = torch.empty((B, D), dtype=f32, device=dev)
+        else:
+            _check(h_final, "h_final", (B, D), f32, dev)
+        nc = -(-T // SS_GR_CKPT)
+        if return_ckpt and h_ckpt is None:
+            h_ckpt = torch.empty((B, nc, D), dtype=f32, device=dev)
+        else:
+            _check(h_ckpt, "h_ckpt", (B, nc, D), f32, dev)
+        if workspace is None and need > 0:
+            workspace = _bytes(need, dev)
+        wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        rc = lib.ss_gr_fwd(dims, _addr(x), _addr(r), _addr(i), _addr(lam), _addr(h0),
+                           _addr(lengths), _addr(reset), _addr(y), _addr(h_final), _addr(h_ckpt),
+                           _addr(workspace), wbytes, _raw_stream(dev))
+    if rc != 0:
+        raise SSError(rc, lib)
+    out = (y,) + ((h_final,) if h_final is not None else ()) + ((h_ckpt,) if h_ckpt is not None else ())
+    return out if len(out) > 1 else y
+
+
+def ss_gr_bwd(x, r, i, lam, dy, h0=None, dh_final=None, *, c=8.0, lengths=None, reset=None,
+              h_ckpt=None, workspace=None, out=None, stream=None):
+    """Gradients of ss_gr_fwd through the C ABI: dy [B, T, D] in x's type, dh_final [B, D] float32;
+    h_ckpt as the forward gave it for the same inputs (None: the states are formed once more).
+    Returns a dict dx, dr, di (x's type, dense), dlam [D], dh0 [B, D] (None without h0), float32.
+    out: a dict of tensors to take them; its dh0 may be dh_final."""
+    import torch
+    lib = load()
+    key, (B, T, D) = _gr_key(x, r, i, lam, c, False)
+    dims, need = _gr_plan(key, True, h_ckpt is not None)
+    dev, dt, f32 = x.device, x.dtype, torch.float32
+    _check(dy, "dy", (B, T, D), dt, dev)
+    _check(h0, "h0", (B, D), f32, dev)
+    _check(dh_final, "dh_final", (B, D), f32, dev)
+    _check(h_ckpt, "h_ckpt", (B, -(-T // SS_GR_CKPT), D), f32, dev)
+    _gr_marks(lengths, reset, B, T, dev)
+    g = {} if out is None else dict(out)
+    with _on(dev, stream, (x, r, i, lam, dy, h0, dh_final, lengths, reset, h_ckpt, workspace,
+                           *g.values())):
+        for name, shape, t in (("dx", (B, T, D), dt), ("dr", (B, T, D), dt), ("di", (B, T, D), dt),
+                               ("dlam", (D,), f32), ("dh0", None if h0 is None else (B, D), f32)):
+            if shape is None:
+                g[name] = None
+            elif g.get(name) is None:
+                g[name] = torch.empty(shape, dtype=t, device=dev)
+            else:
+                _check(g[name], name, shape, t, dev)
+        if workspace is None:
+            workspace = _bytes(need, dev)
+        wbytes = workspace.numel() * workspace.element_size()
+        rc = lib.ss_gr_bwd(dims, _addr(x), _addr(r), _addr(i), _addr(lam), _addr(h0),
+                           _addr(lengths), _addr(reset), _addr(dy), _addr(dh_final),
+                           _addr(h_ckpt), _addr(g["dx"]), _addr(g["dr"]), _addr(g["di"]),
+                           _addr(g["dlam"]), _addr(g["dh0"]), _addr(workspace), wbytes,
+                           _raw_stream(dev))
+    if rc != 0:
+        raise SSError(rc, lib)
+    return g
+
+
+def ss_gr_step(x, r, i, lam, h, *, c=8.0, h_out=None, y=None, stream=None):
+    """One token through the C ABI: x, r, i [B, D], h [B, D] float32, the state before the token.
+    The state after it goes to h_out (default: h itself, updated in place).  Returns y [B, D] in
+    x's type."""
+    import torch
+    lib = load()
+    key, (B, _, D) = _gr_key(x, r, i, lam, c, True)
+    dims, _ = _gr_plan(key, False, False)
+    dev = x.device
+    if h is None:
+        raise TypeError("h must be a torch.Tensor")
+    _check(h, "h", (B, D), torch.float32, dev)
+    with _on(dev, stream, (x, r, i, lam, h, h_out, y)):
+        if h_out is None:
+            h_out = h
+        else:
+            _check(h_out, "h_out", (B, D), torch.float32, dev)
+        if y is None:
+            y = torch.empty((B, D), dtype=x.dtype, device=dev)
+        else:
+            _check(y, "y", (B, D), x.dtype, dev)
+        rc = lib.ss_gr_step(dims, _addr(x), _addr(r), _addr(i), _addr(lam), _addr(h), _addr(h_out),
+                            _addr(y), _raw_stream(dev))
+    if rc != 0:
+        raise SSError(rc, lib)
+    return y
+
+
+# ---- layer norm with the residual's addition -----------------------------------------------------
+
+def make_ln_dims(rows, dim, in_dtype=SS_BF16, res_dtype=SS_BF16, q8=SS_Q8_NONE, eps=1e-5):
+    return ss_ln_dims(rows, dim, in_dtype, res_dtype, q8, eps)
+
+
+def ln_workspace_size(dims) -> int:
+    lib = load()
+    n = ctypes.c_size_t(0)
+    rc = lib.ss_ln_bwd_workspace_size(ctypes.byref(dims), ctypes.byref(n))
+    if rc != 0:
+        raise SSError(rc, lib)
+    return n.value
+
+
+@functools.lru_cache(maxsize=512)
+def _ln_plan(key, backward):
+    dims = make_ln_dims(*key)
+    return dims, ln_workspace_size(dims) if backward else 0
+
+
+def ss_ln_fwd(x, w, b=None, res=None, *, eps=1e-5, q8=SS_Q8_NONE, y=None, y_scale=None, r=None,
+              stream=None):
+    """y = (r - mean(r)) / sqrt(var(r) + eps) · w + b with r = x + res, over the last axis, through
+    the C ABI; types and returns as for ss_rms_fwd.  With q8 = SS_Q4_MX (D a multiple of 32) y holds
+    codes [..., D / 2] and y_scale exponents [..., D / 32], both uint8, as ss_mx4_quant gives
+    them."""
+    import torch
+    lib = load()
+    M, D = _rows_of(x, "x")
+    dev, shape, f32, u8 = x.device, tuple(x.shape), torch.float32, torch.uint8
+    dt = _in_dtype(x, "x")
+    _check(x, "x", shape, x.dtype, dev)
+    _check(w, "w", (D,), f32, dev)
+    _check(b, "b", (D,), f32, dev)
+    rdt = x.dtype if res is None else res.dtype
+    _check(res, "res", shape, rdt, dev)
+    dims, _ = _ln_plan((M, D, dt, dt if res is None else _in_dtype(res, "res"), q8, float(eps)), False)
+    with _on(dev, stream, (x, w, b, res, y, y_scale, r)):
+        if q8 == SS_Q4_MX:
+            if D % 32 != 0:
+                raise ValueError(f"blocks of 32 need a width that is a multiple of 32, got {D}")
+            ys, yt, ss, st = (*shape[:-1], D // 2), u8, (*shape[:-1], D // 32), u8
+        else:
+            yt = {SS_Q8_FP8: torch.float8_e4m3fn, SS_Q8_INT8: torch.int8}.get(q8, x.dtype)
+            ys, ss, st = shape, shape[:-1], f32
+        if y is None:
+            y = torch.empty(ys, dtype=yt, device=dev)
+        else:
+            _check(y, "y", ys, yt, dev)
+        if q8 != SS_Q8_NONE:
+            if y_scale is None:
+                y_scale = torch.empty(ss, dtype=st, device=dev)
+            else:
+                _check(y_scale, "y_scale", ss, st, dev)
+        if res is not None:
+            if r is None:
+                r = torch.empty(shape, dtype=rdt, device=dev)
+            else:
+                _check(r, "r", shape, rdt, dev)
+        rc = lib.ss_ln_fwd(dims, _addr(x), _addr(res), _addr(w), _addr(b), _addr(r), _addr(y),
+                           _addr(y_scale), _raw_stream(dev))
+    if rc != 0:
+        raise SSError(rc, lib)
+    out = (y,) if q8 == SS_Q8_NONE else (y, y_scale)
+    if res is not None:
+        out += (r,)
+    return out if len(out) > 1 else y
+
+
+def ss_ln_bwd(dy, r, w, dr=None, *, eps=1e-5, bias=True, dx=None, dw=None, db=None,
+              workspace=None, stream=None):
+    """Gradients of ss_ln_fwd through the C ABI, as ss_rms_bwd's.  Returns dx (like r: the gradient
+    of x and of res), dw [D] and db [D] float32 (None where bias is false)."""
+    import torch
+    lib = load()
+    M, D = _rows_of(r, "r")
+    dev, shape, f32 = r.device, tuple(r.shape), torch.float32
+    _check(r, "r", shape, r.dtype, dev)
+    _check(dy, "dy", shape, dy.dtype, dev)
+    _check(w, "w", (D,), f32, dev)
+    _check(dr, "dr", shape, r.dtype, dev)
+    dims, need = _ln_plan((M, D, _in_dtype(dy, "dy"), _in_dtype(r, "r"), SS_Q8_NONE, float(eps)), True)
+    if db is not None and not bias:
+        raise ValueError("db goes with bias=True")
+    with _on(dev, stream, (dy, r, w, dr, dx, dw, db, workspace)):
+        if dx is None:
+            dx = torch.empty(shape, dtype=r.dtype, device=dev)
+        else:
+            _check(dx, "dx", shape, r.dtype, dev)
+        if dw is None:
+            dw = torch.empty((D,), dtype=f32, device=dev)
+        else:
+            _check(dw, "dw", (D,), f32, dev)
+        if db is None and bias:
+            db = torch.empty((D,), dtype=f32, device=dev)
+        else:
+            _check(db, "db", (D,), f32, dev)
+        if workspace is None:
+            workspace = _bytes(need, dev)
+        wbytes = workspace.numel() * workspace.element_size()
+        rc = lib.ss_ln_bwd(dims, _addr(dy), _addr(r), _addr(w), _addr(dr), _addr(dx), _addr(dw),
+                           _addr(db), _addr(workspace), wbytes, _raw_stream(dev))
+    if rc != 0:
+        raise SSError(rc, lib)
+    return dx, dw, db
+
+
+# ---- microscaled 4-bit values and their products ---------------------------------------------------
+
+def make_mx4_dims(rows, n, k, in_dtype=SS_BF16, x_q8=SS_Q4_MX, y_dtype=SS_BF16):
+    return ss_mx4_dims(rows, n, k, in_dtype, x_q8, y_dtype)
+
+
+@functools.lru_cache(maxsize=512)
+def _mx4_plan(key):
+    return make_mx4_dims(*key)
+
+
+def ss_mx4_quant(x, *, codes=None, exps=None, stream=None):
+    """x [..., K] (float32 or bfloat16, K a multiple of 32) in 4 bits with a power of two for every
+    32 columns, through the C ABI: codes [..., K / 2] uint8, two e2m1 codes a byte, the first in the
+    low half, and exponents exps [..., K / 32] uint8."""
+    import torch
+    lib = load()
+    M, K = _rows_of(x, "x")
+    dev, lead, u8 = x.device, tuple(x.shape[:-1]), torch.uint8
+    dt = _in_dtype(x, "x")
+    if K % 32 != 0:
+        raise ValueError(f"blocks of 32 need a width that is a multiple of 32, got {K}")
+    _check(x, "x", (*lead, K), x.dtype, dev)
+    dims = _mx4_plan((M, 1, K, dt))
+    with _on(dev, stream, (x, codes, exps)):
+        if codes is None:
+            codes = torch.empty((*lead, K // 2), dtype=u8, device=dev)
+        else:
+            _check(codes, "codes", (*lead, K // 2), u8, dev)
+        if exps is None:
+            exps = torch.empty((*lead, K // 32), dtype=u8, device=dev)
+        else:
+            _check(exps, "exps", (*lead, K // 32), u8, dev)
+        rc = lib.ss_mx4_quant(dims, _addr(x), _addr(codes), _addr(exps), _raw_stream(dev))
+    if rc != 0:
+        raise SSError(rc, lib)
+    return codes, exps
+
+
+def ss_mx4_mm(x, x_scale, wq, w_exps, *, y=None, y_dtype=None, stream=None):
+    """y = x · Wᵀ through the C ABI, W in ss_mx4_quant's format: wq [N, K / 2], w_exps [N, K / 32]
+    uint8.  x is in it too (codes [..., K / 2], x_scale its exponents [..., K / 32]), or
+    float8_e4m3fn [..., K] with x_scale [...] float32 as the norms give it.  Returns y [..., N] in
+    y_dtype (default bfloat16)."""
+    import torch
+    lib = load()
+    dev, u8 = x.device, torch.uint8
+    lead = tuple(x.shape[:-1])
+    M, K = _rows_of(x, "x")
+    if x.dtype == u8:
+        K *= 2
+        q8 = SS_Q4_MX
+        _check(x_scale, "x_scale", (*lead, K // 32), u8, dev)
+    elif x.dtype == torch.float8_e4m3fn:
+        q8 = SS_Q8_FP8
+        _check(x_scale, "x_scale", lead, torch.float32, dev)
+    else:
+        raise ValueError(f"x must be uint8 codes or float8_e4m3fn, got {x.dtype}")
+    if x_scale is None:
+        raise TypeError("x_scale must be a torch.Tensor")
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    if wq.dim() != 2:
+        raise ValueError(f"wq must be [N, K / 2], got {tuple(wq.shape)}")
+    N = wq.shape[0]
+    _check(wq, "wq", (N, K // 2), u8, dev)
+    _check(w_exps, "w_exps", (N, K // 32), u8, dev)
+    if y is not None:
+        y_dtype = y.dtype
+    elif y_dtype is None:
+        y_dtype = torch.bfloat16
+    if y_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"y dtype must be float32 or bfloat16, got {y_dtype}")
+    dims = _mx4_plan((M, N, K, SS_BF16, q8, SS_F32 if y_dtype == torch.float32 else SS_BF16))
+    with _on(dev, stream, (x, x_scale, wq, w_exps, y)):
+        if y is None:
+            y = torch.empty((*lead, N), dtype=y_dtype, device=dev)
+        else:
+            _check(y, "y", (*lead, N), y_dtype, dev)
+        rc = lib.ss_mx4_mm(dims, _addr(x), _addr(x_scale), _addr(wq), _addr(w_exps), _addr(y),
+                           _raw_stream(dev))
     if rc != 0:
         raise SSError(rc, lib)
     return y

@@ -115,4 +115,26 @@ __device__ __forceinline__ void store8(float* __restrict__ p, const float (&v)[8
     *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
 }
 
+// ---- microscaled 4-bit values ----------------------------------------------------------
+// Stored exponent of a block whose largest magnitude has the bit pattern `top` (they order like the
+// magnitudes, infinities and NaN above all): its power of two over 4, e2m1's largest; 255 = NaN.
+__device__ __forceinline__ int mx4_exponent(uint32_t top) {
+    const int e = int(top >> 23) - 2;
+    return top >= 0x7f800000u ? 255 : e < 1 ? 1 : e;
+}
+
+// Eight e2m1 codes of v / 2^(e - 127), the first in the low bits, and e: to the nearest, ties to the
+// even code, past 6 to 6 (the instruction's own rounding, compared with the thresholds 0.25,
+// 0.75, ... over scales of 2^-126 to 2^125).
+__device__ __forceinline__ uint32_t mx4_codes8(const float (&v)[8], uint32_t top, int& e) {
+    e = mx4_exponent(top);
+    const float scale = __uint_as_float(uint32_t(e) << 23);
+    uint32_t q = 0;
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[0], v[1], scale, 0);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[2], v[3], scale, 1);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[4], v[5], scale, 2);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[6], v[7], scale, 3);
+    return e == 255 ? 0u : q;
+}
+
 }  // namespace ss

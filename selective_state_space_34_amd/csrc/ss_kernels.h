@@ -279,6 +279,14 @@ struct RmsLaunch {
 hipError_t launch_rms_fwd(const RmsLaunch& p, hipStream_t s);
 hipError_t launch_rms_bwd(const RmsLaunch& p, float* dw, hipStream_t s);
 
+// Layer norm: as above, with the bias b (nullable); backward: part [grid, 2 D], the sums behind dw
+// and db.  q8 may be SS_Q4_MX: y holds 4-bit codes and y_scale the blocks' exponents, in bytes.
+struct LnLaunch : RmsLaunch {
+    const float* b;
+};
+hipError_t launch_ln_fwd(const LnLaunch& p, hipStream_t s);
+hipError_t launch_ln_bwd(const LnLaunch& p, float* dw, float* db, hipStream_t s);
+
 // ---- products with 4-bit weights (ss_q4.hip) -----------------------------------------------------
 
 struct Q4Launch {
@@ -293,6 +301,65 @@ struct Q4Launch {
     int group, in_dtype, x_q8, y_dtype;
 };
 hipError_t launch_q4(const Q4Launch& p, hipStream_t s);
+
+// ---- gated recurrence (ss_gr.hip) ----------------------------------------------------------------
+
+// Rows of a [B, T, D] operand with a contiguous last axis.
+struct GrRows {
+    const void* p;
+    int64_t sb, st;            // elements from batch row to batch row, token to token
+};
+
+struct GrLaunch {
+    GrRows x, r, i;
+    const float *lam, *h0;     // [D]; nullable [B, D]
+    const int32_t* lengths;    // nullable [B]
+    const uint8_t* reset;      // nullable [B, T]
+    int64_t B, T, D;
+    float c;
+    int in_dtype, vec;         // vec: two neighbouring channels load as one
+    // forward
+    void* y;                   // nullable
+    float *h_final, *h_ckpt;   // nullable
+    // backward (h_ckpt is read)
+    const void* dy;
+    const float* dh_final;     // nullable
+    void *dx, *dr, *di;
+    float *dh0, *part, *dlam;  // nullable; [parts, D]; [D]
+};
+hipError_t launch_gr_fwd(const GrLaunch& p, hipStream_t s);
+hipError_t launch_gr_bwd(const GrLaunch& p, hipStream_t s);
+
+struct GrStep {
+    GrRows x, r, i;            // st unused
+    const float *lam, *h_in;
+    float* h_out;
+    void* y;
+    int64_t B, D;
+    float c;
+    int in_dtype, vec;
+};
+hipError_t launch_gr_step(const GrStep& p, hipStream_t s);
+
+// ---- microscaled 4-bit values (ss_mx4.hip) -------------------------------------------------------
+
+struct Mx4Quant {
+    const void* x;               // [M, K]
+    uint8_t *codes, *exps;       // [M, K / 2], [M, K / 32]
+    int64_t blocks;              // M·K / 32
+    int in_dtype;
+};
+hipError_t launch_mx4_quant(const Mx4Quant& p, hipStream_t s);
+
+struct Mx4Launch {
+    const uint8_t* x;            // [M, K / 2] codes, or [M, K] e4m3
+    const void* x_scale;         // [M, K / 32] exponents, or [M] float32
+    const uint8_t *wq, *w_exps;  // [N, K / 2], [N, K / 32]
+    void* y;                     // [M, N]
+    int64_t M, N, K;
+    int fp8, y_dtype;
+};
+hipError_t launch_mx4_mm(const Mx4Launch& p, hipStream_t s);
 
 // Records a failed HIP call for ss_last_hip_error; returns SS_ERR_HIP.
 int hip_fail(hipError_t e);
