@@ -384,7 +384,7 @@ int ss_q4_mv(const ss_q4_dims* dims, const void* x, const float* x_scale, const 
  *   x, r, i : [B, T, D] (in_dtype), the input and the two gates before their sigmoids.  They may
  *          be strided: dims.*_stride are elements from batch row to batch row and token to token
  *          (the last axis is contiguous); both 0 means dense.  A token stride of less than D (an
- *          expanded or overlapping operand) is taken too.  They need only their type's alignment.
+ *          expanded or overlapping operand) is taken too; the most is 2^25.  They need only their type's alignment.
  *   y, and the gradients of x, r, i : [B, T, D] dense, in_dtype, each rounded once.
  *   lam, dlam [D], h0, h_final, dh_final, dh0 [B, D], h_ckpt [B, ceil(T / SS_GR_CKPT), D] : float32.
  *   lengths : NULL, or [B] int32 on the device: row b has lengths[b] tokens (clamped to [0, T]).
@@ -397,9 +397,9 @@ int ss_q4_mv(const ss_q4_dims* dims, const void* x, const float* x_scale, const 
 #define SS_GR_CKPT 64   /* tokens from one of h_ckpt's states to the next */
 
 typedef struct ss_gr_dims {
-    int64_t batch;        /* B >= 1 */
-    int64_t seqlen;       /* T >= 1 */
-    int64_t dim;          /* D >= 1 */
+    int64_t batch;        /* B: 1 .. 65535 */
+    int64_t seqlen;       /* T >= 1; B · ceil(D / 128) · ceil(T / 64) < 2^23 (forward: T / 128) */
+    int64_t dim;          /* D: 1 .. 2^24 */
     int64_t x_stride[2];  /* batch row, token; both 0: dense */
     int64_t r_stride[2];
     int64_t i_stride[2];

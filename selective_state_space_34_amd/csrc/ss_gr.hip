@@ -8,6 +8,7 @@
 //   ∂/∂log a = g (a h_{t-1} - a²/s v)     dr = ∂/∂log a · log a·(1 - σ(r))
 //   dlam = -c σ(lam) Σ ∂/∂log a · σ(r)
 #include "ss_device.h"
+#include "ss_gr_plan.h"
 #include "ss_kernels.h"
 
 namespace ss {
@@ -35,18 +36,58 @@ __device__ __forceinline__ float one_less_square(float t2, float a) {
     return fabsf(t2) < kSSwitch ? -t2 * p : fmaf(-a, a, 1.0f);
 }
 
-// Two channels of a token as they lie in memory.  kVec: neighbours c0 + 2·lane + {0, 1}, one
-// load; else c0 + lane and c0 + 64 + lane.  Channels behind the last one load that one's value.
+// Two channels of a token as they lie in memory, through a buffer descriptor over a wave's rows:
+// what lies behind the last token loads as 0 and is not stored.  kVec: neighbours c0 + 2·lane +
+// {0, 1}, one access; else c0 + lane and c0 + 64 + lane.
+constexpr int kRsrcFlags = 0x00020000;   // raw buffer, 32-bit elements
+constexpr int kNowhere = int(0x80000000u);   // behind every descriptor's end
+
+struct Cols {
+    int ch[2];           // clamped to the last channel, so that loads have a place
+    bool on[2];
+};
+template <bool kVec>
+__device__ __forceinline__ Cols columns(int64_t c0, int lane, int64_t D) {
+    Cols c;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int ch = int(c0) + (kVec ? 2 * lane + j : lane + 64 * j), n = int(D);
+        c.on[j] = ch < n;
+        // with kVec D is even: a pair is in or out as a whole
+        c.ch[j] = ch < n ? ch : kVec ? n - 2 + j : n - 1;
+    }
+    return c;
+}
+
+// Rows of n tokens (any number, also none) from p on, st elements apart, D wide.
+template <typename T, bool kVec>
+struct Rows {
+    __amdgpu_buffer_rsrc_t d;
+    int step, at[2];
+    __device__ __forceinline__ Rows(const void* p, int64_t st, int64_t n, int64_t D, const Cols& c,
+                                    bool store) {
+        const int bytes = n > 0 ? int(((n - 1) * st + D) * int64_t(sizeof(T))) : 0;
+        d = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, kRsrcFlags);
+        step = int(st) * int(sizeof(T));
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            at[j] = store && !c.on[j] ? kNowhere : c.ch[j] * int(sizeof(T));
+    }
+};
+
 template <typename T> struct Two;
 template <> struct Two<float> {
-    float a, b;
-    __device__ __forceinline__ float get(int j) const { return j ? b : a; }
-    template <bool kVec> __device__ __forceinline__ void load(const float* p, const int (&ch)[2]) {
+    float v[2];
+    __device__ __forceinline__ float get(int j) const { return v[j]; }
+    template <bool kVec> __device__ __forceinline__ void load(const Rows<float, kVec>& r, int s) {
         if constexpr (kVec) {
-            const float2 v = *reinterpret_cast<const float2*>(p + ch[0]);
-            a = v.x; b = v.y;
+            typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+            const u32x2 w = __builtin_amdgcn_raw_buffer_load_b64(r.d, r.at[0], s * r.step, 0);
+            v[0] = __uint_as_float(w[0]); v[1] = __uint_as_float(w[1]);
         } else {
-            a = p[ch[0]]; b = p[ch[1]];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                v[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r.d, r.at[j], s * r.step, 0));
         }
     }
 };
@@ -55,113 +96,268 @@ template <> struct Two<bf16_t> {
     __device__ __forceinline__ float get(int j) const {
         return __uint_as_float(j ? w & 0xffff0000u : w << 16);
     }
-    template <bool kVec> __device__ __forceinline__ void load(const bf16_t* p, const int (&ch)[2]) {
-        if constexpr (kVec) w = *reinterpret_cast<const uint32_t*>(p + ch[0]);
-        else w = uint32_t(p[ch[0]].bits) | uint32_t(p[ch[1]].bits) << 16;
+    template <bool kVec> __device__ __forceinline__ void load(const Rows<bf16_t, kVec>& r, int s) {
+        if constexpr (kVec) {
+            w = __builtin_amdgcn_raw_buffer_load_b32(r.d, r.at[0], s * r.step, 0);
+        } else {
+            const uint32_t a = __builtin_amdgcn_raw_buffer_load_b16(r.d, r.at[0], s * r.step, 0);
+            const uint32_t b = __builtin_amdgcn_raw_buffer_load_b16(r.d, r.at[1], s * r.step, 0);
+            w = a | b << 16;
+        }
     }
 };
 
-// What a lane knows of its two channels.
-struct Cols {
-    int load[2];         // clamped to the last channel
-    bool on[2];
-};
 template <bool kVec>
-__device__ __forceinline__ Cols columns(int64_t c0, int lane, int64_t D) {
-    Cols c;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int64_t ch = c0 + (kVec ? 2 * lane + j : lane + 64 * j);
-        c.on[j] = ch < D;
-        // with kVec D is even: a pair is in or out as a whole
-        c.load[j] = int(ch < D ? ch : kVec ? D - 2 + j : D - 1);
-    }
-    return c;
-}
-
-template <bool kVec>
-__device__ __forceinline__ void store2(float* row, const Cols& c, float a, float b) {
+__device__ __forceinline__ void store2(const Rows<float, kVec>& r, int s, float a, float b) {
     if constexpr (kVec) {
-        if (c.on[0]) *reinterpret_cast<float2*>(row + c.load[0]) = make_float2(a, b);
+        typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+        __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(a), __float_as_uint(b)}, r.d,
+                                              r.at[0], s * r.step, 0);
     } else {
-        if (c.on[0]) row[c.load[0]] = a;
-        if (c.on[1]) row[c.load[1]] = b;
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(a), r.d, r.at[0], s * r.step, 0);
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(b), r.d, r.at[1], s * r.step, 0);
     }
 }
 template <bool kVec>
-__device__ __forceinline__ void store2(bf16_t* row, const Cols& c, float a, float b) {
+__device__ __forceinline__ void store2(const Rows<bf16_t, kVec>& r, int s, float a, float b) {
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
     bf16x2 h;
     h[0] = __bf16(a); h[1] = __bf16(b);
     uint32_t w;
     __builtin_memcpy(&w, &h, 4);
     if constexpr (kVec) {
-        if (c.on[0]) *reinterpret_cast<uint32_t*>(row + c.load[0]) = w;
+        __builtin_amdgcn_raw_buffer_store_b32(w, r.d, r.at[0], s * r.step, 0);
     } else {
-        if (c.on[0]) row[c.load[0]].bits = uint16_t(w);
-        if (c.on[1]) row[c.load[1]].bits = uint16_t(w >> 16);
+        __builtin_amdgcn_raw_buffer_store_b16(uint16_t(w), r.d, r.at[0], s * r.step, 0);
+        __builtin_amdgcn_raw_buffer_store_b16(uint16_t(w >> 16), r.d, r.at[1], s * r.step, 0);
+    }
+}
+
+// One row of float32 (states, partial sums): p + row·D.
+template <bool kVec>
+__device__ __forceinline__ void store_row(float* row, const Cols& c, float a, float b) {
+    if constexpr (kVec) {
+        if (c.on[0]) *reinterpret_cast<float2*>(row + c.ch[0]) = make_float2(a, b);
+    } else {
+        if (c.on[0]) row[c.ch[0]] = a;
+        if (c.on[1]) row[c.ch[1]] = b;
     }
 }
 
 // -c·softplus(lam) in units of log2
 __device__ __forceinline__ float rate2(float lam, float c) { return -c * softplus(lam) * kLog2e; }
 
-// Affine maps h -> A h + H of consecutive stretches, one after the other; an A of 0 cuts off what
-// came before, NaN and infinities included.
+// Affine maps h -> A h + H of consecutive stretches, one after the other.  An A of 0 cuts off what
+// it meets, NaN and infinities included: a document begins there.
+struct Map {
+    float A, H;
+};
 __device__ __forceinline__ float through(float A, float H, float h) {
     return A == 0.0f ? H : fmaf(A, h, H);
 }
+__device__ __forceinline__ Map after(const Map& second, const Map& first) {
+    return Map{first.A == 0.0f ? 0.0f : through(second.A, 0.0f, first.A),
+               through(second.A, second.H, first.H)};
+}
 
-// Which of the kS tokens from t0 on begin a document: bit s for token t0 + s.
-template <int kS>
+// ---- states from tile to tile ----------------------------------------------------------------
+//
+// A workgroup reads its tile once, keeps it in registers, and needs the state that enters it.  It
+// publishes the map of its own tile, then takes those of the tiles before it in its group of
+// kGroup, and what the group before ended with, which that group's last tile publishes.  Maps are
+// joined in the order of the tiles, whoever came first, so results do not depend on timing.
+//
+// A word of 64 bits holds a channel's map (or state, with A = 1) and is stored and loaded in one
+// piece, past the caches of the eight dies (device scope); all ones, which no map has (NaN is
+// stored as 0x7fc00000), means not yet.  So no other memory has to be ordered with it.  Every wait
+// ends: workgroups take their tiles from a counter in the order in which they start to run, and
+// wait for tiles of lower numbers only, whose workgroups run already and publish their maps before
+// they wait themselves.
+constexpr int kGroup = kGrGroup;
+constexpr uint64_t kNotYet = ~uint64_t(0);
+
+__device__ __forceinline__ uint64_t word_of(const Map& m) {
+    const uint32_t a = m.A != m.A ? 0x7fc00000u : __float_as_uint(m.A);
+    return uint64_t(a) << 32 | __float_as_uint(m.H);
+}
+__device__ __forceinline__ Map map_of(uint64_t w) {
+    return Map{__uint_as_float(uint32_t(w >> 32)), __uint_as_float(uint32_t(w))};
+}
+__device__ __forceinline__ void publish(uint64_t* p, const Map& m) {
+    __hip_atomic_store(p, word_of(m), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint64_t peek(const uint64_t* p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// The maps of tiles [from, from + n) of a row (n <= kMost), joined, for the lane's two channels.
+template <int kMost>
+__device__ __forceinline__ void joined(const uint64_t* tiles, int64_t D, const Cols& c, int from, int n,
+                                       Map (&m)[2]) {
+    uint64_t w[kMost][2];
+#pragma unroll
+    for (int q = 0; q < kMost; ++q)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            w[q][j] = q < n ? peek(tiles + int64_t(from + q) * D + c.ch[j]) : 0;
+#pragma unroll
+    for (int q = 0; q < kMost; ++q) {
+        if (q < n) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                while (w[q][j] == kNotYet) {
+                    __builtin_amdgcn_s_sleep(1);
+                    w[q][j] = peek(tiles + int64_t(from + q) * D + c.ch[j]);
+                }
+                m[j] = after(map_of(w[q][j]), m[j]);
+            }
+        }
+    }
+}
+
+// Waits for a load: a tile's map may go out only after the row's first state has come in, since what
+// the row ends with may take its place (h_final over h0, dh0 over dh_final).
+__device__ __forceinline__ void arrived(float v) { asm volatile("" ::"v"(v)); }
+
+// Sets a chain's counter and words (kNotYet) before the launch that uses them.
+__global__ __launch_bounds__(256) void gr_chain_kernel(uint64_t* words, int64_t n, uint64_t* ticket) {
+    const int64_t step = int64_t(gridDim.x) * 256;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += step) words[i] = kNotYet;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *ticket = 0;
+}
+
+// Where a workgroup works: its tile in the chain's order, row and channels.
+struct Place {
+    int tile;
+    int64_t b, c0;
+};
+__device__ __forceinline__ Place place(const GrLaunch& p, int& shared) {
+    const unsigned groups = unsigned((p.D + kCols - 1) / kCols);
+    unsigned n = blockIdx.x;
+    if (p.ticket) {
+        if (threadIdx.x == 0)
+            shared = int(__hip_atomic_fetch_add(reinterpret_cast<unsigned*>(p.ticket), 1u,
+                                                __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+        __syncthreads();
+        n = unsigned(__builtin_amdgcn_readfirstlane(shared));
+    }
+    const unsigned per = groups * unsigned(p.B), in = n % per;
+    return Place{int(n / per), int64_t(in / groups), int64_t(in % groups) * kCols};
+}
+
+// The state that enters tile `tile` of a row, from the one that enters the row; own: the tile's map.
+// Every wave returns it; what leaves a group (or the row: last) is published (stored) by one wave.
+template <bool kVec, int kWaves>
+__device__ __forceinline__ void entering(const GrLaunch& p, const Place& at, const Cols& col, int lane,
+                                         int wave, const Map (&own)[2], float (&h)[2], float* last,
+                                         float (&look)[2][kWaves][kCols], float (&begin)[kCols]) {
+    if (p.ticket) {
+        constexpr int kMost = kGroup / kWaves;
+        const int groups = (p.tiles + kGroup - 1) / kGroup;
+        const int n = at.tile % kGroup, group = at.tile / kGroup;
+        uint64_t* maps = p.maps + at.b * p.tiles * p.D;
+        uint64_t* ends = p.ends + at.b * groups * p.D;
+        if (wave == kWaves - 1 && n < kGroup - 1) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (col.on[j]) publish(maps + int64_t(at.tile) * p.D + col.ch[j], own[j]);
+        }
+        if (n > 0 || group > 0) {
+            Map m[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}};
+            const int lo = n * wave / kWaves, hi = n * (wave + 1) / kWaves;
+            if (hi > lo) joined<kMost>(maps, p.D, col, group * kGroup + lo, hi - lo, m);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                look[0][wave][lane + 64 * j] = m[j].A;
+                look[1][wave][lane + 64 * j] = m[j].H;
+            }
+            if (wave == 0 && group > 0) {
+                Map e[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}};
+                joined<1>(ends, p.D, col, group - 1, 1, e);
+                begin[lane] = e[0].H;
+                begin[lane + 64] = e[1].H;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if (group > 0) h[j] = begin[lane + 64 * j];
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w)
+                    h[j] = through(look[0][w][lane + 64 * j], look[1][w][lane + 64 * j], h[j]);
+            }
+        }
+        if (wave == kWaves - 1 && n == kGroup - 1 && at.tile + 1 < p.tiles) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (col.on[j])
+                    publish(ends + int64_t(group) * p.D + col.ch[j],
+                            Map{1.0f, through(own[j].A, own[j].H, h[j])});
+        }
+    }
+    if (last && wave == kWaves - 1 && at.tile + 1 == p.tiles)
+        store_row<kVec>(last + at.b * p.D, col, through(own[0].A, own[0].H, h[0]),
+                        through(own[1].A, own[1].H, h[1]));
+}
+
+// Which of the `live` tokens from t0 on begin a document: bit s for token t0 + s.
 __device__ __forceinline__ uint32_t reset_bits(const uint8_t* reset, int64_t b, int64_t T,
-                                               int64_t t0, int lane) {
+                                               int64_t t0, int lane, int live) {
     if (!reset) return 0;
     bool set = false;
-    if (lane < kS && t0 + lane < T) set = reset[b * T + t0 + lane] != 0;
+    if (lane < live) set = reset[b * T + t0 + lane] != 0;
     return uint32_t(__ballot(set));
 }
 
-__device__ __forceinline__ int64_t live_tokens(const int32_t* lengths, int64_t b, int64_t T) {
-    if (!lengths) return T;
-    const int64_t n = lengths[b];
-    return n < 0 ? 0 : n < T ? n : T;
+// How many of the kS tokens from t0 on exist in row b.
+template <int kS>
+__device__ __forceinline__ int live_tokens(const int32_t* lengths, int64_t b, int64_t t0, int64_t T) {
+    int64_t n = T;
+    if (lengths) n = lengths[b] < T ? lengths[b] : T;
+    n -= t0;
+    return n < 0 ? 0 : n < kS ? int(n) : kS;
 }
 
 // ---- forward ---------------------------------------------------------------------------------
 
 template <typename T, bool kVec, int kWaves, int kS>
 __global__ __launch_bounds__(64 * kWaves) void gr_fwd_kernel(const GrLaunch p) {
-    __shared__ float sh[2][2][kWaves][kCols];
+    static_assert(SS_GR_CKPT % kS == 0, "checkpoints stand before a wave's first token");
+    __shared__ float sh[2][kWaves][kCols], look[2][kWaves][kCols], begin[kCols];
+    __shared__ int number;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t b = blockIdx.y, D = p.D;
-    const Cols col = columns<kVec>(int64_t(blockIdx.x) * kCols, lane, D);
-    const T* x = static_cast<const T*>(p.x.p) + b * p.x.sb;
-    const T* r = static_cast<const T*>(p.r.p) + b * p.r.sb;
-    const T* g = static_cast<const T*>(p.i.p) + b * p.i.sb;
-    const int64_t live = live_tokens(p.lengths, b, p.T);
+    const Place at = place(p, number);
+    const int64_t b = at.b, D = p.D;
+    const Cols col = columns<kVec>(at.c0, lane, D);
+    const int64_t t0 = (int64_t(at.tile) * kWaves + wave) * kS;
+    const int64_t n = p.T - t0 < kS ? p.T - t0 : kS;
+    Two<T> wx[kS], wr[kS], wi[kS];
+    {
+        const Rows<T, kVec> x(static_cast<const T*>(p.x.p) + b * p.x.sb + t0 * p.x.st, p.x.st, n, D, col, false);
+        const Rows<T, kVec> r(static_cast<const T*>(p.r.p) + b * p.r.sb + t0 * p.r.st, p.r.st, n, D, col, false);
+        const Rows<T, kVec> g(static_cast<const T*>(p.i.p) + b * p.i.sb + t0 * p.i.st, p.i.st, n, D, col, false);
+#pragma unroll
+        for (int s = 0; s < kS; ++s) {
+            wr[s].load(r, s);
+            wi[s].load(g, s);
+            wx[s].load(x, s);
+        }
+    }
+    const int live = live_tokens<kS>(p.lengths, b, t0, p.T);
+    const uint32_t first = reset_bits(p.reset, b, p.T, t0, lane, live);
     float k2[2], h[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        k2[j] = rate2(p.lam[col.load[j]], p.c);
-        h[j] = p.h0 ? p.h0[b * D + col.load[j]] : 0.0f;
+        k2[j] = rate2(p.lam[col.ch[j]], p.c);
+        h[j] = p.h0 ? p.h0[b * D + col.ch[j]] : 0.0f;
     }
-    int slot = 0;
-    for (int64_t tile = 0; tile < p.T; tile += kWaves * kS, slot ^= 1) {
-        const int64_t t0 = tile + wave * kS;
-        Two<T> wx[kS], wr[kS], wi[kS];
+    float a[kS][2], u[kS][2];
+    Map own[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}};
+    // the wave's map; all: every token exists and none begins a document
+    const bool all = first == 0 && live == kS;
+    auto tokens = [&](auto all) {
 #pragma unroll
         for (int s = 0; s < kS; ++s) {
-            const int64_t t = t0 + s < p.T ? t0 + s : p.T - 1;
-            wx[s].template load<kVec>(x + t * p.x.st, col.load);
-            wr[s].template load<kVec>(r + t * p.r.st, col.load);
-            wi[s].template load<kVec>(g + t * p.i.st, col.load);
-        }
-        const uint32_t first = reset_bits<kS>(p.reset, b, p.T, t0, lane);
-        float a[kS][2], u[kS][2], A[2] = {1.0f, 1.0f}, H[2] = {0.0f, 0.0f};
-#pragma unroll
-        for (int s = 0; s < kS; ++s) {
-            const bool cut = first >> s & 1, on = t0 + s < live;
+            const bool cut = !all && (first >> s & 1), on = all || s < live;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const float t2 = k2[j] * sigmoid(wr[s].get(j));
@@ -170,181 +366,202 @@ __global__ __launch_bounds__(64 * kWaves) void gr_fwd_kernel(const GrLaunch p) {
                 const float v = sigmoid(wi[s].get(j)) * wx[s].get(j);
                 a[s][j] = !on ? 1.0f : cut ? 0.0f : e;
                 u[s][j] = !on ? 0.0f : cut ? v : q * v;
-                H[j] = through(a[s][j], u[s][j], H[j]);
-                A[j] *= a[s][j];
+                own[j].H = fmaf(a[s][j], cut ? 0.0f : own[j].H, u[s][j]);
+                own[j].A *= a[s][j];
             }
         }
+    };
+    if (all) tokens(std::true_type{});
+    else tokens(std::false_type{});
+    if (first) own[0].A = own[1].A = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            sh[slot][0][wave][lane + 64 * j] = A[j];
-            sh[slot][1][wave][lane + 64 * j] = H[j];
-        }
-        __syncthreads();
-        float in[2] = {h[0], h[1]};
+    for (int j = 0; j < 2; ++j) {
+        sh[0][wave][lane + 64 * j] = own[j].A;
+        sh[1][wave][lane + 64 * j] = own[j].H;
+        arrived(h[j]);
+    }
+    __syncthreads();
+    // the map of the waves before this one, and of the whole tile
+    Map before[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        Map m = {1.0f, 0.0f};
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                if (w == wave) in[j] = h[j];
-                h[j] = through(sh[slot][0][w][lane + 64 * j], sh[slot][1][w][lane + 64 * j], h[j]);
-            }
+            if (w == wave) before[j] = m;
+            m = after(Map{sh[0][w][lane + 64 * j], sh[1][w][lane + 64 * j]}, m);
         }
-        if (p.h_ckpt && t0 % SS_GR_CKPT == 0 && t0 < p.T) {
-            const int64_t n = (p.T + SS_GR_CKPT - 1) / SS_GR_CKPT;
-            store2<kVec>(p.h_ckpt + (b * n + t0 / SS_GR_CKPT) * D, col, in[0], in[1]);
-        }
-        if (p.y) {
-            T* y = static_cast<T*>(p.y) + b * p.T * D;
+        own[j] = m;
+    }
+    entering<kVec, kWaves>(p, at, col, lane, wave, own, h, p.h_final, look, begin);
 #pragma unroll
-            for (int s = 0; s < kS; ++s) {
+    for (int j = 0; j < 2; ++j) h[j] = through(before[j].A, before[j].H, h[j]);
+    if (p.h_ckpt && t0 % SS_GR_CKPT == 0 && t0 < p.T) {
+        const int64_t nc = (p.T + SS_GR_CKPT - 1) / SS_GR_CKPT;
+        store_row<kVec>(p.h_ckpt + (b * nc + t0 / SS_GR_CKPT) * D, col, h[0], h[1]);
+    }
+    if (p.y) {
+        const Rows<T, kVec> y(static_cast<T*>(p.y) + (b * p.T + t0) * D, D, n, D, col, true);
 #pragma unroll
-                for (int j = 0; j < 2; ++j) in[j] = through(a[s][j], u[s][j], in[j]);
-                const bool on = t0 + s < live;
-                if (t0 + s < p.T)
-                    store2<kVec>(y + (t0 + s) * D, col, on ? in[0] : 0.0f, on ? in[1] : 0.0f);
-            }
+        for (int s = 0; s < kS; ++s) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) h[j] = fmaf(a[s][j], first >> s & 1 ? 0.0f : h[j], u[s][j]);
+            const bool on = s < live;
+            store2(y, s, on ? h[0] : 0.0f, on ? h[1] : 0.0f);
         }
     }
-    if (p.h_final && wave == 0) store2<kVec>(p.h_final + b * D, col, h[0], h[1]);
 }
 
 // ---- backward --------------------------------------------------------------------------------
 
 // The states before a wave's tokens come from the checkpoint that its workgroup's tile starts
-// with; the adjoint c comes from the right.
+// with; the adjoint c comes from the right: the chain's first tile is the row's last.
 template <typename T, bool kVec, int kWaves, int kS>
 __global__ __launch_bounds__(64 * kWaves) void gr_bwd_kernel(const GrLaunch p) {
     static_assert(kWaves * kS == SS_GR_CKPT, "a tile is what one checkpoint starts");
-    __shared__ float sh[2][3][kWaves][kCols];
+    __shared__ float sh[3][kWaves][kCols], look[2][kWaves][kCols], begin[kCols];
+    __shared__ int number;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t b = blockIdx.y, D = p.D, n = (p.T + SS_GR_CKPT - 1) / SS_GR_CKPT;
-    const Cols col = columns<kVec>(int64_t(blockIdx.x) * kCols, lane, D);
-    const T* x = static_cast<const T*>(p.x.p) + b * p.x.sb;
-    const T* r = static_cast<const T*>(p.r.p) + b * p.r.sb;
-    const T* g = static_cast<const T*>(p.i.p) + b * p.i.sb;
-    const T* dy = static_cast<const T*>(p.dy) + b * p.T * D;
-    T* dx = static_cast<T*>(p.dx) + b * p.T * D;
-    T* dr = static_cast<T*>(p.dr) + b * p.T * D;
-    T* di = static_cast<T*>(p.di) + b * p.T * D;
-    const int64_t live = live_tokens(p.lengths, b, p.T);
-    float k2[2], c[2], dl[2] = {0.0f, 0.0f};
+    const Place at = place(p, number);
+    const int64_t b = at.b, D = p.D;
+    const Cols col = columns<kVec>(at.c0, lane, D);
+    const int64_t tile = p.tiles - 1 - at.tile, t0 = tile * SS_GR_CKPT + wave * kS;
+    const int64_t n = p.T - t0 < kS ? p.T - t0 : kS;
+    Two<T> wx[kS], wr[kS], wi[kS], wd[kS];
+    {
+        const Rows<T, kVec> x(static_cast<const T*>(p.x.p) + b * p.x.sb + t0 * p.x.st, p.x.st, n, D, col, false);
+        const Rows<T, kVec> r(static_cast<const T*>(p.r.p) + b * p.r.sb + t0 * p.r.st, p.r.st, n, D, col, false);
+        const Rows<T, kVec> g(static_cast<const T*>(p.i.p) + b * p.i.sb + t0 * p.i.st, p.i.st, n, D, col, false);
+        const Rows<T, kVec> dy(static_cast<const T*>(p.dy) + (b * p.T + t0) * D, D, n, D, col, false);
+#pragma unroll
+        for (int s = 0; s < kS; ++s) {
+            wr[s].load(r, s);
+            wi[s].load(g, s);
+            wx[s].load(x, s);
+            wd[s].load(dy, s);
+        }
+    }
+    const int live = live_tokens<kS>(p.lengths, b, t0, p.T);
+    const uint32_t first = reset_bits(p.reset, b, p.T, t0, lane, live);
+    float k2[2], c[2], h[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        k2[j] = rate2(p.lam[col.load[j]], p.c);
-        c[j] = p.dh_final ? p.dh_final[b * D + col.load[j]] : 0.0f;
+        k2[j] = rate2(p.lam[col.ch[j]], p.c);
+        c[j] = p.dh_final ? p.dh_final[b * D + col.ch[j]] : 0.0f;
+        h[j] = p.h_ckpt[(b * p.tiles + tile) * D + col.ch[j]];
     }
-    int slot = 0;
-    for (int64_t tile = n - 1; tile >= 0; --tile, slot ^= 1) {
-        const int64_t t0 = tile * SS_GR_CKPT + wave * kS;
-        Two<T> wx[kS], wr[kS], wi[kS], wd[kS];
+    float a[kS][2], q[kS][2], sr[kS][2], si[kS][2];
+    Map fwd[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}}, rev[2];
+    // What stands behind a text becomes 0 (and its a 1) before anything is formed from it; a token
+    // that begins a document has a = 0 and s = 1.
+    const bool all = first == 0 && live == kS;
+    auto tokens = [&](auto all) {
 #pragma unroll
         for (int s = 0; s < kS; ++s) {
-            const int64_t t = t0 + s < p.T ? t0 + s : p.T - 1;
-            wx[s].template load<kVec>(x + t * p.x.st, col.load);
-            wr[s].template load<kVec>(r + t * p.r.st, col.load);
-            wi[s].template load<kVec>(g + t * p.i.st, col.load);
-            wd[s].template load<kVec>(dy + t * D, col.load);
-        }
-        float hin[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) hin[j] = p.h_ckpt[(b * n + tile) * D + col.load[j]];
-        const uint32_t first = reset_bits<kS>(p.reset, b, p.T, t0, lane);
-        float a[kS][2], q[kS][2], sr[kS][2], si[kS][2];
-        float A[2] = {1.0f, 1.0f}, H[2] = {0.0f, 0.0f}, G[2] = {0.0f, 0.0f};
-#pragma unroll
-        for (int s = 0; s < kS; ++s) {
-            const bool cut = first >> s & 1, on = t0 + s < live;
+            const bool cut = !all && (first >> s & 1), on = all || s < live;
+            if (!on) wx[s] = wd[s] = Two<T>{};
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                sr[s][j] = sigmoid(wr[s].get(j));
+                sr[s][j] = on ? sigmoid(wr[s].get(j)) : 0.0f;
                 si[s][j] = on ? sigmoid(wi[s].get(j)) : 0.0f;
                 const float t2 = k2[j] * sr[s][j];
                 const float e = exp2_hw(t2);
                 a[s][j] = !on ? 1.0f : cut ? 0.0f : e;
                 q[s][j] = !on ? 0.0f : cut ? 1.0f : __builtin_amdgcn_sqrtf(one_less_square(t2, e));
-                const float v = on ? si[s][j] * wx[s].get(j) : 0.0f;
-                H[j] = through(a[s][j], q[s][j] * v, H[j]);
-                A[j] *= a[s][j];
+                fwd[j].H = fmaf(a[s][j], cut ? 0.0f : fwd[j].H, q[s][j] * (si[s][j] * wx[s].get(j)));
+                fwd[j].A *= a[s][j];
             }
         }
+        rev[0].H = rev[1].H = 0.0f;
 #pragma unroll
         for (int s = kS - 1; s >= 0; --s) {
+            const bool cut = !all && (first >> s & 1);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float d = (t0 + s < live ? wd[s].get(j) : 0.0f) + G[j];
-                G[j] = a[s][j] == 0.0f ? 0.0f : a[s][j] * d;
-            }
+            for (int j = 0; j < 2; ++j)       // c -> a (dy + c)
+                rev[j].H = cut ? 0.0f : a[s][j] * (wd[s].get(j) + rev[j].H);
         }
+    };
+    if (all) tokens(std::true_type{});
+    else tokens(std::false_type{});
+    if (first) fwd[0].A = fwd[1].A = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            sh[slot][0][wave][lane + 64 * j] = A[j];
-            sh[slot][1][wave][lane + 64 * j] = H[j];
-            sh[slot][2][wave][lane + 64 * j] = G[j];
+    for (int j = 0; j < 2; ++j) {
+        sh[0][wave][lane + 64 * j] = fwd[j].A;
+        sh[1][wave][lane + 64 * j] = fwd[j].H;
+        sh[2][wave][lane + 64 * j] = rev[j].H;
+        arrived(c[j]);
+    }
+    __syncthreads();
+    Map right[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        float hh = h[j];
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            if (w == wave) h[j] = hh;
+            hh = through(sh[0][w][lane + 64 * j], sh[1][w][lane + 64 * j], hh);
         }
-        __syncthreads();
-        float cin[2];
+        Map m = {1.0f, 0.0f};
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            float hh = hin[j];
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) {
-                if (w == wave) hin[j] = hh;
-                hh = through(sh[slot][0][w][lane + 64 * j], sh[slot][1][w][lane + 64 * j], hh);
-            }
-#pragma unroll
-            for (int w = kWaves - 1; w >= 0; --w) {
-                if (w == wave) cin[j] = c[j];
-                c[j] = through(sh[slot][0][w][lane + 64 * j], sh[slot][2][w][lane + 64 * j], c[j]);
-            }
+        for (int w = kWaves - 1; w >= 0; --w) {
+            if (w == wave) right[j] = m;
+            m = after(Map{sh[0][w][lane + 64 * j], sh[2][w][lane + 64 * j]}, m);
         }
-        float before[kS][2];
+        rev[j] = m;
+    }
+    entering<kVec, kWaves>(p, at, col, lane, wave, rev, c, p.dh0, look, begin);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) c[j] = through(right[j].A, right[j].H, c[j]);
+    float old[kS][2], dl[2] = {0.0f, 0.0f};
+    const Rows<T, kVec> dx(static_cast<T*>(p.dx) + (b * p.T + t0) * D, D, n, D, col, true);
+    const Rows<T, kVec> dr(static_cast<T*>(p.dr) + (b * p.T + t0) * D, D, n, D, col, true);
+    const Rows<T, kVec> di(static_cast<T*>(p.di) + (b * p.T + t0) * D, D, n, D, col, true);
+    auto gradients = [&](auto all) {
 #pragma unroll
         for (int s = 0; s < kS; ++s) {
+            const bool cut = !all && (first >> s & 1);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                before[s][j] = hin[j];
-                const float v = t0 + s < live ? si[s][j] * wx[s].get(j) : 0.0f;
-                hin[j] = through(a[s][j], q[s][j] * v, hin[j]);
+                old[s][j] = h[j];
+                h[j] = fmaf(a[s][j], cut ? 0.0f : h[j], q[s][j] * (si[s][j] * wx[s].get(j)));
             }
         }
 #pragma unroll
         for (int s = kS - 1; s >= 0; --s) {
-            const bool cut = first >> s & 1, on = t0 + s < live;
+            const bool cut = !all && (first >> s & 1), on = all || s < live;
             float ox[2], orr[2], oi[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const float as = a[s][j], qs = q[s][j], xv = wx[s].get(j);
-                const float gt = (on ? wd[s].get(j) : 0.0f) + cin[j];
-                cin[j] = as == 0.0f ? 0.0f : as * gt;
-                const float gs = gt * qs;
-                ox[j] = on ? gs * si[s][j] : 0.0f;
-                oi[j] = on ? gs * xv * si[s][j] * (1.0f - si[s][j]) : 0.0f;
+                const float as = a[s][j], qs = q[s][j], xv = wx[s].get(j), sg = sr[s][j], sx = si[s][j];
+                const float gt = wd[s].get(j) + c[j], ag = as * gt;
+                c[j] = cut ? 0.0f : ag;
+                ox[j] = gt * qs * sx;
+                oi[j] = ox[j] * xv * (1.0f - sx);
                 // below 1e-15 the root's slope would leave float32; its share is below 1e-15 too
                 const float slope = qs > 1e-15f ? as * rcp_hw(qs) : 0.0f;
-                const float v = si[s][j] * xv;
-                const float dla = on && !cut ? gt * as * fmaf(-slope, v, before[s][j]) : 0.0f;
-                orr[j] = dla * (k2[j] * kLn2) * sr[s][j] * (1.0f - sr[s][j]);
+                const float dla = ag * fmaf(-slope, sx * xv, old[s][j]);
+                orr[j] = dla * (k2[j] * kLn2) * sg * (1.0f - sg);
+                dl[j] = on && !cut ? fmaf(dla, sg, dl[j]) : dl[j];
+                if (!on) ox[j] = oi[j] = 0.0f;
                 if (!on || cut) orr[j] = 0.0f;
-                else dl[j] = fmaf(dla, sr[s][j], dl[j]);
             }
-            if (t0 + s < p.T) {
-                store2<kVec>(dx + (t0 + s) * D, col, ox[0], ox[1]);
-                store2<kVec>(dr + (t0 + s) * D, col, orr[0], orr[1]);
-                store2<kVec>(di + (t0 + s) * D, col, oi[0], oi[1]);
-            }
+            store2(dx, s, ox[0], ox[1]);
+            store2(dr, s, orr[0], orr[1]);
+            store2(di, s, oi[0], oi[1]);
         }
-    }
-    if (p.dh0 && wave == 0) store2<kVec>(p.dh0 + b * D, col, c[0], c[1]);
+    };
+    if (all) gradients(std::true_type{});
+    else gradients(std::false_type{});
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 2; ++j) sh[0][0][wave][lane + 64 * j] = dl[j];
+    for (int j = 0; j < 2; ++j) sh[0][wave][lane + 64 * j] = dl[j];
     __syncthreads();
     if (wave == 0) {
 #pragma unroll
         for (int w = 1; w < kWaves; ++w)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) dl[j] += sh[0][0][w][lane + 64 * j];
-        store2<kVec>(p.part + b * D, col, dl[0], dl[1]);
+            for (int j = 0; j < 2; ++j) dl[j] += sh[0][w][lane + 64 * j];
+        store_row<kVec>(p.part + (b * p.tiles + tile) * D, col, dl[0], dl[1]);
     }
 }
 
@@ -379,19 +596,19 @@ __global__ __launch_bounds__(256) void gr_step_kernel(const GrStep p) {
     if (b >= p.B) return;
     const Cols col = columns<kVec>(int64_t(blockIdx.x) * kCols, lane, D);
     Two<T> x, r, i;
-    x.template load<kVec>(static_cast<const T*>(p.x.p) + b * p.x.sb, col.load);
-    r.template load<kVec>(static_cast<const T*>(p.r.p) + b * p.r.sb, col.load);
-    i.template load<kVec>(static_cast<const T*>(p.i.p) + b * p.i.sb, col.load);
+    x.load(Rows<T, kVec>(static_cast<const T*>(p.x.p) + b * p.x.sb, 0, 1, D, col, false), 0);
+    r.load(Rows<T, kVec>(static_cast<const T*>(p.r.p) + b * p.r.sb, 0, 1, D, col, false), 0);
+    i.load(Rows<T, kVec>(static_cast<const T*>(p.i.p) + b * p.i.sb, 0, 1, D, col, false), 0);
     float h[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        const float t2 = rate2(p.lam[col.load[j]], p.c) * sigmoid(r.get(j));
+        const float t2 = rate2(p.lam[col.ch[j]], p.c) * sigmoid(r.get(j));
         const float a = exp2_hw(t2);
         const float q = __builtin_amdgcn_sqrtf(one_less_square(t2, a));
-        h[j] = fmaf(a, p.h_in[b * D + col.load[j]], q * (sigmoid(i.get(j)) * x.get(j)));
+        h[j] = fmaf(a, p.h_in[b * D + col.ch[j]], q * (sigmoid(i.get(j)) * x.get(j)));
     }
-    store2<kVec>(p.h_out + b * D, col, h[0], h[1]);
-    store2<kVec>(static_cast<T*>(p.y) + b * D, col, h[0], h[1]);
+    store_row<kVec>(p.h_out + b * D, col, h[0], h[1]);
+    store2(Rows<T, kVec>(static_cast<T*>(p.y) + b * D, 0, 1, D, col, true), 0, h[0], h[1]);
 }
 
 template <typename F>
@@ -404,23 +621,41 @@ unsigned groups(int64_t D) { return unsigned((D + kCols - 1) / kCols); }
 
 }  // namespace
 
+namespace {
+
+// The chain's words and counter, where the row has more than one tile.
+hipError_t begin_chain(const GrLaunch& p, hipStream_t s) {
+    if (!p.ticket) return hipSuccess;
+    const int64_t n = p.B * p.D * (p.tiles + (p.tiles + kGroup - 1) / kGroup);
+    const int64_t need = (n + 255) / 256;
+    hipLaunchKernelGGL(gr_chain_kernel, dim3(unsigned(need < 2048 ? need : 2048)), dim3(256), 0, s,
+                       p.maps, n, p.ticket);
+    return hipGetLastError();
+}
+
+}  // namespace
+
 hipError_t launch_gr_fwd(const GrLaunch& p, hipStream_t s) {
+    const hipError_t e = begin_chain(p, s);
+    if (e != hipSuccess) return e;
     return with_type(p.in_dtype, p.vec, [&](auto t, auto v) {
-        hipLaunchKernelGGL((gr_fwd_kernel<decltype(t), decltype(v)::value, 8, 16>),
-                           dim3(groups(p.D), unsigned(p.B)), dim3(512), 0, s, p);
+        hipLaunchKernelGGL((gr_fwd_kernel<decltype(t), decltype(v)::value, 8, kGrFwdTile / 8>),
+                           dim3(groups(p.D) * unsigned(p.B) * unsigned(p.tiles)), dim3(512), 0, s, p);
         return hipGetLastError();
     });
 }
 
 hipError_t launch_gr_bwd(const GrLaunch& p, hipStream_t s) {
-    const hipError_t e = with_type(p.in_dtype, p.vec, [&](auto t, auto v) {
-        hipLaunchKernelGGL((gr_bwd_kernel<decltype(t), decltype(v)::value, 8, 8>),
-                           dim3(groups(p.D), unsigned(p.B)), dim3(512), 0, s, p);
+    hipError_t e = begin_chain(p, s);
+    if (e != hipSuccess) return e;
+    e = with_type(p.in_dtype, p.vec, [&](auto t, auto v) {
+        hipLaunchKernelGGL((gr_bwd_kernel<decltype(t), decltype(v)::value, 8, SS_GR_CKPT / 8>),
+                           dim3(groups(p.D) * unsigned(p.B) * unsigned(p.tiles)), dim3(512), 0, s, p);
         return hipGetLastError();
     });
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(gr_dlam_kernel, dim3(unsigned((p.D + 63) / 64)), dim3(1024), 0, s, p.part,
-                       p.lam, p.dlam, p.c, p.D, p.B);
+                       p.lam, p.dlam, p.c, p.D, p.B * p.tiles);
     return hipGetLastError();
 }
 

@@ -6,21 +6,40 @@
 
 namespace ss {
 
+constexpr int64_t kGrMaxStep = int64_t(1) << 25;   // elements from token to token: 16 tokens' rows
+                                                   // stay within a descriptor's 2^31 bytes
+constexpr int kGrFwdTile = 128;                    // tokens of a workgroup, forward
+constexpr int kGrGroup = 32;                       // tiles of a group
+
+// What links the tiles of a row: a counter, the tiles' maps and the groups' ends.
+struct GrChain {
+    int64_t tiles, groups;
+    size_t off_ticket, off_maps, off_ends;   // tiles > 1
+};
+
 struct GrPlan {
     int64_t B, T, D;
-    int64_t nckpt;              // checkpoints of a row
-    int64_t parts;              // rows of partial sums behind dlam
-    // backward: off_ckpt [B, nckpt, D] where none are given, off_part [parts, D]
+    GrChain fwd, rev;
+    // backward: off_ckpt [B, rev.tiles, D] where none are given, off_part [B, rev.tiles, D]
     size_t off_ckpt, off_part, total;
 };
 
 inline bool gr_strides_ok(const int64_t* s) {
-    const int64_t lim = int64_t(1) << 40;
-    return s[0] >= 0 && s[0] <= lim && s[1] >= 0 && s[1] <= lim;
+    return s[0] >= 0 && s[0] <= (int64_t(1) << 40) && s[1] >= 0 && s[1] <= kGrMaxStep;
+}
+
+inline size_t gr_chain(const GrPlan& p, int64_t tokens, size_t off, GrChain* c) {
+    c->tiles = (p.T + tokens - 1) / tokens;
+    c->groups = (c->tiles + kGrGroup - 1) / kGrGroup;
+    c->off_ticket = off;
+    if (c->tiles <= 1) return off;
+    c->off_maps = off + 256;
+    c->off_ends = c->off_maps + size_t(p.B * c->tiles) * size_t(p.D) * sizeof(uint64_t);
+    return align256(c->off_ends + size_t(p.B * c->groups) * size_t(p.D) * sizeof(uint64_t));
 }
 
 inline int make_gr_plan(const ss_gr_dims& d, bool backward, bool given_ckpt, GrPlan* out) {
-    if (d.batch <= 0 || d.seqlen <= 0 || d.dim <= 0 || d.dim > (int64_t(1) << 28)) return SS_ERR_DIMS;
+    if (d.batch <= 0 || d.seqlen <= 0 || d.dim <= 0 || d.dim > (int64_t(1) << 24)) return SS_ERR_DIMS;
     if (d.in_dtype != SS_F32 && d.in_dtype != SS_BF16) return SS_ERR_DTYPE;
     if (!(d.c > 0.0f) || !(d.c - d.c == 0.0f)) return SS_ERR_DIMS;
     if (!gr_strides_ok(d.x_stride) || !gr_strides_ok(d.r_stride) || !gr_strides_ok(d.i_stride))
@@ -30,15 +49,20 @@ inline int make_gr_plan(const ss_gr_dims& d, bool backward, bool given_ckpt, GrP
     if (d.batch > kMaxGridYZ) return SS_ERR_DIMS;
     GrPlan p{};
     p.B = d.batch; p.T = d.seqlen; p.D = d.dim;
-    if (!launch_ok((p.D + 127) / 128 * p.B, 512)) return SS_ERR_DIMS;
-    p.nckpt = (p.T + SS_GR_CKPT - 1) / SS_GR_CKPT;
     size_t off = 0;
+    if (!backward || !given_ckpt) off = gr_chain(p, kGrFwdTile, off, &p.fwd);
+    const int64_t cols = (p.D + 127) / 128 * p.B;
+    if (!mul_ok(cols, p.fwd.tiles + 1, lim) || !launch_ok(cols * p.fwd.tiles, 512)) return SS_ERR_DIMS;
     if (backward) {
-        p.parts = p.B;
+        // (the states are formed before the gradients' chain begins: both take the same memory)
+        const size_t end = gr_chain(p, SS_GR_CKPT, 0, &p.rev);
+        off = off > end ? off : end;
+        if (!launch_ok(cols * p.rev.tiles, 512)) return SS_ERR_DIMS;
+        const size_t row = size_t(p.B * p.rev.tiles) * size_t(p.D) * sizeof(float);
         p.off_ckpt = off;
-        if (!given_ckpt) off = align256(off + size_t(p.B * p.nckpt) * size_t(p.D) * sizeof(float));
+        if (!given_ckpt) off = align256(off + row);
         p.off_part = off;
-        off = align256(off + size_t(p.parts) * size_t(p.D) * sizeof(float));
+        off = align256(off + row);
     }
     p.total = off;
     *out = p;

@@ -143,7 +143,7 @@ def test_whole(gpu, shape, marks, dt):
     run_all(gpu, p, dt)
 
 
-@pytest.mark.parametrize("shape", [(1, 5000, 9), (2, 9000, 3), (1, 4096, 128)], ids=str)
+@pytest.mark.parametrize("shape", [(1, 5000, 9), (2, 9000, 3), (1, 4096, 128), (1, 4097, 2), (1, 2048, 6), (3, 8321, 4)], ids=str)
 def test_long(gpu, shape):
     note(f"gr long {shape}")
     run_all(gpu, make(7, *shape, "f32", reset=shape[2] == 3), "f32")
@@ -268,6 +268,30 @@ def test_documents_do_not_see_each_other(gpu):
     for n in ("dx", "dr", "di"):
         assert torch.equal(g[n][0, ~bad], g2[n][0, ~bad]), n
     assert torch.equal(g["dh0"], g2["dh0"])
+
+
+@pytest.mark.parametrize("gap", [1, 3, 20, 140])
+def test_nan_gates_end_with_their_document(gpu, gap):
+    """A NaN of the decay's gate shortly before the next document: in the same wave, the same tile,
+    the tile before.  And one shortly behind a document's begin, for the adjoint."""
+    import torch
+    T, D = 600, 5
+    p = make(21, 1, T, D, "f32")
+    reset = torch.zeros(1, T, dtype=torch.bool, device="cuda")
+    cut = 296
+    reset[0, cut] = True
+    args = (p["x"], p["r"], p["i"], p["lam"])
+    y = gpu.ss_gr_fwd(*args, p["h0"], reset=reset)
+    g = gpu.ss_gr_bwd(*args, p["dy"], p["h0"], p["dh"], reset=reset)
+    for at, fine in ((cut - gap, slice(cut, T)), (cut + gap, slice(0, cut))):
+        r = p["r"].clone()
+        r[0, at] = float("nan")
+        y2 = gpu.ss_gr_fwd(p["x"], r, p["i"], p["lam"], p["h0"], reset=reset)
+        g2 = gpu.ss_gr_bwd(p["x"], r, p["i"], p["lam"], p["dy"], p["h0"], p["dh"], reset=reset)
+        assert torch.equal(y[0, fine], y2[0, fine])
+        for n in ("dx", "dr", "di"):
+            assert torch.equal(g[n][0, fine], g2[n][0, fine]), n
+        assert torch.isnan(y2[0, at]).all()
 
 
 def test_extreme_gates(gpu):
