@@ -59,6 +59,12 @@ __device__ __forceinline__ Cols columns(int64_t c0, int lane, int64_t D) {
     return c;
 }
 
+// The wave's place in its workgroup, known to be the same in all its lanes: descriptors stay in
+// scalar registers.
+__device__ __forceinline__ int wave_number() {
+    return __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+}
+
 // Rows of n tokens (any number, also none) from p on, st elements apart, D wide.
 template <typename T, bool kVec>
 struct Rows {
@@ -324,7 +330,7 @@ __global__ __launch_bounds__(64 * kWaves) void gr_fwd_kernel(const GrLaunch p) {
     static_assert(SS_GR_CKPT % kS == 0, "checkpoints stand before a wave's first token");
     __shared__ float sh[2][kWaves][kCols], look[2][kWaves][kCols], begin[kCols];
     __shared__ int number;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = wave_number();
     const Place at = place(p, number);
     const int64_t b = at.b, D = p.D;
     const Cols col = columns<kVec>(at.c0, lane, D);
@@ -421,7 +427,7 @@ __global__ __launch_bounds__(64 * kWaves) void gr_bwd_kernel(const GrLaunch p) {
     static_assert(kWaves * kS == SS_GR_CKPT, "a tile is what one checkpoint starts");
     __shared__ float sh[3][kWaves][kCols], look[2][kWaves][kCols], begin[kCols];
     __shared__ int number;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = wave_number();
     const Place at = place(p, number);
     const int64_t b = at.b, D = p.D;
     const Cols col = columns<kVec>(at.c0, lane, D);
@@ -592,7 +598,7 @@ __global__ __launch_bounds__(1024) void gr_dlam_kernel(const float* __restrict__
 template <typename T, bool kVec>
 __global__ __launch_bounds__(256) void gr_step_kernel(const GrStep p) {
     const int lane = threadIdx.x & 63;
-    const int64_t b = int64_t(blockIdx.y) * 4 + (threadIdx.x >> 6), D = p.D;
+    const int64_t b = int64_t(blockIdx.y) * 4 + wave_number(), D = p.D;
     if (b >= p.B) return;
     const Cols col = columns<kVec>(int64_t(blockIdx.x) * kCols, lane, D);
     Two<T> x, r, i;
