@@ -196,34 +196,30 @@ __device__ __forceinline__ uint64_t peek(const uint64_t* p) {
     return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// The maps of tiles [from, from + n) of a row (n <= kMost), joined, for the lane's two channels.
-template <int kMost>
-__device__ __forceinline__ void joined(const uint64_t* tiles, int64_t D, const Cols& c, int from, int n,
-                                       Map (&m)[2]) {
-    uint64_t w[kMost][2];
+// The maps of tiles [from, from + n) of a row (n <= kMost), joined, for channels ch[0 .. kCh - 1].
+template <int kMost, int kCh>
+__device__ __forceinline__ void joined(const uint64_t* tiles, int64_t D, const int (&ch)[kCh], int from,
+                                       int n, Map (&m)[kCh]) {
+    uint64_t w[kMost][kCh];
 #pragma unroll
     for (int q = 0; q < kMost; ++q)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-            w[q][j] = q < n ? peek(tiles + int64_t(from + q) * D + c.ch[j]) : 0;
+        for (int j = 0; j < kCh; ++j)
+            w[q][j] = q < n ? peek(tiles + int64_t(from + q) * D + ch[j]) : 0;
 #pragma unroll
     for (int q = 0; q < kMost; ++q) {
         if (q < n) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < kCh; ++j) {
                 while (w[q][j] == kNotYet) {
                     __builtin_amdgcn_s_sleep(1);
-                    w[q][j] = peek(tiles + int64_t(from + q) * D + c.ch[j]);
+                    w[q][j] = peek(tiles + int64_t(from + q) * D + ch[j]);
                 }
                 m[j] = after(map_of(w[q][j]), m[j]);
             }
         }
     }
 }
-
-// Waits for a load: a tile's map may go out only after the row's first state has come in, since what
-// the row ends with may take its place (h_final over h0, dh0 over dh_final).
-__device__ __forceinline__ void arrived(float v) { asm volatile("" ::"v"(v)); }
 
 // Sets a chain's counter and words (kNotYet) before the launch that uses them.
 __global__ __launch_bounds__(256) void gr_chain_kernel(uint64_t* words, int64_t n, uint64_t* ticket) {
@@ -251,58 +247,86 @@ __device__ __forceinline__ Place place(const GrLaunch& p, int& shared) {
     return Place{int(n / per), int64_t(in / groups), int64_t(in % groups) * kCols};
 }
 
-// The state that enters tile `tile` of a row, from the one that enters the row; own: the tile's map.
-// Every wave returns it; what leaves a group (or the row: last) is published (stored) by one wave.
-template <bool kVec, int kWaves>
-__device__ __forceinline__ void entering(const GrLaunch& p, const Place& at, const Cols& col, int lane,
-                                         int wave, const Map (&own)[2], float (&h)[2], float* last,
-                                         float (&look)[2][kWaves][kCols], float (&begin)[kCols]) {
-    if (p.ticket) {
-        constexpr int kMost = kGroup / kWaves;
-        const int groups = (p.tiles + kGroup - 1) / kGroup;
-        const int n = at.tile % kGroup, group = at.tile / kGroup;
-        uint64_t* maps = p.maps + at.b * p.tiles * p.D;
-        uint64_t* ends = p.ends + at.b * groups * p.D;
-        if (wave == kWaves - 1 && n < kGroup - 1) {
+// What the waves of a workgroup share: their maps, by the channel's place in the workgroup's 128
+// (a lane's two are neighbours or 64 apart), and the states that enter each of them.
+template <int kWaves>
+struct Shared {
+    float A[kWaves][kCols], H[kWaves][kCols], in[kWaves][kCols];
+    float lookA[kWaves - 2][kCols], lookH[kWaves - 2][kCols];
+    int number;
+};
+
+template <bool kVec> __device__ __forceinline__ int spot(int lane, int j) {
+    return kVec ? 2 * lane + j : lane + 64 * j;
+}
+
+// Sets in[wave] to the states that enter the waves' stretches (kReverse: taken from the last wave to
+// the first) from `first`, the state that enters the row (nullable: 0), and stores what leaves the
+// row in `last` (nullable).  Two waves hold a channel a lane and walk over the waves' maps; the
+// others meanwhile fetch the maps of the tiles before.  All maps are in place (a barrier) before.
+template <bool kVec, bool kReverse, int kWaves, typename Sh>
+__device__ __forceinline__ void link(const GrLaunch& p, const Place& at, const Cols& col, int lane,
+                                     int wave, Sh& sh, const float (&maps_h)[kWaves][kCols],
+                                     const float* first, float* last) {
+    constexpr int kFetch = kWaves - 2, kMost = (kGroup - 1 + kFetch - 1) / kFetch;
+    const int groups = (p.tiles + kGroup - 1) / kGroup;
+    const int n = at.tile % kGroup, group = at.tile / kGroup;
+    uint64_t* maps = p.maps + at.b * p.tiles * p.D;
+    uint64_t* ends = p.ends + at.b * groups * p.D;
+    const int l = lane + 64 * wave;           // of the walking waves
+    const int ch = int(at.c0) + l;
+    const bool on = wave < 2 && ch < int(p.D);
+    float h = 0.0f;
+    Map own = {1.0f, 0.0f};
+    if (wave < 2) {
+        if (on && first && group == 0) h = first[at.b * p.D + ch];
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                if (col.on[j]) publish(maps + int64_t(at.tile) * p.D + col.ch[j], own[j]);
+        for (int w = 0; w < kWaves; ++w) {
+            const int v = kReverse ? kWaves - 1 - w : w;
+            own = after(Map{sh.A[v][l], maps_h[v][l]}, own);
         }
-        if (n > 0 || group > 0) {
-            Map m[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}};
-            const int lo = n * wave / kWaves, hi = n * (wave + 1) / kWaves;
-            if (hi > lo) joined<kMost>(maps, p.D, col, group * kGroup + lo, hi - lo, m);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                look[0][wave][lane + 64 * j] = m[j].A;
-                look[1][wave][lane + 64 * j] = m[j].H;
-            }
-            if (wave == 0 && group > 0) {
-                Map e[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}};
-                joined<1>(ends, p.D, col, group - 1, 1, e);
-                begin[lane] = e[0].H;
-                begin[lane + 64] = e[1].H;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                if (group > 0) h[j] = begin[lane + 64 * j];
-#pragma unroll
-                for (int w = 0; w < kWaves; ++w)
-                    h[j] = through(look[0][w][lane + 64 * j], look[1][w][lane + 64 * j], h[j]);
-            }
+        if (p.ticket && n < kGroup - 1) {
+            // the state that enters the row has come in before this map goes out: what leaves the row
+            // may take its place (h_final over h0, dh0 over dh_final)
+            asm volatile("" ::"v"(h));
+            if (on) publish(maps + int64_t(at.tile) * p.D + ch, own);
         }
-        if (wave == kWaves - 1 && n == kGroup - 1 && at.tile + 1 < p.tiles) {
+    } else if (p.ticket && n > 0) {
+        Map m[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}};
+        const int f = wave - 2, lo = n * f / kFetch, hi = n * (f + 1) / kFetch;
+        if (hi > lo) joined<kMost, 2>(maps, p.D, col.ch, group * kGroup + lo, hi - lo, m);
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                if (col.on[j])
-                    publish(ends + int64_t(group) * p.D + col.ch[j],
-                            Map{1.0f, through(own[j].A, own[j].H, h[j])});
+        for (int j = 0; j < 2; ++j) {
+            sh.lookA[f][spot<kVec>(lane, j)] = m[j].A;
+            sh.lookH[f][spot<kVec>(lane, j)] = m[j].H;
         }
     }
-    if (last && wave == kWaves - 1 && at.tile + 1 == p.tiles)
-        store_row<kVec>(last + at.b * p.D, col, through(own[0].A, own[0].H, h[0]),
-                        through(own[1].A, own[1].H, h[1]));
+    if (p.ticket && (n > 0 || group > 0)) {
+        if (on && group > 0) {
+            Map e[1] = {{1.0f, 0.0f}};
+            const int one[1] = {ch};
+            joined<1, 1>(ends, p.D, one, group - 1, 1, e);
+            h = e[0].H;
+        }
+        __syncthreads();
+        if (wave < 2 && n > 0) {
+#pragma unroll
+            for (int f = 0; f < kFetch; ++f) h = through(sh.lookA[f][l], sh.lookH[f][l], h);
+        }
+    }
+    if (wave < 2) {
+        const float out = through(own.A, own.H, h);
+        if (on && p.ticket && n == kGroup - 1 && at.tile + 1 < p.tiles)
+            publish(ends + int64_t(group) * p.D + ch, Map{1.0f, out});
+        if (on && last && at.tile + 1 == p.tiles) last[at.b * p.D + ch] = out;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            const int v = kReverse ? kWaves - 1 - w : w;
+            sh.in[v][l] = h;
+            h = through(sh.A[v][l], maps_h[v][l], h);
+        }
+    }
+    __syncthreads();
 }
 
 // Which of the `live` tokens from t0 on begin a document: bit s for token t0 + s.
@@ -328,10 +352,9 @@ __device__ __forceinline__ int live_tokens(const int32_t* lengths, int64_t b, in
 template <typename T, bool kVec, int kWaves, int kS>
 __global__ __launch_bounds__(64 * kWaves) void gr_fwd_kernel(const GrLaunch p) {
     static_assert(SS_GR_CKPT % kS == 0, "checkpoints stand before a wave's first token");
-    __shared__ float sh[2][kWaves][kCols], look[2][kWaves][kCols], begin[kCols];
-    __shared__ int number;
+    __shared__ Shared<kWaves> sh;
     const int lane = threadIdx.x & 63, wave = wave_number();
-    const Place at = place(p, number);
+    const Place at = place(p, sh.number);
     const int64_t b = at.b, D = p.D;
     const Cols col = columns<kVec>(at.c0, lane, D);
     const int64_t t0 = (int64_t(at.tile) * kWaves + wave) * kS;
@@ -352,10 +375,7 @@ __global__ __launch_bounds__(64 * kWaves) void gr_fwd_kernel(const GrLaunch p) {
     const uint32_t first = reset_bits(p.reset, b, p.T, t0, lane, live);
     float k2[2], h[2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        k2[j] = rate2(p.lam[col.ch[j]], p.c);
-        h[j] = p.h0 ? p.h0[b * D + col.ch[j]] : 0.0f;
-    }
+    for (int j = 0; j < 2; ++j) k2[j] = rate2(p.lam[col.ch[j]], p.c);
     float a[kS][2], u[kS][2];
     Map own[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}};
     // the wave's map; all: every token exists and none begins a document
@@ -382,26 +402,13 @@ __global__ __launch_bounds__(64 * kWaves) void gr_fwd_kernel(const GrLaunch p) {
     if (first) own[0].A = own[1].A = 0.0f;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        sh[0][wave][lane + 64 * j] = own[j].A;
-        sh[1][wave][lane + 64 * j] = own[j].H;
-        arrived(h[j]);
+        sh.A[wave][spot<kVec>(lane, j)] = own[j].A;
+        sh.H[wave][spot<kVec>(lane, j)] = own[j].H;
     }
     __syncthreads();
-    // the map of the waves before this one, and of the whole tile
-    Map before[2];
+    link<kVec, false, kWaves>(p, at, col, lane, wave, sh, sh.H, p.h0, p.h_final);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        Map m = {1.0f, 0.0f};
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            if (w == wave) before[j] = m;
-            m = after(Map{sh[0][w][lane + 64 * j], sh[1][w][lane + 64 * j]}, m);
-        }
-        own[j] = m;
-    }
-    entering<kVec, kWaves>(p, at, col, lane, wave, own, h, p.h_final, look, begin);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) h[j] = through(before[j].A, before[j].H, h[j]);
+    for (int j = 0; j < 2; ++j) h[j] = sh.in[wave][spot<kVec>(lane, j)];
     if (p.h_ckpt && t0 % SS_GR_CKPT == 0 && t0 < p.T) {
         const int64_t nc = (p.T + SS_GR_CKPT - 1) / SS_GR_CKPT;
         store_row<kVec>(p.h_ckpt + (b * nc + t0 / SS_GR_CKPT) * D, col, h[0], h[1]);
@@ -425,10 +432,10 @@ __global__ __launch_bounds__(64 * kWaves) void gr_fwd_kernel(const GrLaunch p) {
 template <typename T, bool kVec, int kWaves, int kS>
 __global__ __launch_bounds__(64 * kWaves) void gr_bwd_kernel(const GrLaunch p) {
     static_assert(kWaves * kS == SS_GR_CKPT, "a tile is what one checkpoint starts");
-    __shared__ float sh[3][kWaves][kCols], look[2][kWaves][kCols], begin[kCols];
-    __shared__ int number;
+    __shared__ Shared<kWaves> sh;
+    __shared__ float G[kWaves][kCols];
     const int lane = threadIdx.x & 63, wave = wave_number();
-    const Place at = place(p, number);
+    const Place at = place(p, sh.number);
     const int64_t b = at.b, D = p.D;
     const Cols col = columns<kVec>(at.c0, lane, D);
     const int64_t tile = p.tiles - 1 - at.tile, t0 = tile * SS_GR_CKPT + wave * kS;
@@ -453,7 +460,6 @@ __global__ __launch_bounds__(64 * kWaves) void gr_bwd_kernel(const GrLaunch p) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         k2[j] = rate2(p.lam[col.ch[j]], p.c);
-        c[j] = p.dh_final ? p.dh_final[b * D + col.ch[j]] : 0.0f;
         h[j] = p.h_ckpt[(b * p.tiles + tile) * D + col.ch[j]];
     }
     float a[kS][2], q[kS][2], sr[kS][2], si[kS][2];
@@ -492,32 +498,21 @@ __global__ __launch_bounds__(64 * kWaves) void gr_bwd_kernel(const GrLaunch p) {
     if (first) fwd[0].A = fwd[1].A = 0.0f;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        sh[0][wave][lane + 64 * j] = fwd[j].A;
-        sh[1][wave][lane + 64 * j] = fwd[j].H;
-        sh[2][wave][lane + 64 * j] = rev[j].H;
-        arrived(c[j]);
+        sh.A[wave][spot<kVec>(lane, j)] = fwd[j].A;
+        sh.H[wave][spot<kVec>(lane, j)] = fwd[j].H;
+        G[wave][spot<kVec>(lane, j)] = rev[j].H;
     }
     __syncthreads();
-    Map right[2];
+    for (int w = 0; w < wave; ++w) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        float hh = h[j];
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            if (w == wave) h[j] = hh;
-            hh = through(sh[0][w][lane + 64 * j], sh[1][w][lane + 64 * j], hh);
+        for (int j = 0; j < 2; ++j) {
+            const int l = spot<kVec>(lane, j);
+            h[j] = through(sh.A[w][l], sh.H[w][l], h[j]);
         }
-        Map m = {1.0f, 0.0f};
-#pragma unroll
-        for (int w = kWaves - 1; w >= 0; --w) {
-            if (w == wave) right[j] = m;
-            m = after(Map{sh[0][w][lane + 64 * j], sh[2][w][lane + 64 * j]}, m);
-        }
-        rev[j] = m;
     }
-    entering<kVec, kWaves>(p, at, col, lane, wave, rev, c, p.dh0, look, begin);
+    link<kVec, true, kWaves>(p, at, col, lane, wave, sh, G, p.dh_final, p.dh0);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) c[j] = through(right[j].A, right[j].H, c[j]);
+    for (int j = 0; j < 2; ++j) c[j] = sh.in[wave][spot<kVec>(lane, j)];
     float old[kS][2], dl[2] = {0.0f, 0.0f};
     const Rows<T, kVec> dx(static_cast<T*>(p.dx) + (b * p.T + t0) * D, D, n, D, col, true);
     const Rows<T, kVec> dr(static_cast<T*>(p.dr) + (b * p.T + t0) * D, D, n, D, col, true);
@@ -558,16 +553,16 @@ __global__ __launch_bounds__(64 * kWaves) void gr_bwd_kernel(const GrLaunch p) {
     };
     if (all) gradients(std::true_type{});
     else gradients(std::false_type{});
+    // (A is no longer read: link ends with a barrier)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) sh.A[wave][spot<kVec>(lane, j)] = dl[j];
     __syncthreads();
+    const int64_t ch = at.c0 + threadIdx.x;
+    if (threadIdx.x < kCols && ch < D) {
+        float v = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) sh[0][wave][lane + 64 * j] = dl[j];
-    __syncthreads();
-    if (wave == 0) {
-#pragma unroll
-        for (int w = 1; w < kWaves; ++w)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) dl[j] += sh[0][w][lane + 64 * j];
-        store_row<kVec>(p.part + (b * p.tiles + tile) * D, col, dl[0], dl[1]);
+        for (int w = 0; w < kWaves; ++w) v += sh.A[w][threadIdx.x];
+        p.part[(b * p.tiles + tile) * D + ch] = v;
     }
 }
 
