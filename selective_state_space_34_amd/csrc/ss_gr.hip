@@ -85,6 +85,7 @@ template <typename T> struct Two;
 template <> struct Two<float> {
     float v[2];
     __device__ __forceinline__ float get(int j) const { return v[j]; }
+    __device__ __forceinline__ void anew() { asm volatile("" : "+v"(v[0]), "+v"(v[1])); }
     template <bool kVec> __device__ __forceinline__ void load(const Rows<float, kVec>& r, int s) {
         if constexpr (kVec) {
             typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
@@ -102,6 +103,7 @@ template <> struct Two<bf16_t> {
     __device__ __forceinline__ float get(int j) const {
         return __uint_as_float(j ? w & 0xffff0000u : w << 16);
     }
+    __device__ __forceinline__ void anew() { asm volatile("" : "+v"(w)); }
     template <bool kVec> __device__ __forceinline__ void load(const Rows<bf16_t, kVec>& r, int s) {
         if constexpr (kVec) {
             w = __builtin_amdgcn_raw_buffer_load_b32(r.d, r.at[0], s * r.step, 0);
@@ -221,10 +223,12 @@ __device__ __forceinline__ void joined(const uint64_t* tiles, int64_t D, const i
     }
 }
 
-// Sets a chain's counter and words (kNotYet) before the launch that uses them.
-__global__ __launch_bounds__(256) void gr_chain_kernel(uint64_t* words, int64_t n, uint64_t* ticket) {
+// Sets a chain's counter and words (kNotYet) before the launch that uses them; n is even or the words
+// end in padding.
+__global__ __launch_bounds__(256) void gr_chain_kernel(ulonglong2* words, int64_t n, uint64_t* ticket) {
     const int64_t step = int64_t(gridDim.x) * 256;
-    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += step) words[i] = kNotYet;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += step)
+        words[i] = make_ulonglong2(kNotYet, kNotYet);
     if (blockIdx.x == 0 && threadIdx.x == 0) *ticket = 0;
 }
 
@@ -462,7 +466,7 @@ __global__ __launch_bounds__(64 * kWaves) void gr_bwd_kernel(const GrLaunch p) {
         k2[j] = rate2(p.lam[col.ch[j]], p.c);
         h[j] = p.h_ckpt[(b * p.tiles + tile) * D + col.ch[j]];
     }
-    float a[kS][2], q[kS][2], sr[kS][2], si[kS][2];
+    float a[kS][2], q[kS][2], si[kS][2];
     Map fwd[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}}, rev[2];
     // What stands behind a text becomes 0 (and its a 1) before anything is formed from it; a token
     // that begins a document has a = 0 and s = 1.
@@ -474,9 +478,8 @@ __global__ __launch_bounds__(64 * kWaves) void gr_bwd_kernel(const GrLaunch p) {
             if (!on) wx[s] = wd[s] = Two<T>{};
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                sr[s][j] = on ? sigmoid(wr[s].get(j)) : 0.0f;
                 si[s][j] = on ? sigmoid(wi[s].get(j)) : 0.0f;
-                const float t2 = k2[j] * sr[s][j];
+                const float t2 = k2[j] * sigmoid(wr[s].get(j));
                 const float e = exp2_hw(t2);
                 a[s][j] = !on ? 1.0f : cut ? 0.0f : e;
                 q[s][j] = !on ? 0.0f : cut ? 1.0f : __builtin_amdgcn_sqrtf(one_less_square(t2, e));
@@ -513,6 +516,14 @@ __global__ __launch_bounds__(64 * kWaves) void gr_bwd_kernel(const GrLaunch p) {
     link<kVec, true, kWaves>(p, at, col, lane, wave, sh, G, p.dh_final, p.dh0);
 #pragma unroll
     for (int j = 0; j < 2; ++j) c[j] = sh.in[wave][spot<kVec>(lane, j)];
+    // From here on x, dy, σ(r) and their products are formed once more from the packed values: kept
+    // from above, they would take 80 registers a lane.
+#pragma unroll
+    for (int s = 0; s < kS; ++s) {
+        wx[s].anew();
+        wr[s].anew();
+        wd[s].anew();
+    }
     float old[kS][2], dl[2] = {0.0f, 0.0f};
     const Rows<T, kVec> dx(static_cast<T*>(p.dx) + (b * p.T + t0) * D, D, n, D, col, true);
     const Rows<T, kVec> dr(static_cast<T*>(p.dr) + (b * p.T + t0) * D, D, n, D, col, true);
@@ -528,12 +539,15 @@ __global__ __launch_bounds__(64 * kWaves) void gr_bwd_kernel(const GrLaunch p) {
             }
         }
 #pragma unroll
+        for (int s = 0; s < kS; ++s) wx[s].anew();
+#pragma unroll
         for (int s = kS - 1; s >= 0; --s) {
             const bool cut = !all && (first >> s & 1), on = all || s < live;
             float ox[2], orr[2], oi[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const float as = a[s][j], qs = q[s][j], xv = wx[s].get(j), sg = sr[s][j], sx = si[s][j];
+                const float as = a[s][j], qs = q[s][j], xv = wx[s].get(j), sx = si[s][j];
+                const float sg = sigmoid(wr[s].get(j));
                 const float gt = wd[s].get(j) + c[j], ag = as * gt;
                 c[j] = cut ? 0.0f : ag;
                 ox[j] = gt * qs * sx;
@@ -618,6 +632,8 @@ hipError_t with_type(int in_dtype, int vec, F&& f) {
     return vec ? f(0.0f, std::true_type{}) : f(0.0f, std::false_type{});
 }
 
+constexpr int kFwdWaves = 8, kBwdWaves = SS_GR_CKPT / 8;
+
 unsigned groups(int64_t D) { return unsigned((D + kCols - 1) / kCols); }
 
 }  // namespace
@@ -627,10 +643,10 @@ namespace {
 // The chain's words and counter, where the row has more than one tile.
 hipError_t begin_chain(const GrLaunch& p, hipStream_t s) {
     if (!p.ticket) return hipSuccess;
-    const int64_t n = p.B * p.D * (p.tiles + (p.tiles + kGroup - 1) / kGroup);
+    const int64_t n = (p.B * p.D * (p.tiles + (p.tiles + kGroup - 1) / kGroup) + 1) / 2;
     const int64_t need = (n + 255) / 256;
-    hipLaunchKernelGGL(gr_chain_kernel, dim3(unsigned(need < 2048 ? need : 2048)), dim3(256), 0, s,
-                       p.maps, n, p.ticket);
+    hipLaunchKernelGGL(gr_chain_kernel, dim3(unsigned(need < 1024 ? need : 1024)), dim3(256), 0, s,
+                       reinterpret_cast<ulonglong2*>(p.maps), n, p.ticket);
     return hipGetLastError();
 }
 
@@ -640,8 +656,8 @@ hipError_t launch_gr_fwd(const GrLaunch& p, hipStream_t s) {
     const hipError_t e = begin_chain(p, s);
     if (e != hipSuccess) return e;
     return with_type(p.in_dtype, p.vec, [&](auto t, auto v) {
-        hipLaunchKernelGGL((gr_fwd_kernel<decltype(t), decltype(v)::value, 8, kGrFwdTile / 8>),
-                           dim3(groups(p.D) * unsigned(p.B) * unsigned(p.tiles)), dim3(512), 0, s, p);
+        hipLaunchKernelGGL((gr_fwd_kernel<decltype(t), decltype(v)::value, kFwdWaves, kGrFwdTile / kFwdWaves>),
+                           dim3(groups(p.D) * unsigned(p.B) * unsigned(p.tiles)), dim3(64 * kFwdWaves), 0, s, p);
         return hipGetLastError();
     });
 }
@@ -650,8 +666,8 @@ hipError_t launch_gr_bwd(const GrLaunch& p, hipStream_t s) {
     hipError_t e = begin_chain(p, s);
     if (e != hipSuccess) return e;
     e = with_type(p.in_dtype, p.vec, [&](auto t, auto v) {
-        hipLaunchKernelGGL((gr_bwd_kernel<decltype(t), decltype(v)::value, 8, SS_GR_CKPT / 8>),
-                           dim3(groups(p.D) * unsigned(p.B) * unsigned(p.tiles)), dim3(512), 0, s, p);
+        hipLaunchKernelGGL((gr_bwd_kernel<decltype(t), decltype(v)::value, kBwdWaves, SS_GR_CKPT / kBwdWaves>),
+                           dim3(groups(p.D) * unsigned(p.B) * unsigned(p.tiles)), dim3(64 * kBwdWaves), 0, s, p);
         return hipGetLastError();
     });
     if (e != hipSuccess) return e;
