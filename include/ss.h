@@ -474,7 +474,7 @@ int ss_ln_bwd(const ss_ln_dims* dims, const void* dy, const void* r, const float
  * magnitude less two (at least 1), codes go to the nearest value, ties to the even code, and
  * values past 6 to 6.  A block that holds a NaN or an infinity has exponent 255 and zero codes. */
 typedef struct ss_mx4_dims {
-    int64_t rows, n, k;   /* k a multiple of 32; n is not used by ss_mx4_quant */
+    int64_t rows, n, k;   /* k a multiple of 32 (ss_mx4_mm: below 2^23); ss_mx4_quant does not use n */
     int32_t in_dtype;     /* ss_dtype of ss_mx4_quant's x */
     int32_t x_q8;         /* ss_mx4_mm's x: SS_Q4_MX, or SS_Q8_FP8 */
     int32_t y_dtype;      /* ss_dtype of y */

@@ -88,6 +88,7 @@ inline int check_mx4(const ss_mx4_dims& d, bool product) {
     if (!mul_ok(d.rows, d.k, lim)) return SS_ERR_DIMS;
     if (!product) return d.in_dtype == SS_F32 || d.in_dtype == SS_BF16 ? SS_OK : SS_ERR_DTYPE;
     if (!mul_ok(d.n, d.k, lim) || !mul_ok(d.rows, d.n, lim)) return SS_ERR_DIMS;
+    if (d.k >= (int64_t(1) << 23)) return SS_ERR_DIMS;   // 256 rows stay within a descriptor
     if (d.x_q8 != SS_Q4_MX && d.x_q8 != SS_Q8_FP8) return SS_ERR_DTYPE;
     if (d.y_dtype != SS_F32 && d.y_dtype != SS_BF16) return SS_ERR_DTYPE;
     if ((d.rows + 63) / 64 > kMaxGridYZ || !launch_ok((d.n + 15) / 16 * ((d.rows + 63) / 64), 512))

@@ -15,6 +15,7 @@ namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
@@ -158,6 +159,235 @@ __global__ __launch_bounds__(64 * kWaves) void mx4_rows_kernel(const Mx4Launch p
     }
 }
 
+// ---- many rows -------------------------------------------------------------------------------
+
+// A workgroup of four waves takes 128 rows of weights and 32·kM of x; a wave 64 by 16·kM of them.
+// Both operands pass through LDS, 128 columns at a time, in two buffers; loads for the next are in
+// flight while one is used.  A row's 16-byte pieces are placed by their number xor some bits of the
+// row, so that the eight lanes that read at once meet all banks.  Weights' rows are dealt to the four
+// 16-row products of a wave so that a lane ends up with two runs of eight of a row of y, and the four
+// lanes of a row with 64 bytes a store.
+// Exponents come 16 to a row and 512 columns.
+template <int kX, int kM>
+struct Tile {
+    static constexpr int kRowsN = 128, kRowsM = 32 * kM;
+    static constexpr int kBytesX = kX == kX4 ? 64 : 128;      // a row of x, 128 columns
+    static constexpr int kPiecesW = kRowsN * 4, kPiecesX = kRowsM * (kBytesX / 16);
+    static constexpr int kScales = kRowsN + (kX == kX4 ? kRowsM : 0);
+    u32x4 w[2][kPiecesW], x[2][kPiecesX];
+    alignas(16) uint8_t e[2][kScales][16];
+};
+
+__device__ __forceinline__ int turn_w(int row) { return (row >> 1 & 1) | (row >> 3 & 1) << 1; }
+template <int kX> __device__ __forceinline__ int turn_x(int row) {
+    return kX == kX4 ? row >> 1 & 3 : row & 7;
+}
+
+constexpr int kRsrcFlags = 0x00020000;       // raw buffer, 32-bit elements
+constexpr int kNowhere = int(0x80000000u);   // behind every descriptor's end: loads 0
+
+// A tile's rows, `bytes` each, of `rows` from number r0 on; what lies behind the last one loads as 0.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_from(const void* p, int64_t r0, int64_t rows,
+                                                           int64_t most, int64_t bytes) {
+    const int64_t n = rows - r0 < most ? rows - r0 : most;
+    return __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>(static_cast<const uint8_t*>(p)) + r0 * bytes, 0, int(n * bytes), kRsrcFlags);
+}
+
+// Exponents 16·block .. of the row at `at` that has n of them; 0 behind its end (the codes there are
+// 0 as well).
+__device__ __forceinline__ u32x4 exponents(__amdgpu_buffer_rsrc_t d, int at, int block, int n) {
+    const int left = n - 16 * block;
+    at += 16 * block;
+    u32x4 w = {0, 0, 0, 0};
+    if (left >= 16 && n % 4 == 0) {
+        w = __builtin_amdgcn_raw_buffer_load_b128(d, at, 0, 0);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            w[i / 4] |= uint32_t(__builtin_amdgcn_raw_buffer_load_b8(d, i < left ? at + i : kNowhere, 0, 0))
+                        << (8 * (i % 4));
+    }
+    return w;
+}
+
+template <int kX, int kM>
+__global__ __launch_bounds__(256, 2) void mx4_tile_kernel(const Mx4Launch p, int64_t tiles_m,
+                                                          int64_t tiles_n) {
+    using L = Tile<kX, kM>;
+    __shared__ L sh;
+    // Dies get consecutive tiles (blocks go to the eight of them in turn), eight row tiles of x by
+    // one of weights after the other, so that what they read stays in a die's L2.
+    const int64_t total = tiles_m * tiles_n, each = (total + 7) / 8;
+    const int64_t number = int64_t(blockIdx.x % 8) * each + blockIdx.x / 8;
+    if (blockIdx.x / 8 >= each || number >= total) return;
+    const int64_t per = 8 * tiles_n, first = number / per * 8;
+    const int64_t high = tiles_m - first < 8 ? tiles_m - first : 8;
+    const int64_t m0 = (first + number % per % high) * L::kRowsM, n0 = number % per / high * L::kRowsN;
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wn = wave & 1, wm = wave >> 1;
+    const int row = lane & 15, g = lane >> 4;
+    const int K = int(p.K), kb = K / 32, row_w = K / 2, row_x = kX == kX4 ? K / 2 : K;
+    const __amdgpu_buffer_rsrc_t dw = rows_from(p.wq, n0, p.N, L::kRowsN, row_w);
+    const __amdgpu_buffer_rsrc_t dx = rows_from(p.x, m0, p.M, L::kRowsM, row_x);
+    const __amdgpu_buffer_rsrc_t dwe = rows_from(p.w_exps, n0, p.N, L::kRowsN, kb);
+    const __amdgpu_buffer_rsrc_t dxe = rows_from(p.x_scale, m0, p.M, L::kRowsM, kX == kX4 ? kb : 0);
+
+    constexpr int kLoadW = L::kPiecesW / 256, kLoadX = L::kPiecesX / 256, kPer = L::kBytesX / 16;
+    int cw[kLoadW], cx[kLoadX], ow[kLoadW], ox[kLoadX];
+#pragma unroll
+    for (int i = 0; i < kLoadW; ++i) {
+        const int s = tid + 256 * i, r = s / 4;
+        cw[i] = ((s & 3) ^ turn_w(r)) * 16;
+        ow[i] = r * row_w + cw[i];
+    }
+#pragma unroll
+    for (int i = 0; i < kLoadX; ++i) {
+        const int s = tid + 256 * i, r = s / kPer;
+        cx[i] = ((s % kPer) ^ turn_x<kX>(r)) * 16;
+        ox[i] = r * row_x + cx[i];
+    }
+    constexpr int kLoadE = (L::kScales + 255) / 256;
+    u32x4 rw[kLoadW], rx[kLoadX], re[kLoadE];
+    auto fetch = [&](int s) {      // what lies behind the last column is 0
+#pragma unroll
+        for (int i = 0; i < kLoadW; ++i)
+            rw[i] = __builtin_amdgcn_raw_buffer_load_b128(
+                dw, s * 64 + cw[i] < row_w ? ow[i] : kNowhere, s * 64, 0);
+#pragma unroll
+        for (int i = 0; i < kLoadX; ++i)
+            rx[i] = __builtin_amdgcn_raw_buffer_load_b128(
+                dx, s * L::kBytesX + cx[i] < row_x ? ox[i] : kNowhere, s * L::kBytesX, 0);
+        if (s % 4 == 0) {
+            // threads 0 .. 127 take a row of weights, the others one of x, and each 128 of x besides
+            if (wave < 2) re[0] = exponents(dwe, tid * kb, s / 4, kb);
+            else if (kX == kX4) re[0] = exponents(dxe, (tid - 128) * kb, s / 4, kb);
+            if constexpr (kLoadE > 1)
+                if (tid + 256 < L::kScales) re[1] = exponents(dxe, (tid + 128) * kb, s / 4, kb);
+        }
+    };
+    auto keep = [&](int s) {
+        const int to = s & 1;
+#pragma unroll
+        for (int i = 0; i < kLoadW; ++i) sh.w[to][tid + 256 * i] = rw[i];
+#pragma unroll
+        for (int i = 0; i < kLoadX; ++i) sh.x[to][tid + 256 * i] = rx[i];
+        if (s % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < kLoadE; ++i)
+                if (tid + 256 * i < L::kScales)
+                    *reinterpret_cast<u32x4*>(sh.e[s / 4 & 1][tid + 256 * i]) = re[i];
+        }
+    };
+
+    f32x4 acc[4][kM] = {};
+    const int stages = (K + 127) / 128;
+    fetch(0);
+    keep(0);
+    __syncthreads();
+    for (int s = 0; s < stages; ++s) {
+        if (s + 1 < stages) fetch(s + 1);
+        const int from = s & 1, eb = s / 4 & 1, es = (s & 3) * 4 + g;
+        i32x8 a[4] = {};
+        int sa[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 64 * wn + 32 * (i >> 1) + 8 * (row >> 2) + 4 * (i & 1) + (row & 3);
+            const u32x4 v = sh.w[from][r * 4 + (g ^ turn_w(r))];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) a[i][c] = int(v[c]);
+            sa[i] = sh.e[eb][r][es];
+        }
+#pragma unroll
+        for (int t = 0; t < kM; ++t) {
+            const int r = 16 * kM * wm + 16 * t + row;
+            i32x8 b = {};
+            int sb = 127;
+            if constexpr (kX == kX4) {
+                const u32x4 v = sh.x[from][r * 4 + (g ^ turn_x<kX>(r))];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) b[c] = int(v[c]);
+                sb = sh.e[eb][L::kRowsN + r][es];
+            } else {
+                const u32x4 v = sh.x[from][r * 8 + (g ^ turn_x<kX>(r))];
+                const u32x4 u = sh.x[from][r * 8 + ((4 + g) ^ turn_x<kX>(r))];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    b[c] = int(v[c]);
+                    b[4 + c] = int(u[c]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                acc[i][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    a[i], b, acc[i][t], 4, kX == kX4 ? 4 : 0, 0, sa[i], 0, sb);
+        }
+        if (s + 1 < stages) keep(s + 1);
+        __syncthreads();
+    }
+    settle();
+    // Rows behind the last one are behind the descriptor's end.  A wave whose 64 columns all exist, on
+    // rows that start on 4 bytes, stores 16 bytes at a time.
+    const int N = int(p.N), el = p.y_dtype == SS_F32 ? 4 : 2;
+    const __amdgpu_buffer_rsrc_t dy = rows_from(p.y, m0, p.M, L::kRowsM, int64_t(N) * el);
+    const int n = int(n0) + 64 * wn + 8 * g;
+    const bool wide = int(n0) + 64 * wn + 64 <= N && (el == 4 || N % 2 == 0);
+#pragma unroll
+    for (int t = 0; t < kM; ++t) {
+        const int m = 16 * kM * wm + 16 * t + row;
+        float f = 1.0f;
+        if constexpr (kX != kX4)
+            f = static_cast<const float*>(p.x_scale)[m0 + m < p.M ? m0 + m : p.M - 1];
+        if (el == 4) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int at = n + 32 * (i >> 1) + 4 * (i & 1);
+                u32x4 v;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    v[j] = __float_as_uint(kX == kX4 ? acc[i][t][j] : acc[i][t][j] * f);
+                if (wide) {
+                    __builtin_amdgcn_raw_buffer_store_b128(v, dy, (m * N + at) * 4, 0, 0);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        __builtin_amdgcn_raw_buffer_store_b32(
+                            v[j], dy, at + j < N ? (m * N + at + j) * 4 : kNowhere, 0, 0);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int at = n + 32 * i;
+                union { bf16x8 h; u32x4 w; } o;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float v = acc[2 * i + j / 4][t][j % 4];
+                    o.h[j] = __bf16(kX == kX4 ? v : v * f);
+                }
+                if (wide) {
+                    __builtin_amdgcn_raw_buffer_store_b128(o.w, dy, (m * N + at) * 2, 0, 0);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        __builtin_amdgcn_raw_buffer_store_b16(
+                            uint16_t(o.w[j / 2] >> (16 * (j % 2))), dy,
+                            at + j < N ? (m * N + at + j) * 2 : kNowhere, 0, 0);
+                }
+            }
+        }
+    }
+}
+
+template <int kX, int kM>
+hipError_t launch_tiles(const Mx4Launch& p, hipStream_t s) {
+    const int64_t m = (p.M + 32 * kM - 1) / (32 * kM), n = (p.N + 127) / 128;
+    hipLaunchKernelGGL((mx4_tile_kernel<kX, kM>), dim3(unsigned((m * n + 7) / 8 * 8)), dim3(256), 0, s, p,
+                       m, n);
+    return hipGetLastError();
+}
+
 template <int kTiles, int kX>
 hipError_t launch_rows(const Mx4Launch& p, hipStream_t s) {
     const dim3 grid(unsigned((p.N + 15) / 16), unsigned((p.M + 16 * kTiles - 1) / (16 * kTiles)));
@@ -169,6 +399,10 @@ template <int kX>
 hipError_t launch_mm(const Mx4Launch& p, hipStream_t s) {
     if (p.M <= 16) return launch_rows<1, kX>(p, s);
     if (p.M <= 32) return launch_rows<2, kX>(p, s);
+    if constexpr (kX != kX8Wide) {
+        // (256 rows of y stay within a descriptor)
+        if (p.M > 128 && p.N < (1 << 20)) return launch_tiles<kX, kX == kX4 ? 8 : 4>(p, s);
+    }
     return launch_rows<4, kX>(p, s);
 }
 
