@@ -283,11 +283,7 @@ __global__ __launch_bounds__(256, 2) void mx4_tile_kernel(const Mx4Launch p, int
 
     f32x4 acc[4][kM] = {};
     const int stages = (K + 127) / 128;
-    fetch(0);
-    keep(0);
-    __syncthreads();
-    for (int s = 0; s < stages; ++s) {
-        if (s + 1 < stages) fetch(s + 1);
+    auto multiply = [&](int s) {
         const int from = s & 1, eb = s / 4 & 1, es = (s & 3) * 4 + g;
         i32x8 a[4] = {};
         int sa[4];
@@ -323,9 +319,22 @@ __global__ __launch_bounds__(256, 2) void mx4_tile_kernel(const Mx4Launch p, int
                 acc[i][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
                     a[i], b, acc[i][t], 4, kX == kX4 ? 4 : 0, 0, sa[i], 0, sb);
         }
-        if (s + 1 < stages) keep(s + 1);
+        // the products stand here, and not behind the wait for what was fetched meanwhile
+#pragma unroll
+        for (int t = 0; t < kM; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(acc[i][t]));
+    };
+    fetch(0);
+    keep(0);
+    __syncthreads();
+    for (int s = 0; s + 1 < stages; ++s) {
+        fetch(s + 1);
+        multiply(s);
+        keep(s + 1);
         __syncthreads();
     }
+    multiply(stages - 1);
     settle();
     // Rows behind the last one are behind the descriptor's end.  A wave whose 64 columns all exist, on
     // rows that start on 4 bytes, stores 16 bytes at a time.
