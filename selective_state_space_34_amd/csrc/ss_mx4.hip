@@ -161,21 +161,21 @@ __global__ __launch_bounds__(64 * kWaves) void mx4_rows_kernel(const Mx4Launch p
 
 // ---- many rows -------------------------------------------------------------------------------
 
-// A workgroup of four waves takes 128 rows of weights and 32·kM of x; a wave 64 by 16·kM of them.
+// A workgroup of four waves takes 32·kN rows of weights and 32·kM of x; a wave 16·kN by 16·kM.
 // Both operands pass through LDS, 128 columns at a time, in two buffers; loads for the next are in
 // flight while one is used.  A row's 16-byte pieces are placed by their number xor some bits of the
 // row, so that the eight lanes that read at once meet all banks.  Weights' rows are dealt to the four
 // 16-row products of a wave so that a lane ends up with two runs of eight of a row of y, and the four
 // lanes of a row with 64 bytes a store.
 // Exponents come 16 to a row and 512 columns.
-template <int kX, int kM>
+template <int kX, int kN, int kM>
 struct Tile {
-    static constexpr int kRowsN = 128, kRowsM = 32 * kM;
+    static constexpr int kRowsN = 32 * kN, kRowsM = 32 * kM;
     static constexpr int kBytesX = kX == kX4 ? 64 : 128;      // a row of x, 128 columns
     static constexpr int kPiecesW = kRowsN * 4, kPiecesX = kRowsM * (kBytesX / 16);
     static constexpr int kScales = kRowsN + (kX == kX4 ? kRowsM : 0);
     u32x4 w[2][kPiecesW], x[2][kPiecesX];
-    alignas(16) uint8_t e[2][kScales][16];
+    uint32_t e[2][4][kScales];
 };
 
 __device__ __forceinline__ int turn_w(int row) { return (row >> 1 & 1) | (row >> 3 & 1) << 1; }
@@ -211,19 +211,90 @@ __device__ __forceinline__ u32x4 exponents(__amdgpu_buffer_rsrc_t d, int at, int
     return w;
 }
 
-template <int kX, int kM>
-__global__ __launch_bounds__(256, 2) void mx4_tile_kernel(const Mx4Launch p, int64_t tiles_m,
-                                                          int64_t tiles_n) {
-    using L = Tile<kX, kM>;
-    __shared__ L sh;
-    // Dies get consecutive tiles (blocks go to the eight of them in turn), eight row tiles of x by
-    // one of weights after the other, so that what they read stays in a die's L2.
+// A workgroup's tile.  Dies get consecutive tiles (blocks go to the eight of them in turn), eight row
+// tiles of x by one of weights after the other, so that what they read stays in a die's L2.
+__device__ __forceinline__ bool tile_of(int64_t tiles_m, int64_t tiles_n, int64_t& m, int64_t& n) {
     const int64_t total = tiles_m * tiles_n, each = (total + 7) / 8;
     const int64_t number = int64_t(blockIdx.x % 8) * each + blockIdx.x / 8;
-    if (blockIdx.x / 8 >= each || number >= total) return;
+    if (blockIdx.x / 8 >= each || number >= total) return false;
     const int64_t per = 8 * tiles_n, first = number / per * 8;
     const int64_t high = tiles_m - first < 8 ? tiles_m - first : 8;
-    const int64_t m0 = (first + number % per % high) * L::kRowsM, n0 = number % per / high * L::kRowsN;
+    m = first + number % per % high;
+    n = number % per / high;
+    return true;
+}
+
+// Row of weights, of a wave's 16·kN, that product i takes as its row `row`.
+__device__ __forceinline__ int dealt(int i, int row) {
+    return 32 * (i >> 1) + 8 * (row >> 2) + 4 * (i & 1) + (row & 3);
+}
+
+template <int kX, int kN, int kM>
+__device__ __forceinline__ void store_tile(const Mx4Launch& p, int64_t m0, int64_t n0, int wn, int wm,
+                                           int lane, const f32x4 (&acc)[kN][kM]) {
+    const int row = lane & 15, g = lane >> 4;
+    // Rows behind the last one are behind the descriptor's end.  A wave whose columns all exist, on
+    // rows that start on 4 bytes, stores 16 bytes at a time.
+    const int N = int(p.N), el = p.y_dtype == SS_F32 ? 4 : 2;
+    const __amdgpu_buffer_rsrc_t dy = rows_from(p.y, m0, p.M, 32 * kM, int64_t(N) * el);
+    const int n = int(n0) + 16 * kN * wn + 8 * g;
+    const bool wide = int(n0) + 16 * kN * (wn + 1) <= N && (el == 4 || N % 2 == 0);
+#pragma unroll
+    for (int t = 0; t < kM; ++t) {
+        const int m = 16 * kM * wm + 16 * t + row;
+        float f = 1.0f;
+        if constexpr (kX != kX4)
+            f = static_cast<const float*>(p.x_scale)[m0 + m < p.M ? m0 + m : p.M - 1];
+        if (el == 4) {
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+                const int at = n + 32 * (i >> 1) + 4 * (i & 1);
+                u32x4 v;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    v[j] = __float_as_uint(kX == kX4 ? acc[i][t][j] : acc[i][t][j] * f);
+                if (wide) {
+                    __builtin_amdgcn_raw_buffer_store_b128(v, dy, (m * N + at) * 4, 0, 0);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        __builtin_amdgcn_raw_buffer_store_b32(
+                            v[j], dy, at + j < N ? (m * N + at + j) * 4 : kNowhere, 0, 0);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kN / 2; ++i) {
+                const int at = n + 32 * i;
+                union { bf16x8 h; u32x4 w; } o;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float v = acc[2 * i + j / 4][t][j % 4];
+                    o.h[j] = __bf16(kX == kX4 ? v : v * f);
+                }
+                if (wide) {
+                    __builtin_amdgcn_raw_buffer_store_b128(o.w, dy, (m * N + at) * 2, 0, 0);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        __builtin_amdgcn_raw_buffer_store_b16(
+                            uint16_t(o.w[j / 2] >> (16 * (j % 2))), dy,
+                            at + j < N ? (m * N + at + j) * 2 : kNowhere, 0, 0);
+                }
+            }
+        }
+    }
+}
+
+template <int kX, int kN, int kM>
+__global__ __launch_bounds__(256, 2) void mx4_tile_kernel(
+    const Mx4Launch p, int64_t tiles_m, int64_t tiles_n) {
+    using L = Tile<kX, kN, kM>;
+    __shared__ L sh;
+    int64_t m0, n0;
+    if (!tile_of(tiles_m, tiles_n, m0, n0)) return;
+    m0 *= L::kRowsM;
+    n0 *= L::kRowsN;
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wn = wave & 1, wm = wave >> 1;
@@ -248,151 +319,123 @@ __global__ __launch_bounds__(256, 2) void mx4_tile_kernel(const Mx4Launch p, int
         cx[i] = ((s % kPer) ^ turn_x<kX>(r)) * 16;
         ox[i] = r * row_x + cx[i];
     }
-    constexpr int kLoadE = (L::kScales + 255) / 256;
-    u32x4 rw[kLoadW], rx[kLoadX], re[kLoadE];
-    auto fetch = [&](int s) {      // what lies behind the last column is 0
-#pragma unroll
-        for (int i = 0; i < kLoadW; ++i)
-            rw[i] = __builtin_amdgcn_raw_buffer_load_b128(
+    constexpr int kLoadE = (L::kScales + 255) / 256, kLoad = kLoadW + kLoadX;
+    u32x4 re[kLoadE];
+    struct Moved {
+        u32x4 v[kLoad];
+    } one, two;
+    // piece i of a thread: weights' first; what lies behind the last column is 0
+    auto fetch = [&](int s, int i, Moved& r) {
+        if (i < kLoadW)
+            r.v[i] = __builtin_amdgcn_raw_buffer_load_b128(
                 dw, s * 64 + cw[i] < row_w ? ow[i] : kNowhere, s * 64, 0);
+        else
+            r.v[i] = __builtin_amdgcn_raw_buffer_load_b128(
+                dx, s * L::kBytesX + cx[i - kLoadW] < row_x ? ox[i - kLoadW] : kNowhere,
+                s * L::kBytesX, 0);
+    };
+    auto keep = [&](int to, int i, const Moved& r) {
+        if (i < kLoadW) sh.w[to][tid + 256 * i] = r.v[i];
+        else sh.x[to][tid + 256 * (i - kLoadW)] = r.v[i];
+    };
+    auto fetch_e = [&](int block) {    // a thread a row: the weights' first, then those of x
 #pragma unroll
-        for (int i = 0; i < kLoadX; ++i)
-            rx[i] = __builtin_amdgcn_raw_buffer_load_b128(
-                dx, s * L::kBytesX + cx[i] < row_x ? ox[i] : kNowhere, s * L::kBytesX, 0);
-        if (s % 4 == 0) {
-            // threads 0 .. 127 take a row of weights, the others one of x, and each 128 of x besides
-            if (wave < 2) re[0] = exponents(dwe, tid * kb, s / 4, kb);
-            else if (kX == kX4) re[0] = exponents(dxe, (tid - 128) * kb, s / 4, kb);
-            if constexpr (kLoadE > 1)
-                if (tid + 256 < L::kScales) re[1] = exponents(dxe, (tid + 128) * kb, s / 4, kb);
+        for (int i = 0; i < kLoadE; ++i) {
+            const int r = tid + 256 * i;
+            if (256 * i + 64 * wave < L::kRowsN) re[i] = exponents(dwe, r * kb, block, kb);
+            else if (256 * i + 64 * wave < L::kScales)
+                re[i] = exponents(dxe, (r - L::kRowsN) * kb, block, kb);
         }
     };
-    auto keep = [&](int s) {
-        const int to = s & 1;
+    auto keep_e = [&](int block) {
 #pragma unroll
-        for (int i = 0; i < kLoadW; ++i) sh.w[to][tid + 256 * i] = rw[i];
+        for (int i = 0; i < kLoadE; ++i)
+            if (256 * i + 64 * wave < L::kScales)
 #pragma unroll
-        for (int i = 0; i < kLoadX; ++i) sh.x[to][tid + 256 * i] = rx[i];
-        if (s % 4 == 0) {
-#pragma unroll
-            for (int i = 0; i < kLoadE; ++i)
-                if (tid + 256 * i < L::kScales)
-                    *reinterpret_cast<u32x4*>(sh.e[s / 4 & 1][tid + 256 * i]) = re[i];
-        }
+                for (int c = 0; c < 4; ++c) sh.e[block & 1][c][tid + 256 * i] = re[i][c];
     };
 
-    f32x4 acc[4][kM] = {};
+    f32x4 acc[kN][kM] = {};
     const int stages = (K + 127) / 128;
-    auto multiply = [&](int s) {
-        const int from = s & 1, eb = s / 4 & 1, es = (s & 3) * 4 + g;
-        i32x8 a[4] = {};
-        int sa[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = 64 * wn + 32 * (i >> 1) + 8 * (row >> 2) + 4 * (i & 1) + (row & 3);
-            const u32x4 v = sh.w[from][r * 4 + (g ^ turn_w(r))];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) a[i][c] = int(v[c]);
-            sa[i] = sh.e[eb][r][es];
-        }
-#pragma unroll
-        for (int t = 0; t < kM; ++t) {
-            const int r = 16 * kM * wm + 16 * t + row;
-            i32x8 b = {};
-            int sb = 127;
+    // A stage is 128 columns.  While its products run, the next one's columns (fetched during the last
+    // stage: `in`) go into the other buffer and those of the one after are fetched, in steps of one
+    // row tile of x, whose order the compiler keeps.
+    auto stage = [&](int s, const Moved& in, Moved& out) {
+        const int from = s & 1;
+        const uint8_t* e = reinterpret_cast<const uint8_t*>(sh.e[s / 4 & 1][s & 3]) + g;
+        i32x8 a[kN] = {}, b[2] = {};
+        int sa[kN], sb[2];
+        auto read_x = [&](int t) {
+            const int r = 16 * kM * wm + 16 * t + row, o = t & 1;
             if constexpr (kX == kX4) {
                 const u32x4 v = sh.x[from][r * 4 + (g ^ turn_x<kX>(r))];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) b[c] = int(v[c]);
-                sb = sh.e[eb][L::kRowsN + r][es];
+                for (int c = 0; c < 4; ++c) b[o][c] = int(v[c]);
+                sb[o] = e[4 * (L::kRowsN + r)];
             } else {
                 const u32x4 v = sh.x[from][r * 8 + (g ^ turn_x<kX>(r))];
                 const u32x4 u = sh.x[from][r * 8 + ((4 + g) ^ turn_x<kX>(r))];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    b[c] = int(v[c]);
-                    b[4 + c] = int(u[c]);
+                    b[o][c] = int(v[c]);
+                    b[o][4 + c] = int(u[c]);
                 }
+                sb[o] = 127;
+            }
+        };
+        read_x(0);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const int r = 16 * kN * wn + dealt(i, row);
+            const u32x4 v = sh.w[from][r * 4 + (g ^ turn_w(r))];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) a[i][c] = int(v[c]);
+            sa[i] = e[4 * r];
+        }
+#pragma unroll
+        for (int t = 0; t < kM; ++t) {
+            if (t + 1 < kM) read_x(t + 1);
+#pragma unroll
+            for (int i = t; i < kLoad; i += kM) {
+                keep(from ^ 1, i, in);
+                fetch(s + 2, i, out);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < kN; ++i)
                 acc[i][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    a[i], b, acc[i][t], 4, kX == kX4 ? 4 : 0, 0, sa[i], 0, sb);
+                    a[i], b[t & 1], acc[i][t], 4, kX == kX4 ? 4 : 0, 0, sa[i], 0, sb[t & 1]);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        // the products stand here, and not behind the wait for what was fetched meanwhile
+        // (pinned: the compiler would move products behind the branches that follow)
 #pragma unroll
         for (int t = 0; t < kM; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(acc[i][t]));
-    };
-    fetch(0);
-    keep(0);
-    __syncthreads();
-    for (int s = 0; s + 1 < stages; ++s) {
-        fetch(s + 1);
-        multiply(s);
-        keep(s + 1);
+            for (int i = 0; i < kN; ++i) asm volatile("" : "+v"(acc[i][t]));
+        if ((s + 1) % 4 == 0) keep_e((s + 1) / 4);
+        if ((s + 2) % 4 == 0) fetch_e((s + 2) / 4);
         __syncthreads();
+    };
+#pragma unroll
+    for (int i = 0; i < kLoad; ++i) fetch(0, i, two);
+    fetch_e(0);
+#pragma unroll
+    for (int i = 0; i < kLoad; ++i) fetch(1, i, one);
+#pragma unroll
+    for (int i = 0; i < kLoad; ++i) keep(0, i, two);
+    keep_e(0);
+    __syncthreads();
+    for (int s = 0; s < stages; s += 2) {
+        stage(s, one, two);
+        if (s + 1 < stages) stage(s + 1, two, one);
     }
-    multiply(stages - 1);
     settle();
-    // Rows behind the last one are behind the descriptor's end.  A wave whose 64 columns all exist, on
-    // rows that start on 4 bytes, stores 16 bytes at a time.
-    const int N = int(p.N), el = p.y_dtype == SS_F32 ? 4 : 2;
-    const __amdgpu_buffer_rsrc_t dy = rows_from(p.y, m0, p.M, L::kRowsM, int64_t(N) * el);
-    const int n = int(n0) + 64 * wn + 8 * g;
-    const bool wide = int(n0) + 64 * wn + 64 <= N && (el == 4 || N % 2 == 0);
-#pragma unroll
-    for (int t = 0; t < kM; ++t) {
-        const int m = 16 * kM * wm + 16 * t + row;
-        float f = 1.0f;
-        if constexpr (kX != kX4)
-            f = static_cast<const float*>(p.x_scale)[m0 + m < p.M ? m0 + m : p.M - 1];
-        if (el == 4) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int at = n + 32 * (i >> 1) + 4 * (i & 1);
-                u32x4 v;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    v[j] = __float_as_uint(kX == kX4 ? acc[i][t][j] : acc[i][t][j] * f);
-                if (wide) {
-                    __builtin_amdgcn_raw_buffer_store_b128(v, dy, (m * N + at) * 4, 0, 0);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        __builtin_amdgcn_raw_buffer_store_b32(
-                            v[j], dy, at + j < N ? (m * N + at + j) * 4 : kNowhere, 0, 0);
-                }
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int at = n + 32 * i;
-                union { bf16x8 h; u32x4 w; } o;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float v = acc[2 * i + j / 4][t][j % 4];
-                    o.h[j] = __bf16(kX == kX4 ? v : v * f);
-                }
-                if (wide) {
-                    __builtin_amdgcn_raw_buffer_store_b128(o.w, dy, (m * N + at) * 2, 0, 0);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        __builtin_amdgcn_raw_buffer_store_b16(
-                            uint16_t(o.w[j / 2] >> (16 * (j % 2))), dy,
-                            at + j < N ? (m * N + at + j) * 2 : kNowhere, 0, 0);
-                }
-            }
-        }
-    }
+    store_tile<kX, kN, kM>(p, m0, n0, wn, wm, lane, acc);
 }
 
-template <int kX, int kM>
+template <int kX, int kN, int kM>
 hipError_t launch_tiles(const Mx4Launch& p, hipStream_t s) {
-    const int64_t m = (p.M + 32 * kM - 1) / (32 * kM), n = (p.N + 127) / 128;
-    hipLaunchKernelGGL((mx4_tile_kernel<kX, kM>), dim3(unsigned((m * n + 7) / 8 * 8)), dim3(256), 0, s, p,
+    const int64_t m = (p.M + 32 * kM - 1) / (32 * kM), n = (p.N + 32 * kN - 1) / (32 * kN);
+    hipLaunchKernelGGL((mx4_tile_kernel<kX, kN, kM>), dim3(unsigned((m * n + 7) / 8 * 8)), dim3(256), 0, s, p,
                        m, n);
     return hipGetLastError();
 }
@@ -410,7 +453,7 @@ hipError_t launch_mm(const Mx4Launch& p, hipStream_t s) {
     if (p.M <= 32) return launch_rows<2, kX>(p, s);
     if constexpr (kX != kX8Wide) {
         // (256 rows of y stay within a descriptor)
-        if (p.M > 128 && p.N < (1 << 20)) return launch_tiles<kX, kX == kX4 ? 8 : 4>(p, s);
+        if (p.M > 128 && p.N < (1 << 20)) return launch_tiles<kX, 4, kX == kX4 ? 8 : 4>(p, s);
     }
     return launch_rows<4, kX>(p, s);
 }
