@@ -15,6 +15,7 @@ namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -161,32 +162,39 @@ __global__ __launch_bounds__(64 * kWaves) void mx4_rows_kernel(const Mx4Launch p
 
 // ---- many rows -------------------------------------------------------------------------------
 
-// A workgroup of four waves takes 32·kN rows of weights and 32·kM of x; a wave 16·kN by 16·kM.
-// Both operands pass through LDS, 128 columns at a time, in two buffers; loads for the next are in
-// flight while one is used.  A row's 16-byte pieces are placed by their number xor some bits of the
-// row, so that the eight lanes that read at once meet all banks.  Weights' rows are dealt to the four
-// 16-row products of a wave so that a lane ends up with two runs of eight of a row of y, and the four
-// lanes of a row with 64 bytes a store.
-// Exponents come 16 to a row and 512 columns.
-template <int kX, int kN, int kM>
+// A workgroup of four waves takes 128 rows of weights and 64·kM of x; a wave 64 by 32·kM of them, as
+// products of 32 by 32 rows and 64 columns (v_mfma_scale_f32_32x32x64_f8f6f4: lane l row l % 32 and
+// block l / 32; of e4m3 two runs of 16 columns, 32 apart).  Both operands pass through LDS, 128
+// columns (a stage) at a time, in two buffers.  A row's 16-byte pieces are placed by their number xor
+// some bits of the row, so that the 16 lanes that read at once (0-3, 12-15, 20-23, 24-27; the others of 32;
+// and so on) meet all banks: no conflicts counted.  Weights' rows are
+// dealt to the two products of a wave so that a lane ends up with runs of eight of a row of y.
+// Exponents come 16 to a row and four stages.
+template <int kX, int kM>
 struct Tile {
-    static constexpr int kRowsN = 32 * kN, kRowsM = 32 * kM;
+    static constexpr int kRowsN = 128, kRowsM = 64 * kM;
     static constexpr int kBytesX = kX == kX4 ? 64 : 128;      // a row of x, 128 columns
     static constexpr int kPiecesW = kRowsN * 4, kPiecesX = kRowsM * (kBytesX / 16);
-    static constexpr int kScales = kRowsN + (kX == kX4 ? kRowsM : 0);
+    static constexpr int kUsed = kRowsN + (kX == kX4 ? kRowsM : 0);
+    static constexpr int kScales = (kUsed + 255) / 256 * 256;
     u32x4 w[2][kPiecesW], x[2][kPiecesX];
     uint32_t e[2][4][kScales];
 };
 
-__device__ __forceinline__ int turn_w(int row) { return (row >> 1 & 1) | (row >> 3 & 1) << 1; }
+__device__ __forceinline__ int turn_w(int row) { return row >> 3 & 3; }
 template <int kX> __device__ __forceinline__ int turn_x(int row) {
-    return kX == kX4 ? row >> 1 & 3 : row & 7;
+    return kX == kX4 ? row >> 2 & 3 : row >> 1 & 7;
+}
+
+// Row of weights, of a wave's 64, that product u takes as its row r.
+__device__ __forceinline__ int dealt(int u, int r) {
+    return 16 * (r >> 3) + 8 * (r >> 2 & 1) + 4 * u + (r & 3);
 }
 
 constexpr int kRsrcFlags = 0x00020000;       // raw buffer, 32-bit elements
-constexpr int kNowhere = int(0x80000000u);   // behind every descriptor's end: loads 0
+constexpr int kNowhere = int(0x80000000u);   // behind every descriptor's end: loads 0, stores nothing
 
-// A tile's rows, `bytes` each, of `rows` from number r0 on; what lies behind the last one loads as 0.
+// A tile's rows, `bytes` each, of `rows` from number r0 on.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_from(const void* p, int64_t r0, int64_t rows,
                                                            int64_t most, int64_t bytes) {
     const int64_t n = rows - r0 < most ? rows - r0 : most;
@@ -194,19 +202,18 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_from(const void* p, int64
         const_cast<uint8_t*>(static_cast<const uint8_t*>(p)) + r0 * bytes, 0, int(n * bytes), kRsrcFlags);
 }
 
-// Exponents 16·block .. of the row at `at` that has n of them; 0 behind its end (the codes there are
-// 0 as well).
+// Exponents 16·block .. of the row at `at` that has n of them.  kEven: n is a multiple of 4.
+template <bool kEven>
 __device__ __forceinline__ u32x4 exponents(__amdgpu_buffer_rsrc_t d, int at, int block, int n) {
-    const int left = n - 16 * block;
-    at += 16 * block;
     u32x4 w = {0, 0, 0, 0};
-    if (left >= 16 && n % 4 == 0) {
-        w = __builtin_amdgcn_raw_buffer_load_b128(d, at, 0, 0);
+    if constexpr (kEven) {
+        w = __builtin_amdgcn_raw_buffer_load_b128(d, at, 16 * block, 0);
     } else {
+        const int left = n - 16 * block;
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-            w[i / 4] |= uint32_t(__builtin_amdgcn_raw_buffer_load_b8(d, i < left ? at + i : kNowhere, 0, 0))
-                        << (8 * (i % 4));
+            w[i / 4] |= uint32_t(__builtin_amdgcn_raw_buffer_load_b8(
+                            d, i < left ? at + 16 * block + i : kNowhere, 0, 0)) << (8 * (i % 4));
     }
     return w;
 }
@@ -224,54 +231,50 @@ __device__ __forceinline__ bool tile_of(int64_t tiles_m, int64_t tiles_n, int64_
     return true;
 }
 
-// Row of weights, of a wave's 16·kN, that product i takes as its row `row`.
-__device__ __forceinline__ int dealt(int i, int row) {
-    return 32 * (i >> 1) + 8 * (row >> 2) + 4 * (i & 1) + (row & 3);
-}
-
-template <int kX, int kN, int kM>
+// Rows behind the last one are behind the descriptor's end.  A wave whose columns all exist, on rows
+// that start on 4 bytes, stores 16 bytes at a time.
+template <int kX, int kM>
 __device__ __forceinline__ void store_tile(const Mx4Launch& p, int64_t m0, int64_t n0, int wn, int wm,
-                                           int lane, const f32x4 (&acc)[kN][kM]) {
-    const int row = lane & 15, g = lane >> 4;
-    // Rows behind the last one are behind the descriptor's end.  A wave whose columns all exist, on
-    // rows that start on 4 bytes, stores 16 bytes at a time.
+                                           int lane, const f32x16 (&acc)[2][kM]) {
+    const int row = lane & 31, g = lane >> 5;
     const int N = int(p.N), el = p.y_dtype == SS_F32 ? 4 : 2;
-    const __amdgpu_buffer_rsrc_t dy = rows_from(p.y, m0, p.M, 32 * kM, int64_t(N) * el);
-    const int n = int(n0) + 16 * kN * wn + 8 * g;
-    const bool wide = int(n0) + 16 * kN * (wn + 1) <= N && (el == 4 || N % 2 == 0);
+    const __amdgpu_buffer_rsrc_t dy = rows_from(p.y, m0, p.M, 64 * kM, int64_t(N) * el);
+    const int n = int(n0) + 64 * wn + 8 * g;
+    const bool wide = int(n0) + 64 * (wn + 1) <= N && (el == 4 || N % 2 == 0);
 #pragma unroll
     for (int t = 0; t < kM; ++t) {
-        const int m = 16 * kM * wm + 16 * t + row;
+        const int m = 32 * kM * wm + 32 * t + row;
         float f = 1.0f;
         if constexpr (kX != kX4)
             f = static_cast<const float*>(p.x_scale)[m0 + m < p.M ? m0 + m : p.M - 1];
-        if (el == 4) {
 #pragma unroll
-            for (int i = 0; i < kN; ++i) {
-                const int at = n + 32 * (i >> 1) + 4 * (i & 1);
-                u32x4 v;
+        for (int q = 0; q < 4; ++q) {
+            // eight columns from n + 16 q on: four of each product
+            const int at = n + 16 * q;
+            float v[8];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    v[j] = __float_as_uint(kX == kX4 ? acc[i][t][j] : acc[i][t][j] * f);
+            for (int j = 0; j < 8; ++j) {
+                v[j] = acc[j / 4][t][4 * q + j % 4];
+                if constexpr (kX != kX4) v[j] *= f;
+            }
+            if (el == 4) {
                 if (wide) {
-                    __builtin_amdgcn_raw_buffer_store_b128(v, dy, (m * N + at) * 4, 0, 0);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const u32x4 w = {__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                                         __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])};
+                        __builtin_amdgcn_raw_buffer_store_b128(w, dy, (m * N + at + 4 * i) * 4, 0, 0);
+                    }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                    for (int j = 0; j < 8; ++j)
                         __builtin_amdgcn_raw_buffer_store_b32(
-                            v[j], dy, at + j < N ? (m * N + at + j) * 4 : kNowhere, 0, 0);
+                            __float_as_uint(v[j]), dy, at + j < N ? (m * N + at + j) * 4 : kNowhere, 0, 0);
                 }
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kN / 2; ++i) {
-                const int at = n + 32 * i;
+            } else {
                 union { bf16x8 h; u32x4 w; } o;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float v = acc[2 * i + j / 4][t][j % 4];
-                    o.h[j] = __bf16(kX == kX4 ? v : v * f);
-                }
+                for (int j = 0; j < 8; ++j) o.h[j] = __bf16(v[j]);
                 if (wide) {
                     __builtin_amdgcn_raw_buffer_store_b128(o.w, dy, (m * N + at) * 2, 0, 0);
                 } else {
@@ -286,40 +289,30 @@ __device__ __forceinline__ void store_tile(const Mx4Launch& p, int64_t m0, int64
     }
 }
 
-template <int kX, int kN, int kM>
-__global__ __launch_bounds__(256, 2) void mx4_tile_kernel(
-    const Mx4Launch p, int64_t tiles_m, int64_t tiles_n) {
-    using L = Tile<kX, kN, kM>;
+// kEven: K is a multiple of 128.
+template <int kX, int kM, bool kEven>
+__global__ __launch_bounds__(256, 2) void mx4_tile_kernel(const Mx4Launch p, int64_t tiles_m,
+                                                          int64_t tiles_n) {
+    using L = Tile<kX, kM>;
     __shared__ L sh;
     int64_t m0, n0;
     if (!tile_of(tiles_m, tiles_n, m0, n0)) return;
     m0 *= L::kRowsM;
     n0 *= L::kRowsN;
-
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wn = wave & 1, wm = wave >> 1;
-    const int row = lane & 15, g = lane >> 4;
+    const int row = lane & 31, g = lane >> 5;
     const int K = int(p.K), kb = K / 32, row_w = K / 2, row_x = kX == kX4 ? K / 2 : K;
     const __amdgpu_buffer_rsrc_t dw = rows_from(p.wq, n0, p.N, L::kRowsN, row_w);
     const __amdgpu_buffer_rsrc_t dx = rows_from(p.x, m0, p.M, L::kRowsM, row_x);
     const __amdgpu_buffer_rsrc_t dwe = rows_from(p.w_exps, n0, p.N, L::kRowsN, kb);
     const __amdgpu_buffer_rsrc_t dxe = rows_from(p.x_scale, m0, p.M, L::kRowsM, kX == kX4 ? kb : 0);
 
-    constexpr int kLoadW = L::kPiecesW / 256, kLoadX = L::kPiecesX / 256, kPer = L::kBytesX / 16;
-    int cw[kLoadW], cx[kLoadX], ow[kLoadW], ox[kLoadX];
-#pragma unroll
-    for (int i = 0; i < kLoadW; ++i) {
-        const int s = tid + 256 * i, r = s / 4;
-        cw[i] = ((s & 3) ^ turn_w(r)) * 16;
-        ow[i] = r * row_w + cw[i];
-    }
-#pragma unroll
-    for (int i = 0; i < kLoadX; ++i) {
-        const int s = tid + 256 * i, r = s / kPer;
-        cx[i] = ((s % kPer) ^ turn_x<kX>(r)) * 16;
-        ox[i] = r * row_x + cx[i];
-    }
-    constexpr int kLoadE = (L::kScales + 255) / 256, kLoad = kLoadW + kLoadX;
+    constexpr int kLoadW = L::kPiecesW / 256, kLoadX = L::kPiecesX / 256, kLoad = kLoadW + kLoadX;
+    constexpr int kPer = L::kBytesX / 16, kLoadE = L::kScales / 256;
+    // piece tid + 256 i: rows 64 (or 32) apart, whose turns are alike
+    const int cw = ((tid & 3) ^ turn_w(tid >> 2)) * 16, ow = (tid >> 2) * row_w + cw;
+    const int cx = ((tid % kPer) ^ turn_x<kX>(tid / kPer)) * 16, ox = tid / kPer * row_x + cx;
     u32x4 re[kLoadE];
     struct Moved {
         u32x4 v[kLoad];
@@ -328,115 +321,139 @@ __global__ __launch_bounds__(256, 2) void mx4_tile_kernel(
     auto fetch = [&](int s, int i, Moved& r) {
         if (i < kLoadW)
             r.v[i] = __builtin_amdgcn_raw_buffer_load_b128(
-                dw, s * 64 + cw[i] < row_w ? ow[i] : kNowhere, s * 64, 0);
+                dw, kEven || s * 64 + cw < row_w ? ow : kNowhere, s * 64 + i * 64 * row_w, 0);
         else
             r.v[i] = __builtin_amdgcn_raw_buffer_load_b128(
-                dx, s * L::kBytesX + cx[i - kLoadW] < row_x ? ox[i - kLoadW] : kNowhere,
-                s * L::kBytesX, 0);
+                dx, kEven || s * L::kBytesX + cx < row_x ? ox : kNowhere,
+                s * L::kBytesX + (i - kLoadW) * (256 / kPer) * row_x, 0);
     };
     auto keep = [&](int to, int i, const Moved& r) {
         if (i < kLoadW) sh.w[to][tid + 256 * i] = r.v[i];
         else sh.x[to][tid + 256 * (i - kLoadW)] = r.v[i];
     };
-    auto fetch_e = [&](int block) {    // a thread a row: the weights' first, then those of x
+    // a thread a row: the weights' first, then those of x, then none
+    auto fetch_e = [&](int block) {
 #pragma unroll
         for (int i = 0; i < kLoadE; ++i) {
-            const int r = tid + 256 * i;
-            if (256 * i + 64 * wave < L::kRowsN) re[i] = exponents(dwe, r * kb, block, kb);
-            else if (256 * i + 64 * wave < L::kScales)
-                re[i] = exponents(dxe, (r - L::kRowsN) * kb, block, kb);
+            const int r0 = 256 * i + 64 * wave, r = tid + 256 * i;
+            const bool w = r0 < L::kRowsN;
+            re[i] = exponents<kEven>(w ? dwe : dxe, r0 < L::kUsed ? (w ? r : r - L::kRowsN) * kb : kNowhere,
+                                     block, kb);
         }
     };
-    auto keep_e = [&](int block) {
+    auto keep_e = [&](int block) {      // 0 behind a row's end: the codes there are 0 as well
 #pragma unroll
         for (int i = 0; i < kLoadE; ++i)
-            if (256 * i + 64 * wave < L::kScales)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) sh.e[block & 1][c][tid + 256 * i] = re[i][c];
+            for (int c = 0; c < 4; ++c)
+                sh.e[block & 1][c][tid + 256 * i] = 4 * (4 * block + c) < kb ? re[i][c] : 0;
     };
 
-    f32x4 acc[kN][kM] = {};
+    // Operands of a wave are the first + a constant: dealt() and 32 t leave the bits of the turns alone.
+    const int rn = 64 * wn + dealt(0, row), rm = 32 * kM * wm + row;
+    const int at_w = rn * 4, tw = turn_w(rn), at_x = rm * kPer, tx = turn_x<kX>(rm);
+    f32x16 acc[2][kM] = {};
     const int stages = (K + 127) / 128;
-    // A stage is 128 columns.  While its products run, the next one's columns (fetched during the last
-    // stage: `in`) go into the other buffer and those of the one after are fetched, in steps of one
-    // row tile of x, whose order the compiler keeps.
-    auto stage = [&](int s, const Moved& in, Moved& out) {
-        const int from = s & 1;
-        const uint8_t* e = reinterpret_cast<const uint8_t*>(sh.e[s / 4 & 1][s & 3]) + g;
-        i32x8 a[kN] = {}, b[2] = {};
-        int sa[kN], sb[2];
-        auto read_x = [&](int t) {
-            const int r = 16 * kM * wm + 16 * t + row, o = t & 1;
+    // Stage 4 block + j.  While a stage's products run, the next one's columns (fetched during the last stage: `in`) go into
+    // the other buffer and those of the one after are fetched, in steps of two products, whose order
+    // the compiler keeps.
+    auto stage = [&](int block, auto j) {
+        constexpr int kJ = decltype(j)::value, from = kJ & 1;
+        const int s = 4 * block + kJ;
+        const uint8_t* e = reinterpret_cast<const uint8_t*>(sh.e[block & 1][kJ]);
+        i32x8 a[2][2] = {}, b[2] = {};        // weights: half of the stage, product
+        int sa[2][2], sb[2];
+        auto read_w = [&](int h, int u) {
+            const u32x4 v = sh.w[from][at_w + 16 * u + ((2 * h + g) ^ tw)];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) a[h][u][c] = int(v[c]);
+            sa[h][u] = e[4 * (rn + 4 * u) + 2 * h + g];
+        };
+        auto read_x = [&](int step) {
+            const int o = step & 1, h = step / kM, t = step % kM;
             if constexpr (kX == kX4) {
-                const u32x4 v = sh.x[from][r * 4 + (g ^ turn_x<kX>(r))];
+                const u32x4 v = sh.x[from][at_x + 128 * t + ((2 * h + g) ^ tx)];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) b[o][c] = int(v[c]);
-                sb[o] = e[4 * (L::kRowsN + r)];
+                sb[o] = e[4 * (L::kRowsN + rm + 32 * t) + 2 * h + g];
             } else {
-                const u32x4 v = sh.x[from][r * 8 + (g ^ turn_x<kX>(r))];
-                const u32x4 u = sh.x[from][r * 8 + ((4 + g) ^ turn_x<kX>(r))];
+                const u32x4 v = sh.x[from][at_x + 256 * t + ((4 * h + g) ^ tx)];
+                const u32x4 w = sh.x[from][at_x + 256 * t + ((4 * h + 2 + g) ^ tx)];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     b[o][c] = int(v[c]);
-                    b[o][4 + c] = int(u[c]);
+                    b[o][4 + c] = int(w[c]);
                 }
                 sb[o] = 127;
             }
         };
         read_x(0);
+        read_w(0, 0);
+        read_w(0, 1);
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
-            const int r = 16 * kN * wn + dealt(i, row);
-            const u32x4 v = sh.w[from][r * 4 + (g ^ turn_w(r))];
+        for (int step = 0; step < 2 * kM; ++step) {
+            const int h = step / kM, t = step % kM, o = step & 1;
+            if (step + 1 < 2 * kM) read_x(step + 1);
+            if (step < 2) read_w(1, step);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) a[i][c] = int(v[c]);
-            sa[i] = e[4 * r];
-        }
-#pragma unroll
-        for (int t = 0; t < kM; ++t) {
-            if (t + 1 < kM) read_x(t + 1);
-#pragma unroll
-            for (int i = t; i < kLoad; i += kM) {
-                keep(from ^ 1, i, in);
-                fetch(s + 2, i, out);
+            for (int i = step; i < kLoad; i += 2 * kM) {
+                keep(from ^ 1, i, from ? one : two);
+                if constexpr (from == 0) {
+                    fetch(s + 2, i, one);
+                    fetch(s + 3, i, two);
+                }
             }
 #pragma unroll
-            for (int i = 0; i < kN; ++i)
-                acc[i][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    a[i], b[t & 1], acc[i][t], 4, kX == kX4 ? 4 : 0, 0, sa[i], 0, sb[t & 1]);
+            for (int u = 0; u < 2; ++u)
+                acc[u][t] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    a[h][u], b[o], acc[u][t], 4, kX == kX4 ? 4 : 0, 0, sa[h][u], 0, sb[o]);
             __builtin_amdgcn_sched_barrier(0);
         }
-        // (pinned: the compiler would move products behind the branches that follow)
+        // (pinned: the compiler would move products behind branches that follow)
 #pragma unroll
-        for (int t = 0; t < kM; ++t)
-#pragma unroll
-            for (int i = 0; i < kN; ++i) asm volatile("" : "+v"(acc[i][t]));
-        if ((s + 1) % 4 == 0) keep_e((s + 1) / 4);
-        if ((s + 2) % 4 == 0) fetch_e((s + 2) / 4);
+        for (int t = 0; t < kM; ++t) asm volatile("" : "+v"(acc[0][t]), "+v"(acc[1][t]));
+        if constexpr (kJ == 3) keep_e(block + 1);
+        if constexpr (kJ == 0) fetch_e(block + 1);
         __syncthreads();
     };
 #pragma unroll
-    for (int i = 0; i < kLoad; ++i) fetch(0, i, two);
+    for (int i = 0; i < kLoad; ++i) {
+        fetch(0, i, one);
+        fetch(1, i, two);
+    }
     fetch_e(0);
 #pragma unroll
-    for (int i = 0; i < kLoad; ++i) fetch(1, i, one);
-#pragma unroll
-    for (int i = 0; i < kLoad; ++i) keep(0, i, two);
+    for (int i = 0; i < kLoad; ++i) keep(0, i, one);
     keep_e(0);
     __syncthreads();
-    for (int s = 0; s < stages; s += 2) {
-        stage(s, one, two);
-        if (s + 1 < stages) stage(s + 1, two, one);
+    // four stages at a time without a branch, so that the waits inside are counted for what they wait
+    const std::integral_constant<int, 0> j0;
+    const std::integral_constant<int, 1> j1;
+    const std::integral_constant<int, 2> j2;
+    const std::integral_constant<int, 3> j3;
+    int block = 0;
+    for (; 4 * block + 4 <= stages; ++block) {
+        stage(block, j0);
+        stage(block, j1);
+        stage(block, j2);
+        stage(block, j3);
     }
+    if (4 * block < stages) stage(block, j0);
+    if (4 * block + 1 < stages) stage(block, j1);
+    if (4 * block + 2 < stages) stage(block, j2);
+    settle();      // (a product of 32 by 32 takes up to twice the wait)
     settle();
-    store_tile<kX, kN, kM>(p, m0, n0, wn, wm, lane, acc);
+    store_tile<kX, kM>(p, m0, n0, wn, wm, lane, acc);
 }
 
-template <int kX, int kN, int kM>
+template <int kX, int kM>
 hipError_t launch_tiles(const Mx4Launch& p, hipStream_t s) {
-    const int64_t m = (p.M + 32 * kM - 1) / (32 * kM), n = (p.N + 32 * kN - 1) / (32 * kN);
-    hipLaunchKernelGGL((mx4_tile_kernel<kX, kN, kM>), dim3(unsigned((m * n + 7) / 8 * 8)), dim3(256), 0, s, p,
-                       m, n);
+    const int64_t m = (p.M + 64 * kM - 1) / (64 * kM), n = (p.N + 127) / 128;
+    const dim3 grid(unsigned((m * n + 7) / 8 * 8));
+    if (p.K % 128 == 0)
+        hipLaunchKernelGGL((mx4_tile_kernel<kX, kM, true>), grid, dim3(256), 0, s, p, m, n);
+    else
+        hipLaunchKernelGGL((mx4_tile_kernel<kX, kM, false>), grid, dim3(256), 0, s, p, m, n);
     return hipGetLastError();
 }
 
@@ -453,7 +470,7 @@ hipError_t launch_mm(const Mx4Launch& p, hipStream_t s) {
     if (p.M <= 32) return launch_rows<2, kX>(p, s);
     if constexpr (kX != kX8Wide) {
         // (256 rows of y stay within a descriptor)
-        if (p.M > 128 && p.N < (1 << 20)) return launch_tiles<kX, 4, kX == kX4 ? 8 : 4>(p, s);
+        if (p.M > 128 && p.N < (1 << 20)) return launch_tiles<kX, kX == kX4 ? 4 : 2>(p, s);
     }
     return launch_rows<4, kX>(p, s);
 }
