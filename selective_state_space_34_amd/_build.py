@@ -18,10 +18,10 @@ LIB = os.path.join(LIBDIR, "libss.so")
 
 SOURCES = ["ss_api.cpp", "ss_fwd.hip", "ss_fwdg.hip", "ss_carry.hip", "ss_bwd.hip", "ss_step.hip",
            "ss_block.hip", "ss_la_api.cpp", "ss_la.hip", "ss_la_bf16.hip", "ss_la_f32.hip",
-           "ss_la_bf16_any.hip", "ss_la_f32_any.hip", "ss_norm.hip", "ss_q4.hip", "ss_gr_api.cpp",
+           "ss_la_bf16_any.hip", "ss_la_f32_any.hip", "ss_norm.hip", "ss_q4.hip", "ss_ln.hip", "ss_gr_api.cpp",
            "ss_gr.hip", "ss_mx4.hip"]
 HEADERS = ["ss_device.h", "ss_kernels.h", "ss_plan.h", "ss_la_plan.h", "ss_la_sweep.h",
-           "ss_gr_plan.h"]
+           "ss_gr_plan.h", "ss_norm_rows.h"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

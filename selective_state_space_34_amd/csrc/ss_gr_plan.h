@@ -69,17 +69,38 @@ inline int make_gr_plan(const ss_gr_dims& d, bool backward, bool given_ckpt, GrP
     return SS_OK;
 }
 
-// The layer norm shares the norm's split of a row; the gradient keeps two rows of partial sums.
+// The layer norm: its own split of a row over threads; the gradient keeps two rows of partial sums.
 inline int make_ln_plan(const ss_ln_dims& d, bool backward, RmsPlan* out) {
     ss_rms_dims r{d.rows, d.dim, d.in_dtype, d.res_dtype, d.q8, d.eps};
     if (d.q8 == SS_Q4_MX && !backward) {
         if (d.dim % 32 != 0) return SS_ERR_DIMS;
         r.q8 = SS_Q8_NONE;
     }
-    const int rc = make_rms_plan(r, backward, out);
-    if (rc == SS_OK && backward)
-        out->total = align256(size_t(out->grid) * size_t(2 * out->D) * sizeof(float));
-    return rc;
+    RmsPlan p;
+    const int rc = make_rms_plan(r, backward, &p);
+    if (rc != SS_OK) return rc;
+    const int64_t pieces = (p.D + 7) / 8;
+    const bool whole = p.D % 8 == 0, many = p.M >= 1024;
+    if (pieces <= 128) {
+        p.threads = pieces <= 8 ? 8 : pieces <= 32 ? 32 : 64;
+        p.pieces = pieces <= 64 ? 1 : 2;
+    } else if (!backward && whole && many && pieces <= 64 * 6) {
+        p.threads = 64;
+        p.pieces = int((pieces + 63) / 64);
+    } else if (pieces <= 512) {
+        p.threads = pieces <= 256 ? 256 : !whole ? 512 : pieces <= 320 ? 320 : pieces <= 384 ? 384 : 512;
+        p.pieces = 1;
+    } else {
+        p.threads = pieces <= 1024 ? 512 : 1024;
+        p.pieces = pieces <= 2048 ? 2 : 4;
+    }
+    const int64_t wg_rows = p.threads >= 256 ? 1 : 256 / p.threads;
+    const int64_t need = (p.M + wg_rows - 1) / wg_rows;
+    const int64_t most = p.threads >= 512 ? 512 : backward ? 1024 : 2048;
+    p.grid = int(need < most ? need : most);
+    p.total = backward ? align256(size_t(p.grid) * size_t(2 * p.D) * sizeof(float)) : 0;
+    *out = p;
+    return SS_OK;
 }
 
 inline int check_mx4(const ss_mx4_dims& d, bool product) {
