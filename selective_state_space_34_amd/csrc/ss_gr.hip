@@ -223,13 +223,12 @@ __device__ __forceinline__ void joined(const uint64_t* tiles, int64_t D, const i
     }
 }
 
-// Sets a chain's counter and words (kNotYet) before the launch that uses them; n is even or the words
-// end in padding.
-__global__ __launch_bounds__(256) void gr_chain_kernel(ulonglong2* words, int64_t n, uint64_t* ticket) {
+// Sets the counters and words (two at a time; the last may be padding) of a call's chains.
+__global__ __launch_bounds__(256) void gr_chain_kernel(uint64_t* tickets, ulonglong2* words, int64_t n) {
     const int64_t step = int64_t(gridDim.x) * 256;
     for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += step)
         words[i] = make_ulonglong2(kNotYet, kNotYet);
-    if (blockIdx.x == 0 && threadIdx.x == 0) *ticket = 0;
+    if (blockIdx.x == 0 && threadIdx.x < 2) tickets[16 * threadIdx.x] = 0;
 }
 
 // Where a workgroup works: its tile in the chain's order, row and channels.
@@ -638,23 +637,14 @@ unsigned groups(int64_t D) { return unsigned((D + kCols - 1) / kCols); }
 
 }  // namespace
 
-namespace {
-
-// The chain's words and counter, where the row has more than one tile.
-hipError_t begin_chain(const GrLaunch& p, hipStream_t s) {
-    if (!p.ticket) return hipSuccess;
-    const int64_t n = (p.B * p.D * (p.tiles + (p.tiles + kGroup - 1) / kGroup) + 1) / 2;
-    const int64_t need = (n + 255) / 256;
+hipError_t launch_gr_chains(uint64_t* tickets, uint64_t* maps, int64_t words, hipStream_t s) {
+    const int64_t n = (words + 1) / 2, need = (n + 255) / 256;
     hipLaunchKernelGGL(gr_chain_kernel, dim3(unsigned(need < 1024 ? need : 1024)), dim3(256), 0, s,
-                       reinterpret_cast<ulonglong2*>(p.maps), n, p.ticket);
+                       tickets, reinterpret_cast<ulonglong2*>(maps), n);
     return hipGetLastError();
 }
 
-}  // namespace
-
 hipError_t launch_gr_fwd(const GrLaunch& p, hipStream_t s) {
-    const hipError_t e = begin_chain(p, s);
-    if (e != hipSuccess) return e;
     return with_type(p.in_dtype, p.vec, [&](auto t, auto v) {
         hipLaunchKernelGGL((gr_fwd_kernel<decltype(t), decltype(v)::value, kFwdWaves, kGrFwdTile / kFwdWaves>),
                            dim3(groups(p.D) * unsigned(p.B) * unsigned(p.tiles)), dim3(64 * kFwdWaves), 0, s, p);
@@ -663,9 +653,7 @@ hipError_t launch_gr_fwd(const GrLaunch& p, hipStream_t s) {
 }
 
 hipError_t launch_gr_bwd(const GrLaunch& p, hipStream_t s) {
-    hipError_t e = begin_chain(p, s);
-    if (e != hipSuccess) return e;
-    e = with_type(p.in_dtype, p.vec, [&](auto t, auto v) {
+    const hipError_t e = with_type(p.in_dtype, p.vec, [&](auto t, auto v) {
         hipLaunchKernelGGL((gr_bwd_kernel<decltype(t), decltype(v)::value, kBwdWaves, SS_GR_CKPT / kBwdWaves>),
                            dim3(groups(p.D) * unsigned(p.B) * unsigned(p.tiles)), dim3(64 * kBwdWaves), 0, s, p);
         return hipGetLastError();

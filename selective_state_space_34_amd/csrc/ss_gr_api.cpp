@@ -62,6 +62,13 @@ void chain(GrLaunch* l, const ss::GrChain& c, char* ws) {
     l->ends = reinterpret_cast<uint64_t*>(ws + c.off_ends);
 }
 
+// Sets the chains' counters and words.
+hipError_t begin(const GrPlan& p, char* ws, hipStream_t stream) {
+    if (p.words == 0) return hipSuccess;
+    return ss::launch_gr_chains(reinterpret_cast<uint64_t*>(ws),
+                                reinterpret_cast<uint64_t*>(ws + p.off_words), p.words, stream);
+}
+
 ss::LnLaunch ln_launch(const ss_ln_dims& d, const ss::RmsPlan& p) {
     ss::LnLaunch l{};
     l.M = p.M; l.D = p.D; l.eps = d.eps; l.inv_d = float(1.0 / double(p.D));
@@ -104,8 +111,11 @@ int ss_gr_fwd(const ss_gr_dims* dims, const void* x, const void* r, const void* 
     if (!aligned(workspace, 16)) return SS_ERR_ALIGN;
     GrLaunch l = launch(dims, p, x, r, i, lam, h0, lengths, reset);
     l.y = y; l.h_final = h_final; l.h_ckpt = h_ckpt;
-    chain(&l, p.fwd, static_cast<char*>(workspace));
-    const hipError_t e = ss::launch_gr_fwd(l, stream);
+    char* ws = static_cast<char*>(workspace);
+    hipError_t e = begin(p, ws, stream);
+    if (e != hipSuccess) return hip_fail(e);
+    chain(&l, p.fwd, ws);
+    e = ss::launch_gr_fwd(l, stream);
     return e == hipSuccess ? SS_OK : hip_fail(e);
 }
 
@@ -125,18 +135,20 @@ int ss_gr_bwd(const ss_gr_dims* dims, const void* x, const void* r, const void* 
     if (!aligned(workspace, 16)) return SS_ERR_ALIGN;
     char* ws = static_cast<char*>(workspace);
     GrLaunch l = launch(dims, p, x, r, i, lam, h0, lengths, reset);
+    hipError_t e = begin(p, ws, stream);
+    if (e != hipSuccess) return hip_fail(e);
     if (h_ckpt) {
         l.h_ckpt = const_cast<float*>(h_ckpt);   // read only
     } else {
         l.h_ckpt = reinterpret_cast<float*>(ws + p.off_ckpt);
         chain(&l, p.fwd, ws);
-        const hipError_t e = ss::launch_gr_fwd(l, stream);
+        e = ss::launch_gr_fwd(l, stream);
         if (e != hipSuccess) return hip_fail(e);
     }
     l.dy = dy; l.dh_final = dh_final; l.dx = dx; l.dr = dr; l.di = di; l.dlam = dlam; l.dh0 = dh0;
     l.part = reinterpret_cast<float*>(ws + p.off_part);
     chain(&l, p.rev, ws);
-    const hipError_t e = ss::launch_gr_bwd(l, stream);
+    e = ss::launch_gr_bwd(l, stream);
     return e == hipSuccess ? SS_OK : hip_fail(e);
 }
 

@@ -11,15 +11,20 @@ constexpr int64_t kGrMaxStep = int64_t(1) << 25;   // elements from token to tok
 constexpr int kGrFwdTile = 128;                    // tokens of a workgroup, forward
 constexpr int kGrGroup = 32;                       // tiles of a group
 
-// What links the tiles of a row: a counter, the tiles' maps and the groups' ends.
+// What links the tiles of a row: the tiles' maps and, right behind them, the groups' ends (words of
+// 8 bytes), and a counter (tiles > 1).
 struct GrChain {
     int64_t tiles, groups;
-    size_t off_ticket, off_maps, off_ends;   // tiles > 1
+    size_t off_ticket, off_maps, off_ends;
 };
 
+// The chains' counters come first (256 bytes), then the words of the forward's, then those of the
+// gradient's: one launch sets them all.  words: how many.
 struct GrPlan {
     int64_t B, T, D;
     GrChain fwd, rev;
+    size_t off_words;
+    int64_t words;
     // backward: off_ckpt [B, rev.tiles, D] where none are given, off_part [B, rev.tiles, D]
     size_t off_ckpt, off_part, total;
 };
@@ -28,14 +33,14 @@ inline bool gr_strides_ok(const int64_t* s) {
     return s[0] >= 0 && s[0] <= (int64_t(1) << 40) && s[1] >= 0 && s[1] <= kGrMaxStep;
 }
 
-inline size_t gr_chain(const GrPlan& p, int64_t tokens, size_t off, GrChain* c) {
-    c->tiles = (p.T + tokens - 1) / tokens;
+inline void gr_chain(GrPlan* p, int64_t tokens, size_t ticket, GrChain* c) {
+    c->tiles = (p->T + tokens - 1) / tokens;
     c->groups = (c->tiles + kGrGroup - 1) / kGrGroup;
-    c->off_ticket = off;
-    if (c->tiles <= 1) return off;
-    c->off_maps = off + 256;
-    c->off_ends = c->off_maps + size_t(p.B * c->tiles) * size_t(p.D) * sizeof(uint64_t);
-    return align256(c->off_ends + size_t(p.B * c->groups) * size_t(p.D) * sizeof(uint64_t));
+    if (c->tiles <= 1) return;
+    c->off_ticket = ticket;
+    c->off_maps = p->off_words + size_t(p->words) * sizeof(uint64_t);
+    c->off_ends = c->off_maps + size_t(p->B * c->tiles) * size_t(p->D) * sizeof(uint64_t);
+    p->words += p->B * (c->tiles + c->groups) * p->D;
 }
 
 inline int make_gr_plan(const ss_gr_dims& d, bool backward, bool given_ckpt, GrPlan* out) {
@@ -49,15 +54,15 @@ inline int make_gr_plan(const ss_gr_dims& d, bool backward, bool given_ckpt, GrP
     if (d.batch > kMaxGridYZ) return SS_ERR_DIMS;
     GrPlan p{};
     p.B = d.batch; p.T = d.seqlen; p.D = d.dim;
-    size_t off = 0;
-    if (!backward || !given_ckpt) off = gr_chain(p, kGrFwdTile, off, &p.fwd);
+    p.off_words = 256;
+    if (!backward || !given_ckpt) gr_chain(&p, kGrFwdTile, 0, &p.fwd);
+    if (backward) gr_chain(&p, SS_GR_CKPT, 128, &p.rev);
     const int64_t cols = (p.D + 127) / 128 * p.B;
-    if (!mul_ok(cols, p.fwd.tiles + 1, lim) || !launch_ok(cols * p.fwd.tiles, 512)) return SS_ERR_DIMS;
+    if (!mul_ok(cols, p.fwd.tiles + p.rev.tiles, lim) || !launch_ok(cols * p.fwd.tiles, 512) ||
+        !launch_ok(cols * p.rev.tiles, 512))
+        return SS_ERR_DIMS;
+    size_t off = p.words ? align256(p.off_words + size_t(p.words) * sizeof(uint64_t)) : 0;
     if (backward) {
-        // (the states are formed before the gradients' chain begins: both take the same memory)
-        const size_t end = gr_chain(p, SS_GR_CKPT, 0, &p.rev);
-        off = off > end ? off : end;
-        if (!launch_ok(cols * p.rev.tiles, 512)) return SS_ERR_DIMS;
         const size_t row = size_t(p.B * p.rev.tiles) * size_t(p.D) * sizeof(float);
         p.off_ckpt = off;
         if (!given_ckpt) off = align256(off + row);

@@ -331,6 +331,9 @@ struct GrLaunch {
     void *dx, *dr, *di;
     float *dh0, *part, *dlam;  // nullable; [parts, D]; [D]
 };
+// Before them: `words` words from maps on say that nothing is there yet, and the two counters (at
+// `tickets` and 128 bytes behind) begin at 0.
+hipError_t launch_gr_chains(uint64_t* tickets, uint64_t* maps, int64_t words, hipStream_t s);
 hipError_t launch_gr_fwd(const GrLaunch& p, hipStream_t s);
 hipError_t launch_gr_bwd(const GrLaunch& p, hipStream_t s);
 

@@ -468,9 +468,13 @@ template <int kX>
 hipError_t launch_mm(const Mx4Launch& p, hipStream_t s) {
     if (p.M <= 16) return launch_rows<1, kX>(p, s);
     if (p.M <= 32) return launch_rows<2, kX>(p, s);
+    // Tiles take a time of their own for a walk over K however few they are, rows a time for every 64
+    // of them and every 16 of the weights.  us with rows and with tiles, x in 4 bits: 2560 x 2560, 64 rows
+    // 9 and 12, 128 11 and 12, 256 16 and 13; 10240 x 2560, 64 rows 16 and 13; 2560 x 5120, 64 rows
+    // 14 and 20, 128 25 and 21; 5120 x 5120, 64 rows 25 and 22.
+    // (256 rows of y stay within a descriptor)
     if constexpr (kX != kX8Wide) {
-        // (256 rows of y stay within a descriptor)
-        if (p.M > 128 && p.N < (1 << 20)) return launch_tiles<kX, kX == kX4 ? 4 : 2>(p, s);
+        if (p.N * ((p.M + 63) / 64) >= 5120 && p.N < (1 << 20)) return launch_tiles<kX, kX == kX4 ? 4 : 2>(p, s);
     }
     return launch_rows<4, kX>(p, s);
 }
