@@ -171,8 +171,8 @@ __device__ __forceinline__ Map after(const Map& second, const Map& first) {
 // ---- states from tile to tile ----------------------------------------------------------------
 //
 // A workgroup reads its tile once, keeps it in registers, and needs the state that enters it.  It
-// publishes the map of its own tile, then takes those of the tiles before it in its group of
-// kGroup, and what the group before ended with, which that group's last tile publishes.  Maps are
+// publishes the map of its own tile, then takes those of the tiles before it in its group (of
+// kGroup), and what the group before ended with, which that group's last tile publishes.  Maps are
 // joined in the order of the tiles, whoever came first, so results do not depend on timing.
 //
 // A word of 64 bits holds a channel's map (or state, with A = 1) and is stored and loaded in one
@@ -181,7 +181,6 @@ __device__ __forceinline__ Map after(const Map& second, const Map& first) {
 // ends: workgroups take their tiles from a counter in the order in which they start to run, and
 // wait for tiles of lower numbers only, whose workgroups run already and publish their maps before
 // they wait themselves.
-constexpr int kGroup = kGrGroup;
 constexpr uint64_t kNotYet = ~uint64_t(0);
 
 __device__ __forceinline__ uint64_t word_of(const Map& m) {
@@ -267,7 +266,7 @@ template <bool kVec> __device__ __forceinline__ int spot(int lane, int j) {
 // the first) from `first`, the state that enters the row (nullable: 0), and stores what leaves the
 // row in `last` (nullable).  Two waves hold a channel a lane and walk over the waves' maps; the
 // others meanwhile fetch the maps of the tiles before.  All maps are in place (a barrier) before.
-template <bool kVec, bool kReverse, int kWaves, typename Sh>
+template <bool kVec, bool kReverse, int kGroup, int kWaves, typename Sh>
 __device__ __forceinline__ void link(const GrLaunch& p, const Place& at, const Cols& col, int lane,
                                      int wave, Sh& sh, const float (&maps_h)[kWaves][kCols],
                                      const float* first, float* last) {
@@ -409,7 +408,7 @@ __global__ __launch_bounds__(64 * kWaves) void gr_fwd_kernel(const GrLaunch p) {
         sh.H[wave][spot<kVec>(lane, j)] = own[j].H;
     }
     __syncthreads();
-    link<kVec, false, kWaves>(p, at, col, lane, wave, sh, sh.H, p.h0, p.h_final);
+    link<kVec, false, kGrFwdGroup, kWaves>(p, at, col, lane, wave, sh, sh.H, p.h0, p.h_final);
 #pragma unroll
     for (int j = 0; j < 2; ++j) h[j] = sh.in[wave][spot<kVec>(lane, j)];
     if (p.h_ckpt && t0 % SS_GR_CKPT == 0 && t0 < p.T) {
@@ -512,7 +511,7 @@ __global__ __launch_bounds__(64 * kWaves) void gr_bwd_kernel(const GrLaunch p) {
             h[j] = through(sh.A[w][l], sh.H[w][l], h[j]);
         }
     }
-    link<kVec, true, kWaves>(p, at, col, lane, wave, sh, G, p.dh_final, p.dh0);
+    link<kVec, true, kGrBwdGroup, kWaves>(p, at, col, lane, wave, sh, G, p.dh_final, p.dh0);
 #pragma unroll
     for (int j = 0; j < 2; ++j) c[j] = sh.in[wave][spot<kVec>(lane, j)];
     // From here on x, dy, σ(r) and their products are formed once more from the packed values: kept

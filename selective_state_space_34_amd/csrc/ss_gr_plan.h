@@ -9,7 +9,10 @@ namespace ss {
 constexpr int64_t kGrMaxStep = int64_t(1) << 25;   // elements from token to token: 16 tokens' rows
                                                    // stay within a descriptor's 2^31 bytes
 constexpr int kGrFwdTile = 128;                    // tokens of a workgroup, forward
-constexpr int kGrGroup = 32;                       // tiles of a group
+// Tiles of a group.  us with 16, 24, 32 and 48: forward 8 x 2048 x 5120 (16 tiles a row) 153, 152, 147, 147,
+// 1 x 262144 x 256 160, 148, 149, 154; a training step of 4 x 4096 x 2048 with the same in both
+// directions 202, 204, 210, 214.
+constexpr int kGrFwdGroup = 32, kGrBwdGroup = 16;
 
 // What links the tiles of a row: the tiles' maps and, right behind them, the groups' ends (words of
 // 8 bytes), and a counter (tiles > 1).
@@ -33,9 +36,9 @@ inline bool gr_strides_ok(const int64_t* s) {
     return s[0] >= 0 && s[0] <= (int64_t(1) << 40) && s[1] >= 0 && s[1] <= kGrMaxStep;
 }
 
-inline void gr_chain(GrPlan* p, int64_t tokens, size_t ticket, GrChain* c) {
+inline void gr_chain(GrPlan* p, int64_t tokens, int64_t group, size_t ticket, GrChain* c) {
     c->tiles = (p->T + tokens - 1) / tokens;
-    c->groups = (c->tiles + kGrGroup - 1) / kGrGroup;
+    c->groups = (c->tiles + group - 1) / group;
     if (c->tiles <= 1) return;
     c->off_ticket = ticket;
     c->off_maps = p->off_words + size_t(p->words) * sizeof(uint64_t);
@@ -55,8 +58,8 @@ inline int make_gr_plan(const ss_gr_dims& d, bool backward, bool given_ckpt, GrP
     GrPlan p{};
     p.B = d.batch; p.T = d.seqlen; p.D = d.dim;
     p.off_words = 256;
-    if (!backward || !given_ckpt) gr_chain(&p, kGrFwdTile, 0, &p.fwd);
-    if (backward) gr_chain(&p, SS_GR_CKPT, 128, &p.rev);
+    if (!backward || !given_ckpt) gr_chain(&p, kGrFwdTile, kGrFwdGroup, 0, &p.fwd);
+    if (backward) gr_chain(&p, SS_GR_CKPT, kGrBwdGroup, 128, &p.rev);
     const int64_t cols = (p.D + 127) / 128 * p.B;
     if (!mul_ok(cols, p.fwd.tiles + p.rev.tiles, lim) || !launch_ok(cols * p.fwd.tiles, 512) ||
         !launch_ok(cols * p.rev.tiles, 512))
