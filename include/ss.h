@@ -384,7 +384,8 @@ int ss_q4_mv(const ss_q4_dims* dims, const void* x, const float* x_scale, const 
  *   x, r, i : [B, T, D] (in_dtype), the input and the two gates before their sigmoids.  They may
  *          be strided: dims.*_stride are elements from batch row to batch row and token to token
  *          (the last axis is contiguous); both 0 means dense.  A token stride of less than D (an
- *          expanded or overlapping operand) is taken too; the most is 2^25.  They need only their type's alignment.
+ *          expanded or overlapping operand) is taken too; the most is 2^25.  With one token its stride is
+ *          not used.  They need only their type's alignment.
  *   y, and the gradients of x, r, i : [B, T, D] dense, in_dtype, each rounded once.
  *   lam, dlam [D], h0, h_final, dh_final, dh0 [B, D], h_ckpt [B, ceil(T / SS_GR_CKPT), D] : float32.
  *   lengths : NULL, or [B] int32 on the device: row b has lengths[b] tokens (clamped to [0, T]).
@@ -430,7 +431,7 @@ int ss_gr_bwd(const ss_gr_dims* dims, const void* x, const void* r, const void* 
               const float* dh_final, const float* h_ckpt, void* dx, void* dr, void* di, float* dlam,
               float* dh0, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
-/* One token: x, r, i, y [B, D]; dims.seqlen must be 1 (token strides are not used).  h_in [B, D] is
+/* One token: x, r, i, y [B, D]; dims.seqlen must be 1.  h_in [B, D] is
  * the state before the token, h_out the state after it; h_out may equal h_in (updated in place),
  * otherwise they must not overlap.  Needs no workspace. */
 int ss_gr_step(const ss_gr_dims* dims, const void* x, const void* r, const void* i, const float* lam,
@@ -486,7 +487,8 @@ int ss_mx4_quant(const ss_mx4_dims* dims, const void* x, void* codes, void* exps
  *   w: codes wq [n, k / 2] and exponents w_exps [n, k / 32]
  *   x: codes [rows, k / 2] with x_scale its exponents [rows, k / 32] bytes, or e4m3 [rows, k] with
  *      x_scale [rows] float32, as the norms give them.
- * Needs no workspace. */
+ * For any number of rows: up to 32 (64 or more where the weights are few) are kept together over the
+ * whole of w, more go in tiles.  rows · n / 2^15 (x in e4m3: 2^14) < 2^24.  Needs no workspace. */
 int ss_mx4_mm(const ss_mx4_dims* dims, const void* x, const void* x_scale, const void* wq,
               const void* w_exps, void* y, hipStream_t stream);
 

@@ -18,7 +18,7 @@ using ss::hip_fail;
 bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 GrRows rows(const void* p, const int64_t* stride, int64_t T, int64_t D) {
-    if (stride[0] || stride[1]) return GrRows{p, stride[0], stride[1]};
+    if (stride[0] || stride[1]) return GrRows{p, stride[0], T == 1 ? D : stride[1]};
     return GrRows{p, T * D, D};
 }
 
@@ -165,7 +165,6 @@ int ss_gr_step(const ss_gr_dims* dims, const void* x, const void* r, const void*
     s.x = rows(x, dims->x_stride, 1, p.D);
     s.r = rows(r, dims->r_stride, 1, p.D);
     s.i = rows(i, dims->i_stride, 1, p.D);
-    s.x.st = s.r.st = s.i.st = 0;
     s.lam = lam; s.h_in = h_in; s.h_out = h_out; s.y = y;
     s.B = p.B; s.D = p.D; s.c = dims->c; s.in_dtype = dims->in_dtype;
     s.vec = pairs(dims, s.x, s.r, s.i);

@@ -32,8 +32,10 @@ struct GrPlan {
     size_t off_ckpt, off_part, total;
 };
 
-inline bool gr_strides_ok(const int64_t* s) {
-    return s[0] >= 0 && s[0] <= (int64_t(1) << 40) && s[1] >= 0 && s[1] <= kGrMaxStep;
+// (with one token its stride says nothing)
+inline bool gr_strides_ok(const int64_t* s, int64_t T) {
+    const int64_t lim = int64_t(1) << 40;
+    return s[0] >= 0 && s[0] <= lim && s[1] >= 0 && s[1] <= (T == 1 ? lim : kGrMaxStep);
 }
 
 inline void gr_chain(GrPlan* p, int64_t tokens, int64_t group, size_t ticket, GrChain* c) {
@@ -50,7 +52,8 @@ inline int make_gr_plan(const ss_gr_dims& d, bool backward, bool given_ckpt, GrP
     if (d.batch <= 0 || d.seqlen <= 0 || d.dim <= 0 || d.dim > (int64_t(1) << 24)) return SS_ERR_DIMS;
     if (d.in_dtype != SS_F32 && d.in_dtype != SS_BF16) return SS_ERR_DTYPE;
     if (!(d.c > 0.0f) || !(d.c - d.c == 0.0f)) return SS_ERR_DIMS;
-    if (!gr_strides_ok(d.x_stride) || !gr_strides_ok(d.r_stride) || !gr_strides_ok(d.i_stride))
+    if (!gr_strides_ok(d.x_stride, d.seqlen) || !gr_strides_ok(d.r_stride, d.seqlen) ||
+        !gr_strides_ok(d.i_stride, d.seqlen))
         return SS_ERR_DIMS;
     const int64_t lim = int64_t(1) << 40;   // elements of any tensor
     if (!mul_ok(d.batch, d.seqlen, lim) || !mul_ok(d.batch * d.seqlen, d.dim, lim)) return SS_ERR_DIMS;
@@ -111,6 +114,16 @@ inline int make_ln_plan(const ss_ln_dims& d, bool backward, RmsPlan* out) {
     return SS_OK;
 }
 
+// Products of microscaled weights: whether 256 (x in 4 bits) or 128 by 128 rows go to a workgroup, or 16 rows
+// of weights by up to 64 of x.  Tiles take a time of their own for a walk over K however few they
+// are, rows a time for every 64 of them and every 16 of the weights.  us with rows and with tiles, x in
+// 4 bits: 2560 x 2560, 64 rows 9 and 12, 128 11 and 12, 256 16 and 13; 10240 x 2560, 64 rows 16 and 13;
+// 2560 x 5120, 64 rows 14 and 20, 128 25 and 21; 5120 x 5120, 64 rows 25 and 22.
+// (A tile's rows of y stay within a descriptor's 2^31 bytes.)
+inline bool mx4_tiled(int64_t rows, int64_t n) {
+    return rows > 32 && n * ((rows + 63) / 64) >= 5120 && n < (int64_t(1) << 20);
+}
+
 inline int check_mx4(const ss_mx4_dims& d, bool product) {
     if (d.rows <= 0 || d.k <= 0 || d.k % 32 != 0 || (product && d.n <= 0)) return SS_ERR_DIMS;
     const int64_t lim = int64_t(1) << 38;
@@ -120,8 +133,13 @@ inline int check_mx4(const ss_mx4_dims& d, bool product) {
     if (d.k >= (int64_t(1) << 23)) return SS_ERR_DIMS;   // 256 rows stay within a descriptor
     if (d.x_q8 != SS_Q4_MX && d.x_q8 != SS_Q8_FP8) return SS_ERR_DTYPE;
     if (d.y_dtype != SS_F32 && d.y_dtype != SS_BF16) return SS_ERR_DTYPE;
-    if ((d.rows + 63) / 64 > kMaxGridYZ || !launch_ok((d.n + 15) / 16 * ((d.rows + 63) / 64), 512))
+    if (mx4_tiled(d.rows, d.n)) {
+        const int64_t m = d.x_q8 == SS_Q4_MX ? 256 : 128;
+        if (!launch_ok((d.n + 127) / 128 * ((d.rows + m - 1) / m) + 7, 256)) return SS_ERR_DIMS;
+    } else if ((d.rows + 63) / 64 > kMaxGridYZ ||
+               !launch_ok((d.n + 15) / 16 * ((d.rows + 63) / 64), 512)) {
         return SS_ERR_DIMS;
+    }
     return SS_OK;
 }
 

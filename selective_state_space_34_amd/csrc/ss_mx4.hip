@@ -7,6 +7,7 @@
 // 32 codes of a block (16 bytes) and the block's exponent from a lane, lane l row l % 16 and block
 // l / 16 of the 128 columns; of e4m3 two runs of 16, at 16·(l / 16) and at 64 more.
 #include "ss_device.h"
+#include "ss_gr_plan.h"
 #include "ss_kernels.h"
 
 namespace ss {
@@ -377,8 +378,10 @@ __global__ __launch_bounds__(256, 2) void mx4_tile_kernel(const Mx4Launch p, int
                 for (int c = 0; c < 4; ++c) b[o][c] = int(v[c]);
                 sb[o] = e[4 * (L::kRowsN + rm + 32 * t) + 2 * h + g];
             } else {
-                const u32x4 v = sh.x[from][at_x + 256 * t + ((4 * h + g) ^ tx)];
-                const u32x4 w = sh.x[from][at_x + 256 * t + ((4 * h + 2 + g) ^ tx)];
+                // kX8: as the instruction takes them; kX8Wide: the 32 columns of one block
+                constexpr bool kBlock = kX == kX8Wide;
+                const u32x4 v = sh.x[from][at_x + 256 * t + ((4 * h + (kBlock ? 2 * g : g)) ^ tx)];
+                const u32x4 w = sh.x[from][at_x + 256 * t + ((4 * h + (kBlock ? 2 * g + 1 : 2 + g)) ^ tx)];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     b[o][c] = int(v[c]);
@@ -403,10 +406,21 @@ __global__ __launch_bounds__(256, 2) void mx4_tile_kernel(const Mx4Launch p, int
                     fetch(s + 3, i, two);
                 }
             }
+            if constexpr (kX == kX8Wide) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-                acc[u][t] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                    a[h][u], b[o], acc[u][t], 4, kX == kX4 ? 4 : 0, 0, sa[h][u], 0, sb[o]);
+                for (int q = 0; q < 4; ++q) {
+                    const bf16x8 v = widen8(uint32_t(b[o][2 * q]), uint32_t(b[o][2 * q + 1]));
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                        acc[u][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                            widen4(uint32_t(a[h][u][q]), sa[h][u]), v, acc[u][t], 0, 0, 0);
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    acc[u][t] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                        a[h][u], b[o], acc[u][t], 4, kX == kX4 ? 4 : 0, 0, sa[h][u], 0, sb[o]);
+            }
             __builtin_amdgcn_sched_barrier(0);
         }
         // (pinned: the compiler would move products behind branches that follow)
@@ -468,14 +482,7 @@ template <int kX>
 hipError_t launch_mm(const Mx4Launch& p, hipStream_t s) {
     if (p.M <= 16) return launch_rows<1, kX>(p, s);
     if (p.M <= 32) return launch_rows<2, kX>(p, s);
-    // Tiles take a time of their own for a walk over K however few they are, rows a time for every 64
-    // of them and every 16 of the weights.  us with rows and with tiles, x in 4 bits: 2560 x 2560, 64 rows
-    // 9 and 12, 128 11 and 12, 256 16 and 13; 10240 x 2560, 64 rows 16 and 13; 2560 x 5120, 64 rows
-    // 14 and 20, 128 25 and 21; 5120 x 5120, 64 rows 25 and 22.
-    // (256 rows of y stay within a descriptor)
-    if constexpr (kX != kX8Wide) {
-        if (p.N * ((p.M + 63) / 64) >= 5120 && p.N < (1 << 20)) return launch_tiles<kX, kX == kX4 ? 4 : 2>(p, s);
-    }
+    if (mx4_tiled(p.M, p.N)) return launch_tiles<kX, kX == kX4 ? 4 : 2>(p, s);
     return launch_rows<4, kX>(p, s);
 }
 

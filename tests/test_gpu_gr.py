@@ -405,3 +405,24 @@ def test_refusals(gpu):
     with pytest.raises(gpu.SSError) as e:
         gpu.ss_gr_bwd(x, r, i, lam, p["dy"], workspace=small)
     assert e.value.code == -5
+
+
+def test_far_strides(gpu):
+    """Single tokens out of long texts: with one token its stride says nothing, however far the rows are
+    apart (here 2^26 elements)."""
+    import torch
+    B, D, far = 2, 130, 1 << 26
+    flat = torch.randn((B - 1) * far + 3 * D, device="cuda", dtype=torch.bfloat16)
+    x, r, i = (flat.as_strided((B, D), (far, 1), o) for o in (0, D, 2 * D))
+    lam = make(1, 1, 1, D, "f32")["lam"]
+    h, h2 = torch.ones(B, D, device="cuda"), torch.ones(B, D, device="cuda")
+    y = gpu.ss_gr_step(x, r, i, lam, h)
+    dense = [t.contiguous() for t in (x, r, i)]
+    assert torch.equal(y, gpu.ss_gr_step(*dense, lam, h2)) and torch.equal(h, h2)
+    one = [t[:, None] for t in (x, r, i)]
+    y3 = gpu.ss_gr_fwd(*one, lam, torch.ones(B, D, device="cuda"))
+    assert torch.equal(y3, gpu.ss_gr_fwd(*[t[:, None] for t in dense], lam, torch.ones(B, D, device="cuda")))
+    with pytest.raises(gpu.SSError) as e:      # two tokens that far apart are refused
+        t = flat.as_strided((1, 2, D), (1, far, 1))
+        gpu.ss_gr_fwd(t, t, t, lam)
+    assert e.value.code == -2

@@ -74,7 +74,11 @@ def test_rounding_over_the_range(gpu):
 
 SHAPES = [(1, 1, 32), (1, 16, 64), (1, 40, 128), (2, 17, 96), (16, 48, 544), (17, 33, 160), (31, 256, 1024),
           (33, 100, 288), (64, 64, 2560), (65, 130, 96), (100, 1, 2048), (128, 128, 128), (129, 257, 416),
-          (200, 300, 1056), (255, 250, 64), (256, 256, 256), (300, 520, 32), (513, 129, 672), (1000, 384, 512)]
+          (200, 300, 1056), (255, 250, 64), (256, 256, 256), (300, 520, 32), (513, 129, 672), (1000, 384, 512),
+          # in tiles: N · ceil(M / 64) of 5120 and more
+          (33, 5121, 96), (40, 5250, 640), (65, 2600, 160), (100, 2688, 1024), (129, 1801, 416), (257, 1100, 544),
+          (300, 1030, 1056), (511, 640, 32), (512, 1024, 128), (700, 500, 672), (1025, 385, 288),
+          (2050, 160, 384), (5200, 64, 64), (5121, 65, 256), (700, 513, 2560)]
 
 
 @pytest.mark.parametrize("x", ["mx4", "fp8"])
@@ -111,7 +115,7 @@ def test_products(gpu, shape, x):
     assert y.dtype == torch.float32 and (np.abs(num(y) - want) <= tol).all()
 
 
-@pytest.mark.parametrize("M", [1, 40, 300])
+@pytest.mark.parametrize("M", [1, 40, 300, 1400])
 def test_every_code_and_exponent(gpu, M):
     """One code of weights against one of x, over all codes and exponents: exact, NaN at 255."""
     import torch
@@ -141,7 +145,7 @@ def test_rows_stay_apart(gpu):
     """NaN in a row of x (a block's exponent, a code, a scale) or of the weights stays in its row or
     column."""
     import torch
-    for M, N, K in ((20, 40, 256), (300, 200, 320)):
+    for M, N, K in ((20, 40, 256), (300, 200, 320), (1700, 200, 320), (2000, 192, 256)):
         wq, we = weights(3, N, K)
         xq, xe = weights(4, M, K)
         y = gpu.ss_mx4_mm(cuda(xq), cuda(xe), cuda(wq), cuda(we))
