@@ -973,12 +973,18 @@ def _gr_key(x, r, i, lam, c, step):
     if x.dim() != nd or x.numel() == 0:
         raise ValueError(f"x must be {nd}-D and hold something, got shape {tuple(x.shape)}")
     dev, dt, shape = x.device, x.dtype, x.shape
-    D = shape[-1]
-    B, T = (shape[0], 1) if step else shape[:2]
-    key = (B, T, D, _in_dtype(x, "x"), float(c), _gr_rows(x, "x", shape, dt, dev),
-           _gr_rows(r, "r", shape, dt, dev), _gr_rows(i, "i", shape, dt, dev))
+    B, T, D = (shape[0], 1, shape[1]) if step else shape
     _check(lam, "lam", (D,), torch.float32, dev)
-    return key, (B, T, D)
+    sx = x.stride()
+    try:  # operands laid out alike pass with the fewest steps, as in _check
+        if (sx[-1] == 1 and sx[0] and sx[-2] and r.stride() == sx and i.stride() == sx and r.shape == shape
+                and i.shape == shape and r.dtype is dt and i.dtype is dt and r.device == dev and i.device == dev):
+            sx = sx[:2] if nd == 3 else (sx[0], sx[0])
+            return (B, T, D, _in_dtype(x, "x"), float(c), sx, sx, sx), (B, T, D)
+    except AttributeError:
+        pass
+    return (B, T, D, _in_dtype(x, "x"), float(c), _gr_rows(x, "x", shape, dt, dev),
+            _gr_rows(r, "r", shape, dt, dev), _gr_rows(i, "i", shape, dt, dev)), (B, T, D)
 
 
 def _gr_marks(lengths, reset, B, T, device):
@@ -1008,16 +1014,16 @@ def ss_gr_fwd(x, r, i, lam, h0=None, *, c=8.0, lengths=None, reset=None, return_
     _gr_marks(lengths, reset, B, T, dev)
     with _on(dev, stream, (x, r, i, lam, h0, lengths, reset, y, h_final, h_ckpt, workspace)):
         if y is None:
-            y = torch.empty((B, T, D), dtype=x.dtype, device=dev)
+            y = x.new_empty((B, T, D))
         else:
             _check(y, "y", (B, T, D), x.dtype, dev)
         if return_final and h_final is None:
-            h_final = torch.empty((B, D), dtype=f32, device=dev)
+            h_final = lam.new_empty((B, D))
         else:
             _check(h_final, "h_final", (B, D), f32, dev)
         nc = -(-T // SS_GR_CKPT)
         if return_ckpt and h_ckpt is None:
-            h_ckpt = torch.empty((B, nc, D), dtype=f32, device=dev)
+            h_ckpt = lam.new_empty((B, nc, D))
         else:
             _check(h_ckpt, "h_ckpt", (B, nc, D), f32, dev)
         if workspace is None and need > 0:
@@ -1051,14 +1057,13 @@ def ss_gr_bwd(x, r, i, lam, dy, h0=None, dh_final=None, *, c=8.0, lengths=None, 
     g = {} if out is None else dict(out)
     with _on(dev, stream, (x, r, i, lam, dy, h0, dh_final, lengths, reset, h_ckpt, workspace,
                            *g.values())):
-        for name, shape, t in (("dx", (B, T, D), dt), ("dr", (B, T, D), dt), ("di", (B, T, D), dt),
-                               ("dlam", (D,), f32), ("dh0", None if h0 is None else (B, D), f32)):
-            if shape is None:
+        for name, like in (("dx", dy), ("dr", dy), ("di", dy), ("dlam", lam), ("dh0", h0)):
+            if like is None:
                 g[name] = None
             elif g.get(name) is None:
-                g[name] = torch.empty(shape, dtype=t, device=dev)
+                g[name] = torch.empty_like(like)
             else:
-                _check(g[name], name, shape, t, dev)
+                _check(g[name], name, like.shape, like.dtype, dev)
         if workspace is None:
             workspace = _bytes(need, dev)
         wbytes = workspace.numel() * workspace.element_size()
@@ -1090,7 +1095,7 @@ def ss_gr_step(x, r, i, lam, h, *, c=8.0, h_out=None, y=None, stream=None):
         else:
             _check(h_out, "h_out", (B, D), torch.float32, dev)
         if y is None:
-            y = torch.empty((B, D), dtype=x.dtype, device=dev)
+            y = torch.empty_like(h, dtype=x.dtype)
         else:
             _check(y, "y", (B, D), x.dtype, dev)
         rc = lib.ss_gr_step(dims, _addr(x), _addr(r), _addr(i), _addr(lam), _addr(h), _addr(h_out),
@@ -1130,9 +1135,10 @@ def ss_ln_fwd(x, w, b=None, res=None, *, eps=1e-5, q8=SS_Q8_NONE, y=None, y_scal
     import torch
     lib = load()
     M, D = _rows_of(x, "x")
-    dev, shape, f32, u8 = x.device, tuple(x.shape), torch.float32, torch.uint8
+    dev, shape, f32, u8 = x.device, x.shape, torch.float32, torch.uint8
     dt = _in_dtype(x, "x")
-    _check(x, "x", shape, x.dtype, dev)
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
     _check(w, "w", (D,), f32, dev)
     _check(b, "b", (D,), f32, dev)
     rdt = x.dtype if res is None else res.dtype
@@ -1144,20 +1150,20 @@ def ss_ln_fwd(x, w, b=None, res=None, *, eps=1e-5, q8=SS_Q8_NONE, y=None, y_scal
                 raise ValueError(f"blocks of 32 need a width that is a multiple of 32, got {D}")
             ys, yt, ss, st = (*shape[:-1], D // 2), u8, (*shape[:-1], D // 32), u8
         else:
-            yt = {SS_Q8_FP8: torch.float8_e4m3fn, SS_Q8_INT8: torch.int8}.get(q8, x.dtype)
+            yt = (x.dtype if q8 == SS_Q8_NONE else torch.float8_e4m3fn if q8 == SS_Q8_FP8 else torch.int8)
             ys, ss, st = shape, shape[:-1], f32
         if y is None:
-            y = torch.empty(ys, dtype=yt, device=dev)
+            y = x.new_empty(ys, dtype=yt) if q8 == SS_Q4_MX else torch.empty_like(x, dtype=yt)
         else:
             _check(y, "y", ys, yt, dev)
         if q8 != SS_Q8_NONE:
             if y_scale is None:
-                y_scale = torch.empty(ss, dtype=st, device=dev)
+                y_scale = x.new_empty(ss, dtype=st)
             else:
                 _check(y_scale, "y_scale", ss, st, dev)
         if res is not None:
             if r is None:
-                r = torch.empty(shape, dtype=rdt, device=dev)
+                r = torch.empty_like(res)
             else:
                 _check(r, "r", shape, rdt, dev)
         rc = lib.ss_ln_fwd(dims, _addr(x), _addr(res), _addr(w), _addr(b), _addr(r), _addr(y),
@@ -1177,8 +1183,9 @@ def ss_ln_bwd(dy, r, w, dr=None, *, eps=1e-5, bias=True, dx=None, dw=None, db=No
     import torch
     lib = load()
     M, D = _rows_of(r, "r")
-    dev, shape, f32 = r.device, tuple(r.shape), torch.float32
-    _check(r, "r", shape, r.dtype, dev)
+    dev, shape, f32 = r.device, r.shape, torch.float32
+    if not r.is_contiguous():
+        raise ValueError("r must be contiguous")
     _check(dy, "dy", shape, dy.dtype, dev)
     _check(w, "w", (D,), f32, dev)
     _check(dr, "dr", shape, r.dtype, dev)
@@ -1187,15 +1194,15 @@ def ss_ln_bwd(dy, r, w, dr=None, *, eps=1e-5, bias=True, dx=None, dw=None, db=No
         raise ValueError("db goes with bias=True")
     with _on(dev, stream, (dy, r, w, dr, dx, dw, db, workspace)):
         if dx is None:
-            dx = torch.empty(shape, dtype=r.dtype, device=dev)
+            dx = torch.empty_like(r)
         else:
             _check(dx, "dx", shape, r.dtype, dev)
         if dw is None:
-            dw = torch.empty((D,), dtype=f32, device=dev)
+            dw = torch.empty_like(w)
         else:
             _check(dw, "dw", (D,), f32, dev)
         if db is None and bias:
-            db = torch.empty((D,), dtype=f32, device=dev)
+            db = torch.empty_like(w)
         else:
             _check(db, "db", (D,), f32, dev)
         if workspace is None:
@@ -1226,19 +1233,20 @@ def ss_mx4_quant(x, *, codes=None, exps=None, stream=None):
     import torch
     lib = load()
     M, K = _rows_of(x, "x")
-    dev, lead, u8 = x.device, tuple(x.shape[:-1]), torch.uint8
+    dev, lead, u8 = x.device, x.shape[:-1], torch.uint8
     dt = _in_dtype(x, "x")
     if K % 32 != 0:
         raise ValueError(f"blocks of 32 need a width that is a multiple of 32, got {K}")
-    _check(x, "x", (*lead, K), x.dtype, dev)
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
     dims = _mx4_plan((M, 1, K, dt))
     with _on(dev, stream, (x, codes, exps)):
         if codes is None:
-            codes = torch.empty((*lead, K // 2), dtype=u8, device=dev)
+            codes = x.new_empty((*lead, K // 2), dtype=u8)
         else:
             _check(codes, "codes", (*lead, K // 2), u8, dev)
         if exps is None:
-            exps = torch.empty((*lead, K // 32), dtype=u8, device=dev)
+            exps = x.new_empty((*lead, K // 32), dtype=u8)
         else:
             _check(exps, "exps", (*lead, K // 32), u8, dev)
         rc = lib.ss_mx4_quant(dims, _addr(x), _addr(codes), _addr(exps), _raw_stream(dev))
@@ -1255,7 +1263,7 @@ def ss_mx4_mm(x, x_scale, wq, w_exps, *, y=None, y_dtype=None, stream=None):
     import torch
     lib = load()
     dev, u8 = x.device, torch.uint8
-    lead = tuple(x.shape[:-1])
+    lead = x.shape[:-1]
     M, K = _rows_of(x, "x")
     if x.dtype == u8:
         K *= 2
@@ -1284,7 +1292,7 @@ def ss_mx4_mm(x, x_scale, wq, w_exps, *, y=None, y_dtype=None, stream=None):
     dims = _mx4_plan((M, N, K, SS_BF16, q8, SS_F32 if y_dtype == torch.float32 else SS_BF16))
     with _on(dev, stream, (x, x_scale, wq, w_exps, y)):
         if y is None:
-            y = torch.empty((*lead, N), dtype=y_dtype, device=dev)
+            y = x.new_empty((*lead, N), dtype=y_dtype)
         else:
             _check(y, "y", (*lead, N), y_dtype, dev)
         rc = lib.ss_mx4_mm(dims, _addr(x), _addr(x_scale), _addr(wq), _addr(w_exps), _addr(y),
