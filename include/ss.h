@@ -487,8 +487,9 @@ int ss_mx4_quant(const ss_mx4_dims* dims, const void* x, void* codes, void* exps
  *   w: codes wq [n, k / 2] and exponents w_exps [n, k / 32]
  *   x: codes [rows, k / 2] with x_scale its exponents [rows, k / 32] bytes, or e4m3 [rows, k] with
  *      x_scale [rows] float32, as the norms give them.
- * For any number of rows: up to 32 (64 or more where the weights are few) are kept together over the
- * whole of w, more go in tiles.  rows · n / 2^15 (x in e4m3: 2^14) < 2^24.  Needs no workspace. */
+ * For any number of rows: a few, or few by the weights' number, are kept together over w, more go in
+ * tiles.  ceil(rows / 256) · ceil(n / 128) < 2^24 (x in e4m3: rows / 128); for n of 2^20 and more
+ * rows · n < 2^33.  Needs no workspace. */
 int ss_mx4_mm(const ss_mx4_dims* dims, const void* x, const void* x_scale, const void* wq,
               const void* w_exps, void* y, hipStream_t stream);
 

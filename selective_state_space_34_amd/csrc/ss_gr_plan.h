@@ -114,14 +114,37 @@ inline int make_ln_plan(const ss_ln_dims& d, bool backward, RmsPlan* out) {
     return SS_OK;
 }
 
-// Products of microscaled weights: whether 256 (x in 4 bits) or 128 by 128 rows go to a workgroup, or 16 rows
-// of weights by up to 64 of x.  Tiles take a time of their own for a walk over K however few they
-// are, rows a time for every 64 of them and every 16 of the weights.  us with rows and with tiles, x in
-// 4 bits: 2560 x 2560, 64 rows 9 and 12, 128 11 and 12, 256 16 and 13; 10240 x 2560, 64 rows 16 and 13;
-// 2560 x 5120, 64 rows 14 and 20, 128 25 and 21; 5120 x 5120, 64 rows 25 and 22.
+// Products of microscaled weights.  Either 16 rows of weights by 16·high of x go to a workgroup of
+// `waves` waves, which share the columns (rows), or 128 by 64·high (tiles).
+struct Mx4Plan {
+    bool tiled;
+    int high, waves;
+};
+
+// us, x in 4 bits / in 8:
+// Tiles take a time of their own for a walk over K however few they are, rows a time for every 64 of
+// them and every 16 of the weights.  N x K, rows of x: with rows and with tiles.
+//   2560 x 2560,  192: 7.8 and 8.4 / 9.0 and 8.9,      256: 9.9 and 8.5 / 11.6 and 9.1
+//   10240 x 2560, 64:  10.0 and 10.8 / 13.3 and 11.5,  128: 13.9 and 10.4 / 17.4 and 11.4
+//   5120 x 5120,  64:  12.8 and 16.9 / 14.1 and 18.4,  128: 16.6 and 16.4 / 19.3 and 18.0
+// Tiles of 64 and of 128 rows of x, up to 256 of them (a compute unit one) and more; of 128 and 256:
+//   2560 x 2560,  768 rows of x: 10.3 and 10.4 / 11.4 and 13.1, 1024: 12.5 and 11.2 / 14.5 and 13.7
+//   10240 x 2560, 192: 10.6 and 11.7 / 11.8 and 13.5,           256: 13.0 and 12.0 / 14.9 and 14.1
+//   x in 4 bits, 128 and 256: 10240 x 2560, 384: 12.7 and 16.0, 512: 17.2 and 16.3, 4096: 78 and 71
+// Rows: as high as leaves two workgroups to a compute unit, else lower; 64 rows of x, high 4, 2, 1:
+//   2560 x 5120:  7.0, 6.8, 7.0 / 8.4, 8.2, 7.6        640 x 1024: 3.5, 3.0, 2.7 / 3.8, 3.1, 2.8
+// 8 and 16 waves where each compute unit has one workgroup: 2560 x 5120, 1 row of x, 4.4 and 3.9 / 5.3
+// and 4.4; 2560 x 10240, 7.0 and 5.4 / 9.0 and 6.5.
 // (A tile's rows of y stay within a descriptor's 2^31 bytes.)
-inline bool mx4_tiled(int64_t rows, int64_t n) {
-    return rows > 32 && n * ((rows + 63) / 64) >= 5120 && n < (int64_t(1) << 20);
+inline Mx4Plan mx4_plan(int64_t rows, int64_t n, int64_t k, bool fp8) {
+    if (rows > 32 && n * ((rows + 63) / 64) >= 10240 && n < (int64_t(1) << 20)) {
+        auto tiles = [&](int64_t high) { return (rows + 64 * high - 1) / (64 * high) * ((n + 127) / 128); };
+        return {true, tiles(1) <= 256 ? 1 : fp8 || tiles(2) <= 256 ? 2 : 4, 4};
+    }
+    auto groups = [&](int64_t high) { return (rows + 16 * high - 1) / (16 * high) * ((n + 15) / 16); };
+    if (rows > 32 && groups(4) >= 512) return {false, 4, 8};
+    const int high = rows > 16 && groups(2) >= 512 ? 2 : 1;
+    return {false, high, groups(high) <= 256 && k >= 2048 ? 16 : 8};
 }
 
 inline int check_mx4(const ss_mx4_dims& d, bool product) {
@@ -133,13 +156,11 @@ inline int check_mx4(const ss_mx4_dims& d, bool product) {
     if (d.k >= (int64_t(1) << 23)) return SS_ERR_DIMS;   // 256 rows stay within a descriptor
     if (d.x_q8 != SS_Q4_MX && d.x_q8 != SS_Q8_FP8) return SS_ERR_DTYPE;
     if (d.y_dtype != SS_F32 && d.y_dtype != SS_BF16) return SS_ERR_DTYPE;
-    if (mx4_tiled(d.rows, d.n)) {
-        const int64_t m = d.x_q8 == SS_Q4_MX ? 256 : 128;
-        if (!launch_ok((d.n + 127) / 128 * ((d.rows + m - 1) / m) + 7, 256)) return SS_ERR_DIMS;
-    } else if ((d.rows + 63) / 64 > kMaxGridYZ ||
-               !launch_ok((d.n + 15) / 16 * ((d.rows + 63) / 64), 512)) {
+    const Mx4Plan p = mx4_plan(d.rows, d.n, d.k, d.x_q8 == SS_Q8_FP8);
+    const int64_t m = (p.tiled ? 64 : 16) * p.high, high = (d.rows + m - 1) / m;
+    if (p.tiled ? !launch_ok((d.n + 127) / 128 * high + 7, 256)
+                : !launch_ok((d.n + 15) / 16 * high, 64 * p.waves))
         return SS_ERR_DIMS;
-    }
     return SS_OK;
 }
 

@@ -48,12 +48,20 @@ __global__ __launch_bounds__(256) void mx4_quant_kernel(const Mx4Quant p) {
     }
 }
 
-// ---- few rows --------------------------------------------------------------------------------
+// ---- buffers ---------------------------------------------------------------------------------
 
-__device__ __forceinline__ void load16(i32x8& f, int at, const uint8_t* p) {
-    const int4 w = *reinterpret_cast<const int4*>(p);
-    f[at] = w.x; f[at + 1] = w.y; f[at + 2] = w.z; f[at + 3] = w.w;
+constexpr int kRsrcFlags = 0x00020000;       // raw buffer, 32-bit elements
+constexpr int kNowhere = int(0x80000000u);   // behind every descriptor's end: loads 0, stores nothing
+
+// Up to `most` rows, `bytes` each, from number r0 of `rows` on.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_from(const void* p, int64_t r0, int64_t rows,
+                                                           int64_t most, int64_t bytes) {
+    const int64_t n = rows - r0 < most ? rows - r0 : most;
+    return __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>(static_cast<const uint8_t*>(p)) + r0 * bytes, 0, int(n * bytes), kRsrcFlags);
 }
+
+// ---- few rows --------------------------------------------------------------------------------
 
 // Eight e2m1 codes times 2^(e - 127) and four e4m3 values as bfloat16, exact (where the product is
 // a normal number).
@@ -84,62 +92,81 @@ __device__ __forceinline__ bf16x8 widen8(uint32_t lo, uint32_t hi) {
 enum { kX4, kX8, kX8Wide };
 
 // 16 rows of weights and 16·kTiles rows of x a workgroup; its waves take the columns, 128 at a time,
-// in turn and meet in LDS.
+// in turn and meet in LDS.  The matrix cores want 16 rows in neighbouring lanes; the cache takes four
+// neighbouring lanes at a time if they share a line, else one.  So four lanes load a row's 64 bytes
+// and exponents, and ds_bpermute brings them where they belong.  With loads straight into place the
+// cache's one access a clock bound this kernel: 64 rows by 2560 x 5120, 14.2 us, now 7.0 (x in e4m3
+// 14.1, now 7.6); 1 row by 10240 x 2560 5.9, now 5.0, of which 2.6 at the rate of a large copy and
+// 2.4 the shortest launch of all.  Loading the next columns ahead made no case faster.
+// What lies behind the last row or column loads as 0, exponents too.
 template <int kTiles, int kX, int kWaves>
 __global__ __launch_bounds__(64 * kWaves) void mx4_rows_kernel(const Mx4Launch p) {
     __shared__ float red[kWaves][kTiles][64][4];
     constexpr bool kFp8 = kX != kX4;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int row = lane & 15, g = lane >> 4;
-    const int64_t K = p.K, kb = K / 32, n0 = int64_t(blockIdx.x) * 16;
-    const int64_t m0 = int64_t(blockIdx.y) * 16 * kTiles;
-    const int64_t wr = n0 + row < p.N ? n0 + row : p.N - 1;
-    const uint8_t* w = p.wq + wr * (K / 2);
-    const uint8_t* we = p.w_exps + wr * kb;
-    const uint8_t* xs[kTiles];
-    const uint8_t* xe[kTiles];
+    constexpr int kPieces = kFp8 ? 2 : 1;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int row = lane >> 2, g = lane & 3, from = ((lane & 15) * 4 + (lane >> 4)) * 4;
+    const int K = int(p.K), kb = K / 32, row_x = kFp8 ? K : K / 2;
+    const int64_t n0 = int64_t(blockIdx.x) * 16, m0 = int64_t(blockIdx.y) * 16 * kTiles;
+    const __amdgpu_buffer_rsrc_t dw = rows_from(p.wq, n0, p.N, 16, K / 2);
+    const __amdgpu_buffer_rsrc_t dwe = rows_from(p.w_exps, n0, p.N, 16, kb);
+    const __amdgpu_buffer_rsrc_t dx = rows_from(p.x, m0, p.M, 16 * kTiles, row_x);
+    const __amdgpu_buffer_rsrc_t dxe = rows_from(p.x_scale, m0, p.M, 16 * kTiles, kFp8 ? 0 : kb);
+    // a lane's pieces of x in 128 columns: of e4m3 as the instruction takes them, or a block's halves
+    constexpr int kApart = kX == kX8Wide ? 16 : 64;
+    const int x0 = kX == kX8Wide ? 32 * g : 16 * g;
+    struct Operands {
+        u32x4 w, x[kTiles][kPieces];
+        int we, xe[kTiles];
+    };
+    auto fetch = [&](int k0, Operands& s) {
+        const bool in = k0 + 32 * g < K;
+        s.w = __builtin_amdgcn_raw_buffer_load_b128(dw, in ? row * (K / 2) + 16 * g : kNowhere, k0 / 2, 0);
+        s.we = __builtin_amdgcn_raw_buffer_load_b8(dwe, in ? row * kb + g : kNowhere, k0 / 32, 0);
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t) {
-        const int64_t m = m0 + 16 * t + row, mr = m < p.M ? m : p.M - 1;
-        xs[t] = p.x + mr * (kFp8 ? K : K / 2);
-        xe[t] = static_cast<const uint8_t*>(p.x_scale) + mr * kb;
-    }
-    f32x4 acc[kTiles] = {};
-    for (int64_t k0 = int64_t(wave) * 128; k0 < K; k0 += kWaves * 128) {
-        const int blocks = int(K - k0 < 128 ? (K - k0) / 32 : 4);
-        i32x8 a = {};
-        int sa = 127;
-        if (g < blocks) {
-            load16(a, 0, w + k0 / 2 + 16 * g);
-            sa = we[k0 / 32 + g];
+        for (int t = 0; t < kTiles; ++t) {
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                const int at = x0 + kApart * i;
+                s.x[t][i] = __builtin_amdgcn_raw_buffer_load_b128(
+                    dx, (kFp8 ? k0 + at < K : in) ? (16 * t + row) * row_x + at : kNowhere,
+                    kFp8 ? k0 : k0 / 2, 0);
+            }
+            if constexpr (!kFp8)
+                s.xe[t] = __builtin_amdgcn_raw_buffer_load_b8(dxe, in ? (16 * t + row) * kb + g : kNowhere,
+                                                              k0 / 32, 0);
         }
+    };
+    f32x4 acc[kTiles] = {};
+    auto add = [&](const Operands& s) {
+        i32x8 a = {};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) a[c] = __builtin_amdgcn_ds_bpermute(from, int(s.w[c]));
+        const int sa = __builtin_amdgcn_ds_bpermute(from, s.we);
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
             i32x8 b = {};
-            int sb = 127;
+#pragma unroll
+            for (int c = 0; c < 4 * kPieces; ++c)
+                b[c] = __builtin_amdgcn_ds_bpermute(from, int(s.x[t][c / 4][c % 4]));
             if constexpr (kX == kX8Wide) {
-                if (g < blocks) {
-                    load16(b, 0, xs[t] + k0 + 32 * g);
-                    load16(b, 4, xs[t] + k0 + 32 * g + 16);
-                }
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
                     acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
                         widen4(uint32_t(a[q]), sa), widen8(uint32_t(b[2 * q]), uint32_t(b[2 * q + 1])),
                         acc[t], 0, 0, 0);
-                continue;
+            } else {
+                const int sb = kFp8 ? 127 : __builtin_amdgcn_ds_bpermute(from, s.xe[t]);
+                acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc[t], 4, kFp8 ? 0 : 4,
+                                                                          0, sa, 0, sb);
             }
-            if constexpr (kFp8) {
-                if (g / 2 < blocks) load16(b, 0, xs[t] + k0 + 16 * g);
-                if (2 + g / 2 < blocks) load16(b, 4, xs[t] + k0 + 64 + 16 * g);
-            } else if (g < blocks) {
-                load16(b, 0, xs[t] + k0 / 2 + 16 * g);
-                sb = xe[t][k0 / 32 + g];
-            }
-            acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc[t], 4, kFp8 ? 0 : 4,
-                                                                      0, sa, 0, sb);
         }
         settle();   // the sums may change registers where the loop ends
+    };
+    for (int k0 = wave * 128; k0 < K; k0 += kWaves * 128) {
+        Operands s;
+        fetch(k0, s);
+        add(s);
     }
 #pragma unroll
     for (int t = 0; t < kTiles; ++t)
@@ -190,17 +217,6 @@ template <int kX> __device__ __forceinline__ int turn_x(int row) {
 // Row of weights, of a wave's 64, that product u takes as its row r.
 __device__ __forceinline__ int dealt(int u, int r) {
     return 16 * (r >> 3) + 8 * (r >> 2 & 1) + 4 * u + (r & 3);
-}
-
-constexpr int kRsrcFlags = 0x00020000;       // raw buffer, 32-bit elements
-constexpr int kNowhere = int(0x80000000u);   // behind every descriptor's end: loads 0, stores nothing
-
-// A tile's rows, `bytes` each, of `rows` from number r0 on.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_from(const void* p, int64_t r0, int64_t rows,
-                                                           int64_t most, int64_t bytes) {
-    const int64_t n = rows - r0 < most ? rows - r0 : most;
-    return __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint8_t*>(static_cast<const uint8_t*>(p)) + r0 * bytes, 0, int(n * bytes), kRsrcFlags);
 }
 
 // Exponents 16·block .. of the row at `at` that has n of them.  kEven: n is a multiple of 4.
@@ -471,19 +487,25 @@ hipError_t launch_tiles(const Mx4Launch& p, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <int kTiles, int kX>
+template <int kTiles, int kX, int kWaves>
 hipError_t launch_rows(const Mx4Launch& p, hipStream_t s) {
     const dim3 grid(unsigned((p.N + 15) / 16), unsigned((p.M + 16 * kTiles - 1) / (16 * kTiles)));
-    hipLaunchKernelGGL((mx4_rows_kernel<kTiles, kX, 8>), grid, dim3(512), 0, s, p);
+    hipLaunchKernelGGL((mx4_rows_kernel<kTiles, kX, kWaves>), grid, dim3(64 * kWaves), 0, s, p);
     return hipGetLastError();
 }
 
 template <int kX>
 hipError_t launch_mm(const Mx4Launch& p, hipStream_t s) {
-    if (p.M <= 16) return launch_rows<1, kX>(p, s);
-    if (p.M <= 32) return launch_rows<2, kX>(p, s);
-    if (mx4_tiled(p.M, p.N)) return launch_tiles<kX, kX == kX4 ? 4 : 2>(p, s);
-    return launch_rows<4, kX>(p, s);
+    const Mx4Plan m = mx4_plan(p.M, p.N, p.K, kX != kX4);
+    if (m.tiled) {
+        if (m.high == 1) return launch_tiles<kX, 1>(p, s);
+        if constexpr (kX == kX4)
+            if (m.high == 4) return launch_tiles<kX, 4>(p, s);
+        return launch_tiles<kX, 2>(p, s);
+    }
+    if (m.high == 4) return launch_rows<4, kX, 8>(p, s);
+    if (m.high == 2) return m.waves == 16 ? launch_rows<2, kX, 16>(p, s) : launch_rows<2, kX, 8>(p, s);
+    return m.waves == 16 ? launch_rows<1, kX, 16>(p, s) : launch_rows<1, kX, 8>(p, s);
 }
 
 }  // namespace

@@ -75,10 +75,15 @@ def test_rounding_over_the_range(gpu):
 SHAPES = [(1, 1, 32), (1, 16, 64), (1, 40, 128), (2, 17, 96), (16, 48, 544), (17, 33, 160), (31, 256, 1024),
           (33, 100, 288), (64, 64, 2560), (65, 130, 96), (100, 1, 2048), (128, 128, 128), (129, 257, 416),
           (200, 300, 1056), (255, 250, 64), (256, 256, 256), (300, 520, 32), (513, 129, 672), (1000, 384, 512),
-          # in tiles: N · ceil(M / 64) of 5120 and more
           (33, 5121, 96), (40, 5250, 640), (65, 2600, 160), (100, 2688, 1024), (129, 1801, 416), (257, 1100, 544),
           (300, 1030, 1056), (511, 640, 32), (512, 1024, 128), (700, 500, 672), (1025, 385, 288),
           (2050, 160, 384), (5200, 64, 64), (5121, 65, 256), (700, 513, 2560)]
+# N · ceil(M / 64) of 10240 and more go in tiles of 64 rows of x; more than 256 tiles of 64 in tiles of 128,
+# and of x in 4 bits, with more than 256 tiles of 128, of 256
+TILES = [(33, 10241, 96), (65, 5130, 640), (100, 5250, 160), (129, 3500, 416), (257, 2100, 1056), (511, 1285, 32),
+         (1025, 610, 288), (5200, 128, 64), (5121, 131, 256), (700, 1024, 2560),
+         (1090, 2050, 96), (1300, 1700, 288), (1100, 1920, 512), (2113, 1025, 544), (40, 33000, 96),
+         (2177, 2100, 96), (4200, 1030, 160), (2304, 2048, 640), (8200, 515, 32), (2500, 1793, 1152)]
 
 
 @pytest.mark.parametrize("x", ["mx4", "fp8"])
@@ -115,7 +120,40 @@ def test_products(gpu, shape, x):
     assert y.dtype == torch.float32 and (np.abs(num(y) - want) <= tol).all()
 
 
-@pytest.mark.parametrize("M", [1, 40, 300, 1400])
+@pytest.mark.parametrize("x", ["mx4", "fp8"])
+@pytest.mark.parametrize("M,N,K", TILES)
+def test_tiles(gpu, M, N, K, x):
+    """As test_products, the oracle's float64 products on the GPU."""
+    import torch
+    note(f"mx4 tiles {x} M={M} N={N} K={K}")
+    wq, we = weights(M + N, N, K)
+    W, xs = cuda(ref.mx4_values(ref.unpack(wq), we)), None
+    if x == "mx4":
+        xq, xe = weights(M * 7 + K, M, K)
+        X, args = cuda(ref.mx4_values(ref.unpack(xq), xe)), (cuda(xq), cuda(xe))
+    else:
+        r = np.random.default_rng(M + K)
+        t = torch.from_numpy((100 * r.normal(size=(M, K))).astype(np.float32)).cuda().clamp(-448, 448).to(torch.float8_e4m3fn)
+        X, xs = t.double(), cuda((0.01 + r.random(M)).astype(np.float32))
+        args = (t, xs)
+    want, terms = X @ W.T, X.abs() @ W.abs().T
+    tol = 2 * (K / 128 + 16) * U * terms
+    cut = torch.zeros_like(want)
+    if x == "fp8":
+        for k in range(0, K, 32):
+            top = torch.zeros_like(want)
+            for j in range(k, k + 32):
+                top = torch.maximum(top, X[:, j:j + 1].abs() * W[:, j].abs())
+            cut += 4 * 2.0 ** -13 * top
+        f = xs.double()[:, None]
+        want, tol, cut = want * f, (tol + U * terms) * f, cut * f
+    y = gpu.ss_mx4_mm(*args, cuda(wq), cuda(we))
+    assert ((y.double() - want).abs() <= tol + cut + 1.001 * 2.0 ** -8 * want.abs()).all()
+    y = gpu.ss_mx4_mm(*args, cuda(wq), cuda(we), y_dtype=torch.float32)
+    assert ((y.double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("M", [1, 40, 300, 2700, 9000])
 def test_every_code_and_exponent(gpu, M):
     """One code of weights against one of x, over all codes and exponents: exact, NaN at 255."""
     import torch
@@ -145,7 +183,7 @@ def test_rows_stay_apart(gpu):
     """NaN in a row of x (a block's exponent, a code, a scale) or of the weights stays in its row or
     column."""
     import torch
-    for M, N, K in ((20, 40, 256), (300, 200, 320), (1700, 200, 320), (2000, 192, 256)):
+    for M, N, K in ((20, 40, 256), (300, 200, 320), (3400, 200, 320), (4000, 192, 256), (10000, 290, 160)):
         wq, we = weights(3, N, K)
         xq, xe = weights(4, M, K)
         y = gpu.ss_mx4_mm(cuda(xq), cuda(xe), cuda(wq), cuda(we))
