@@ -377,14 +377,14 @@ __global__ __launch_bounds__(256, 2) void mx4_tile_kernel(const Mx4Launch p, int
     auto stage = [&](int block, auto j) {
         constexpr int kJ = decltype(j)::value, from = kJ & 1;
         const int s = 4 * block + kJ;
-        const uint8_t* e = reinterpret_cast<const uint8_t*>(sh.e[block & 1][kJ]);
+        const uint32_t* e = sh.e[block & 1][kJ];      // a row's four blocks
         i32x8 a[2][2] = {}, b[2] = {};        // weights: half of the stage, product
-        int sa[2][2], sb[2];
+        int sa[2], sb[kM];       // from block g on
         auto read_w = [&](int h, int u) {
             const u32x4 v = sh.w[from][at_w + 16 * u + ((2 * h + g) ^ tw)];
 #pragma unroll
             for (int c = 0; c < 4; ++c) a[h][u][c] = int(v[c]);
-            sa[h][u] = e[4 * (rn + 4 * u) + 2 * h + g];
+            if (h == 0) sa[u] = int(e[rn + 4 * u] >> (8 * g));
         };
         auto read_x = [&](int step) {
             const int o = step & 1, h = step / kM, t = step % kM;
@@ -392,7 +392,7 @@ __global__ __launch_bounds__(256, 2) void mx4_tile_kernel(const Mx4Launch p, int
                 const u32x4 v = sh.x[from][at_x + 128 * t + ((2 * h + g) ^ tx)];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) b[o][c] = int(v[c]);
-                sb[o] = e[4 * (L::kRowsN + rm + 32 * t) + 2 * h + g];
+                if (h == 0) sb[t] = int(e[L::kRowsN + rm + 32 * t] >> (8 * g));
             } else {
                 // kX8: as the instruction takes them; kX8Wide: the 32 columns of one block
                 constexpr bool kBlock = kX == kX8Wide;
@@ -403,7 +403,6 @@ __global__ __launch_bounds__(256, 2) void mx4_tile_kernel(const Mx4Launch p, int
                     b[o][c] = int(v[c]);
                     b[o][4 + c] = int(w[c]);
                 }
-                sb[o] = 127;
             }
         };
         read_x(0);
@@ -429,13 +428,18 @@ __global__ __launch_bounds__(256, 2) void mx4_tile_kernel(const Mx4Launch p, int
 #pragma unroll
                     for (int u = 0; u < 2; ++u)
                         acc[u][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                            widen4(uint32_t(a[h][u][q]), sa[h][u]), v, acc[u][t], 0, 0, 0);
+                            widen4(uint32_t(a[h][u][q]), sa[u] >> (16 * h) & 255), v, acc[u][t], 0, 0, 0);
                 }
             } else {
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
-                    acc[u][t] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                        a[h][u], b[o], acc[u][t], 4, kX == kX4 ? 4 : 0, 0, sa[h][u], 0, sb[o]);
+                for (int u = 0; u < 2; ++u) {
+                    const int one = kX == kX4 ? sb[t] : 127;
+                    constexpr int kOf = kX == kX4 ? 2 : 0;
+                    acc[u][t] = h == 0 ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                                             a[h][u], b[o], acc[u][t], 4, kX == kX4 ? 4 : 0, 0, sa[u], 0, one)
+                                       : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                                             a[h][u], b[o], acc[u][t], 4, kX == kX4 ? 4 : 0, 2, sa[u], kOf, one);
+                }
             }
             __builtin_amdgcn_sched_barrier(0);
         }
