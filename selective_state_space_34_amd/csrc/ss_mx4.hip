@@ -53,6 +53,8 @@ __global__ __launch_bounds__(256) void mx4_quant_kernel(const Mx4Quant p) {
 constexpr int kRsrcFlags = 0x00020000;       // raw buffer, 32-bit elements
 constexpr int kNowhere = int(0x80000000u);   // behind every descriptor's end: loads 0, stores nothing
 
+constexpr int kPast = 2;                     // a store that the caches do not keep (nt)
+
 // Up to `most` rows, `bytes` each, from number r0 of `rows` on.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_from(const void* p, int64_t r0, int64_t rows,
                                                            int64_t most, int64_t bytes) {
@@ -249,57 +251,83 @@ __device__ __forceinline__ bool tile_of(int64_t tiles_m, int64_t tiles_n, int64_
 }
 
 // Rows behind the last one are behind the descriptor's end.  A wave whose columns all exist, on rows
-// that start on 4 bytes, stores 16 bytes at a time.
+// that start on 4 bytes, turns 32 rows of 128 bytes at a time in LDS (`own`: 4 KB of the wave's, twice)
+// and stores whole lines; where the lines are memory's own, past the caches, which keep x and w
+// instead.  16384 x 10240 x 2560: 278 us with 16 bytes of a row to a lane, 257 so, 250 past the caches
+// (which made the pieces of 16 bytes slower, 480).
 template <int kX, int kM>
 __device__ __forceinline__ void store_tile(const Mx4Launch& p, int64_t m0, int64_t n0, int wn, int wm,
-                                           int lane, const f32x16 (&acc)[2][kM]) {
+                                           int lane, const f32x16 (&acc)[2][kM], u32x4* own) {
     const int row = lane & 31, g = lane >> 5;
     const int N = int(p.N), el = p.y_dtype == SS_F32 ? 4 : 2;
     const __amdgpu_buffer_rsrc_t dy = rows_from(p.y, m0, p.M, 64 * kM, int64_t(N) * el);
-    const int n = int(n0) + 64 * wn + 8 * g;
-    const bool wide = int(n0) + 64 * (wn + 1) <= N && (el == 4 || N % 2 == 0);
+    const int c0 = int(n0) + 64 * wn, n = c0 + 8 * g;
+    const bool wide = c0 + 64 <= N && (el == 4 || N % 2 == 0), whole = N * el % 128 == 0;
 #pragma unroll
     for (int t = 0; t < kM; ++t) {
-        const int m = 32 * kM * wm + 32 * t + row;
+        const int top = 32 * kM * wm + 32 * t, m = top + row;
         float f = 1.0f;
         if constexpr (kX != kX4)
             f = static_cast<const float*>(p.x_scale)[m0 + m < p.M ? m0 + m : p.M - 1];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            // eight columns from n + 16 q on: four of each product
-            const int at = n + 16 * q;
-            float v[8];
+        // eight columns from n + 16 q on: four of each product
+        auto eight = [&](int q, float (&v)[8]) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 v[j] = acc[j / 4][t][4 * q + j % 4];
                 if constexpr (kX != kX4) v[j] *= f;
             }
-            if (el == 4) {
-                if (wide) {
+        };
+        if (wide) {
+            const int lines = el / 2;       // of 128 bytes in a row
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const u32x4 w = {__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
-                                         __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])};
-                        __builtin_amdgcn_raw_buffer_store_b128(w, dy, (m * N + at + 4 * i) * 4, 0, 0);
+            for (int half = 0; half < 2; ++half) {
+                if (half >= lines) break;
+                u32x4* at = own + 256 * ((t + half) & 1);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float v[8];
+                    if (el == 2) {
+                        eight(q, v);
+                        union { bf16x8 h; u32x4 w; } o;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) o.h[j] = __bf16(v[j]);
+                        at[8 * row + ((2 * q + g) ^ (row & 7))] = o.w;
+                    } else if (q < 2) {
+                        eight(2 * half + q, v);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            at[8 * row + ((4 * q + 2 * g + i) ^ (row & 7))] =
+                                u32x4{__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                                      __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])};
                     }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        __builtin_amdgcn_raw_buffer_store_b32(
-                            __float_as_uint(v[j]), dy, at + j < N ? (m * N + at + j) * 4 : kNowhere, 0, 0);
                 }
-            } else {
-                union { bf16x8 h; u32x4 w; } o;
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                __builtin_amdgcn_wave_barrier();
 #pragma unroll
-                for (int j = 0; j < 8; ++j) o.h[j] = __bf16(v[j]);
-                if (wide) {
-                    __builtin_amdgcn_raw_buffer_store_b128(o.w, dy, (m * N + at) * 2, 0, 0);
+                for (int i = 0; i < 4; ++i) {
+                    const int r = 8 * i + (lane >> 3), piece = lane & 7;
+                    const u32x4 w = at[8 * r + (piece ^ (r & 7))];
+                    const int to = ((top + r) * N + c0) * el + 128 * half + 16 * piece;
+                    if (whole) __builtin_amdgcn_raw_buffer_store_b128(w, dy, to, 0, kPast);
+                    else __builtin_amdgcn_raw_buffer_store_b128(w, dy, to, 0, 0);
+                }
+            }
+            continue;
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int at = n + 16 * q;
+            float v[8];
+            eight(q, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int to = at + j < N ? (m * N + at + j) * el : kNowhere;
+                if (el == 4) {
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[j]), dy, to, 0, 0);
                 } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        __builtin_amdgcn_raw_buffer_store_b16(
-                            uint16_t(o.w[j / 2] >> (16 * (j % 2))), dy,
-                            at + j < N ? (m * N + at + j) * 2 : kNowhere, 0, 0);
+                    union { __bf16 h; uint16_t w; } o;
+                    o.h = __bf16(v[j]);
+                    __builtin_amdgcn_raw_buffer_store_b16(o.w, dy, to, 0, 0);
                 }
             }
         }
@@ -477,7 +505,9 @@ __global__ __launch_bounds__(256, 2) void mx4_tile_kernel(const Mx4Launch p, int
     if (4 * block + 2 < stages) stage(block, j2);
     settle();      // (a product of 32 by 32 takes up to twice the wait)
     settle();
-    store_tile<kX, kM>(p, m0, n0, wn, wm, lane, acc);
+    // (no wave reads columns from LDS any more)
+    static_assert(sizeof(L) >= 4 * 512 * sizeof(u32x4), "8 KB a wave");
+    store_tile<kX, kM>(p, m0, n0, wn, wm, lane, acc, reinterpret_cast<u32x4*>(&sh) + 512 * wave);
 }
 
 template <int kX, int kM>
