@@ -20,6 +20,8 @@
 #include "ss_gr_plan.h"
 #include "ss_kernels.h"
 
+#include <algorithm>
+
 namespace ss {
 
 namespace {
@@ -436,6 +438,66 @@ __global__ __launch_bounds__(64 * kWaves) void gr_fwd_kernel(const GrLaunch p) {
     }
 }
 
+// Short rows: a wave takes 128 channels of a row from its first token to its last, kS at a time, the next
+// ones on their way.  1024 rows of 1 token, 2560 channels, bfloat16: 15 us (a tile's workgroup for each 374),
+// of 32 tokens, 671 MB, 135 us (374).
+template <typename T, bool kVec, int kS>
+__global__ __launch_bounds__(256) void gr_walk_kernel(const GrLaunch p) {
+    const int lane = threadIdx.x & 63;
+    const unsigned groups = unsigned((p.D + kCols - 1) / kCols);
+    const unsigned number = blockIdx.x * 4 + unsigned(wave_number());
+    if (number >= groups * unsigned(p.B)) return;
+    const int64_t b = number / groups, D = p.D, nc = (p.T + SS_GR_CKPT - 1) / SS_GR_CKPT;
+    const Cols col = columns<kVec>(int64_t(number % groups) * kCols, lane, D);
+    const Rows<T, kVec> x(static_cast<const T*>(p.x.p) + b * p.x.sb, p.x.st, p.T, D, col, false);
+    const Rows<T, kVec> r(static_cast<const T*>(p.r.p) + b * p.r.sb, p.r.st, p.T, D, col, false);
+    const Rows<T, kVec> g(static_cast<const T*>(p.i.p) + b * p.i.sb, p.i.st, p.T, D, col, false);
+    const Rows<T, kVec> y(static_cast<T*>(p.y) + b * p.T * D, D, p.T, D, col, true);
+    struct In {
+        Two<T> x[kS], r[kS], i[kS];
+    };
+    auto load = [&](int t0, In& in) {
+#pragma unroll
+        for (int s = 0; s < kS; ++s) {
+            in.r[s].load(r, t0 + s);
+            in.i[s].load(g, t0 + s);
+            in.x[s].load(x, t0 + s);
+        }
+    };
+    In now;
+    load(0, now);
+    float k2[2], h[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        k2[j] = rate2(p.lam[col.ch[j]], p.c);
+        h[j] = p.h0 ? p.h0[b * D + col.ch[j]] : 0.0f;
+    }
+    for (int64_t t0 = 0; t0 < p.T; t0 += kS) {
+        In next;
+        if (t0 + kS < p.T) load(int(t0) + kS, next);
+        const int live = live_tokens<kS>(p.lengths, b, t0, p.T);
+        const uint32_t first = reset_bits(p.reset, b, p.T, t0, lane, live);
+        if (p.h_ckpt && t0 % SS_GR_CKPT == 0) store_row<kVec>(p.h_ckpt + (b * nc + t0 / SS_GR_CKPT) * D, col, h[0], h[1]);
+#pragma unroll
+        for (int s = 0; s < kS; ++s) {
+            const bool cut = first >> s & 1, on = s < live;
+            float o[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float t2 = k2[j] * sigmoid(now.r[s].get(j));
+                const float e = exp2_hw(t2);
+                const float q = __builtin_amdgcn_sqrtf(one_less_square(t2, e));
+                const float v = sigmoid(now.i[s].get(j)) * now.x[s].get(j);
+                if (on) h[j] = cut ? v : fmaf(e, h[j], q * v);
+                o[j] = on ? h[j] : 0.0f;
+            }
+            store2(y, int(t0) + s, o[0], o[1]);
+        }
+        now = next;
+    }
+    if (p.h_final) store_row<kVec>(p.h_final + b * D, col, h[0], h[1]);
+}
+
 // ---- backward --------------------------------------------------------------------------------
 
 // The states before a wave's tokens come from the checkpoint that its workgroup's tile starts
@@ -654,6 +716,11 @@ hipError_t launch_gr_chains(uint64_t* tickets, uint64_t* maps, int64_t words, hi
 
 hipError_t launch_gr_fwd(const GrLaunch& p, hipStream_t s) {
     return with_type(p.in_dtype, p.vec, [&](auto t, auto v) {
+        if (p.y && gr_walks(p.T, int64_t(groups(p.D)) * p.B, std::max({p.x.st, p.r.st, p.i.st, p.D}))) {
+            hipLaunchKernelGGL((gr_walk_kernel<decltype(t), decltype(v)::value, 8>),
+                               dim3((groups(p.D) * unsigned(p.B) + 3) / 4), dim3(256), 0, s, p);
+            return hipGetLastError();
+        }
         hipLaunchKernelGGL((gr_fwd_kernel<decltype(t), decltype(v)::value, kFwdWaves, kGrFwdTile / kFwdWaves>),
                            dim3(groups(p.D) * unsigned(p.B) * unsigned(p.tiles)), dim3(64 * kFwdWaves), 0, s, p);
         return hipGetLastError();

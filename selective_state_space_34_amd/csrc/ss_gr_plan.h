@@ -14,6 +14,15 @@ constexpr int kGrFwdTile = 128;                    // tokens of a workgroup, for
 // directions 202, 204, 210, 214.
 constexpr int kGrFwdGroup = 32, kGrBwdGroup = 16;
 
+// Whether rows are walked by a wave for each 128 channels (`waves` of them in all) rather than taken by a
+// workgroup each: 4 us and 0.22 a token against 10, or, where there are many, what their bytes take against
+// 75 ns each.  us by walk and by workgroups, 2560 channels, bfloat16: 4 rows of 32 tokens 11.1 and 10.2, of
+// 48 14 and 10; 64 rows of 48 22 and 31, of 96 37 and 34; 256 of 128 138 and 137.  st: the widest step
+// from token to token; all tokens of a row, and eight more, stay within a descriptor's 2^31 bytes.
+inline bool gr_walks(int64_t T, int64_t waves, int64_t st) {
+    return T <= kGrFwdTile && (T <= 32 || waves >= 16 * T) && (T + 8) * st < (int64_t(1) << 28);
+}
+
 // What links the tiles of a row: the tiles' maps and, right behind them, the groups' ends (words of
 // 8 bytes), and a counter (tiles > 1).
 struct GrChain {
@@ -91,15 +100,15 @@ inline int make_ln_plan(const ss_ln_dims& d, bool backward, RmsPlan* out) {
     const int rc = make_rms_plan(r, backward, &p);
     if (rc != SS_OK) return rc;
     const int64_t pieces = (p.D + 7) / 8;
-    const bool whole = p.D % 8 == 0, many = p.M >= 1024;
+    const bool many = p.M >= 1024;
     if (pieces <= 128) {
         p.threads = pieces <= 8 ? 8 : pieces <= 32 ? 32 : 64;
         p.pieces = pieces <= 64 ? 1 : 2;
-    } else if (!backward && whole && many && pieces <= 64 * 6) {
+    } else if (!backward && many && pieces <= 64 * 6) {
         p.threads = 64;
         p.pieces = int((pieces + 63) / 64);
     } else if (pieces <= 512) {
-        p.threads = pieces <= 256 ? 256 : !whole ? 512 : pieces <= 320 ? 320 : pieces <= 384 ? 384 : 512;
+        p.threads = pieces <= 256 ? 256 : pieces <= 320 ? 320 : pieces <= 384 ? 384 : 512;
         p.pieces = 1;
     } else {
         p.threads = pieces <= 1024 ? 512 : 1024;
@@ -107,7 +116,12 @@ inline int make_ln_plan(const ss_ln_dims& d, bool backward, RmsPlan* out) {
     }
     const int64_t wg_rows = p.threads >= 256 ? 1 : 256 / p.threads;
     const int64_t need = (p.M + wg_rows - 1) / wg_rows;
-    const int64_t most = p.threads >= 512 ? 512 : backward ? 1024 : 2048;
+    // (a gradient's workgroups each write two rows of sums: 256 or 512 of them, us, bfloat16 / float32,
+    // 8192 wide 68 and 73 / 94 and 99, 16384 96 and 109 / 182 and 196)
+    const int64_t most = backward && p.pieces * p.threads >= 768 ? 256
+                         : p.threads >= 512                      ? 512
+                         : backward                              ? 1024
+                                                                 : 2048;
     p.grid = int(need < most ? need : most);
     p.total = backward ? align256(size_t(p.grid) * size_t(2 * p.D) * sizeof(float)) : 0;
     *out = p;

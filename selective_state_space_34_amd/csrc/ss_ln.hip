@@ -9,6 +9,8 @@
 // bounds both directions: 16384 rows of 2560 bfloat16, r = x + res, 335 MB, 71 us (4.7 TB/s; a copy
 // 5.06); gradient, with dr, 335 MB, 76 us (4.4 TB/s), 5 of them the sum of the workgroups' partial dw and db.
 // One row takes 3.3 us, a launch's own time and two rounds of memory latency.
+// Rows of odd widths start anywhere and end inside a piece: 26512 x 1471 79 us, gradient 118 (1472: 60 and
+// 87); 181 and 185 with the last elements one by one.
 #include "ss_norm_rows.h"
 
 namespace ss {
@@ -36,10 +38,13 @@ __device__ __forceinline__ void give(T* row, int64_t col, int64_t dim, const flo
         put8(row, col, dim, v);
     }
 }
-template <int P, bool kWhole>
+// Where the piece at col is taken from: other rows' last pieces are their last eight elements, and
+// `twice` of those, the piece before has them too, are left out of the sums.  (A row's loads all come
+// before the barrier of its first sum, and its stores behind it, so this holds in place as well.)
+template <bool kWhole>
 __device__ __forceinline__ Span place(int64_t col, int64_t dim) {
-    if constexpr (kWhole) return Span{col, 0};
-    return span_of<P>(col, dim);
+    if (!kWhole && dim >= 8 && col < dim && col + 8 > dim) return Span{dim - 8, int(col + 8 - dim)};
+    return Span{col, 0};
 }
 
 // v less m in the elements of the piece at c that are the row's own, 0 in the others.
@@ -81,19 +86,18 @@ __global__ __launch_bounds__(P > 256 ? P : 256) void ln_fwd_kernel(const LnLaunc
         float v[NV][8], m = 0.0f, sq = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const Span c = place<P, kWhole>((int64_t(j) * P + tid) * 8, D);
+            const Span c = place<kWhole>((int64_t(j) * P + tid) * 8, D);
             px[j] = take<Tx, kWhole>(x, c.at, D);
             if (p.res) pr[j] = take<Tr, kWhole>(res, c.at, D);
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const Span c = place<P, kWhole>((int64_t(j) * P + tid) * 8, D);
+            const Span c = place<kWhole>((int64_t(j) * P + tid) * 8, D);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[j][e] = px[j].get(e);
             if (p.res) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[j][e] += pr[j].get(e);
-                give<Tr, kWhole>(static_cast<Tr*>(p.r) + row * D, c.at, D, v[j]);
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) m += kWhole || e >= c.twice ? v[j][e] : 0.0f;
@@ -102,8 +106,9 @@ __global__ __launch_bounds__(P > 256 ? P : 256) void ln_fwd_kernel(const LnLaunc
         // (elements that two threads hold keep their value: both store them)
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const Span c = place<P, kWhole>((int64_t(j) * P + tid) * 8, D);
+            const Span c = place<kWhole>((int64_t(j) * P + tid) * 8, D);
             const float own = kWhole && c.at >= D ? 0.0f : m;
+            if (p.res) give<Tr, kWhole>(static_cast<Tr*>(p.r) + row * D, c.at, D, v[j]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float d = less<kWhole>(v[j][e], own, c, e, D);
@@ -116,7 +121,7 @@ __global__ __launch_bounds__(P > 256 ? P : 256) void ln_fwd_kernel(const LnLaunc
         uint32_t top = 0;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int64_t at = place<P, kWhole>((int64_t(j) * P + tid) * 8, D).at;
+            const int64_t at = place<kWhole>((int64_t(j) * P + tid) * 8, D).at;
             const Piece<float> w = take<float, kWhole>(p.w, at, D);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[j][e] = v[j][e] * c * w.get(e);
@@ -136,7 +141,7 @@ __global__ __launch_bounds__(P > 256 ? P : 256) void ln_fwd_kernel(const LnLaunc
             Tx* y = static_cast<Tx*>(p.y) + row * D;
 #pragma unroll
             for (int j = 0; j < NV; ++j)
-                give<Tx, kWhole>(y, place<P, kWhole>((int64_t(j) * P + tid) * 8, D).at, D, v[j]);
+                give<Tx, kWhole>(y, place<kWhole>((int64_t(j) * P + tid) * 8, D).at, D, v[j]);
         } else if (p.q8 == SS_Q4_MX) {
             // D is a multiple of 32: four lanes hold a block
             uint8_t* y = static_cast<uint8_t*>(p.y) + row * (D / 2);
@@ -159,7 +164,7 @@ __global__ __launch_bounds__(P > 256 ? P : 256) void ln_fwd_kernel(const LnLaunc
             uint8_t* y = static_cast<uint8_t*>(p.y) + row * D;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                const int64_t col = place<P, kWhole>((int64_t(j) * P + tid) * 8, D).at;
+                const int64_t col = place<kWhole>((int64_t(j) * P + tid) * 8, D).at;
                 // a row that is not finite keeps NaN codes where e4m3 has them
                 const uint2 q = codes8(v[j], amax != amax ? amax : inv, p.q8);
                 if (col + 8 <= D) {
@@ -197,14 +202,14 @@ __global__ __launch_bounds__(P > 256 ? P : 256) void ln_bwd_kernel(const LnLaunc
         float m = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int64_t col = place<P, kWhole>((int64_t(j) * P + tid) * 8, D).at;
+            const int64_t col = place<kWhole>((int64_t(j) * P + tid) * 8, D).at;
             r[j] = take<Tr, kWhole>(rr, col, D);
             dy[j] = take<Tx, kWhole>(dyr, col, D);
             if (p.dr) g[j] = take<Tr, kWhole>(static_cast<const Tr*>(p.dr) + row * D, col, D);
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const Span c = place<P, kWhole>((int64_t(j) * P + tid) * 8, D);
+            const Span c = place<kWhole>((int64_t(j) * P + tid) * 8, D);
 #pragma unroll
             for (int e = 0; e < 8; ++e) m += kWhole || e >= c.twice ? r[j].get(e) : 0.0f;
         }
@@ -214,7 +219,7 @@ __global__ __launch_bounds__(P > 256 ? P : 256) void ln_bwd_kernel(const LnLaunc
         float sq = 0.0f, dot = 0.0f, all = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const Span c = place<P, kWhole>((int64_t(j) * P + tid) * 8, D);
+            const Span c = place<kWhole>((int64_t(j) * P + tid) * 8, D);
             const Piece<float> w = take<float, kWhole>(p.w, c.at, D);
             const float own = kWhole && c.at >= D ? 0.0f : m;
 #pragma unroll
@@ -235,7 +240,7 @@ __global__ __launch_bounds__(P > 256 ? P : 256) void ln_bwd_kernel(const LnLaunc
         Tr* dx = static_cast<Tr*>(p.r) + row * D;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const Span at = place<P, kWhole>((int64_t(j) * P + tid) * 8, D);
+            const Span at = place<kWhole>((int64_t(j) * P + tid) * 8, D);
             const Piece<float> w = take<float, kWhole>(p.w, at.at, D);
             float o[8];
 #pragma unroll
@@ -255,7 +260,7 @@ __global__ __launch_bounds__(P > 256 ? P : 256) void ln_bwd_kernel(const LnLaunc
     for (int which = 0; which < 2; ++which) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const Span c = place<P, kWhole>((int64_t(j) * P + tid) * 8, D);
+            const Span c = place<kWhole>((int64_t(j) * P + tid) * 8, D);
             if constexpr (kRowsWG > 1) {
                 // the workgroup's row slots one after the other
                 for (int s = 0; s < kRowsWG; ++s) {
@@ -319,41 +324,31 @@ hipError_t launch_t(const LnLaunch& p, bool backward, hipStream_t s) {
 }
 
 // The shapes that make_ln_plan gives.
-template <typename Tx, typename Tr>
-hipError_t launch_shape(const LnLaunch& p, bool backward, hipStream_t s) {
-    const int shape = p.threads * 10 + p.pieces;
-    if (p.D % 8 == 0) {
-        switch (shape) {
-            case 81: return launch_t<Tx, Tr, 8, 1, true>(p, backward, s);
-            case 321: return launch_t<Tx, Tr, 32, 1, true>(p, backward, s);
-            case 641: return launch_t<Tx, Tr, 64, 1, true>(p, backward, s);
-            case 642: return launch_t<Tx, Tr, 64, 2, true>(p, backward, s);
-            case 643: return launch_t<Tx, Tr, 64, 3, true>(p, backward, s);
-            case 644: return launch_t<Tx, Tr, 64, 4, true>(p, backward, s);
-            case 645: return launch_t<Tx, Tr, 64, 5, true>(p, backward, s);
-            case 646: return launch_t<Tx, Tr, 64, 6, true>(p, backward, s);
-            case 2561: return launch_t<Tx, Tr, 256, 1, true>(p, backward, s);
-            case 3201: return launch_t<Tx, Tr, 320, 1, true>(p, backward, s);
-            case 3841: return launch_t<Tx, Tr, 384, 1, true>(p, backward, s);
-            case 5121: return launch_t<Tx, Tr, 512, 1, true>(p, backward, s);
-            case 5122: return launch_t<Tx, Tr, 512, 2, true>(p, backward, s);
-            case 10242: return launch_t<Tx, Tr, 1024, 2, true>(p, backward, s);
-            case 10244: return launch_t<Tx, Tr, 1024, 4, true>(p, backward, s);
-            default: return hipErrorInvalidValue;
-        }
-    }
-    switch (shape) {
-        case 81: return launch_t<Tx, Tr, 8, 1, false>(p, backward, s);
-        case 321: return launch_t<Tx, Tr, 32, 1, false>(p, backward, s);
-        case 641: return launch_t<Tx, Tr, 64, 1, false>(p, backward, s);
-        case 642: return launch_t<Tx, Tr, 64, 2, false>(p, backward, s);
-        case 2561: return launch_t<Tx, Tr, 256, 1, false>(p, backward, s);
-        case 5121: return launch_t<Tx, Tr, 512, 1, false>(p, backward, s);
-        case 5122: return launch_t<Tx, Tr, 512, 2, false>(p, backward, s);
-        case 10242: return launch_t<Tx, Tr, 1024, 2, false>(p, backward, s);
-        case 10244: return launch_t<Tx, Tr, 1024, 4, false>(p, backward, s);
+template <typename Tx, typename Tr, bool kWhole>
+hipError_t launch_of(const LnLaunch& p, bool backward, hipStream_t s) {
+    switch (p.threads * 10 + p.pieces) {
+        case 81: return launch_t<Tx, Tr, 8, 1, kWhole>(p, backward, s);
+        case 321: return launch_t<Tx, Tr, 32, 1, kWhole>(p, backward, s);
+        case 641: return launch_t<Tx, Tr, 64, 1, kWhole>(p, backward, s);
+        case 642: return launch_t<Tx, Tr, 64, 2, kWhole>(p, backward, s);
+        case 643: return launch_t<Tx, Tr, 64, 3, kWhole>(p, backward, s);
+        case 644: return launch_t<Tx, Tr, 64, 4, kWhole>(p, backward, s);
+        case 645: return launch_t<Tx, Tr, 64, 5, kWhole>(p, backward, s);
+        case 646: return launch_t<Tx, Tr, 64, 6, kWhole>(p, backward, s);
+        case 2561: return launch_t<Tx, Tr, 256, 1, kWhole>(p, backward, s);
+        case 3201: return launch_t<Tx, Tr, 320, 1, kWhole>(p, backward, s);
+        case 3841: return launch_t<Tx, Tr, 384, 1, kWhole>(p, backward, s);
+        case 5121: return launch_t<Tx, Tr, 512, 1, kWhole>(p, backward, s);
+        case 5122: return launch_t<Tx, Tr, 512, 2, kWhole>(p, backward, s);
+        case 10242: return launch_t<Tx, Tr, 1024, 2, kWhole>(p, backward, s);
+        case 10244: return launch_t<Tx, Tr, 1024, 4, kWhole>(p, backward, s);
         default: return hipErrorInvalidValue;
     }
+}
+
+template <typename Tx, typename Tr>
+hipError_t launch_shape(const LnLaunch& p, bool backward, hipStream_t s) {
+    return p.D % 8 == 0 ? launch_of<Tx, Tr, true>(p, backward, s) : launch_of<Tx, Tr, false>(p, backward, s);
 }
 
 hipError_t launch(const LnLaunch& p, bool backward, hipStream_t s) {

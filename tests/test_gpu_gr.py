@@ -426,3 +426,41 @@ def test_far_strides(gpu):
         t = flat.as_strided((1, 2, D), (1, far, 1))
         gpu.ss_gr_fwd(t, t, t, lam)
     assert e.value.code == -2
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(700, 40, 130), (600, 65, 200), (2100, 128, 33), (5000, 3, 20), (300, 32, 257)], ids=str)
+def test_many_short_texts(gpu, shape, dt):
+    note(f"gr many short {shape} {dt}")
+    run_all(gpu, make(sum(shape), *shape, dt, lengths=True, reset=True), dt)
+
+
+@pytest.mark.parametrize("T,st", [(2, 1 << 25), (2, 1 << 24), (9, 1 << 23), (9, 1 << 24), (30, 1 << 22), (32, 1 << 23)])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_wide_steps_from_token_to_token(gpu, T, st, dt):
+    import torch
+    D = 70
+    note(f"gr steps {T} {st} {dt}")
+    flat = torch.zeros((T - 1) * st + 3 * D, device="cuda", dtype=torch.float32 if dt == "f32" else torch.bfloat16)
+    own = [flat.as_strided((1, T, D), (0, st, 1), o) for o in (0, D, 2 * D)]
+    p = make(T, 1, T, D, dt, h0=False)
+    for a, b in zip(own, (p["x"], p["r"], p["i"])):
+        a.copy_(b)
+    want = gpu.ss_gr_fwd(p["x"], p["r"], p["i"], p["lam"])
+    got = gpu.ss_gr_fwd(*own, p["lam"])
+    w, b = oracle(p)
+    gr = gpu.ss_gr_bwd(*own, p["lam"], p["dy"])
+    near(got, w["y"], b["y"], dt, "y")
+    near(want, w["y"], b["y"], dt, "y")
+    near(gr["dx"], w["dx"], b["dx"], dt, "dx")
+
+
+def test_short_texts_equal_single_tokens(gpu):
+    import torch
+    p = make(3, 5, 30, 200, "bf16")
+    y, h = gpu.ss_gr_fwd(p["x"], p["r"], p["i"], p["lam"], p["h0"], return_final=True)
+    own = p["h0"].clone()
+    for t in range(30):
+        yt = gpu.ss_gr_step(p["x"][:, t], p["r"][:, t], p["i"][:, t], p["lam"], own)
+        assert torch.equal(yt, y[:, t])
+    assert torch.equal(own, h)

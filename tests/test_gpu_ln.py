@@ -21,7 +21,7 @@ pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
 SHAPES = [(1, 1), (1, 8), (3, 7), (5, 64), (2, 96), (2, 511), (4, 512), (7, 513), (3, 1000), (1, 2048),
           (2, 2049), (1, 2560), (1100, 520), (1030, 1536), (1025, 2560), (2, 4099), (3, 8192),
-          (2, 8200), (1, 16384), (1, 16416), (2, 20001), (1, 32768)]
+          (2, 8200), (1, 16384), (1, 16416), (2, 20001), (1, 32768), (1200, 1471), (1030, 2563), (1100, 3001)]
 TYPES = [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32")]
 
 
