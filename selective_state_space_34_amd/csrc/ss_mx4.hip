@@ -231,18 +231,37 @@ __device__ __forceinline__ int dealt(int u, int r) {
     return 16 * (r >> 3) + 8 * (r >> 2 & 1) + 4 * u + (r & 3);
 }
 
-// Exponents 16·block .. of the row at `at` that has n of them.  kEven: n is a multiple of 4.
+// Exponents 16·block .. of the row at `at` that has n of them.  kEven: n is a multiple of 4; others'
+// rows start on any byte, and a row's last 16 are taken whole and shifted.  (Behind the row's end:
+// anything.)
 template <bool kEven>
 __device__ __forceinline__ u32x4 exponents(__amdgpu_buffer_rsrc_t d, int at, int block, int n) {
-    u32x4 w = {0, 0, 0, 0};
-    if constexpr (kEven) {
-        w = __builtin_amdgcn_raw_buffer_load_b128(d, at, 16 * block, 0);
-    } else {
-        const int left = n - 16 * block;
+    if constexpr (kEven) return __builtin_amdgcn_raw_buffer_load_b128(d, at, 16 * block, 0);
+    const int from = 16 * block + 16 <= n ? 16 * block : n - 16;
+    if (n < 16) {
+        u32x4 w = {0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
+        for (int i = 0; i < 15; ++i)
             w[i / 4] |= uint32_t(__builtin_amdgcn_raw_buffer_load_b8(
-                            d, i < left ? at + 16 * block + i : kNowhere, 0, 0)) << (8 * (i % 4));
+                            d, i < n && block == 0 ? at + i : kNowhere, 0, 0)) << (8 * (i % 4));
+        return w;
+    }
+    return __builtin_amdgcn_raw_buffer_load_b128(d, at, from, 0);
+}
+// Exponents 16·block .. out of what came for them.
+template <bool kEven>
+__device__ __forceinline__ u32x4 in_place(u32x4 w, int block, int n) {
+    if constexpr (!kEven) {
+        const int left = n - 16 * block, off = n < 16 || left >= 16 ? 0 : 16 - left;   // bytes
+        uint64_t lo = uint64_t(w[1]) << 32 | w[0], hi = uint64_t(w[3]) << 32 | w[2];
+        if (off >= 8) {
+            lo = off >= 16 ? 0 : hi >> (8 * (off - 8));
+            hi = 0;
+        } else if (off > 0) {
+            lo = lo >> (8 * off) | hi << (64 - 8 * off);
+            hi >>= 8 * off;
+        }
+        w = u32x4{uint32_t(lo), uint32_t(lo >> 32), uint32_t(hi), uint32_t(hi >> 32)};
     }
     return w;
 }
@@ -260,8 +279,7 @@ __device__ __forceinline__ bool tile_of(int64_t tiles_m, int64_t tiles_n, int64_
     return true;
 }
 
-// Rows behind the last one are behind the descriptor's end.  A wave whose columns all exist, on rows
-// that start on 4 bytes, turns 32 rows of 128 bytes at a time in LDS (`own`: 4 KB of the wave's, twice)
+// Rows behind the last one are behind the descriptor's end.  A wave whose columns all exist turns 32 rows of 128 bytes at a time in LDS (`own`: 4 KB of the wave's, twice)
 // and stores whole lines; where the lines are memory's own, past the caches, which keep x and w
 // instead.  16384 x 10240 x 2560: 278 us with 16 bytes of a row to a lane, 257 so, 250 past the caches
 // (which made the pieces of 16 bytes slower, 480).
@@ -271,8 +289,9 @@ __device__ __forceinline__ void store_tile(const Mx4Launch& p, int64_t m0, int64
     const int row = lane & 31, g = lane >> 5;
     const int N = int(p.N), el = p.y_dtype == SS_F32 ? 4 : 2;
     const __amdgpu_buffer_rsrc_t dy = rows_from(p.y, m0, p.M, 64 * kM, int64_t(N) * el);
+    char* rows = static_cast<char*>(p.y) + m0 * N * el;
     const int c0 = int(n0) + 64 * wn, n = c0 + 8 * g;
-    const bool wide = c0 + 64 <= N && (el == 4 || N % 2 == 0), whole = N * el % 128 == 0;
+    const bool wide = c0 + 64 <= N, whole = N * el % 128 == 0, words = N * el % 4 == 0;
 #pragma unroll
     for (int t = 0; t < kM; ++t) {
         const int top = 32 * kM * wm + 32 * t, m = top + row;
@@ -319,7 +338,8 @@ __device__ __forceinline__ void store_tile(const Mx4Launch& p, int64_t m0, int64
                     const u32x4 w = at[8 * r + (piece ^ (r & 7))];
                     const int to = ((top + r) * N + c0) * el + 128 * half + 16 * piece;
                     if (whole) __builtin_amdgcn_raw_buffer_store_b128(w, dy, to, 0, kPast);
-                    else __builtin_amdgcn_raw_buffer_store_b128(w, dy, to, 0, 0);
+                    else if (words) __builtin_amdgcn_raw_buffer_store_b128(w, dy, to, 0, 0);
+                    else if (m0 + top + r < p.M) __builtin_memcpy(rows + to, &w, 16);   // (any 2 bytes)
                 }
             }
             continue;
@@ -398,10 +418,12 @@ __global__ __launch_bounds__(256, 2) void mx4_tile_kernel(const Mx4Launch p, int
     };
     auto keep_e = [&](int block) {      // 0 behind a row's end: the codes there are 0 as well
 #pragma unroll
-        for (int i = 0; i < kLoadE; ++i)
+        for (int i = 0; i < kLoadE; ++i) {
+            const u32x4 w = in_place<kEven>(re[i], block, kb);
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-                sh.e[block & 1][c][tid + 256 * i] = 4 * (4 * block + c) < kb ? re[i][c] : 0;
+                sh.e[block & 1][c][tid + 256 * i] = 4 * (4 * block + c) < kb ? w[c] : 0;
+        }
     };
 
     // Operands of a wave are the first + a constant: dealt() and 32 t leave the bits of the turns alone.

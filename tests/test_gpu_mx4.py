@@ -83,7 +83,8 @@ SHAPES = [(1, 1, 32), (1, 16, 64), (1, 40, 128), (2, 17, 96), (16, 48, 544), (17
 TILES = [(33, 10241, 96), (65, 5130, 640), (100, 5250, 160), (129, 3500, 416), (257, 2100, 1056), (511, 1285, 32),
          (1025, 610, 288), (5200, 128, 64), (5121, 131, 256), (700, 1024, 2560),
          (1090, 2050, 96), (1300, 1700, 288), (1100, 1920, 512), (2113, 1025, 544), (40, 33000, 96),
-         (2177, 2100, 96), (4200, 1030, 160), (2304, 2048, 640), (8200, 515, 32), (2500, 1793, 1152)]
+         (2177, 2100, 96), (4200, 1030, 160), (2304, 2048, 640), (8200, 515, 32), (2500, 1793, 1152),
+         (700, 1100, 2592), (130, 5203, 1632), (64, 10241, 608), (2300, 2049, 736)]
 
 
 @pytest.mark.parametrize("x", ["mx4", "fp8"])
@@ -183,7 +184,7 @@ def test_rows_stay_apart(gpu):
     """NaN in a row of x (a block's exponent, a code, a scale) or of the weights stays in its row or
     column."""
     import torch
-    for M, N, K in ((20, 40, 256), (300, 200, 320), (3400, 200, 320), (4000, 192, 256), (10000, 290, 160)):
+    for M, N, K in ((20, 40, 256), (300, 200, 320), (3400, 200, 320), (4000, 192, 256), (10000, 290, 160), (4000, 193, 1056), (5000, 211, 864)):
         wq, we = weights(3, N, K)
         xq, xe = weights(4, M, K)
         y = gpu.ss_mx4_mm(cuda(xq), cuda(xe), cuda(wq), cuda(we))
