@@ -116,12 +116,19 @@ inline int make_ln_plan(const ss_ln_dims& d, bool backward, RmsPlan* out) {
     }
     const int64_t wg_rows = p.threads >= 256 ? 1 : 256 / p.threads;
     const int64_t need = (p.M + wg_rows - 1) / wg_rows;
-    // (a gradient's workgroups each write two rows of sums: 256 or 512 of them, us, bfloat16 / float32,
-    // 8192 wide 68 and 73 / 94 and 99, 16384 96 and 109 / 182 and 196)
-    const int64_t most = backward && p.pieces * p.threads >= 768 ? 256
-                         : p.threads >= 512                      ? 512
-                         : backward                              ? 1024
-                                                                 : 2048;
+    // A gradient's workgroups each write two rows of sums; as many as run at once.  us, bfloat16 / float32
+    // (rows times width 2^25 / 2^24), of 768, 1024, 1280, 1536 and 2048 of them:
+    //   512 wide 67 58 53 51 64 / 46 44 45 47 51    1472  92 76 66 62 81 / 57 51 51 50 59
+    //   1471    116 103 91 121 109 / 65 60 58 75 68  1024  55 51 67 62 57 / 43 46 50 49 51
+    //   2560     66 57 77 70 76 / 49 48 61 58 61     3000  63 77 74 82 78 / 65 59 62 61 64
+    // 256 and 512 of them: 8192 wide 68 and 73 / 94 and 99, 16384 96 and 109 / 182 and 196.
+    int64_t most = p.threads >= 512 ? 512 : 2048;
+    if (backward) {
+        if (p.pieces * p.threads >= 768) most = 256;
+        else if (p.pieces == 1 && p.threads <= 256) most = p.D % 8 == 0 ? 1536 : 1280;
+        else if (p.threads == 384 && p.D % 8 == 0 && d.in_dtype == SS_BF16) most = 768;
+        else if (p.threads < 512) most = 1024;
+    }
     p.grid = int(need < most ? need : most);
     p.total = backward ? align256(size_t(p.grid) * size_t(2 * p.D) * sizeof(float)) : 0;
     *out = p;

@@ -9,8 +9,8 @@
 // bounds both directions: 16384 rows of 2560 bfloat16, r = x + res, 335 MB, 71 us (4.7 TB/s; a copy
 // 5.06); gradient, with dr, 335 MB, 76 us (4.4 TB/s), 5 of them the sum of the workgroups' partial dw and db.
 // One row takes 3.3 us, a launch's own time and two rounds of memory latency.
-// Rows of odd widths start anywhere and end inside a piece: 26512 x 1471 79 us, gradient 118 (1472: 60 and
-// 87); 181 and 185 with the last elements one by one.
+// Rows of odd widths start anywhere and end inside a piece: 26155 x 1471 76 us, gradient 101 (1472: 59 and
+// 70); 181 and 185 with the last elements one by one.
 #include "ss_norm_rows.h"
 
 namespace ss {
