@@ -78,7 +78,7 @@ SHAPES = [(1, 1, 32), (1, 16, 64), (1, 40, 128), (2, 17, 96), (16, 48, 544), (17
           (33, 5121, 96), (40, 5250, 640), (65, 2600, 160), (100, 2688, 1024), (129, 1801, 416), (257, 1100, 544),
           (300, 1030, 1056), (511, 640, 32), (512, 1024, 128), (700, 500, 672), (1025, 385, 288),
           (2050, 160, 384), (5200, 64, 64), (5121, 65, 256), (700, 513, 2560)]
-# N · ceil(M / 64) of 10240 and more go in tiles of 64 rows of x; more than 256 tiles of 64 in tiles of 128,
+# N · ceil(M / 64) of 7680 and more go in tiles of 64 rows of x; more than 256 tiles of 64 in tiles of 128,
 # and of x in 4 bits, with more than 256 tiles of 128, of 256
 TILES = [(33, 10241, 96), (65, 5130, 640), (100, 5250, 160), (129, 3500, 416), (257, 2100, 1056), (511, 1285, 32),
          (1025, 610, 288), (5200, 128, 64), (5121, 131, 256), (700, 1024, 2560),
