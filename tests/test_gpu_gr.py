@@ -464,3 +464,37 @@ def test_short_texts_equal_single_tokens(gpu):
         yt = gpu.ss_gr_step(p["x"][:, t], p["r"][:, t], p["i"][:, t], p["lam"], own)
         assert torch.equal(yt, y[:, t])
     assert torch.equal(own, h)
+
+
+def test_graphs_that_share_a_workspace(gpu):
+    """Two captured calls of different sizes and an eager one take turns on one workspace, whatever the one
+    before left in it."""
+    import torch
+    note("gr shared workspace")
+    a, b = make(21, 2, 1500, 130, "bf16", reset=True), make(22, 3, 700, 260, "f32")
+    args = lambda p: (p["x"], p["r"], p["i"], p["lam"])  # noqa: E731
+
+    def fwd(ws):
+        return gpu.ss_gr_fwd(*args(a), a["h0"], reset=a["reset"], workspace=ws)
+
+    def bwd(ws):
+        g = gpu.ss_gr_bwd(*args(b), b["dy"], b["h0"], b["dh"], workspace=ws)
+        return [g[n] for n in sorted(g)]
+    want_y, want_g = fwd(None), bwd(None)
+    ws = torch.zeros(1 << 24, dtype=torch.uint8, device="cuda")
+    one, two = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(one):
+        y = fwd(ws)
+    with torch.cuda.graph(two):
+        g = bwd(ws)
+    for n in range(5):
+        ws.fill_((0, 255, 1, 128, 77)[n])
+        for graph in ((one, two), (two, one, one), (two, two, one))[n % 3]:
+            graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want_y) and all(torch.equal(s, t) for s, t in zip(g, want_g))
+        y.zero_()
+        one.replay()
+        assert torch.equal(fwd(ws), want_y)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want_y)
