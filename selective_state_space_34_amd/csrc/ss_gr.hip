@@ -502,7 +502,7 @@ __global__ __launch_bounds__(256) void gr_walk_kernel(const GrLaunch p) {
 
 // The states before a wave's tokens come from the checkpoint that its workgroup's tile starts
 // with; the adjoint c comes from the right: the chain's first tile is the row's last.
-template <typename T, bool kVec, int kWaves, int kS>
+template <typename T, bool kVec, int kWaves, int kS, int kGroup>
 __global__ __launch_bounds__(64 * kWaves) void gr_bwd_kernel(const GrLaunch p) {
     static_assert(kWaves * kS == SS_GR_CKPT, "a tile is what one checkpoint starts");
     __shared__ Shared<kWaves> sh;
@@ -582,7 +582,7 @@ __global__ __launch_bounds__(64 * kWaves) void gr_bwd_kernel(const GrLaunch p) {
             h[j] = through(sh.A[w][l], sh.H[w][l], h[j]);
         }
     }
-    link<kVec, true, kGrBwdGroup, kWaves>(p, at, col, lane, wave, sh, G, p.dh_final, p.dh0);
+    link<kVec, true, kGroup, kWaves>(p, at, col, lane, wave, sh, G, p.dh_final, p.dh0);
 #pragma unroll
     for (int j = 0; j < 2; ++j) c[j] = sh.in[wave][spot<kVec>(lane, j)];
     // From here on x, dy, σ(r) and their products are formed once more from the packed values: kept
@@ -729,8 +729,12 @@ hipError_t launch_gr_fwd(const GrLaunch& p, hipStream_t s) {
 
 hipError_t launch_gr_bwd(const GrLaunch& p, hipStream_t s) {
     const hipError_t e = with_type(p.in_dtype, p.vec, [&](auto t, auto v) {
-        hipLaunchKernelGGL((gr_bwd_kernel<decltype(t), decltype(v)::value, kBwdWaves, SS_GR_CKPT / kBwdWaves>),
-                           dim3(groups(p.D) * unsigned(p.B) * unsigned(p.tiles)), dim3(64 * kBwdWaves), 0, s, p);
+        constexpr int kS = SS_GR_CKPT / kBwdWaves;
+        const dim3 grid(groups(p.D) * unsigned(p.B) * unsigned(p.tiles)), block(64 * kBwdWaves);
+        if (p.group == kGrBwdLong)
+            hipLaunchKernelGGL((gr_bwd_kernel<decltype(t), decltype(v)::value, kBwdWaves, kS, kGrBwdLong>), grid, block, 0, s, p);
+        else
+            hipLaunchKernelGGL((gr_bwd_kernel<decltype(t), decltype(v)::value, kBwdWaves, kS, kGrBwdGroup>), grid, block, 0, s, p);
         return hipGetLastError();
     });
     if (e != hipSuccess) return e;

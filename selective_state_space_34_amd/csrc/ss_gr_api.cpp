@@ -55,6 +55,7 @@ GrLaunch launch(const ss_gr_dims* d, const GrPlan& p, const void* x, const void*
 
 void chain(GrLaunch* l, const ss::GrChain& c, char* ws) {
     l->tiles = int(c.tiles);
+    l->group = int(c.group);
     l->maps = l->ends = l->ticket = nullptr;
     if (c.tiles <= 1) return;
     l->ticket = reinterpret_cast<uint64_t*>(ws + c.off_ticket);

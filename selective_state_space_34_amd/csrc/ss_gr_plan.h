@@ -12,7 +12,10 @@ constexpr int kGrFwdTile = 128;                    // tokens of a workgroup, for
 // Tiles of a group.  us with 16, 24, 32 and 48: forward 8 x 2048 x 5120 (16 tiles a row) 153, 152, 147, 147,
 // 1 x 262144 x 256 160, 148, 149, 154; a training step of 4 x 4096 x 2048 with the same in both
 // directions 202, 204, 210, 214.
-constexpr int kGrFwdGroup = 32, kGrBwdGroup = 16;
+// In the gradient, twice as many tiles make twice as many links of a row's chain, which one or two
+// workgroups at a time (for 128 channels each) wait for: 1 x 262144 x 256 322 and 285 with 16 and 32, x 128 252 and 179; where there
+// are more, 2 x 131072 x 256 268 and 277.
+constexpr int kGrFwdGroup = 32, kGrBwdGroup = 16, kGrBwdLong = 32;
 
 // Whether rows are walked by a wave for each 128 channels (`waves` of them in all) rather than taken by a
 // workgroup each: 4 us and 0.22 a token against 10, or, where there are many, what their bytes take against
@@ -26,7 +29,7 @@ inline bool gr_walks(int64_t T, int64_t waves, int64_t st) {
 // What links the tiles of a row: the tiles' maps and, right behind them, the groups' ends (words of
 // 8 bytes), and a counter (tiles > 1).
 struct GrChain {
-    int64_t tiles, groups;
+    int64_t tiles, groups, group;
     size_t off_ticket, off_maps, off_ends;
 };
 
@@ -49,6 +52,7 @@ inline bool gr_strides_ok(const int64_t* s, int64_t T) {
 
 inline void gr_chain(GrPlan* p, int64_t tokens, int64_t group, size_t ticket, GrChain* c) {
     c->tiles = (p->T + tokens - 1) / tokens;
+    c->group = group;
     c->groups = (c->tiles + group - 1) / group;
     if (c->tiles <= 1) return;
     c->off_ticket = ticket;
@@ -71,8 +75,8 @@ inline int make_gr_plan(const ss_gr_dims& d, bool backward, bool given_ckpt, GrP
     p.B = d.batch; p.T = d.seqlen; p.D = d.dim;
     p.off_words = 256;
     if (!backward || !given_ckpt) gr_chain(&p, kGrFwdTile, kGrFwdGroup, 0, &p.fwd);
-    if (backward) gr_chain(&p, SS_GR_CKPT, kGrBwdGroup, 128, &p.rev);
     const int64_t cols = (p.D + 127) / 128 * p.B;
+    if (backward) gr_chain(&p, SS_GR_CKPT, cols <= 2 ? kGrBwdLong : kGrBwdGroup, 128, &p.rev);
     if (!mul_ok(cols, p.fwd.tiles + p.rev.tiles, lim) || !launch_ok(cols * p.fwd.tiles, 512) ||
         !launch_ok(cols * p.rev.tiles, 512))
         return SS_ERR_DIMS;

@@ -318,9 +318,9 @@ struct GrLaunch {
     int64_t B, T, D;
     float c;
     int in_dtype, vec;         // vec: two neighbouring channels load as one
-    int tiles;                 // of a row: kGrFwdTile tokens (forward, ss_gr_plan.h), SS_GR_CKPT (backward)
-    // where there are more than one: the tiles' maps [B, tiles, D] and, right behind them, the
-    // groups' ends [B, ceil(tiles / 32), D]; the workgroups' counter
+    int tiles, group;          // of a row: kGrFwdTile tokens (forward, ss_gr_plan.h), SS_GR_CKPT (backward)
+    // where there are more than one: the tiles' maps [B, tiles, D] and, right behind them, the ends of
+    // groups of `group` of them [B, ceil(tiles / group), D]; the workgroups' counter
     uint64_t *maps, *ends, *ticket;
     // forward
     void* y;                   // nullable

@@ -498,3 +498,11 @@ def test_graphs_that_share_a_workspace(gpu):
         assert torch.equal(fwd(ws), want_y)
         torch.cuda.synchronize()
         assert torch.equal(y, want_y)
+
+
+@pytest.mark.parametrize("shape", [(1, 2100, 40), (1, 4200, 200), (2, 2049, 10), (1, 6500, 129)], ids=str)
+def test_long_rows_of_few_channels(gpu, shape):
+    """Gradients whose chain has groups of 32 tiles: one or two columns of workgroups."""
+    note(f"gr few channels {shape}")
+    run_all(gpu, make(31, *shape, "bf16", reset=True), "bf16")
+    run_all(gpu, make(32, *shape, "f32"), "f32")
