@@ -49,24 +49,28 @@ __device__ __forceinline__ float one_less_square(float t2, float a) {
 
 // Two channels of a token as they lie in memory, through a buffer descriptor over a wave's rows:
 // what lies behind the last token loads as 0 and is not stored.  kVec: neighbours c0 + 2·lane +
-// {0, 1}, one access; else c0 + lane and c0 + 64 + lane.
+// {0, 1}, one access, which needs the elements' alignment only (8 x 2048 x 2561, bfloat16: 121 us, gradient
+// 219, with two accesses, 96 and 183 so).  2: the number of channels is odd; the lane of the last one
+// loads it as the second of a pair.  0 (a single channel): c0 + lane and c0 + 64 + lane.
 constexpr int kRsrcFlags = 0x00020000;   // raw buffer, 32-bit elements
 constexpr int kNowhere = int(0x80000000u);   // behind every descriptor's end
 
 struct Cols {
     int ch[2];           // clamped to the last channel, so that loads have a place
     bool on[2];
+    bool tail;           // kVec 2: the last channel is among the workgroup's
 };
-template <bool kVec>
+template <int kVec>
 __device__ __forceinline__ Cols columns(int64_t c0, int lane, int64_t D) {
     Cols c;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int ch = int(c0) + (kVec ? 2 * lane + j : lane + 64 * j), n = int(D);
         c.on[j] = ch < n;
-        // with kVec D is even: a pair is in or out as a whole
-        c.ch[j] = ch < n ? ch : kVec ? n - 2 + j : n - 1;
+        // with kVec 1 a pair is in or out as a whole
+        c.ch[j] = ch < n ? ch : kVec == 1 ? n - 2 + j : n - 1;
     }
+    c.tail = kVec == 2 && c0 + kCols > D;
     return c;
 }
 
@@ -77,18 +81,27 @@ __device__ __forceinline__ int wave_number() {
 }
 
 // Rows of n tokens (any number, also none) from p on, st elements apart, D wide.
-template <typename T, bool kVec>
+template <typename T, int kVec>
 struct Rows {
     __amdgpu_buffer_rsrc_t d;
-    int step, at[2];
+    int step, at[2];      // kVec 2, to store: of a pair, and of a last channel alone
+    int low;              // kVec 2, to load: bits before a last channel alone
+    bool tail;
     __device__ __forceinline__ Rows(const void* p, int64_t st, int64_t n, int64_t D, const Cols& c,
                                     bool store) {
         const int bytes = n > 0 ? int(((n - 1) * st + D) * int64_t(sizeof(T))) : 0;
         d = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, kRsrcFlags);
         step = int(st) * int(sizeof(T));
+        tail = c.tail;
+        if constexpr (kVec == 2) {
+            low = c.on[0] && !c.on[1] ? 8 * int(sizeof(T)) : 0;
+            at[0] = c.on[1] ? c.ch[0] * int(sizeof(T)) : store ? kNowhere : (int(D) - 2) * int(sizeof(T));
+            at[1] = c.on[0] && !c.on[1] ? c.ch[0] * int(sizeof(T)) : kNowhere;
+        } else {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-            at[j] = store && !c.on[j] ? kNowhere : c.ch[j] * int(sizeof(T));
+            for (int j = 0; j < 2; ++j)
+                at[j] = store && !c.on[j] ? kNowhere : c.ch[j] * int(sizeof(T));
+        }
     }
 };
 
@@ -97,11 +110,11 @@ template <> struct Two<float> {
     float v[2];
     __device__ __forceinline__ float get(int j) const { return v[j]; }
     __device__ __forceinline__ void anew() { asm volatile("" : "+v"(v[0]), "+v"(v[1])); }
-    template <bool kVec> __device__ __forceinline__ void load(const Rows<float, kVec>& r, int s) {
+    template <int kVec> __device__ __forceinline__ void load(const Rows<float, kVec>& r, int s) {
         if constexpr (kVec) {
             typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
             const u32x2 w = __builtin_amdgcn_raw_buffer_load_b64(r.d, r.at[0], s * r.step, 0);
-            v[0] = __uint_as_float(w[0]); v[1] = __uint_as_float(w[1]);
+            v[0] = __uint_as_float(kVec == 2 && r.low ? w[1] : w[0]); v[1] = __uint_as_float(w[1]);
         } else {
 #pragma unroll
             for (int j = 0; j < 2; ++j)
@@ -115,9 +128,10 @@ template <> struct Two<bf16_t> {
         return __uint_as_float(j ? w & 0xffff0000u : w << 16);
     }
     __device__ __forceinline__ void anew() { asm volatile("" : "+v"(w)); }
-    template <bool kVec> __device__ __forceinline__ void load(const Rows<bf16_t, kVec>& r, int s) {
+    template <int kVec> __device__ __forceinline__ void load(const Rows<bf16_t, kVec>& r, int s) {
         if constexpr (kVec) {
             w = __builtin_amdgcn_raw_buffer_load_b32(r.d, r.at[0], s * r.step, 0);
+            if constexpr (kVec == 2) w >>= r.low;
         } else {
             const uint32_t a = __builtin_amdgcn_raw_buffer_load_b16(r.d, r.at[0], s * r.step, 0);
             const uint32_t b = __builtin_amdgcn_raw_buffer_load_b16(r.d, r.at[1], s * r.step, 0);
@@ -126,18 +140,19 @@ template <> struct Two<bf16_t> {
     }
 };
 
-template <bool kVec>
+template <int kVec>
 __device__ __forceinline__ void store2(const Rows<float, kVec>& r, int s, float a, float b) {
     if constexpr (kVec) {
         typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
         __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(a), __float_as_uint(b)}, r.d,
                                               r.at[0], s * r.step, 0);
+        if (r.tail) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(a), r.d, r.at[1], s * r.step, 0);
     } else {
         __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(a), r.d, r.at[0], s * r.step, 0);
         __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(b), r.d, r.at[1], s * r.step, 0);
     }
 }
-template <bool kVec>
+template <int kVec>
 __device__ __forceinline__ void store2(const Rows<bf16_t, kVec>& r, int s, float a, float b) {
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
     bf16x2 h;
@@ -146,6 +161,7 @@ __device__ __forceinline__ void store2(const Rows<bf16_t, kVec>& r, int s, float
     __builtin_memcpy(&w, &h, 4);
     if constexpr (kVec) {
         __builtin_amdgcn_raw_buffer_store_b32(w, r.d, r.at[0], s * r.step, 0);
+        if (r.tail) __builtin_amdgcn_raw_buffer_store_b16(uint16_t(w), r.d, r.at[1], s * r.step, 0);
     } else {
         __builtin_amdgcn_raw_buffer_store_b16(uint16_t(w), r.d, r.at[0], s * r.step, 0);
         __builtin_amdgcn_raw_buffer_store_b16(uint16_t(w >> 16), r.d, r.at[1], s * r.step, 0);
@@ -153,9 +169,9 @@ __device__ __forceinline__ void store2(const Rows<bf16_t, kVec>& r, int s, float
 }
 
 // One row of float32 (states, partial sums): p + row·D.
-template <bool kVec>
+template <int kVec>
 __device__ __forceinline__ void store_row(float* row, const Cols& c, float a, float b) {
-    if constexpr (kVec) {
+    if constexpr (kVec == 1) {
         if (c.on[0]) *reinterpret_cast<float2*>(row + c.ch[0]) = make_float2(a, b);
     } else {
         if (c.on[0]) row[c.ch[0]] = a;
@@ -269,7 +285,7 @@ struct Shared {
     int number;
 };
 
-template <bool kVec> __device__ __forceinline__ int spot(int lane, int j) {
+template <int kVec> __device__ __forceinline__ int spot(int lane, int j) {
     return kVec ? 2 * lane + j : lane + 64 * j;
 }
 
@@ -277,7 +293,7 @@ template <bool kVec> __device__ __forceinline__ int spot(int lane, int j) {
 // the first) from `first`, the state that enters the row (nullable: 0), and stores what leaves the
 // row in `last` (nullable).  Two waves hold a channel a lane and walk over the waves' maps; the
 // others meanwhile fetch the maps of the tiles before.  All maps are in place (a barrier) before.
-template <bool kVec, bool kReverse, int kGroup, int kWaves, typename Sh>
+template <int kVec, bool kReverse, int kGroup, int kWaves, typename Sh>
 __device__ __forceinline__ void link(const GrLaunch& p, const Place& at, const Cols& col, int lane,
                                      int wave, Sh& sh, const float (&maps_h)[kWaves][kCols],
                                      const float* first, float* last) {
@@ -362,7 +378,7 @@ __device__ __forceinline__ int live_tokens(const int32_t* lengths, int64_t b, in
 
 // ---- forward ---------------------------------------------------------------------------------
 
-template <typename T, bool kVec, int kWaves, int kS>
+template <typename T, int kVec, int kWaves, int kS>
 __global__ __launch_bounds__(64 * kWaves) void gr_fwd_kernel(const GrLaunch p) {
     static_assert(SS_GR_CKPT % kS == 0, "checkpoints stand before a wave's first token");
     __shared__ Shared<kWaves> sh;
@@ -441,7 +457,7 @@ __global__ __launch_bounds__(64 * kWaves) void gr_fwd_kernel(const GrLaunch p) {
 // Short rows: a wave takes 128 channels of a row from its first token to its last, kS at a time, the next
 // ones on their way.  1024 rows of 1 token, 2560 channels, bfloat16: 15 us (a tile's workgroup for each 374),
 // of 32 tokens, 671 MB, 135 us (374).
-template <typename T, bool kVec, int kS>
+template <typename T, int kVec, int kS>
 __global__ __launch_bounds__(256) void gr_walk_kernel(const GrLaunch p) {
     const int lane = threadIdx.x & 63;
     const unsigned groups = unsigned((p.D + kCols - 1) / kCols);
@@ -502,7 +518,7 @@ __global__ __launch_bounds__(256) void gr_walk_kernel(const GrLaunch p) {
 
 // The states before a wave's tokens come from the checkpoint that its workgroup's tile starts
 // with; the adjoint c comes from the right: the chain's first tile is the row's last.
-template <typename T, bool kVec, int kWaves, int kS, int kGroup>
+template <typename T, int kVec, int kWaves, int kS, int kGroup>
 __global__ __launch_bounds__(64 * kWaves) void gr_bwd_kernel(const GrLaunch p) {
     static_assert(kWaves * kS == SS_GR_CKPT, "a tile is what one checkpoint starts");
     __shared__ Shared<kWaves> sh;
@@ -673,7 +689,7 @@ __global__ __launch_bounds__(1024) void gr_dlam_kernel(const float* __restrict__
 
 // ---- one token -------------------------------------------------------------------------------
 
-template <typename T, bool kVec>
+template <typename T, int kVec>
 __global__ __launch_bounds__(256) void gr_step_kernel(const GrStep p) {
     const int lane = threadIdx.x & 63;
     const int64_t b = int64_t(blockIdx.y) * 4 + wave_number(), D = p.D;
@@ -697,8 +713,12 @@ __global__ __launch_bounds__(256) void gr_step_kernel(const GrStep p) {
 
 template <typename F>
 hipError_t with_type(int in_dtype, int vec, F&& f) {
-    if (in_dtype == SS_BF16) return vec ? f(bf16_t{}, std::true_type{}) : f(bf16_t{}, std::false_type{});
-    return vec ? f(0.0f, std::true_type{}) : f(0.0f, std::false_type{});
+    auto typed = [&](auto t) {
+        return vec == 1   ? f(t, std::integral_constant<int, 1>())
+               : vec == 2 ? f(t, std::integral_constant<int, 2>())
+                          : f(t, std::integral_constant<int, 0>());
+    };
+    return in_dtype == SS_BF16 ? typed(bf16_t{}) : typed(0.0f);
 }
 
 constexpr int kFwdWaves = 8, kBwdWaves = SS_GR_CKPT / 8;

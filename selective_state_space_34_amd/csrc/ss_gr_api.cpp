@@ -34,12 +34,8 @@ int check(const ss_gr_dims* d, bool backward, bool given_ckpt, const void* x, co
     return SS_OK;
 }
 
-// Whether neighbouring channels of every row lie on their pairs' own size.
-bool pairs(const ss_gr_dims* d, const GrRows& x, const GrRows& r, const GrRows& i) {
-    const size_t two = d->in_dtype == SS_BF16 ? 4 : 8;
-    const int64_t odd = d->dim | x.sb | x.st | r.sb | r.st | i.sb | i.st;
-    return (odd & 1) == 0 && aligned(x.p, two) && aligned(r.p, two) && aligned(i.p, two);
-}
+// How neighbouring channels are taken (GrLaunch::vec).
+int pairs(int64_t D) { return D == 1 ? 0 : D % 2 ? 2 : 1; }
 
 GrLaunch launch(const ss_gr_dims* d, const GrPlan& p, const void* x, const void* r, const void* i,
                 const float* lam, const float* h0, const int32_t* lengths, const void* reset) {
@@ -49,7 +45,7 @@ GrLaunch launch(const ss_gr_dims* d, const GrPlan& p, const void* x, const void*
     l.i = rows(i, d->i_stride, p.T, p.D);
     l.lam = lam; l.h0 = h0; l.lengths = lengths; l.reset = static_cast<const uint8_t*>(reset);
     l.B = p.B; l.T = p.T; l.D = p.D; l.c = d->c; l.in_dtype = d->in_dtype;
-    l.vec = pairs(d, l.x, l.r, l.i);
+    l.vec = pairs(p.D);
     return l;
 }
 
@@ -168,7 +164,7 @@ int ss_gr_step(const ss_gr_dims* dims, const void* x, const void* r, const void*
     s.i = rows(i, dims->i_stride, 1, p.D);
     s.lam = lam; s.h_in = h_in; s.h_out = h_out; s.y = y;
     s.B = p.B; s.D = p.D; s.c = dims->c; s.in_dtype = dims->in_dtype;
-    s.vec = pairs(dims, s.x, s.r, s.i);
+    s.vec = pairs(p.D);
     const hipError_t e = ss::launch_gr_step(s, stream);
     return e == hipSuccess ? SS_OK : hip_fail(e);
 }

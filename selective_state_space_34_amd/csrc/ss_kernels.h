@@ -317,7 +317,7 @@ struct GrLaunch {
     const uint8_t* reset;      // nullable [B, T]
     int64_t B, T, D;
     float c;
-    int in_dtype, vec;         // vec: two neighbouring channels load as one
+    int in_dtype, vec;         // vec: two neighbouring channels load as one (2: their number is odd)
     int tiles, group;          // of a row: kGrFwdTile tokens (forward, ss_gr_plan.h), SS_GR_CKPT (backward)
     // where there are more than one: the tiles' maps [B, tiles, D] and, right behind them, the ends of
     // groups of `group` of them [B, ceil(tiles / group), D]; the workgroups' counter

@@ -506,3 +506,23 @@ def test_long_rows_of_few_channels(gpu, shape):
     note(f"gr few channels {shape}")
     run_all(gpu, make(31, *shape, "bf16", reset=True), "bf16")
     run_all(gpu, make(32, *shape, "f32"), "f32")
+
+
+@pytest.mark.parametrize("D", [1, 2, 3, 64, 127, 128, 129, 130, 255, 257])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_rows_that_start_anywhere(gpu, dt, D):
+    """Slices of wider rows, an odd number of elements apart and from the memory's beginning on; what stands
+    between them stays as it is and is not taken in."""
+    import torch
+    note(f"gr anywhere {dt} {D}")
+    for T in (5, 150):
+        p = make(D + T, 2, T, D, dt, lengths=True, reset=True)
+        for n, (before, after) in {"x": (1, 2), "r": (3, 1), "i": (2, 2 + D % 2)}.items():
+            wide = torch.full((2, T, before + D + after), float("nan"), device="cuda", dtype=p[n].dtype)
+            wide[..., before:before + D] = p[n]
+            p[n] = wide[..., before:before + D]
+        run_all(gpu, p, dt)
+        h, g = p["h0"].clone(), p["h0"].clone()
+        args = [p[n][:, 0] for n in ("x", "r", "i")]
+        assert torch.equal(gpu.ss_gr_step(*args, p["lam"], h), gpu.ss_gr_step(*[t.contiguous() for t in args], p["lam"], g))
+        assert torch.equal(h, g) and torch.isfinite(h).all()
