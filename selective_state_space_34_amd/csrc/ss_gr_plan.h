@@ -146,26 +146,29 @@ struct Mx4Plan {
     int high, waves;
 };
 
-// us, x in 4 bits / in 8:
+// us, x in 4 bits / in 8 (which takes two matrix instructions where 4 bits take one):
 // Tiles take a time of their own for a walk over K however few they are, rows a time for every 64 of
 // them and every 16 of the weights.  N x K, rows of x: with rows and with tiles.
-//   2560 x 2560,  128: 7.0 and 8.0 / 7.7 and 9.3,      192: 8.2 and 8.1 / 9.8 and 9.4
-//   10240 x 2560, 64:  10.3 and 9.3 / 12.7 and 10.2,   128: 14.9 and 9.0 / 18.4 and 10.3
-//   2560 x 10240, 128: 18.2 and 22.5 / 20.7 and 25.5,  192: 24.2 and 24.3 / 27.8 and 25.8
-//   5120 x 5120,  64:  11.1 and 13.8 / 13.1 and 14.9,  128: 17.1 and 13.2 / 20.3 and 15.2
-// Tiles of 64 and of 128 rows of x, up to 256 of them (a compute unit one) and more; of 128 and 256:
-//   2560 x 2560,  768 rows of x: 9.3 and 10.1 / 10.6 and 12.7, 1024: 12.1 and 10.4 / 14.2 and 13.6
-//   10240 x 2560, 192: 9.4 and 10.7 / 10.7 and 13.4,           256: 13.0 and 10.8 / 14.9 and 13.7
-//   x in 4 bits, 128 and 256: 10240 x 2560, 384: 11.9 and 15.4, 512: 16.9 and 15.9, 4096: 80 and 67
+//   2560 x 2560,  128: 7.0 and 8.0 / 8.4 and 14.1,      192: 8.2 and 8.1 / 10.3 and 14.3
+//   10240 x 2560, 64:  10.3 and 9.3 / 14.4 and 15.0,    128: 14.9 and 9.0 / 20.6 and 15.4
+//   2560 x 10240, 128: 18.2 and 22.5 / 24.2 and 44.0,   192: 24.2 and 24.3 / 30.0 and 44.1
+//   5120 x 5120,  64:  11.1 and 13.8 / 14.9 and 24.7,   128: 17.1 and 13.2 / 22.8 and 24.7
+//   in 8 bits:    2560 x 2560, 256: 13.7 and 14.5, 384: 17.0 and 14.9; 5120 x 5120, 192: 28.1 and 25.0
+// Tiles of 64 and of 128 rows of x, up to 256 of them (a compute unit one), in 8 bits up to 768, and more:
+//   2560 x 2560,  768 rows of x: 9.3 and 10.1 / 15.8 and 22.6, 1024: 12.1 and 10.4 / 20.9 and 23.1
+//   10240 x 2560, 192: 9.4 and 10.7 / 16.0 and 22.3,           256: 13.0 and 10.8 / 21.1 and 22.9
+//   in 8 bits:    2560 x 2560, 2048: 30.5 and 35.2, 2500: 38.7 and 34.9; 10240 x 2560, 512: 28.5 and 32.5,
+//                 768: 38.1 and 34.8, 16384: 669 and 622
+// and of 128 and 256, in 4 bits: 10240 x 2560, 384: 11.9 and 15.4, 512: 16.9 and 15.9, 4096: 80 and 67
 // Rows: as high as leaves two workgroups to a compute unit, else lower; 64 rows of x, high 4, 2, 1:
-//   2560 x 5120:  7.0, 6.8, 7.0 / 8.4, 8.2, 7.6        640 x 1024: 3.5, 3.0, 2.7 / 3.8, 3.1, 2.8
-// 8 and 16 waves where each compute unit has one workgroup: 2560 x 5120, 1 row of x, 4.4 and 3.9 / 5.3
-// and 4.4; 2560 x 10240, 7.0 and 5.4 / 9.0 and 6.5.
+//   2560 x 5120:  7.0, 6.8, 7.0 / 10.2, 10.2, 10.0     640 x 1024: 3.5, 3.0, 2.7 / 5.0, 4.2, 3.8
+// 8 and 16 waves where each compute unit has one workgroup: 2560 x 5120, 1 row of x, 4.4 and 3.9 / 5.2
+// and 5.0; 2560 x 10240, 7.0 and 5.4 / 10.3 and 7.7.
 // (A tile's rows of y stay within a descriptor's 2^31 bytes.)
 inline Mx4Plan mx4_plan(int64_t rows, int64_t n, int64_t k, bool fp8) {
-    if (rows > 32 && n * ((rows + 63) / 64) >= 7680 && n < (int64_t(1) << 20)) {
+    if (rows > 32 && n * ((rows + 63) / 64) >= (fp8 ? 12800 : 7680) && n < (int64_t(1) << 20)) {
         auto tiles = [&](int64_t high) { return (rows + 64 * high - 1) / (64 * high) * ((n + 127) / 128); };
-        return {true, tiles(1) <= 256 ? 1 : fp8 || tiles(2) <= 256 ? 2 : 4, 4};
+        return {true, tiles(1) <= (fp8 ? 768 : 256) ? 1 : fp8 || tiles(2) <= 256 ? 2 : 4, 4};
     }
     auto groups = [&](int64_t high) { return (rows + 16 * high - 1) / (16 * high) * ((n + 15) / 16); };
     if (rows > 32 && groups(4) >= 512) return {false, 4, 8};
