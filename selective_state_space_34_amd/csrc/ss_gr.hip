@@ -21,6 +21,7 @@
 #include "ss_kernels.h"
 
 #include <algorithm>
+#include <cfloat>
 
 namespace ss {
 
@@ -29,7 +30,7 @@ namespace {
 constexpr int kCols = 128;     // channels of a workgroup, two a lane
 
 // s² = 1 - a² = -(e^u - 1), u = 2 log a = 2 ln2·t2: the series of e^u - 1 for |u| < 1/4 (its rest is
-// below 5e-8 of the sum), where the difference would lose the small ones' digits.
+// below 6e-8 of the sum), where the difference would lose the small ones' digits.
 constexpr float kS1 = 1.3862943611198906f;    // (2 ln2)^n / n!
 constexpr float kS2 = 0.9609060278364028f;
 constexpr float kS3 = 0.4440328693185726f;
@@ -46,6 +47,17 @@ __device__ __forceinline__ float one_less_square(float t2, float a) {
     p = fmaf(t2, p, kS1);
     return fabsf(t2) < kSSwitch ? -t2 * p : fmaf(-a, a, 1.0f);
 }
+
+// σ(x) and 1 - σ(x), each relative to itself (a subtraction from 1 would lose the digits of an open gate's
+// rest), in one number: the smaller of the two, with a minus where it is the rest.  (Of a rest at least
+// 2^-126 stays, so that the sign does.)  What is left above a number's floor unfolds it.  s: σ(x).
+__device__ __forceinline__ float folded(float x, float& s) {
+    const float e = exp2_hw(-x * kLog2e);
+    s = rcp_hw(1.0f + e);
+    return x < 0.0f ? s : fmaf(-e, s, -0x1p-126f);
+}
+__device__ __forceinline__ float gate_of(float f) { return __builtin_amdgcn_fractf(f); }
+__device__ __forceinline__ float rest_of(float f) { return __builtin_amdgcn_fractf(-f); }
 
 // Two channels of a token as they lie in memory, through a buffer descriptor over a wave's rows:
 // what lies behind the last token loads as 0 and is not stored.  kVec: neighbours c0 + 2·lane +
@@ -525,9 +537,11 @@ __global__ __launch_bounds__(256) void gr_walk_kernel(const GrLaunch p) {
 // ---- backward --------------------------------------------------------------------------------
 
 // The states before a wave's tokens come from the checkpoint that its workgroup's tile starts
-// with; the adjoint c comes from the right: the chain's first tile is the row's last.
+// with; the adjoint c comes from the right: the chain's first tile is the row's last.  Two workgroups share a
+// compute unit where a lane has 128 registers: 4 x 4096 x 2048, bfloat16, 132 us, 168 with the 138 that the
+// compiler takes by itself (float32 has no room for two).
 template <typename T, int kVec, int kWaves, int kS, int kGroup>
-__global__ __launch_bounds__(64 * kWaves) void gr_bwd_kernel(const GrLaunch p) {
+__global__ __launch_bounds__(64 * kWaves, sizeof(T) == 2 && kVec ? 4 : 1) void gr_bwd_kernel(const GrLaunch p) {
     static_assert(kWaves * kS == SS_GR_CKPT, "a tile is what one checkpoint starts");
     __shared__ Shared<kWaves> sh;
     __shared__ float G[kWaves][kCols];
@@ -559,7 +573,7 @@ __global__ __launch_bounds__(64 * kWaves) void gr_bwd_kernel(const GrLaunch p) {
         k2[j] = rate2(p.lam[col.ch[j]], p.c);
         h[j] = p.h_ckpt[(b * p.tiles + tile) * D + col.ch[j]];
     }
-    float a[kS][2], q[kS][2], si[kS][2];
+    float a[kS][2], q[kS][2], fi[kS][2];          // fi: the input's gate, folded
     Map fwd[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}}, rev[2];
     // What stands behind a text becomes 0 (and its a 1) before anything is formed from it; a token
     // that begins a document has a = 0 and s = 1.
@@ -571,12 +585,16 @@ __global__ __launch_bounds__(64 * kWaves) void gr_bwd_kernel(const GrLaunch p) {
             if (!on) wx[s] = wd[s] = Two<T>{};
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                si[s][j] = on ? sigmoid(wi[s].get(j)) : 0.0f;
+                float sx;
+                const float f = folded(wi[s].get(j), sx);
+                fi[s][j] = on ? f : 0.0f;
+                asm volatile("" : "+v"(fi[s][j]));    // (formed here: its parts would live on)
+                if (!on) sx = 0.0f;
                 const float t2 = k2[j] * sigmoid(wr[s].get(j));
                 const float e = exp2_hw(t2);
                 a[s][j] = !on ? 1.0f : cut ? 0.0f : e;
                 q[s][j] = !on ? 0.0f : cut ? 1.0f : __builtin_amdgcn_sqrtf(one_less_square(t2, e));
-                fwd[j].H = fmaf(a[s][j], cut ? 0.0f : fwd[j].H, q[s][j] * (si[s][j] * wx[s].get(j)));
+                fwd[j].H = fmaf(a[s][j], cut ? 0.0f : fwd[j].H, q[s][j] * (sx * wx[s].get(j)));
                 fwd[j].A *= a[s][j];
             }
         }
@@ -609,13 +627,14 @@ __global__ __launch_bounds__(64 * kWaves) void gr_bwd_kernel(const GrLaunch p) {
     link<kVec, true, kGroup, kWaves>(p, at, col, lane, wave, sh, G, p.dh_final, p.dh0);
 #pragma unroll
     for (int j = 0; j < 2; ++j) c[j] = sh.in[wave][spot<kVec>(lane, j)];
-    // From here on x, dy, σ(r) and their products are formed once more from the packed values: kept
+    // From here on x, dy, both gates and their products are formed once more from the packed values: kept
     // from above, they would take 80 registers a lane.
 #pragma unroll
     for (int s = 0; s < kS; ++s) {
         wx[s].anew();
         wr[s].anew();
         wd[s].anew();
+        asm volatile("" : "+v"(fi[s][0]), "+v"(fi[s][1]));
     }
     float old[kS][2], dl[2] = {0.0f, 0.0f};
     const Rows<T, kVec> dx(static_cast<T*>(p.dx) + (b * p.T + t0) * D, D, n, D, col, true);
@@ -628,7 +647,7 @@ __global__ __launch_bounds__(64 * kWaves) void gr_bwd_kernel(const GrLaunch p) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 old[s][j] = h[j];
-                h[j] = fmaf(a[s][j], cut ? 0.0f : h[j], q[s][j] * (si[s][j] * wx[s].get(j)));
+                h[j] = fmaf(a[s][j], cut ? 0.0f : h[j], q[s][j] * (gate_of(fi[s][j]) * wx[s].get(j)));
             }
         }
 #pragma unroll
@@ -639,16 +658,18 @@ __global__ __launch_bounds__(64 * kWaves) void gr_bwd_kernel(const GrLaunch p) {
             float ox[2], orr[2], oi[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const float as = a[s][j], qs = q[s][j], xv = wx[s].get(j), sx = si[s][j];
-                const float sg = sigmoid(wr[s].get(j));
+                const float as = a[s][j], qs = q[s][j], xv = wx[s].get(j), sx = gate_of(fi[s][j]);
+                // σ(r), and σ(r)(1 - σ(r)) as its square times e^-r (0 where that is infinite)
+                const float e = exp2_hw(-wr[s].get(j) * kLog2e), sg = rcp_hw(1.0f + e);
+                const float both = fminf(e, FLT_MAX) * sg * sg;
                 const float gt = wd[s].get(j) + c[j], ag = as * gt;
                 c[j] = cut ? 0.0f : ag;
                 ox[j] = gt * qs * sx;
-                oi[j] = ox[j] * xv * (1.0f - sx);
-                // below 1e-15 the root's slope would leave float32; its share is below 1e-15 too
+                oi[j] = ox[j] * xv * rest_of(fi[s][j]);
+                // a slope past 1e15 is taken as 0: its share of the gradient is below 1e-15
                 const float slope = qs > 1e-15f ? as * rcp_hw(qs) : 0.0f;
                 const float dla = ag * fmaf(-slope, sx * xv, old[s][j]);
-                orr[j] = dla * (k2[j] * kLn2) * sg * (1.0f - sg);
+                orr[j] = dla * (k2[j] * kLn2) * both;
                 dl[j] = on && !cut ? fmaf(dla, sg, dl[j]) : dl[j];
                 if (!on) ox[j] = oi[j] = 0.0f;
                 if (!on || cut) orr[j] = 0.0f;
