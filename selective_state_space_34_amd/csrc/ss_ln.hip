@@ -113,7 +113,8 @@ __global__ __launch_bounds__(P > 256 ? P : 256) void ln_fwd_kernel(const LnLaunc
             for (int e = 0; e < 8; ++e) {
                 const float d = less<kWhole>(v[j][e], own, c, e, D);
                 sq = fmaf(d, d, sq);
-                v[j][e] -= own;
+                // (0 behind the row's end: -m·c there may be infinite, and has no part in the row's scale)
+                v[j][e] = kWhole || c.at + e < D ? v[j][e] - own : 0.0f;
             }
         }
         sq = rs.sum(sq);
