@@ -996,6 +996,20 @@ def _gr_marks(lengths, reset, B, T, device):
         _check(reset, "reset", (B, T), reset.dtype, device)
 
 
+def _check_workspace(t, device):
+    """A workspace's size is taken from its elements, so they have to be memory of the call's own device and
+    all there."""
+    import torch
+    if t is None:
+        return
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"workspace is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+
+
 def ss_gr_fwd(x, r, i, lam, h0=None, *, c=8.0, lengths=None, reset=None, return_final=False,
               return_ckpt=False, y=None, h_final=None, h_ckpt=None, workspace=None, stream=None):
     """Gated linear recurrence through the C ABI: a_t = exp(-c softplus(lam) sigmoid(r_t)),
@@ -1012,6 +1026,7 @@ def ss_gr_fwd(x, r, i, lam, h0=None, *, c=8.0, lengths=None, reset=None, return_
     dev, f32 = x.device, torch.float32
     _check(h0, "h0", (B, D), f32, dev)
     _gr_marks(lengths, reset, B, T, dev)
+    _check_workspace(workspace, dev)
     with _on(dev, stream, (x, r, i, lam, h0, lengths, reset, y, h_final, h_ckpt, workspace)):
         if y is None:
             y = x.new_empty((B, T, D))
@@ -1054,6 +1069,7 @@ def ss_gr_bwd(x, r, i, lam, dy, h0=None, dh_final=None, *, c=8.0, lengths=None, 
     _check(dh_final, "dh_final", (B, D), f32, dev)
     _check(h_ckpt, "h_ckpt", (B, -(-T // SS_GR_CKPT), D), f32, dev)
     _gr_marks(lengths, reset, B, T, dev)
+    _check_workspace(workspace, dev)
     g = {} if out is None else dict(out)
     with _on(dev, stream, (x, r, i, lam, dy, h0, dh_final, lengths, reset, h_ckpt, workspace,
                            *g.values())):
@@ -1192,6 +1208,7 @@ def ss_ln_bwd(dy, r, w, dr=None, *, eps=1e-5, bias=True, dx=None, dw=None, db=No
     dims, need = _ln_plan((M, D, _in_dtype(dy, "dy"), _in_dtype(r, "r"), SS_Q8_NONE, float(eps)), True)
     if db is not None and not bias:
         raise ValueError("db goes with bias=True")
+    _check_workspace(workspace, dev)
     with _on(dev, stream, (dy, r, w, dr, dx, dw, db, workspace)):
         if dx is None:
             dx = torch.empty_like(r)
