@@ -476,7 +476,8 @@ int ss_ln_bwd(const ss_ln_dims* dims, const void* dy, const void* r, const float
  * magnitude less two (at least 1), codes go to the nearest value, ties to the even code, and
  * values past 6 to 6.  A block that holds a NaN or an infinity has exponent 255 and zero codes. */
 typedef struct ss_mx4_dims {
-    int64_t rows, n, k;   /* k a multiple of 32 (ss_mx4_mm: below 2^23); ss_mx4_quant does not use n */
+    int64_t rows, n, k;   /* k a multiple of 32 (ss_mx4_mm: below 2^23); rows · k and n · k at most
+                             2^38; ss_mx4_quant does not use n */
     int32_t in_dtype;     /* ss_dtype of ss_mx4_quant's x */
     int32_t x_q8;         /* ss_mx4_mm's x: SS_Q4_MX, or SS_Q8_FP8 */
     int32_t y_dtype;      /* ss_dtype of y */
@@ -489,8 +490,8 @@ int ss_mx4_quant(const ss_mx4_dims* dims, const void* x, void* codes, void* exps
  *   x: codes [rows, k / 2] with x_scale its exponents [rows, k / 32] bytes, or e4m3 [rows, k] with
  *      x_scale [rows] float32, as the norms give them.
  * For any number of rows: a few, or few by the weights' number, are kept together over w, more go in
- * tiles.  ceil(rows / 256) · ceil(n / 128) < 2^24 (x in e4m3: rows / 128); for n of 2^20 and more
- * rows · n < 2^33.  Needs no workspace. */
+ * tiles.  rows · n is at most 2^38 and ceil(rows / 256) · ceil(n / 128) at most 2^24 - 8 (x in e4m3:
+ * rows / 128); for n of 2^20 and more ceil(n / 16) · ceil(rows / 64) < 2^23.  Needs no workspace. */
 int ss_mx4_mm(const ss_mx4_dims* dims, const void* x, const void* x_scale, const void* wq,
               const void* w_exps, void* y, hipStream_t stream);
 
