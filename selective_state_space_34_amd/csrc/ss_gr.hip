@@ -10,10 +10,13 @@
 //
 // Everything is read once and written once: a workgroup's tile stays in registers while it waits for
 // the state that enters it ("states from tile to tile" below).  Bound by memory, then by the vector
-// ALUs (37 instructions an element, six of them transcendental; the gradient 72): bfloat16, forward
-// 8 x 2048 x 5120, 671 MB, 147 us (4.6 TB/s; a copy 5.06), 1 x 262144 x 256, 537 MB, 150 us (3.6);
-// 4 x 4096 x 2048 with documents, forward 268 MB in 79 us, gradient 470 MB in 123 (3.8 TB/s, ALUs 57 %
-// busy).  Tiles: forward 8 waves of 16 tokens (of 8 tokens, one and a half times the waves in flight:
+// ALUs (37 instructions an element, six of them transcendental; the gradient 78, nine): bfloat16, forward
+// 8 x 2048 x 5120, 671 MB, 148 us (4.6 TB/s; a copy 5.06), 4 x 4096 x 2048 with documents, forward 268 MB in
+// 78 us, gradient 470 MB in 131 (3.6 TB/s, ALUs 58 % busy), 10 of them the words' launch and dlam's sums.
+// A long sequence of few channels waits for its chain, a link for each group of 32 tiles: 1 x 262144 x 256, 537 MB,
+// 151 us (3.6 TB/s; waves wait 57 % of their time, of the prompts' 43), gradient 288, of 128 channels 181,
+// 1.4 us for each of 128 links; dlam's 4096 rows of partial sums take 20 us of it on four workgroups.
+// Tiles: forward 8 waves of 16 tokens (of 8 tokens, one and a half times the waves in flight:
 // 169 and 191 us for the first two); gradient 8 of 8, a checkpoint's 64.  Workgroups that took one tile
 // after the other and asked for the next one's number ahead needed more registers: 165 to 185 us.
 #include "ss_device.h"

@@ -20,7 +20,8 @@ constexpr int kGrFwdGroup = 32, kGrBwdGroup = 16, kGrBwdLong = 32;
 // Whether rows are walked by a wave for each 128 channels (`waves` of them in all) rather than taken by a
 // workgroup each: 4 us and 0.22 a token against 10, or, where there are many, what their bytes take against
 // 75 ns each.  us by walk and by workgroups, 2560 channels, bfloat16: 4 rows of 32 tokens 11.1 and 10.2, of
-// 48 14 and 10; 64 rows of 48 22 and 31, of 96 37 and 34; 256 of 128 138 and 137.  st: the widest step
+// 48 14 and 10; 64 rows of 48 22 and 31, of 96 37 and 34; 256 of 128 138 and 137.  (A few rows of up to 32
+// tokens would gain up to a microsecond from workgroups; they walk, as the more usual many do.)  st: the widest step
 // from token to token; all tokens of a row, and eight more, stay within a descriptor's 2^31 bytes.
 inline bool gr_walks(int64_t T, int64_t waves, int64_t st) {
     return T <= kGrFwdTile && (T <= 32 || waves >= 16 * T) && (T + 8) * st < (int64_t(1) << 28);
@@ -105,6 +106,8 @@ inline int make_ln_plan(const ss_ln_dims& d, bool backward, RmsPlan* out) {
     if (rc != SS_OK) return rc;
     const int64_t pieces = (p.D + 7) / 8;
     const bool many = p.M >= 1024;
+    // Whole waves of threads, a piece each; 448 have no step of their own (3584 wide with 512: 11702 rows
+    // forward 69 us, as many bytes 2560 wide 70; gradient 87, 4096 wide 77).
     if (pieces <= 128) {
         p.threads = pieces <= 8 ? 8 : pieces <= 32 ? 32 : 64;
         p.pieces = pieces <= 64 ? 1 : 2;

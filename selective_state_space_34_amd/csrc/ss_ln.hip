@@ -4,13 +4,19 @@
 //   y = n·w + b                  8 bits as the RMS norm's; 4 bits: e2m1 blocks of 32 columns
 //   dx = dr + c·(w·dy - mean(w·dy) - n·mean(w·dy·n))      dw = Σ_rows dy·n      db = Σ_rows dy
 //
-// A row stays in its threads' registers from its one reading on: the mean, the sum of squares about it
-// (so that a row far from 0 keeps its digits) and the result are three walks over registers.  Memory
+// A row stays in its threads' registers from its one reading on, up to a width of 16384 forward and 8192 in the
+// gradient: the mean, the sum of squares about it (so that a row far from 0 keeps its digits) and the result
+// are three walks over registers.  (Beyond, 1024 threads leave a thread 128 registers, and some of the row and of
+// the columns' sums is kept in scratch: of the gradient 20 to 45 up to 16384 and 112 to 204 above, in rows
+// that are no multiple of 8 wide 81 to 163 and 307 to 487; forward, above 16384, 2 to 18 and 35 to 63.  bfloat16,
+// 67 MB of rows, forward and gradient: 8192 wide 49 and 68 us, 16384 55 and 97, 32768 63 and 281, where
+// scratch writes 335 MB.)  Memory
 // bounds both directions: 16384 rows of 2560 bfloat16, r = x + res, 335 MB, 71 us (4.7 TB/s; a copy
-// 5.06); gradient, with dr, 335 MB, 76 us (4.4 TB/s), 5 of them the sum of the workgroups' partial dw and db.
+// 5.06); gradient, with dr, 335 MB, 76 us (4.4 TB/s), 6 of them the sum of the workgroups' partial dw and db.
 // One row takes 3.3 us, a launch's own time and two rounds of memory latency.
-// Rows of odd widths start anywhere and end inside a piece: 26155 x 1471 76 us, gradient 101 (1472: 59 and
-// 70); 181 and 185 with the last elements one by one.
+// Rows of odd widths start anywhere and end inside a piece: 26155 x 1471 76 us, gradient 102 (1472: 59 and
+// 71; waves wait for memory 76 % of their time: pieces of a row that starts between lines touch one line more for
+// every eight, and a wave's last pieces are read twice); 181 and 185 with the last elements one by one.
 #include "ss_norm_rows.h"
 
 namespace ss {
