@@ -47,12 +47,13 @@ def test_columns_that_stand_out(gpu, shape, y_dtype):
     assert over <= 0, (float(over), float((y - want).norm() / want.norm()))
 
 
+@pytest.mark.parametrize("top", [448.0, 1.875])
 @pytest.mark.parametrize("M", [1, 33, 300, 8200])
-def test_products_of_every_size(gpu, M):
-    """One e4m3 value against one code, over all of both, beside the largest product of all and its
-    negative: the sum is the product, exactly."""
+def test_products_of_every_size(gpu, M, top):
+    """One e4m3 value against one code, over all of both, beside a large product and its negative (the
+    largest of all; the largest of values below 2): the sum is the product, exactly."""
     import torch
-    note(f"mx4 sizes {M}")
+    note(f"mx4 sizes {M} {top}")
     v = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn)
     v = v[torch.isfinite(v.float())].float()
     K, N = 64, 256
@@ -62,7 +63,7 @@ def test_products_of_every_size(gpu, M):
         codes[:, big[0]], codes[:, big[1]] = 7, 15
         x = torch.zeros(M, K)
         x[:, at] = v[torch.arange(M) % len(v)] if M > 1 else 9.0 * 2.0 ** -9
-        x[:, big[0]] = x[:, big[1]] = 448.0
+        x[:, big[0]] = x[:, big[1]] = top
         t = x.to(torch.float8_e4m3fn).cuda()
         we = np.full((N, K // 32), 127, np.uint8)
         want = num(x)[:, at:at + 1] * ref.mx4_values(codes, we.astype(np.int64))[:, at]
