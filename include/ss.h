@@ -393,9 +393,9 @@ int ss_q4_mv(const ss_q4_dims* dims, const void* x, const float* x_scale, const 
  *   reset   : NULL, or [B, T] bytes on the device: a token with a byte other than 0 begins a
  *          document: its a_t is 0 (and sqrt(1 - a_t²) is 1), nothing of the state before it, NaN
  *          and infinities included, reaches it, and no gradient comes back.
- * A state or adjoint that is NaN or infinite stays so until then (an infinity may become NaN where an
- * a_t itself is below float32's range).  States, sums and gates are float32.  Where 1 - a_t² is below 1e-30 the gradient of the square
- * root is taken as 0. */
+ * A state or adjoint that is NaN or infinite stays so until then (an infinity may become NaN where
+ * an a_t itself is below float32's range).  States, sums and gates are float32.  Where 1 - a_t² is
+ * below 1e-30 the gradient of the square root is taken as 0. */
 #define SS_GR_CKPT 64   /* tokens from one of h_ckpt's states to the next */
 
 typedef struct ss_gr_dims {
