@@ -163,6 +163,11 @@ struct Mx4Plan {
 //   in 8 bits:    2560 x 2560, 2048: 30.5 and 35.2, 2500: 38.7 and 34.9; 10240 x 2560, 512: 28.5 and 32.5,
 //                 768: 38.1 and 34.8, 16384: 669 and 622
 // and of 128 and 256, in 4 bits: 10240 x 2560, 384: 11.9 and 15.4, 512: 16.9 and 15.9, 4096: 80 and 67
+// But none taller than the rows there are, nor, in 8 bits, where a tile of 128 rows, by 5 % the cheaper, would be half
+// empty; weights of 33000 and 151936 by 2560, tiles of 64, 128 and 256 (8 bits: 64 and 128):
+//   64 rows: 18.5, 19.4, 24.7 and 62, 59, 69 / 23.3, 32.9 and 66, 88      128: 22.3, 21.8, 27.0 and 87, 66, 75 /
+//   30.9, 35.6 and 103, 99      192: 25.7, 26.9, 28.1 and 108, 94, 81 / 39.9, 51.3 and 134, 172
+//   513: 55, 46, 48 and 264, 193, 181 / 88, 95 and 371, 386
 // Rows: as high as leaves two workgroups to a compute unit, else lower; 64 rows of x, high 4, 2, 1:
 //   2560 x 5120:  7.0, 6.8, 7.0 / 10.2, 10.2, 10.0     640 x 1024: 3.5, 3.0, 2.7 / 5.0, 4.2, 3.8
 // 8 and 16 waves where each compute unit has one workgroup: 2560 x 5120, 1 row of x, 4.4 and 3.9 / 5.2
@@ -171,7 +176,12 @@ struct Mx4Plan {
 inline Mx4Plan mx4_plan(int64_t rows, int64_t n, int64_t k, bool fp8) {
     if (rows > 32 && n * ((rows + 63) / 64) >= (fp8 ? 12800 : 7680) && n < (int64_t(1) << 20)) {
         auto tiles = [&](int64_t high) { return (rows + 64 * high - 1) / (64 * high) * ((n + 127) / 128); };
-        return {true, tiles(1) <= (fp8 ? 768 : 256) ? 1 : fp8 || tiles(2) <= 256 ? 2 : 4, 4};
+        if (fp8) {
+            const bool tall = tiles(1) > 768 && 19 * ((rows + 127) / 128) < 10 * ((rows + 63) / 64);
+            return {true, tall ? 2 : 1, 4};
+        }
+        const int high = tiles(1) <= 256 ? 1 : tiles(2) <= 256 ? 2 : 4;
+        return {true, rows <= 64 ? 1 : rows <= 128 && high > 2 ? 2 : high, 4};
     }
     auto groups = [&](int64_t high) { return (rows + 16 * high - 1) / (16 * high) * ((n + 15) / 16); };
     if (rows > 32 && groups(4) >= 512) return {false, 4, 8};

@@ -121,6 +121,7 @@ void check_mx4(int64_t M, int64_t N, int64_t K) {
         if (p.tiled ? !(p.high == 1 || p.high == 2 || (p.high == 4 && !fp8))
                     : !((p.high == 4 && p.waves == 8) || ((p.high == 1 || p.high == 2) && (p.waves == 8 || p.waves == 16))))
             fail("product without a kernel", M, N, K, fp8);
+        if (p.tiled && p.high > 1 && M <= 32 * p.high) fail("a tile taller than its rows", M, N, K, fp8);
         // two stages beyond the last are asked for (and are behind the descriptor's end, or not issued)
         if (wide * row_w >= kDescriptor || tall * row_x >= kDescriptor) fail("a tile's operands", M, N, K, fp8);
         if (p.tiled && tall * N * 4 >= kDescriptor) fail("a tile's results", M, N, K, fp8);

@@ -14,10 +14,10 @@ from tests.test_gpu_mx4 import U, cuda, num
 
 pytestmark = pytest.mark.gpu
 
-# (M, N, K): rows of 16, 32 and 64 a workgroup; tiles of 64 and (the last three) 128 rows; odd sizes
+# (M, N, K): rows of 16, 32 and 64 a workgroup; tiles of 64 rows and, where there are many, of 128; odd sizes
 SHAPES = [(1, 40, 2048), (7, 300, 96), (20, 4100, 640), (40, 8200, 160), (64, 2560, 1024), (64, 7680, 160),
           (100, 5250, 672), (1100, 1920, 512), (2113, 1025, 96), (5200, 128, 128), (4500, 1500, 96),
-          (6200, 1025, 128), (3300, 2050, 672)]
+          (6200, 1025, 128), (3300, 2050, 672), (64, 99000, 64), (70, 70000, 64)]
 
 
 @pytest.mark.parametrize("y_dtype", ["bf16", "f32"])
